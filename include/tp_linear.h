@@ -216,8 +216,8 @@ int tp_attn_proj_forward(tp_linear_t* h, int64_t T, const void* x, void* qkv_out
  *     attn_out[r][:, i*hd:(i+1)*hd] = softmax(q_h k_g^T / sqrt(hd) + causal) v_g,
  *     g = the kv head of h's group (h / (nq/nkv)), held by shard r
  *   sequence s is tokens [cu_seqlens[s], cu_seqlens[s+1]); a query sees the keys of
- *   its own sequence at or before it. q and k are used as given (no positional
- *   rotation is applied).
+ *   its own sequence at or before it. q and k are used as given (tp_qk_norm_rope
+ *   rotates them).
  * qkv: [t][T][w_s] bf16, tp_attn_proj_forward's qkv_out. attn_out: [t][T][nq*hd/t]
  * bf16, the layout of tp_attn_proj_forward's attn_in. cu_seqlens: DEVICE int32
  * [n_seqs + 1], 0 = cu_seqlens[0] <= ... <= cu_seqlens[n_seqs] = T, 4-byte aligned.
@@ -231,6 +231,77 @@ int tp_attn_proj_forward(tp_linear_t* h, int64_t T, const void* x, void* qkv_out
 int tp_attention_forward(tp_linear_t* h, int64_t T, const void* qkv, const int32_t* cu_seqlens,
                          int32_t n_seqs, int32_t max_seqlen, void* attn_out, void* workspace,
                          int64_t workspace_bytes, tp_stream_t stream);
+
+/*
+ * Rotary positions, with an optional RMSNorm of every q and k head in the same pass.
+ * The pages use q and k as projected; models that rotate them call this between
+ * tp_attn_proj_forward and the attention (tp_attention_forward, tp_paged_attention,
+ * tp_tree_attention), or bind it to a layer (tp_layer_set_rope).
+ *   x' = x / sqrt(mean(x^2) + eps) * gamma     per head, where q_gamma (q heads) or
+ *                                              k_gamma (k heads) is given; else x' = x
+ *   (a, b) -> (a c - b s, b c + a s)           c = m cos(p f_i), s = m sin(p f_i)
+ * for the pairs i < rotary_dim / 2: (x'_i, x'_{i + rotary_dim/2}) in TP_ROPE_HALF,
+ * (x'_2i, x'_2i+1) in TP_ROPE_INTERLEAVED; elements from rotary_dim on are not rotated.
+ * fp32 arithmetic, one rounding to bf16.
+ *
+ * Frequencies f_i, from base^(-2i / rotary_dim), and m (tp_rope_frequencies, on the host):
+ *   TP_ROPE_SCALE_NONE    as they are
+ *   TP_ROPE_SCALE_LINEAR  f / factor (position interpolation)
+ *   TP_ROPE_SCALE_NTK     base * factor^(d / (d - 2)) in place of base, d = rotary_dim >= 4
+ *   TP_ROPE_SCALE_BANDS   with w = original_max_position f / 2 pi turns over the original
+ *                         context: f / factor where w < low_freq_factor, f where
+ *                         w > high_freq_factor, between them
+ *                         (1 - u) f / factor + u f, u = (w - low) / (high - low)
+ *   TP_ROPE_SCALE_YARN    f / factor * u + f * (1 - u), u = clamp((i - lo) / (hi - lo), 0, 1),
+ *                         lo, hi = the pair indices (rounded down, up, within [0, d - 1]) that
+ *                         make beta_fast and beta_slow turns over the original context;
+ *                         m = 0.1 ln(factor) + 1 (1 for factor <= 1)
+ * attn_factor > 0 replaces m, for every kind; 0 keeps the kind's own m (1 but for YARN).
+ *
+ * tp_rope_table fills table [n_pos][rotary_dim] fp32 (device): for every position the
+ * rotary_dim / 2 values c, then the s. Angles are computed in 64 bits. Build it once per
+ * model; a caller may also fill a table of that form itself.
+ *
+ * tp_qk_norm_rope: qkv as tp_attn_proj_forward writes it (shard-major or gathered, any
+ *   head_dim up to 256); qkv_out the same layout, either qkv itself (in place; v is left
+ *   alone) or a buffer that does not overlap it (v is copied). positions: device int32 [T];
+ *   a negative one marks a padding token: nothing is written for it. With slot_mapping
+ *   (device int32 [T], head_dim 128) the token's k and v also go to their cache slot as
+ *   tp_kv_cache_write would put them (negative: none; no slot twice in a call). A position
+ *   past the table (the token is skipped) or a slot past the cache (the cache write is
+ *   skipped) writes TP_ERR_SHAPE to the status word (workspace bytes [0, 4); 16 bytes).
+ *   slot_mapping NULL: cache_k, cache_v, num_blocks and block_size are ignored.
+ */
+enum { TP_ROPE_HALF = 0, TP_ROPE_INTERLEAVED = 1 };
+enum {
+  TP_ROPE_SCALE_NONE = 0, TP_ROPE_SCALE_LINEAR = 1, TP_ROPE_SCALE_NTK = 2, TP_ROPE_SCALE_BANDS = 3,
+  TP_ROPE_SCALE_YARN = 4
+};
+typedef struct {
+  int32_t rotary_dim;                        /* even, 2..256 */
+  int32_t scaling;                           /* TP_ROPE_SCALE_* */
+  double base;                               /* > 1 */
+  double factor;                             /* > 0; all kinds but NONE */
+  double low_freq_factor, high_freq_factor;  /* BANDS: 0 < low < high */
+  double beta_slow, beta_fast;               /* YARN: 0 < slow < fast */
+  double attn_factor;                        /* 0: the kind's own */
+  int64_t original_max_position;             /* BANDS, YARN: >= 1 */
+} tp_rope_config_t;
+typedef struct {
+  const float* table;    /* device [n_pos][rotary_dim] */
+  int64_t n_pos;
+  int32_t rotary_dim;    /* even, <= head_dim */
+  int32_t layout;        /* TP_ROPE_HALF or TP_ROPE_INTERLEAVED */
+  const void* q_gamma;   /* device [head_dim] bf16, or NULL: q heads are not normalised */
+  const void* k_gamma;
+  float eps;             /* >= 0 */
+} tp_rope_t;
+int tp_rope_frequencies(const tp_rope_config_t* cfg, double* inv_freq, double* scale);
+int tp_rope_table(const tp_rope_config_t* cfg, int64_t n_pos, float* table, tp_stream_t stream);
+int tp_qk_norm_rope(tp_linear_t* h, int64_t T, const void* qkv, void* qkv_out, const int32_t* positions,
+                    const tp_rope_t* rope, const int32_t* slot_mapping, void* cache_k, void* cache_v,
+                    int64_t num_blocks, int32_t block_size, void* workspace, int64_t workspace_bytes,
+                    tp_stream_t stream);
 
 /*
  * Paged KV cache ("vLLM Code Reading (Section 5)" §13: each rank's attention kernel
@@ -274,6 +345,75 @@ int tp_paged_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t
                        const int32_t* block_tables, int32_t max_blocks_per_req, const int32_t* slot_mapping,
                        void* cache_k, void* cache_v, int64_t num_blocks, int32_t block_size, void* attn_out,
                        void* workspace, int64_t workspace_bytes, tp_stream_t stream);
+
+/*
+ * Attention of a tree of drafted tokens over the paged cache. The drafted tokens of
+ * request b are rows [query_start_loc[b], query_start_loc[b+1]) of qkv, n of them, and its
+ * seq_lens[b] tokens count them: drafted token j is in the cache at position ctx + j,
+ * ctx = seq_lens[b] - n (written before, by tp_kv_cache_write or tp_qk_norm_rope). Token i
+ * sees positions 0 .. ctx - 1 and position ctx + j for every j < n whose bit is set in its
+ * mask row: bit j % 32 of word tree_mask[i][j / 32] (int32 [T][mask_words], 32 * mask_words
+ * >= max_query_len). Any mask is legal, not only a tree's; a token that sees nothing gets 0.
+ * What it does not see has no effect on it, NaN and infinities included. Other arguments,
+ * layouts, bounds and errors as for tp_paged_attention; max_query_len <= TP_TREE_MAX_DRAFT.
+ * Rows of attn_out that belong to no request are left as they were. Scores, softmax and
+ * sums in fp32, P rounded to bf16 for the P V product, output rounded to bf16. The
+ * workspace (tp_tree_attention_workspace_size; caller-owned, ZERO-FILLED before first use)
+ * holds the status word and partial results.
+ *
+ * tp_tree_mask: the mask rows and positions of trees. parents[i] (int32 [T], device) is the
+ * index of token i's parent among its request's drafted tokens, less than its own, or -1: a
+ * child of the last cached token. Token i's row gets its ancestors' bits and its own;
+ * positions[i] (may be NULL) = ctx + its depth, the position to rotate it by. A parent that
+ * does not come before its child writes TP_ERR_SHAPE to the status word (workspace bytes
+ * [0, 4); 16 bytes); that token and its descendants get an empty row and position -1. A
+ * request whose counts do not fit (more than max_query_len or fewer than 0 tokens, rows
+ * outside [0, T), seq_lens[b] < n) does too, and its rows are left as they were.
+ */
+#define TP_TREE_MAX_DRAFT 256
+int tp_tree_mask(int64_t T, int32_t n_reqs, int32_t max_query_len, const int32_t* parents,
+                 const int32_t* query_start_loc, const int32_t* seq_lens, int32_t* tree_mask, int32_t mask_words,
+                 int32_t* positions, void* workspace, int64_t workspace_bytes, tp_stream_t stream);
+int tp_tree_attention_workspace_size(const tp_linear_t* h, int32_t n_reqs, int32_t max_query_len,
+                                     int32_t max_seq_len, int64_t* bytes);
+int tp_tree_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t* query_start_loc,
+                      const int32_t* seq_lens, int32_t n_reqs, int32_t max_query_len, int32_t max_seq_len,
+                      const int32_t* block_tables, int32_t max_blocks_per_req, const int32_t* tree_mask,
+                      int32_t mask_words, const void* cache_k, const void* cache_v, int64_t num_blocks,
+                      int32_t block_size, void* attn_out, void* workspace, int64_t workspace_bytes,
+                      tp_stream_t stream);
+
+/*
+ * Pages moved inside the cache, in the caches of n_layers layers (1..TP_KV_MAX_LAYERS) in
+ * one launch. caches_k, caches_v: HOST arrays of n_layers device pointers, each a cache of
+ * the layout above. Copies, bit-exact. head_dim 128. Status: workspace bytes [0, 4); 16 bytes.
+ *
+ * tp_kv_cache_copy_blocks: for every pair (src, dst) of block_pairs (device int32
+ *   [n_pairs][2], 8-byte aligned) block dst = block src, k and v of every shard and layer
+ *   (forks, copy on write, defragmentation). src < 0 = padding entry. An id past the cache or
+ *   dst < 0 writes TP_ERR_SHAPE and skips the pair. A block that is a dst appears in no other
+ *   pair of the call, as src or dst; a src may repeat.
+ * tp_kv_cache_compact: keeps the accepted path of every request's drafted tokens.
+ *   query_start_loc, seq_lens as for tp_tree_attention; accepted[b] (device int32
+ *   [n_reqs][max_accepted]) lists rising draft indices, ended by a negative one or the row's
+ *   end. k and v at position ctx + accepted[b][j] of block table src_tables[b] go to position
+ *   ctx + j of dst_tables[b] (both int32 [n_reqs][max_blocks_per_req], device), and
+ *   new_seq_lens[b] = ctx + the number kept (may not be seq_lens itself). The tables may be
+ *   the same array (in place); where they differ, a slot that is written is read by no entry
+ *   of the call but one that moves within its own request's pages. An index that does not
+ *   rise, is past the request's drafts or whose block id is out of range writes TP_ERR_SHAPE
+ *   and ends the request's list there; a request whose counts do not fit (fewer than 0
+ *   drafts, seq_lens[b] below them or past the tables) also does and keeps its length.
+ */
+#define TP_KV_MAX_LAYERS 128
+int tp_kv_cache_copy_blocks(tp_linear_t* h, const int32_t* block_pairs, int32_t n_pairs, int32_t n_layers,
+                            void* const* caches_k, void* const* caches_v, int64_t num_blocks, int32_t block_size,
+                            void* workspace, int64_t workspace_bytes, tp_stream_t stream);
+int tp_kv_cache_compact(tp_linear_t* h, int32_t n_reqs, const int32_t* query_start_loc, const int32_t* seq_lens,
+                        const int32_t* accepted, int32_t max_accepted, const int32_t* src_tables,
+                        const int32_t* dst_tables, int32_t max_blocks_per_req, int32_t n_layers,
+                        void* const* caches_k, void* const* caches_v, int64_t num_blocks, int32_t block_size,
+                        int32_t* new_seq_lens, void* workspace, int64_t workspace_bytes, tp_stream_t stream);
 
 /*
  * Mixture-of-experts block with within-expert tensor parallelism ("Tensor
@@ -339,6 +479,15 @@ typedef struct {
 int tp_layer_create(tp_linear_t* attn, tp_linear_t* mlp, int64_t max_tokens, tp_layer_t** out);
 int tp_layer_destroy(tp_layer_t* layer);
 int tp_layer_workspace_size(const tp_layer_t* layer, int64_t* bytes);
+/*
+ * Bind rotary positions (and the norms of q and k heads) to a layer: from now on
+ * tp_decoder_layer_forward runs tp_qk_norm_rope in place between the QKV projection and the
+ * attention core, token i at positions[i] (device int32 [max_tokens], the first T read at
+ * every call; negative: q and k of the token stay as projected, past the table: the same, and
+ * TP_ERR_SHAPE in the status word). The structure is copied; its arrays and `positions` are
+ * borrowed. rope NULL: no rotation again.
+ */
+int tp_layer_set_rope(tp_layer_t* layer, const tp_rope_t* rope, const int32_t* positions);
 int tp_decoder_layer_forward(tp_layer_t* layer, int64_t T, const tp_layer_io_t* io, void* workspace,
                              int64_t workspace_bytes, tp_stream_t stream);
 

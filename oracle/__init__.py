@@ -30,7 +30,10 @@ mixture-of-experts block whose experts are split by the same column/row
 pattern (within-expert tensor parallelism); its routing is an input.
 ``kv_cache.py`` is the paged KV cache: the write of each new token's keys and
 values to its slot, and attention of new tokens over their requests' cached
-keys through the block tables.
+keys through the block tables. ``rope.py`` rotates q and k by their positions
+(and norms their heads); ``drafts.py`` is attention of drafted token trees over
+the paged cache and the moves of pages inside it. The pages define neither:
+both are the published formulas.
 
 Every function computes in float64 from bf16 inputs converted exactly. Where
 the block has a plain definition (the unsharded Y = XW, SiLU, RMSNorm, row
@@ -53,3 +56,5 @@ from .attention import attention_core, attention_rows, kv_head_of  # noqa: F401
 from .decoder_layer import decoder_layer  # noqa: F401
 from .moe import moe_block, moe_block_tp  # noqa: F401
 from .kv_cache import kv_cache_write, paged_attention, slot_of  # noqa: F401
+from .rope import rope_frequencies, qk_norm_rope  # noqa: F401
+from .drafts import tree_sees, mask_words, tree_attention, copy_blocks, compact  # noqa: F401

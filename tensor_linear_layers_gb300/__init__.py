@@ -23,6 +23,10 @@ TP_ERR_ARG, TP_ERR_SHAPE, TP_ERR_UNSUPPORTED, TP_ERR_CUDA, TP_ERR_CAPACITY, TP_E
 TP_BLOCK_MLP, TP_BLOCK_ATTN_PROJ, TP_BLOCK_MOE = 0, 1, 2
 TP_FLAG_HAS_NORM = 1
 TP_FLAG_GATHERED = 2
+TP_ROPE_HALF, TP_ROPE_INTERLEAVED = 0, 1
+TP_TREE_MAX_DRAFT = 256
+TP_KV_MAX_LAYERS = 128
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
 
 ABI_SYMBOLS = (
     "tp_packed_weight_bytes", "tp_linear_create", "tp_linear_destroy", "tp_workspace_size",
@@ -31,6 +35,8 @@ ABI_SYMBOLS = (
     "tp_describe_plan", "tp_mlp_forward_no_alloc", "tp_set_wait_timeout", "tp_attention_forward",
     "tp_layer_create", "tp_layer_destroy", "tp_layer_workspace_size", "tp_decoder_layer_forward",
     "tp_moe_forward", "tp_kv_cache_write", "tp_paged_attention_workspace_size", "tp_paged_attention",
+    "tp_rope_frequencies", "tp_rope_table", "tp_qk_norm_rope", "tp_layer_set_rope", "tp_tree_mask",
+    "tp_tree_attention_workspace_size", "tp_tree_attention", "tp_kv_cache_copy_blocks", "tp_kv_cache_compact",
 )
 
 
@@ -53,6 +59,19 @@ class LayerIO(ctypes.Structure):
                 ("residual_attn", ctypes.c_void_p), ("attn_out", ctypes.c_void_p),
                 ("residual_mlp", ctypes.c_void_p), ("mlp_out", ctypes.c_void_p),
                 ("residual_stream", ctypes.c_void_p)]
+
+
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("low_freq_factor", ctypes.c_double),
+                ("high_freq_factor", ctypes.c_double), ("beta_slow", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("attn_factor", ctypes.c_double), ("original_max_position", ctypes.c_int64)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_pos", ctypes.c_int64), ("rotary_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("q_gamma", ctypes.c_void_p), ("k_gamma", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
 
 
 class GemmPlan(ctypes.Structure):
@@ -101,6 +120,17 @@ def lib() -> ctypes.CDLL:
         "tp_kv_cache_write": [P, I64, P, P, P, P, I64, I32, P, I64, P],
         "tp_paged_attention_workspace_size": [P, I32, I32, I32, PI64],
         "tp_paged_attention": [P, I64, P, P, P, I32, I32, I32, P, I32, P, P, P, I64, I32, P, P, I64, P],
+        "tp_rope_frequencies": [ctypes.POINTER(RopeConfig), ctypes.POINTER(ctypes.c_double),
+                                ctypes.POINTER(ctypes.c_double)],
+        "tp_rope_table": [ctypes.POINTER(RopeConfig), I64, P, P],
+        "tp_qk_norm_rope": [P, I64, P, P, P, ctypes.POINTER(RopeArgs), P, P, P, I64, I32, P, I64, P],
+        "tp_layer_set_rope": [P, ctypes.POINTER(RopeArgs), P],
+        "tp_tree_mask": [I64, I32, I32, P, P, P, P, I32, P, P, I64, P],
+        "tp_tree_attention_workspace_size": [P, I32, I32, I32, PI64],
+        "tp_tree_attention": [P, I64, P, P, P, I32, I32, I32, P, I32, P, I32, P, P, I64, I32, P, P, I64, P],
+        "tp_kv_cache_copy_blocks": [P, P, I32, I32, ctypes.POINTER(P), ctypes.POINTER(P), I64, I32, P, I64, P],
+        "tp_kv_cache_compact": [P, I32, P, P, P, I32, P, P, I32, I32, ctypes.POINTER(P), ctypes.POINTER(P), I64, I32,
+                                P, P, I64, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -133,6 +163,32 @@ def _bf16(t: torch.Tensor, name: str) -> torch.Tensor:
     if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA bf16 tensor")
     return t
+
+
+def _i32(t: torch.Tensor, name: str, device: torch.device, numel: int = -1) -> int:
+    """Device pointer of a contiguous int32 tensor on `device` (of `numel` elements at least)."""
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 tensor on {device}")
+    if t.numel() < numel:
+        raise ValueError(f"{name} has {t.numel()} elements, {numel} needed")
+    return t.data_ptr()
+
+
+def _bf16_on(t: torch.Tensor, name: str, device: torch.device, shape=None) -> int:
+    """Device pointer of a contiguous bf16 tensor on `device` (of this shape)."""
+    if t.dtype != torch.bfloat16 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous bf16 tensor on {device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _workspace(ws: Optional[torch.Tensor], need: int, device: torch.device) -> torch.Tensor:
+    if ws is None:
+        return torch.zeros(need, dtype=torch.uint8, device=device)
+    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
+    return ws
 
 
 def make_config(kind: int, t: int, hidden: int, intermediate: int = 0, n_q_heads: int = 0,
@@ -291,6 +347,129 @@ class TPLinear:
         kv_per = 1 if c.t >= c.n_kv_heads else c.n_kv_heads // c.t
         return (c.t, num_blocks, block_size, kv_per, c.head_dim)
 
+    @property
+    def _qkv_width(self) -> int:
+        c = self.cfg
+        kv_per = 1 if c.t >= c.n_kv_heads else c.n_kv_heads // c.t
+        return (c.n_q_heads // c.t + 2 * kv_per) * c.head_dim
+
+    def _qkv_shape(self, T: int):
+        w, t = self._qkv_width, self.cfg.t
+        return (T, t * w) if self.gathered else (t, T, w)
+
+    def _layer_pointers(self, caches_k: Sequence[torch.Tensor], caches_v: Sequence[torch.Tensor]):
+        """HOST pointer arrays of the layers' caches (all of one shape), and that shape's blocks and block size."""
+        if len(caches_k) != len(caches_v) or not caches_k:
+            raise ValueError("caches_k and caches_v must list the same layers, one at least")
+        shape = caches_k[0].shape
+        if len(shape) != 5 or shape != self.kv_cache_shape(shape[1], shape[2]):
+            raise ValueError(f"a cache has the shape of kv_cache_shape(), not {tuple(shape)}")
+        dev, n = self.w_col.device, len(caches_k)
+        ks = (ctypes.c_void_p * n)(*[_bf16_on(c, "cache_k", dev, shape) for c in caches_k])
+        vs = (ctypes.c_void_p * n)(*[_bf16_on(c, "cache_v", dev, shape) for c in caches_v])
+        return n, ks, vs, shape[1], shape[2]
+
+    def qk_norm_rope(self, qkv: torch.Tensor, positions: torch.Tensor, rope: "Rope", out: Optional[torch.Tensor] = None,
+                     slot_mapping: Optional[torch.Tensor] = None, cache_k: Optional[torch.Tensor] = None,
+                     cache_v: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None):
+        """Per-head norm (where the Rope has gammas) and rotation of q and k at positions (int32 [T],
+        negative = padding); out: a new tensor of qkv's shape, or qkv itself (in place). With slot_mapping
+        (int32 [T], negative = none) k and v also go to their cache slots. Returns (out, 16-byte workspace
+        whose first word is the status)."""
+        dev = self.w_col.device
+        T = qkv.shape[0] if self.gathered else qkv.shape[1]
+        src = _bf16_on(qkv, "qkv", dev, self._qkv_shape(T))
+        if out is None:
+            out = torch.empty_like(qkv)
+        ws = _workspace(ws, 16, dev)
+        ck = cv = slots = None
+        nb = bs = 0
+        if slot_mapping is not None:
+            if cache_k is None or cache_v is None:
+                raise ValueError("slot_mapping needs cache_k and cache_v")
+            slots = _i32(slot_mapping, "slot_mapping", dev, T)
+            nb, bs = cache_k.shape[1], cache_k.shape[2]
+            shape = self.kv_cache_shape(nb, bs)
+            ck, cv = _bf16_on(cache_k, "cache_k", dev, shape), _bf16_on(cache_v, "cache_v", dev, shape)
+        if rope.table.device != dev:
+            raise ValueError(f"the rope table is on {rope.table.device}, not {dev}")
+        _check(lib().tp_qk_norm_rope(self.handle, T, src, _bf16_on(out, "out", dev, qkv.shape),
+                                     _i32(positions, "positions", dev, T), rope.args, slots, ck, cv, nb, bs,
+                                     ws.data_ptr(), ws.numel(), _stream(stream)))
+        return out, ws
+
+    def kv_cache_copy_blocks(self, block_pairs: torch.Tensor, caches_k: Sequence[torch.Tensor],
+                             caches_v: Sequence[torch.Tensor], ws: Optional[torch.Tensor] = None,
+                             stream=None) -> torch.Tensor:
+        """Copy block src to block dst for every (src, dst) row of block_pairs (int32 [n, 2], src < 0 = skip)
+        in the caches of all listed layers. Returns the workspace whose first word is the status."""
+        if block_pairs.dim() != 2 or block_pairs.shape[1] != 2:
+            raise ValueError("block_pairs must be [n, 2]")
+        dev = self.w_col.device
+        n, ks, vs, nb, bs = self._layer_pointers(caches_k, caches_v)
+        ws = _workspace(ws, 16, dev)
+        _check(lib().tp_kv_cache_copy_blocks(self.handle, _i32(block_pairs, "block_pairs", dev), block_pairs.shape[0],
+                                             n, ks, vs, nb, bs, ws.data_ptr(), ws.numel(), _stream(stream)))
+        return ws
+
+    def kv_cache_compact(self, query_start_loc: torch.Tensor, seq_lens: torch.Tensor, accepted: torch.Tensor,
+                         src_tables: torch.Tensor, dst_tables: torch.Tensor, caches_k: Sequence[torch.Tensor],
+                         caches_v: Sequence[torch.Tensor], out: Optional[torch.Tensor] = None,
+                         ws: Optional[torch.Tensor] = None, stream=None):
+        """Move the accepted drafted tokens of every request (accepted int32 [n_reqs, m], rising draft
+        indices, ended by -1) from src_tables' pages to the positions after the cached tokens in dst_tables'
+        (the same tensor: in place), in the caches of all listed layers. Returns (new lengths, workspace)."""
+        dev = self.w_col.device
+        n_reqs = seq_lens.numel()
+        if accepted.dim() != 2 or src_tables.dim() != 2 or src_tables.shape != dst_tables.shape:
+            raise ValueError("accepted is [n_reqs, m], src_tables and dst_tables [n_reqs, max_blocks]")
+        n, ks, vs, nb, bs = self._layer_pointers(caches_k, caches_v)
+        if out is None:
+            out = torch.empty(n_reqs, dtype=torch.int32, device=dev)
+        ws = _workspace(ws, 16, dev)
+        mb = src_tables.shape[1]
+        _check(lib().tp_kv_cache_compact(
+            self.handle, n_reqs, _i32(query_start_loc, "query_start_loc", dev, n_reqs + 1),
+            _i32(seq_lens, "seq_lens", dev), _i32(accepted, "accepted", dev, n_reqs * accepted.shape[1]),
+            accepted.shape[1], _i32(src_tables, "src_tables", dev, n_reqs * mb), _i32(dst_tables, "dst_tables", dev),
+            mb, n, ks, vs, nb, bs, _i32(out, "out", dev, n_reqs), ws.data_ptr(), ws.numel(), _stream(stream)))
+        return out, ws
+
+    def tree_attention_workspace_size(self, n_reqs: int, max_query_len: int, max_seq_len: int) -> int:
+        b = ctypes.c_int64()
+        _check(lib().tp_tree_attention_workspace_size(self.handle, n_reqs, max_query_len, max_seq_len,
+                                                      ctypes.byref(b)))
+        return b.value
+
+    def tree_attention(self, qkv: torch.Tensor, query_start_loc: torch.Tensor, seq_lens: torch.Tensor,
+                       block_tables: torch.Tensor, mask: torch.Tensor, cache_k: torch.Tensor, cache_v: torch.Tensor,
+                       max_query_len: int, max_seq_len: int, out=None, ws=None, stream=None):
+        """Attention of every request's drafted tokens (rows of qkv, already in the cache as its last
+        positions) over its cached tokens and over the drafted ones that their mask rows (tree_mask) name.
+        Returns (attn in the attention core's output layout, workspace)."""
+        c, dev = self.cfg, self.w_col.device
+        T = qkv.shape[0] if self.gathered else qkv.shape[1]
+        n_reqs = seq_lens.numel()
+        nb, bs = cache_k.shape[1], cache_k.shape[2]
+        shape = self.kv_cache_shape(nb, bs)
+        w = c.n_q_heads // c.t * c.head_dim
+        out_shape = (T, c.t * w) if self.gathered else (c.t, T, w)
+        if out is None:
+            out = torch.empty(out_shape, dtype=torch.bfloat16, device=dev)
+        if ws is None:
+            ws = torch.zeros(self.tree_attention_workspace_size(n_reqs, max_query_len, max_seq_len),
+                             dtype=torch.uint8, device=dev)
+        if block_tables.dim() != 2 or mask.dim() != 2:
+            raise ValueError("block_tables is [n_reqs, max_blocks], mask [T, words]")
+        _check(lib().tp_tree_attention(
+            self.handle, T, _bf16_on(qkv, "qkv", dev, self._qkv_shape(T)),
+            _i32(query_start_loc, "query_start_loc", dev, n_reqs + 1), _i32(seq_lens, "seq_lens", dev), n_reqs,
+            max_query_len, max_seq_len, _i32(block_tables, "block_tables", dev, n_reqs * block_tables.shape[1]),
+            block_tables.shape[1], _i32(mask, "mask", dev, T * mask.shape[1]), mask.shape[1],
+            _bf16_on(cache_k, "cache_k", dev, shape), _bf16_on(cache_v, "cache_v", dev, shape), nb, bs,
+            _bf16_on(out, "out", dev, out_shape), _workspace(ws, 0, dev).data_ptr(), ws.numel(), _stream(stream)))
+        return out, ws
+
     def kv_cache_write(self, qkv: torch.Tensor, slot_mapping: torch.Tensor, cache_k: torch.Tensor,
                        cache_v: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """Copy every token's k and v heads into its slot (slot_mapping int32 [T], -1 = skip).
@@ -423,6 +602,18 @@ class TPLayer:
             self._ws = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.attn.w_col.device)
         return self._ws
 
+    def set_rope(self, rope: Optional["Rope"], positions: Optional[torch.Tensor] = None) -> None:
+        """Rotate (and norm) q and k of every later forward() between the projection and the attention:
+        token i at positions[i] (int32 [max_tokens] on the GPU, read at each call). None: no rotation again."""
+        if rope is None:
+            _check(lib().tp_layer_set_rope(self.handle, None, None))
+        else:
+            dev = self.attn.w_col.device
+            if positions is None or rope.table.device != dev:
+                raise ValueError(f"set_rope needs positions, and the rope table on {dev}")
+            _check(lib().tp_layer_set_rope(self.handle, rope.args, _i32(positions, "positions", dev, self.max_tokens)))
+        self._rope = (rope, positions)     # borrowed by the handle
+
     def forward(self, hidden: torch.Tensor, residual: Optional[torch.Tensor], cu_seqlens: torch.Tensor,
                 max_seqlen: int, out: Optional[dict] = None, residual_stream: bool = True, ws=None,
                 stream=None) -> dict:
@@ -444,6 +635,72 @@ class TPLayer:
         _check(lib().tp_decoder_layer_forward(self.handle, T, ctypes.byref(io), _ptr(ws), ws.numel(),
                                               _stream(stream)))
         return o
+
+
+def rope_frequencies(cfg: RopeConfig):
+    """(angle per position of every rotated pair, factor of cos and sin) of a configuration, on the host."""
+    f, m = (ctypes.c_double * 128)(), ctypes.c_double()
+    _check(lib().tp_rope_frequencies(ctypes.byref(cfg), f, ctypes.byref(m)))
+    return list(f[:cfg.rotary_dim // 2]), m.value
+
+
+class Rope:
+    """Rotary positions of a model: the cos/sin table of n_pos positions (built here, on `device`), the
+    layout of the rotated pairs and the gammas of the q and k heads' norms (bf16 [head_dim] or None).
+
+    scaling: "none", "linear", "ntk", "bands" or "yarn" (see include/tp_linear.h for the formulas).
+    """
+
+    def __init__(self, n_pos: int, rotary_dim: int, base: float = 10000.0, layout: int = TP_ROPE_HALF,
+                 scaling: str = "none", factor: float = 1.0, original_max_position: int = 0,
+                 low_freq_factor: float = 1.0, high_freq_factor: float = 4.0, beta_slow: float = 1.0,
+                 beta_fast: float = 32.0, attn_factor: float = 0.0, q_gamma: Optional[torch.Tensor] = None,
+                 k_gamma: Optional[torch.Tensor] = None, eps: float = 1e-6, device=None, stream=None):
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {', '.join(ROPE_SCALINGS)}")
+        self.config = RopeConfig(rotary_dim, ROPE_SCALINGS[scaling], base, factor, low_freq_factor, high_freq_factor,
+                                 beta_slow, beta_fast, attn_factor, original_max_position)
+        rope_frequencies(self.config)      # refuses a bad configuration before anything is allocated
+        if n_pos < 1:
+            raise ValueError("n_pos must be >= 1")
+        self.table = torch.empty(n_pos, rotary_dim, dtype=torch.float32,
+                                 device=torch.device("cuda", torch.cuda.current_device()) if device is None else device)
+        with torch.cuda.device(self.table.device):
+            _check(lib().tp_rope_table(ctypes.byref(self.config), n_pos, self.table.data_ptr(), _stream(stream)))
+        for name, g in (("q_gamma", q_gamma), ("k_gamma", k_gamma)):
+            if g is not None:
+                _bf16_on(g, name, self.table.device)
+        self.gammas = (q_gamma, k_gamma)
+        self.args = RopeArgs(self.table.data_ptr(), n_pos, rotary_dim, layout,
+                             None if q_gamma is None else q_gamma.data_ptr(),
+                             None if k_gamma is None else k_gamma.data_ptr(), eps)
+
+
+def tree_mask(parents: torch.Tensor, query_start_loc: torch.Tensor, seq_lens: torch.Tensor, max_query_len: int,
+              out=None, ws: Optional[torch.Tensor] = None, stream=None):
+    """Mask rows and positions of drafted token trees: parents int32 [T], each token's parent among its
+    request's drafted tokens (before it) or -1. Returns (mask int32 [T, words], positions int32 [T],
+    workspace whose first word is the status); out: (mask, positions) to write instead of new tensors."""
+    dev, T = parents.device, parents.numel()
+    if not parents.is_cuda or dev.index != torch.cuda.current_device():
+        raise TypeError("parents must be a tensor on the current CUDA device")
+    words = (max_query_len + 31) // 32
+    if out is None:
+        mask = torch.empty(T, words, dtype=torch.int32, device=dev)
+        positions = torch.empty(T, dtype=torch.int32, device=dev)
+    else:
+        mask, positions = out
+        if mask.dim() != 2 or mask.shape[0] != T:
+            raise ValueError("the mask is [T, words]")
+        words = mask.shape[1]
+    n_reqs = seq_lens.numel()
+    ws = _workspace(ws, 16, dev)
+    _check(lib().tp_tree_mask(T, n_reqs, max_query_len, _i32(parents, "parents", dev),
+                              _i32(query_start_loc, "query_start_loc", dev, n_reqs + 1),
+                              _i32(seq_lens, "seq_lens", dev), _i32(mask, "mask", dev), words,
+                              None if positions is None else _i32(positions, "positions", dev, T), ws.data_ptr(),
+                              ws.numel(), _stream(stream)))
+    return mask, positions, ws
 
 
 def add_rms_norm(a: torch.Tensor, residual: Optional[torch.Tensor], gamma: torch.Tensor, eps: float,

@@ -112,6 +112,76 @@ cudaError_t launch_kv_write(const void* qkv, int T, int t, long long sstride, in
                             cudaStream_t st);
 cudaError_t launch_paged_attention(const PagedAttnParams& p, int n_reqs, cudaStream_t st);
 
+// Rotary positions (rope.cu).
+constexpr int kRopeMaxDim = 256;
+struct RopeFreqs {
+  double inv_freq[kRopeMaxDim / 2];
+  double scale;                      // multiplies cos and sin
+};
+struct RopeParams {
+  const __nv_bfloat16* in;           // shard r, token i at in + r * sstride + i * rstride (out likewise)
+  __nv_bfloat16* out;
+  long long sstride;
+  int rstride;
+  const int* pos;                    // [T]
+  const float* table;                // [n_pos][rd]: cos, then sin, of each pair
+  long long n_pos;
+  const __nv_bfloat16* q_gamma;      // [hd] or null
+  const __nv_bfloat16* k_gamma;
+  float eps;
+  const int* slots;                  // [T] or null: no cache write
+  long long n_slots;
+  __nv_bfloat16* cache_k;
+  __nv_bfloat16* cache_v;
+  int* status;
+  int T, t, q_per, kv_per, hd, rd, interleaved;
+};
+cudaError_t launch_rope_table(const RopeFreqs& f, long long n_pos, int rotary_dim, float* table, int nsm, cudaStream_t st);
+cudaError_t launch_qk_norm_rope(const RopeParams& p, int nsm, cudaStream_t st);
+
+// Pages moved inside the cache (kv_pages.cu), the caches of all layers in one launch.
+constexpr int kMaxKvLayers = 128;
+struct KvLayers {
+  void* k[kMaxKvLayers];
+  void* v[kMaxKvLayers];
+};
+struct CompactParams {
+  const int* qsl;                    // [n_reqs + 1]
+  const int* seq_lens;               // [n_reqs], drafted tokens included
+  const int* accepted;               // [n_reqs][max_accepted] rising draft indices, ended by a negative one
+  const int* src_tables;             // [n_reqs][max_blocks]
+  const int* dst_tables;
+  int* new_lens;                     // [n_reqs]
+  int* status;
+  long long n_slots;                 // num_blocks * block_size
+  int t, kv_per, max_blocks, num_blocks, block_size, max_accepted;
+};
+cudaError_t launch_kv_copy_blocks(const KvLayers& layers, int n_layers, const int* pairs, int n_pairs,
+                                  long long num_blocks, int block_size, int kv_per, int t, int* status, cudaStream_t st);
+cudaError_t launch_kv_compact(const KvLayers& layers, int n_layers, const CompactParams& p, int n_reqs, cudaStream_t st);
+
+// Attention of drafted token trees over the cache (tree_attention.cu).
+struct TreeAttnParams {
+  const __nv_bfloat16* qkv;          // drafted tokens: shard r, token i at qkv + r * sstride_in + i * rstride_in
+  long long sstride_in;
+  int rstride_in;
+  const int* qsl;                    // [n_reqs + 1]
+  const int* seq_lens;               // [n_reqs], drafted tokens included
+  const int* block_tables;           // [n_reqs][max_blocks]
+  const int* mask;                   // [T][mask_words]
+  const __nv_bfloat16* cache_k;      // [t][num_blocks][block_size][kv_per][128]
+  const __nv_bfloat16* cache_v;
+  __nv_bfloat16* out;                // shard r, token i at out + r * sstride_out + i * rstride_out
+  long long sstride_out;
+  int rstride_out;
+  int* status;
+  int T, n_reqs, t, q_per, kv_per, max_blocks, num_blocks, block_size, max_query_len, max_seq_len, mask_words;
+  float scale_log2;                  // log2(e) / sqrt(hd)
+};
+cudaError_t launch_tree_mask(int T, int n_reqs, int max_query_len, int words, const int* parents, const int* qsl,
+                             const int* seq_lens, int* mask, int* positions, int* status, cudaStream_t st);
+cudaError_t launch_tree_attention(const TreeAttnParams& p, cudaStream_t st);
+
 // Mixture of experts (moe.cu): routing sort, row gather, weighted combine.
 cudaError_t launch_moe_route(const int* ids, int n_entries, int k, int E, int max_rows, int* rank, int* perm_row,
                              int* row_src, int* tile_expert, int* m_valid, int* pair_tiles, int* pair_count,

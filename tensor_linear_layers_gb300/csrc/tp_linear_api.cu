@@ -1523,6 +1523,353 @@ int tp_capture_rows(int64_t T, int64_t H, const int32_t* row_req, const int32_t*
 
 }  // extern "C"
 
+// ============================================================================ rotary positions
+namespace {
+// The arguments of a rotation that do not depend on the call (tp_qk_norm_rope, tp_layer_set_rope).
+int check_rope(const tp_linear* h, const tp_rope_t* rope, const int32_t* positions) {
+  if (rope == nullptr) return fail(TP_ERR_ARG, "rope is null");
+  const int hd = h->cfg.head_dim;
+  if (hd > kRopeMaxDim) return fail(TP_ERR_UNSUPPORTED, "head_dim > %d", kRopeMaxDim);
+  TP_CHECK_PTR(rope->table, "rope table");
+  if (rope->n_pos < 1 || rope->n_pos > INT32_MAX) return fail(TP_ERR_SHAPE, "n_pos must be in [1, 2^31)");
+  if (rope->rotary_dim < 2 || rope->rotary_dim % 2 != 0 || rope->rotary_dim > hd)
+    return fail(TP_ERR_SHAPE, "rotary_dim must be even and in [2, head_dim] (got %d)", rope->rotary_dim);
+  if (rope->layout != TP_ROPE_HALF && rope->layout != TP_ROPE_INTERLEAVED)
+    return fail(TP_ERR_ARG, "unknown rope layout %d", rope->layout);
+  if (!(rope->eps >= 0.0f)) return fail(TP_ERR_ARG, "eps must be >= 0");
+  if (!aligned16(rope->q_gamma) || !aligned16(rope->k_gamma))
+    return fail(TP_ERR_ARG, "q_gamma and k_gamma must be null or 16-byte aligned");
+  if (positions == nullptr || (reinterpret_cast<uintptr_t>(positions) & 3u) != 0)
+    return fail(TP_ERR_ARG, "positions is null or not 4-byte aligned");
+  return TP_OK;
+}
+bool ranges_overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+int check_status_ws(const void* ws, int64_t bytes) {
+  if (ws == nullptr || !aligned16(ws) || bytes < 16)
+    return fail(TP_ERR_ARG, "workspace is null, not 16-byte aligned or under 16 bytes");
+  return TP_OK;
+}
+// The bounds every call over the paged cache has to stay in (slots are counted in 32 bits).
+int check_cache_size(const tp_linear* h, int64_t num_blocks, int32_t block_size) {
+  if (num_blocks < 1 || block_size < 1) return fail(TP_ERR_SHAPE, "num_blocks and block_size must be >= 1");
+  if (num_blocks > INT32_MAX) return fail(TP_ERR_UNSUPPORTED, "more than 2^31 - 1 cache blocks");
+  if (num_blocks * (int64_t)block_size * h->kv_per * 128 > (int64_t(1) << 40))
+    return fail(TP_ERR_UNSUPPORTED, "cache larger than 2^40 elements per shard");
+  if (num_blocks * (int64_t)block_size * h->cfg.t > INT32_MAX)
+    return fail(TP_ERR_UNSUPPORTED, "more than 2^31 - 1 cache slots over all shards");
+  return TP_OK;
+}
+int check_attn_handle(const tp_linear* h) {
+  if (h == nullptr) return fail(TP_ERR_ARG, "handle is null");
+  if (h->cfg.kind != TP_BLOCK_ATTN_PROJ) return fail(TP_ERR_ARG, "not an attention handle");
+  return TP_OK;
+}
+int check_paged_handle(const tp_linear* h) {
+  const int rc = check_attn_handle(h);
+  if (rc) return rc;
+  if (h->cfg.head_dim != 128) return fail(TP_ERR_UNSUPPORTED, "the KV cache is built for head_dim 128");
+  return TP_OK;
+}
+}  // namespace
+
+extern "C" {
+
+int tp_rope_frequencies(const tp_rope_config_t* c, double* inv_freq, double* scale) {
+  if (c == nullptr || inv_freq == nullptr || scale == nullptr) return fail(TP_ERR_ARG, "null argument");
+  const int d = c->rotary_dim;
+  if (d < 2 || d % 2 != 0 || d > kRopeMaxDim)
+    return fail(TP_ERR_SHAPE, "rotary_dim must be even and in [2, %d] (got %d)", kRopeMaxDim, d);
+  if (c->scaling < TP_ROPE_SCALE_NONE || c->scaling > TP_ROPE_SCALE_YARN)
+    return fail(TP_ERR_ARG, "unknown rope scaling %d", c->scaling);
+  if (!(c->base > 1.0) || !std::isfinite(c->base)) return fail(TP_ERR_ARG, "base must be finite and > 1");
+  if (!(c->attn_factor >= 0.0) || !std::isfinite(c->attn_factor))
+    return fail(TP_ERR_ARG, "attn_factor must be finite and >= 0");
+  if (c->scaling != TP_ROPE_SCALE_NONE && (!(c->factor > 0.0) || !std::isfinite(c->factor)))
+    return fail(TP_ERR_ARG, "factor must be finite and > 0");
+  if (c->scaling == TP_ROPE_SCALE_NTK && d < 4) return fail(TP_ERR_SHAPE, "NTK scaling needs rotary_dim >= 4");
+  if ((c->scaling == TP_ROPE_SCALE_BANDS || c->scaling == TP_ROPE_SCALE_YARN) && c->original_max_position < 1)
+    return fail(TP_ERR_ARG, "original_max_position must be >= 1");
+  if (c->scaling == TP_ROPE_SCALE_BANDS &&
+      !(c->low_freq_factor > 0.0 && c->low_freq_factor < c->high_freq_factor && std::isfinite(c->high_freq_factor)))
+    return fail(TP_ERR_ARG, "need 0 < low_freq_factor < high_freq_factor");
+  if (c->scaling == TP_ROPE_SCALE_YARN &&
+      !(c->beta_slow > 0.0 && c->beta_slow < c->beta_fast && std::isfinite(c->beta_fast)))
+    return fail(TP_ERR_ARG, "need 0 < beta_slow < beta_fast");
+  const double two_pi = 6.283185307179586476925;
+  double base = c->base, m = 1.0, lo = 0.0, hi = 0.0;
+  if (c->scaling == TP_ROPE_SCALE_NTK) base *= std::pow(c->factor, (double)d / (d - 2));
+  if (c->scaling == TP_ROPE_SCALE_YARN) {
+    // the pair that makes `turns` turns over the original context: orig * base^(-2i/d) = 2 pi turns
+    auto pair = [&](double turns) {
+      return d * std::log(c->original_max_position / (turns * two_pi)) / (2.0 * std::log(c->base));
+    };
+    lo = std::max(std::floor(pair(c->beta_fast)), 0.0);
+    hi = std::min(std::ceil(pair(c->beta_slow)), d - 1.0);
+    m = c->factor > 1.0 ? 0.1 * std::log(c->factor) + 1.0 : 1.0;
+  }
+  for (int i = 0; i < d / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / d);
+    if (c->scaling == TP_ROPE_SCALE_LINEAR) {
+      f /= c->factor;
+    } else if (c->scaling == TP_ROPE_SCALE_BANDS) {
+      const double w = c->original_max_position * f / two_pi;
+      const double u = std::min(1.0, std::max(0.0, (w - c->low_freq_factor) / (c->high_freq_factor - c->low_freq_factor)));
+      f = (1.0 - u) * f / c->factor + u * f;
+    } else if (c->scaling == TP_ROPE_SCALE_YARN) {
+      const double u = std::min(1.0, std::max(0.0, (i - lo) / (hi > lo ? hi - lo : 0.001)));
+      f = f / c->factor * u + f * (1.0 - u);
+    }
+    inv_freq[i] = f;
+  }
+  *scale = c->attn_factor > 0.0 ? c->attn_factor : m;
+  return ok();
+}
+
+int tp_rope_table(const tp_rope_config_t* cfg, int64_t n_pos, float* table, tp_stream_t stream) {
+  RopeFreqs f{};
+  int rc = tp_rope_frequencies(cfg, f.inv_freq, &f.scale);
+  if (rc) return rc;
+  if (n_pos < 1 || n_pos > INT32_MAX) return fail(TP_ERR_SHAPE, "n_pos must be in [1, 2^31)");
+  TP_CHECK_PTR(table, "table");
+  int dev = 0, nsm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = launch_rope_table(f, n_pos, cfg->rotary_dim, table, nsm, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rope table launch");
+  return ok();
+}
+
+int tp_qk_norm_rope(tp_linear_t* h, int64_t T, const void* qkv, void* qkv_out, const int32_t* positions,
+                    const tp_rope_t* rope, const int32_t* slot_mapping, void* cache_k, void* cache_v,
+                    int64_t num_blocks, int32_t block_size, void* workspace, int64_t workspace_bytes,
+                    tp_stream_t stream) {
+  int rc = check_attn_handle(h);
+  if (rc || (rc = check_T(T))) return rc;
+  if (T == 0) return ok();
+  if ((rc = check_rope(h, rope, positions))) return rc;
+  TP_CHECK_PTR(qkv, "qkv");
+  TP_CHECK_PTR(qkv_out, "qkv_out");
+  const int64_t bytes = h->cfg.t * T * h->ws_qkv * 2;
+  if (qkv_out != qkv && ranges_overlap(qkv, bytes, qkv_out, bytes))
+    return fail(TP_ERR_ARG, "qkv_out overlaps qkv without being it");
+  if (slot_mapping != nullptr) {
+    if ((rc = check_paged_handle(h)) || (rc = check_cache_size(h, num_blocks, block_size))) return rc;
+    if (!aligned4(slot_mapping)) return fail(TP_ERR_ARG, "slot_mapping must be null or 4-byte aligned");
+    TP_CHECK_PTR(cache_k, "cache_k");
+    TP_CHECK_PTR(cache_v, "cache_v");
+  }
+  if ((rc = check_status_ws(workspace, workspace_bytes)) || (rc = check_device(h))) return rc;
+  const bool gath = gathered(h);
+  RopeParams p{};
+  p.in = static_cast<const __nv_bfloat16*>(qkv);
+  p.out = static_cast<__nv_bfloat16*>(qkv_out);
+  p.sstride = gath ? h->ws_qkv : T * h->ws_qkv;
+  p.rstride = (int)(gath ? h->cfg.t * h->ws_qkv : h->ws_qkv);
+  p.pos = positions;
+  p.table = rope->table;
+  p.n_pos = rope->n_pos;
+  p.q_gamma = static_cast<const __nv_bfloat16*>(rope->q_gamma);
+  p.k_gamma = static_cast<const __nv_bfloat16*>(rope->k_gamma);
+  p.eps = rope->eps;
+  p.slots = slot_mapping;
+  p.n_slots = slot_mapping != nullptr ? num_blocks * (int64_t)block_size : 0;
+  p.cache_k = static_cast<__nv_bfloat16*>(cache_k);
+  p.cache_v = static_cast<__nv_bfloat16*>(cache_v);
+  p.status = t_status != nullptr ? t_status : reinterpret_cast<int*>(workspace);
+  p.T = (int)T;
+  p.t = h->cfg.t;
+  p.q_per = h->q_per;
+  p.kv_per = h->kv_per;
+  p.hd = h->cfg.head_dim;
+  p.rd = rope->rotary_dim;
+  p.interleaved = rope->layout == TP_ROPE_INTERLEAVED;
+  const cudaError_t e = launch_qk_norm_rope(p, h->nsm, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qk norm and rope launch");
+  return ok();
+}
+
+// ============================================================================ drafted token trees
+int tp_tree_mask(int64_t T, int32_t n_reqs, int32_t max_query_len, const int32_t* parents,
+                 const int32_t* query_start_loc, const int32_t* seq_lens, int32_t* tree_mask, int32_t mask_words,
+                 int32_t* positions, void* workspace, int64_t workspace_bytes, tp_stream_t stream) {
+  int rc = check_T(T);
+  if (rc) return rc;
+  if (T == 0) return ok();
+  if (n_reqs < 1 || max_query_len < 1) return fail(TP_ERR_SHAPE, "need n_reqs >= 1 and max_query_len >= 1");
+  if (max_query_len > TP_TREE_MAX_DRAFT)
+    return fail(TP_ERR_UNSUPPORTED, "more than %d drafted tokens per request", TP_TREE_MAX_DRAFT);
+  if (mask_words < 1 || mask_words > 65536 || (int64_t)mask_words * 32 < max_query_len)
+    return fail(TP_ERR_SHAPE, "mask_words does not cover max_query_len bits");
+  for (const int32_t* q : {parents, query_start_loc, seq_lens, (const int32_t*)tree_mask})
+    if (!aligned4(q))
+      return fail(TP_ERR_ARG, "parents, query_start_loc, seq_lens and tree_mask must be 4-byte aligned device arrays");
+  if ((reinterpret_cast<uintptr_t>(positions) & 3u) != 0)
+    return fail(TP_ERR_ARG, "positions must be null or a 4-byte aligned device array");
+  if ((rc = check_status_ws(workspace, workspace_bytes))) return rc;
+  const cudaError_t e = launch_tree_mask((int)T, n_reqs, max_query_len, mask_words, parents, query_start_loc, seq_lens,
+                                         tree_mask, positions, reinterpret_cast<int*>(workspace),
+                                         static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "tree mask launch");
+  return ok();
+}
+
+int tp_tree_attention_workspace_size(const tp_linear_t* h, int32_t n_reqs, int32_t max_query_len,
+                                     int32_t max_seq_len, int64_t* bytes) {
+  if (bytes == nullptr) return fail(TP_ERR_ARG, "null argument");
+  const int rc = check_attn_handle(h);
+  if (rc) return rc;
+  if (n_reqs < 1 || max_query_len < 1 || max_seq_len < max_query_len)
+    return fail(TP_ERR_SHAPE, "need n_reqs >= 1 and 1 <= max_query_len <= max_seq_len");
+  *bytes = 256;
+  return ok();
+}
+
+int tp_tree_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t* query_start_loc,
+                      const int32_t* seq_lens, int32_t n_reqs, int32_t max_query_len, int32_t max_seq_len,
+                      const int32_t* block_tables, int32_t max_blocks_per_req, const int32_t* tree_mask,
+                      int32_t mask_words, const void* cache_k, const void* cache_v, int64_t num_blocks,
+                      int32_t block_size, void* attn_out, void* workspace, int64_t workspace_bytes,
+                      tp_stream_t stream) {
+  int rc = check_paged_handle(h);
+  if (rc || (rc = check_T(T))) return rc;
+  if (T == 0) return ok();
+  if (n_reqs < 1 || max_query_len < 1 || max_seq_len < max_query_len)
+    return fail(TP_ERR_SHAPE, "need n_reqs >= 1 and 1 <= max_query_len <= max_seq_len");
+  if (max_query_len > TP_TREE_MAX_DRAFT)
+    return fail(TP_ERR_UNSUPPORTED, "more than %d drafted tokens per request", TP_TREE_MAX_DRAFT);
+  if (mask_words < 1 || mask_words > 65536 || (int64_t)mask_words * 32 < max_query_len)
+    return fail(TP_ERR_SHAPE, "mask_words does not cover max_query_len bits");
+  if ((rc = check_cache_size(h, num_blocks, block_size))) return rc;
+  if (max_blocks_per_req < 1 || (int64_t)max_blocks_per_req * block_size < max_seq_len)
+    return fail(TP_ERR_SHAPE, "the block tables cannot hold max_seq_len tokens");
+  TP_CHECK_PTR(qkv, "qkv");
+  TP_CHECK_PTR(cache_k, "cache_k");
+  TP_CHECK_PTR(cache_v, "cache_v");
+  TP_CHECK_PTR(attn_out, "attn_out");
+  for (const int32_t* q : {query_start_loc, seq_lens, block_tables, tree_mask})
+    if (!aligned4(q))
+      return fail(TP_ERR_ARG,
+                  "query_start_loc, seq_lens, block_tables and tree_mask must be 4-byte aligned device arrays");
+  int64_t need = 0;
+  if ((rc = tp_tree_attention_workspace_size(h, n_reqs, max_query_len, max_seq_len, &need))) return rc;
+  if (workspace == nullptr || !aligned16(workspace)) return fail(TP_ERR_ARG, "workspace is null or not 16-byte aligned");
+  if (workspace_bytes < need)
+    return fail(TP_ERR_ARG, "workspace too small: %lld bytes, %lld needed", (long long)workspace_bytes, (long long)need);
+  if ((rc = check_device(h))) return rc;
+  const bool gath = gathered(h);
+  TreeAttnParams p{};
+  p.qkv = static_cast<const __nv_bfloat16*>(qkv);
+  p.sstride_in = gath ? h->ws_qkv : T * h->ws_qkv;
+  p.rstride_in = (int)(gath ? h->cfg.t * h->ws_qkv : h->ws_qkv);
+  p.qsl = query_start_loc;
+  p.seq_lens = seq_lens;
+  p.block_tables = block_tables;
+  p.mask = tree_mask;
+  p.cache_k = static_cast<const __nv_bfloat16*>(cache_k);
+  p.cache_v = static_cast<const __nv_bfloat16*>(cache_v);
+  p.out = static_cast<__nv_bfloat16*>(attn_out);
+  p.sstride_out = gath ? h->Ks : T * h->Ks;
+  p.rstride_out = (int)(gath ? h->cfg.t * h->Ks : h->Ks);
+  p.status = reinterpret_cast<int*>(workspace);
+  p.T = (int)T;
+  p.n_reqs = n_reqs;
+  p.t = h->cfg.t;
+  p.q_per = h->q_per;
+  p.kv_per = h->kv_per;
+  p.max_blocks = max_blocks_per_req;
+  p.num_blocks = (int)num_blocks;
+  p.block_size = block_size;
+  p.max_query_len = max_query_len;
+  p.max_seq_len = max_seq_len;
+  p.mask_words = mask_words;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt(128.0));
+  const cudaError_t e = launch_tree_attention(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
+  return ok();
+}
+
+// ============================================================================ pages of the cache
+static int gather_layers(int32_t n_layers, void* const* caches_k, void* const* caches_v, KvLayers* out) {
+  if (n_layers < 1) return fail(TP_ERR_SHAPE, "n_layers must be >= 1");
+  if (n_layers > TP_KV_MAX_LAYERS) return fail(TP_ERR_UNSUPPORTED, "more than %d layers in one call", TP_KV_MAX_LAYERS);
+  if (caches_k == nullptr || caches_v == nullptr) return fail(TP_ERR_ARG, "caches_k or caches_v is null");
+  for (int i = 0; i < n_layers; ++i) {
+    TP_CHECK_PTR(caches_k[i], "caches_k[i]");
+    TP_CHECK_PTR(caches_v[i], "caches_v[i]");
+    out->k[i] = caches_k[i];
+    out->v[i] = caches_v[i];
+  }
+  return TP_OK;
+}
+
+int tp_kv_cache_copy_blocks(tp_linear_t* h, const int32_t* block_pairs, int32_t n_pairs, int32_t n_layers,
+                            void* const* caches_k, void* const* caches_v, int64_t num_blocks, int32_t block_size,
+                            void* workspace, int64_t workspace_bytes, tp_stream_t stream) {
+  int rc = check_paged_handle(h);
+  if (rc) return rc;
+  if (n_pairs < 0) return fail(TP_ERR_SHAPE, "n_pairs must be >= 0");
+  if (n_pairs > (1 << 24)) return fail(TP_ERR_UNSUPPORTED, "more than 16777216 pairs in one call");
+  if ((rc = check_cache_size(h, num_blocks, block_size))) return rc;
+  if (n_pairs == 0) return ok();
+  KvLayers layers{};
+  if ((rc = gather_layers(n_layers, caches_k, caches_v, &layers))) return rc;
+  if (block_pairs == nullptr || (reinterpret_cast<uintptr_t>(block_pairs) & 7u) != 0)
+    return fail(TP_ERR_ARG, "block_pairs is null or not 8-byte aligned");
+  if ((rc = check_status_ws(workspace, workspace_bytes)) || (rc = check_device(h))) return rc;
+  const cudaError_t e = launch_kv_copy_blocks(layers, n_layers, block_pairs, n_pairs, num_blocks, block_size, h->kv_per,
+                                              h->cfg.t, reinterpret_cast<int*>(workspace),
+                                              static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "KV cache block copy launch");
+  return ok();
+}
+
+int tp_kv_cache_compact(tp_linear_t* h, int32_t n_reqs, const int32_t* query_start_loc, const int32_t* seq_lens,
+                        const int32_t* accepted, int32_t max_accepted, const int32_t* src_tables,
+                        const int32_t* dst_tables, int32_t max_blocks_per_req, int32_t n_layers,
+                        void* const* caches_k, void* const* caches_v, int64_t num_blocks, int32_t block_size,
+                        int32_t* new_seq_lens, void* workspace, int64_t workspace_bytes, tp_stream_t stream) {
+  int rc = check_paged_handle(h);
+  if (rc) return rc;
+  if (n_reqs < 0 || max_accepted < 1 || max_blocks_per_req < 1)
+    return fail(TP_ERR_SHAPE, "need n_reqs >= 0, max_accepted >= 1 and max_blocks_per_req >= 1");
+  if (n_reqs > (1 << 24)) return fail(TP_ERR_UNSUPPORTED, "more than 16777216 requests in one call");
+  if ((rc = check_cache_size(h, num_blocks, block_size))) return rc;
+  if (n_reqs == 0) return ok();
+  KvLayers layers{};
+  if ((rc = gather_layers(n_layers, caches_k, caches_v, &layers))) return rc;
+  for (const int32_t* q : {query_start_loc, seq_lens, accepted, src_tables, dst_tables, (const int32_t*)new_seq_lens})
+    if (!aligned4(q))
+      return fail(TP_ERR_ARG, "query_start_loc, seq_lens, accepted, src_tables, dst_tables and new_seq_lens must be "
+                              "4-byte aligned device arrays");
+  if (ranges_overlap(seq_lens, 4LL * n_reqs, new_seq_lens, 4LL * n_reqs))
+    return fail(TP_ERR_ARG, "new_seq_lens overlaps seq_lens");
+  if ((rc = check_status_ws(workspace, workspace_bytes)) || (rc = check_device(h))) return rc;
+  CompactParams p{};
+  p.qsl = query_start_loc;
+  p.seq_lens = seq_lens;
+  p.accepted = accepted;
+  p.src_tables = src_tables;
+  p.dst_tables = dst_tables;
+  p.new_lens = new_seq_lens;
+  p.status = reinterpret_cast<int*>(workspace);
+  p.n_slots = num_blocks * (int64_t)block_size;
+  p.t = h->cfg.t;
+  p.kv_per = h->kv_per;
+  p.max_blocks = max_blocks_per_req;
+  p.num_blocks = (int)num_blocks;
+  p.block_size = block_size;
+  p.max_accepted = max_accepted;
+  const cudaError_t e = launch_kv_compact(layers, n_layers, p, n_reqs, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "KV cache compaction launch");
+  return ok();
+}
+
+}  // extern "C"
+
 // ============================================================================ decoder layer
 // One layer = the attention handle's half, then the MLP handle's half, on one
 // stream. The workspace layout is fixed by max_tokens: the attention half's
@@ -1533,6 +1880,8 @@ struct tp_layer {
   tp_linear* mlp;
   int64_t max_tokens;
   int64_t attn_ws, mlp_off, mlp_ws, x1_off, qkv_off, a_off, total;
+  tp_rope_t rope;               // rotation of q and k after the projection, when positions is set
+  const int32_t* positions;
 };
 
 extern "C" {
@@ -1582,6 +1931,19 @@ int tp_layer_workspace_size(const tp_layer_t* layer, int64_t* bytes) {
   return ok();
 }
 
+int tp_layer_set_rope(tp_layer_t* layer, const tp_rope_t* rope, const int32_t* positions) {
+  if (layer == nullptr) return fail(TP_ERR_ARG, "layer is null");
+  if (rope == nullptr) {
+    layer->positions = nullptr;
+    return ok();
+  }
+  const int rc = check_rope(layer->attn, rope, positions);
+  if (rc) return rc;
+  layer->rope = *rope;
+  layer->positions = positions;
+  return ok();
+}
+
 int tp_decoder_layer_forward(tp_layer_t* layer, int64_t T, const tp_layer_io_t* io, void* workspace,
                              int64_t workspace_bytes, tp_stream_t stream) {
   if (layer == nullptr || io == nullptr) return fail(TP_ERR_ARG, "null argument");
@@ -1620,6 +1982,10 @@ int tp_decoder_layer_forward(tp_layer_t* layer, int64_t T, const tp_layer_io_t* 
                             io->residual_attn, x1, stream)))
     return rc;
   if ((rc = tp_attn_proj_forward(at, T, x1, qkv, nullptr, nullptr, ws, layer->attn_ws, stream))) return rc;
+  if (layer->positions != nullptr &&
+      (rc = tp_qk_norm_rope(at, T, qkv, qkv, layer->positions, &layer->rope, nullptr, nullptr, nullptr, 0, 0, ws,
+                            layer->attn_ws, stream)))
+    return rc;
   if ((rc = tp_attention_forward(at, T, qkv, io->cu_seqlens, io->n_seqs, io->max_seqlen, A, ws,
                                  layer->attn_ws, stream)))
     return rc;
