@@ -177,10 +177,15 @@ struct TreeAttnParams {
   int* status;
   int T, n_reqs, t, q_per, kv_per, max_blocks, num_blocks, block_size, max_query_len, max_seq_len, mask_words;
   float scale_log2;                  // log2(e) / sqrt(hd)
+  long long* prefix;                 // [n_reqs + 1] chunks before each request, written for the merge
+  float* partials;                   // [2 * grid] slots of part_rows x (128 + 2)
+  int part_rows;
+  unsigned long long timeout_ns;
 };
+int tree_group_rows(int max_rows);   // query rows of one item: 128 or 256
 cudaError_t launch_tree_mask(int T, int n_reqs, int max_query_len, int words, const int* parents, const int* qsl,
                              const int* seq_lens, int* mask, int* positions, int* status, cudaStream_t st);
-cudaError_t launch_tree_attention(const TreeAttnParams& p, cudaStream_t st);
+cudaError_t launch_tree_attention(const TreeAttnParams& p, int grid, cudaStream_t st);
 
 // Mixture of experts (moe.cu): routing sort, row gather, weighted combine.
 cudaError_t launch_moe_route(const int* ids, int n_entries, int k, int E, int max_rows, int* rank, int* perm_row,

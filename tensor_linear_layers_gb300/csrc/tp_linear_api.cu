@@ -1717,6 +1717,26 @@ int tp_tree_mask(int64_t T, int32_t n_reqs, int32_t max_query_len, const int32_t
   return ok();
 }
 
+// Tree attention: at most one CTA per SM, no more than there are chunks of keys. Workspace: the
+// status word, the requests' prefix sums, two partial slots per CTA.
+namespace {
+struct TreePlan {
+  int grid, part_rows;
+  int64_t partials_off, ws_bytes;
+};
+TreePlan tree_plan(const tp_linear* h, int n_reqs, int max_query_len, int max_seq_len) {
+  const int max_rows = max_query_len * (h->q_per / h->kv_per), rows = tree_group_rows(max_rows);
+  const int64_t chunks = (int64_t)n_reqs * h->cfg.t * h->kv_per * ceil_div(max_rows, rows) * ceil_div(max_seq_len, 128);
+  TreePlan pl{};
+  pl.grid = (int)std::min<int64_t>(h->nsm, chunks);
+  pl.part_rows = (std::min(rows, max_rows) + 7) / 8 * 8;    // a slot is a multiple of 32 bytes (32-byte stores)
+  pl.partials_off = align256(256 + 8 * ((int64_t)n_reqs + 1));
+  // the workspace itself is 16-byte aligned: room to start the slots on a 32-byte boundary
+  pl.ws_bytes = align256(pl.partials_off + 32 + 2LL * pl.grid * pl.part_rows * (128 + 2) * 4);
+  return pl;
+}
+}  // namespace
+
 int tp_tree_attention_workspace_size(const tp_linear_t* h, int32_t n_reqs, int32_t max_query_len,
                                      int32_t max_seq_len, int64_t* bytes) {
   if (bytes == nullptr) return fail(TP_ERR_ARG, "null argument");
@@ -1724,7 +1744,9 @@ int tp_tree_attention_workspace_size(const tp_linear_t* h, int32_t n_reqs, int32
   if (rc) return rc;
   if (n_reqs < 1 || max_query_len < 1 || max_seq_len < max_query_len)
     return fail(TP_ERR_SHAPE, "need n_reqs >= 1 and 1 <= max_query_len <= max_seq_len");
-  *bytes = 256;
+  if (max_query_len > TP_TREE_MAX_DRAFT)
+    return fail(TP_ERR_UNSUPPORTED, "more than %d drafted tokens per request", TP_TREE_MAX_DRAFT);
+  *bytes = tree_plan(h, n_reqs, max_query_len, max_seq_len).ws_bytes;
   return ok();
 }
 
@@ -1754,11 +1776,11 @@ int tp_tree_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t*
     if (!aligned4(q))
       return fail(TP_ERR_ARG,
                   "query_start_loc, seq_lens, block_tables and tree_mask must be 4-byte aligned device arrays");
-  int64_t need = 0;
-  if ((rc = tp_tree_attention_workspace_size(h, n_reqs, max_query_len, max_seq_len, &need))) return rc;
+  const TreePlan pl = tree_plan(h, n_reqs, max_query_len, max_seq_len);
   if (workspace == nullptr || !aligned16(workspace)) return fail(TP_ERR_ARG, "workspace is null or not 16-byte aligned");
-  if (workspace_bytes < need)
-    return fail(TP_ERR_ARG, "workspace too small: %lld bytes, %lld needed", (long long)workspace_bytes, (long long)need);
+  if (workspace_bytes < pl.ws_bytes)
+    return fail(TP_ERR_ARG, "workspace too small: %lld bytes, %lld needed", (long long)workspace_bytes,
+                (long long)pl.ws_bytes);
   if ((rc = check_device(h))) return rc;
   const bool gath = gathered(h);
   TreeAttnParams p{};
@@ -1787,7 +1809,12 @@ int tp_tree_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t*
   p.max_seq_len = max_seq_len;
   p.mask_words = mask_words;
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt(128.0));
-  const cudaError_t e = launch_tree_attention(p, static_cast<cudaStream_t>(stream));
+  p.prefix = reinterpret_cast<long long*>(static_cast<char*>(workspace) + 256);
+  p.partials = reinterpret_cast<float*>(
+      (reinterpret_cast<uintptr_t>(workspace) + (uintptr_t)pl.partials_off + 31) & ~uintptr_t(31));
+  p.part_rows = pl.part_rows;
+  p.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
+  const cudaError_t e = launch_tree_attention(p, pl.grid, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   return ok();
 }

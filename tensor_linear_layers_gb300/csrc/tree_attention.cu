@@ -9,9 +9,11 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "gemm_tc.cuh"
 #include "internal.h"
+#include "tree_plan.h"
 
 namespace tpl {
 
@@ -61,43 +63,696 @@ __global__ void __launch_bounds__(kMaxDraft)
   if (positions != nullptr) positions[q0 + i] = ok ? ctx + depth : -1;
 }
 
-// One warp per (token, shard, q head): a lane holds four head dimensions.
-__global__ void __launch_bounds__(128) tree_attn_kernel(const TreeAttnParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long it = blockIdx.x * 4LL + (threadIdx.x >> 5);
-  const int h = (int)(it % p.q_per), r = (int)(it / p.q_per % p.t);
-  const long long ti = it / p.q_per / p.t;
-  if (ti >= (long long)p.n_reqs * p.max_query_len) return;
-  const int b = (int)(ti / p.max_query_len), i = (int)(ti % p.max_query_len);
-  const int q0 = p.qsl[b], n = p.qsl[b + 1] - q0, L = p.seq_lens[b], ctx = L - n;
-  if (q0 < 0 || n < 0 || n > p.max_query_len || q0 > p.T - n || ctx < 0 || L > p.max_seq_len) {
-    if (lane == 0) atomicExch(p.status, kStatusShape);
-    return;
+// ---------------------------------------------------------------- attention kernel
+// The queries that read one kv head of a request (its drafted tokens x the q heads of the
+// group) are the rows of 128-row tensor-core tiles; its keys go by in chunks of 128, read
+// once from the cache for all of them:
+//   S = Q K^T  (tcgen05, 128 x 128 x 128, fp32 in tensor memory)
+//   P = 2^(s c - m) as bf16, written over S (tensor memory, the A operand of P V)
+//   O += P V   (tcgen05, O in tensor memory)
+// with the running max m and sum l of every row in its thread's registers. Persistent, one
+// CTA per SM; the chunks of all items are one line cut into equal ranges (tree_plan.h), so
+// the CTAs stream the same number of keys whatever the requests' lengths.
+//
+// MT = 1: up to 128 rows per item, S/P in three buffers. MT = 2: up to 256 rows as two tiles
+// on the same K and V, one S/P buffer each (tensor memory holds 512 columns: 2 x (S + O)).
+//
+//   warp 0      issues S;  warp 1 issues P V (an elected lane of a converged warp);
+//   warp 2      walks the CTA's range and publishes segments; warp 3 idle
+//   warps 4-7   copies: K and V rows through the block table with 16-byte cp.async into
+//               128-byte-swizzled tiles (any block size: a key's row is found on its own),
+//               a ring of tiles K0 V0 K1 V1 ...; Q rows of a segment
+//   warps 8-    softmax, a row per thread, four warps per tile; at a segment's end O / l to
+//               global memory, or the unnormalised O with (m, l) to a partial slot
+//
+// A row's mask applies to the chunks that hold drafted tokens alone. There, V values that
+// are not finite are set to zero in shared memory, so that 0 * v of a token that does not
+// see the key stays 0, and the rows that do see it get the value added at the end.
+//
+// Bound by HBM up to 256 rows: a chunk is 64 KB, 1.47 us of one SM's share of the measured
+// bandwidth; its products take 1024 tensor cycles (0.55 us) per tile.
+namespace {
+constexpr int kTileBytes = 128 * 128 * 2;      // 128 rows x 128 bf16: two 64-column boxes
+constexpr int kUnitSlots = 4;
+constexpr float kRescaleLog2 = 8.0f;           // rescale O when the row max grows by more than this
+constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128);
+constexpr uint32_t kIdescO = idesc_bf16_f32(128, 128) | kIdescBMnMajor;
+constexpr int kTmemCols = 512;
+
+template <int MT>
+struct TreeCfg {
+  static constexpr int kThreads = 256 + 128 * MT;
+  static constexpr int kTiles = MT == 1 ? 6 : 5;           // K/V ring
+  static constexpr int kSBufs = MT == 1 ? 3 : 1;           // S/P buffers of a tile
+  static constexpr int kRingOff = MT * kTileBytes;         // after Q
+  static constexpr int kBarOff = kRingOff + kTiles * kTileBytes;
+  // registers: issuers, copies, softmax
+  static constexpr int kRegs0 = 56, kRegs1 = MT == 1 ? 120 : 72, kRegsS = MT == 1 ? 232 : 192;
+  static constexpr int kLaunchRegs = MT == 1 ? 168 : 128;
+  static_assert(128 * (kRegs0 + kRegs1 + MT * kRegsS) <= kThreads * kLaunchRegs, "register split within the launch's");
+  // tensor memory: MT = 1: S/P at 0, 128, 256, O at 384; MT = 2: tile m S/P at 256 m, O at 256 m + 128
+  static __device__ __forceinline__ uint32_t s_col(int tile, int buf) { return MT == 1 ? buf * 128 : tile * 256; }
+  static __device__ __forceinline__ uint32_t o_col(int tile) { return MT == 1 ? 384 : tile * 256 + 128; }
+  enum {
+    Q_FULL = 0, Q_EMPTY, FULL, EMPTY = FULL + kTiles,
+    S_FULL = EMPTY + kTiles,          // per S/P buffer of every tile
+    P_READY = S_FULL + MT * kSBufs,
+    S_FREE = P_READY + MT * kSBufs,
+    PV_DONE = S_FREE + MT * kSBufs,   // per tile
+    O_FREE = PV_DONE + MT,
+    U_FULL = O_FREE + MT, U_EMPTY = U_FULL + kUnitSlots,
+    DONE_S = U_EMPTY + kUnitSlots, DONE_PV, NBARS
+  };
+  static constexpr int kMiscOff = kBarOff + 8 * NBARS;     // tensor memory address, abort flag
+  static constexpr int kUnitOff = (kMiscOff + 8 + 15) / 16 * 16;
+  static constexpr int kSmem = 1024 + kUnitOff + kUnitSlots * 64;
+  static_assert(kSmem <= 232448, "shared memory of one CTA");
+};
+
+// A segment: chunks [c0, c1) of one item. b < 0: no more.
+struct __align__(16) Segment {
+  int b, r, g, row0;                 // request, shard, kv head of the shard, first query row of the item
+  int c0, c1, q0, n;                 // chunks; first drafted token and their number
+  int len, part, rows, bad;          // tokens of the request; partial slot or -1; query rows of the item; V not finite
+  int pad[4];
+};
+static_assert(sizeof(Segment) == 64, "unit slots");
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int src_bytes, uint64_t pol) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(src_bytes),
+               "l"(pol)
+               : "memory");
+}
+// One arrival on bar once all cp.async of this thread so far have landed (counted in the barrier's own count).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Shared memory written by ordinary copies and stores, seen by this thread through a barrier,
+// is ordered before the tensor core's reads that it issues next.
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// bf16 pairs of a 32-bit word whose exponent is all ones become zero; true if one was
+__device__ __forceinline__ bool drop_nonfinite(uint32_t& w) {
+  bool any = false;
+  if ((w & 0x7f80u) == 0x7f80u) {
+    w &= 0xffff0000u;
+    any = true;
   }
-  if (i >= n) return;
-  const int g = h / (p.q_per / p.kv_per);
-  float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-  const __nv_bfloat16* qp = p.qkv + (size_t)r * p.sstride_in + (size_t)(q0 + i) * p.rstride_in + h * kHd + lane * 4;
-  for (int e = 0; e < 4; ++e) q[e] = __bfloat162float(qp[e]) * p.scale_log2;
-  for (int k = 0; k < L; ++k) {
-    if (k >= ctx && !((unsigned)p.mask[(size_t)(q0 + i) * p.mask_words + ((k - ctx) >> 5)] >> ((k - ctx) & 31) & 1u)) continue;
-    const int blk = p.block_tables[(size_t)b * p.max_blocks + k / p.block_size];
-    if (blk < 0 || blk >= p.num_blocks) {
-      if (lane == 0) atomicExch(p.status, kStatusShape);
-      continue;
+  if ((w & 0x7f800000u) == 0x7f800000u) {
+    w &= 0x0000ffffu;
+    any = true;
+  }
+  return any;
+}
+}  // namespace
+
+// Partial results of a slot: [rows][128] fp32 O, then [rows][2] (max in the exp2 domain, sum).
+// part_rows is a multiple of 8 and the first slot 32-byte aligned: every row starts on 32 bytes.
+__device__ __forceinline__ float* part_o(const TreeAttnParams& p, int slot) {
+  return p.partials + (size_t)slot * p.part_rows * (kHd + 2);
+}
+
+template <int MT>
+__global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(const TreeAttnParams p) {
+  using C = TreeCfg<MT>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  uint8_t* base_ptr = smem_raw + (base - raw_addr);
+  auto bar = [&](int b) { return base + C::kBarOff + 8u * b; };
+  volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(base_ptr + C::kMiscOff);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(base_ptr + C::kMiscOff + 4);
+  Segment* s_seg = reinterpret_cast<Segment*>(base_ptr + C::kUnitOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  griddep_launch_dependents();   // the merge grid may be scheduled; it waits for this one to complete
+
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < C::NBARS; ++b) {
+      int count = 1;
+      if (b == C::Q_FULL || (b >= C::FULL && b < C::EMPTY)) count = 128;        // every copying thread
+      if (b >= C::P_READY && b < C::S_FREE) count = 4;                          // the tile's softmax warps
+      if (b >= C::PV_DONE && b < C::O_FREE) count = 2;                          // the MMAs, and their issuer
+      if (b >= C::O_FREE && b < C::U_FULL) count = 4;
+      if (b >= C::U_EMPTY && b < C::DONE_S) count = 2 + 4 + 4 * MT;             // issuers, copy and softmax warps
+      mbar_init(bar(b), count);
     }
-    const size_t row = ((((size_t)r * p.num_blocks + blk) * p.block_size + k % p.block_size) * p.kv_per + g) * kHd + lane * 4;
-    float s = 0.f;
-    for (int e = 0; e < 4; ++e) s += q[e] * __bfloat162float(p.cache_k[row + e]);
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float mn = fmaxf(m, s);
-    const float f = m == -INFINITY ? 0.f : exp2f(m - mn), w = mn == -INFINITY ? 0.f : exp2f(s - mn);
-    l = l * f + w;
-    for (int e = 0; e < 4; ++e) o[e] = o[e] * f + w * __bfloat162float(p.cache_v[row + e]);
-    m = mn;
+    *s_abort = 0;
+    fence_barrier_init();
   }
-  __nv_bfloat16* op = p.out + (size_t)r * p.sstride_out + (size_t)(q0 + i) * p.rstride_out + h * kHd + lane * 4;
-  for (int e = 0; e < 4; ++e) op[e] = __float2bfloat16_rn(l == 0.f ? 0.f : o[e] / l);
+  if (warp == 1) {
+    tmem_alloc(smem_u32(const_cast<uint32_t*>(s_tmem)), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+  const unsigned long long timeout = p.timeout_ns;
+  const int gq = p.q_per / p.kv_per;                // q heads of a kv head
+  constexpr int kGroupRows = 128 * MT;
+  bool ok = true;
+  // a wait of a whole warp
+  auto wait = [&](int b, uint32_t ph) -> bool {
+    bool w = mbar_wait_bounded(bar(b), ph, s_abort, timeout);
+    w = __all_sync(0xffffffffu, w);
+    if (!w) {
+      if (lane == 0 && !*s_abort) {
+        atomicExch(p.status, kStatusTimeout);
+        *s_abort = 1;
+      }
+      ok = false;
+    }
+    return w;
+  };
+  // the next segment's slot, or -1 at the end
+  int nu = 0;
+  auto next_segment = [&]() -> int {
+    const int slot = nu % kUnitSlots;
+    if (!wait(C::U_FULL + slot, (nu / kUnitSlots) & 1)) return -1;
+    ++nu;
+    return s_seg[slot].b < 0 ? -1 : slot;
+  };
+  auto release_segment = [&](int slot) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::U_EMPTY + slot));
+  };
+
+  if (warp < 4) {
+    regs_dec<C::kRegs0>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ S = Q K^T
+      const uint64_t q_desc = smem_desc_k128(base);
+      const uint64_t k_desc = smem_desc_k128(base + C::kRingOff);
+      constexpr uint64_t kTileDesc = kTileBytes >> 4;
+      int ring = 0;                                   // tile of the next K
+      uint32_t ring_ph = 0;
+      int cnt[MT] = {};                               // chunks of each tile so far
+      for (int seg_no = 0;; ++seg_no) {
+        const int slot = next_segment();
+        if (slot < 0) break;
+        const int n = s_seg[slot].c1 - s_seg[slot].c0, rows = s_seg[slot].rows;
+        release_segment(slot);
+        if (!wait(C::Q_FULL, seg_no & 1)) break;
+        for (int j = 0; j < n && ok; ++j) {
+          if (!wait(C::FULL + ring, ring_ph)) break;
+          fence_async_proxy();
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            if (m * 128 >= rows) break;
+            const int buf = m * C::kSBufs + cnt[m] % C::kSBufs;
+            if (!wait(C::S_FREE + buf, ((cnt[m] / C::kSBufs) & 1) ^ 1)) break;
+            ++cnt[m];
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t d = tmem_base + C::s_col(m, buf);
+              const uint64_t qd = q_desc + m * kTileDesc, kd = k_desc + ring * kTileDesc;
+              tc_mma_bf16_c<false>(d, qd, kd, kIdescS);
+#pragma unroll
+              for (int k = 1; k < 8; ++k) {
+                const uint64_t o = (uint64_t)(((k >> 2) * (kTileBytes / 2) + (k & 3) * 32) >> 4);
+                tc_mma_bf16_c<true>(d, qd + o, kd + o, kIdescS);
+              }
+              tc_commit(bar(C::S_FULL + buf));
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (elect_one()) {
+            tc_commit(bar(C::EMPTY + ring));
+            if (j == n - 1) tc_commit(bar(C::Q_EMPTY));
+          }
+          __syncwarp();
+          ring += 2;
+          if (ring >= C::kTiles) {
+            ring -= C::kTiles;
+            ring_ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+      }
+      if (elect_one()) tc_commit(bar(C::DONE_S));
+      __syncwarp();
+      mbar_wait_bounded(bar(C::DONE_S), 0, nullptr, kTeardownNs);
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ O += P V
+      const uint64_t v_desc = smem_desc_mn128(base + C::kRingOff, kTileBytes / 2);
+      constexpr uint64_t kTileDesc = kTileBytes >> 4;
+      int ring = 1;                                   // tile of the next V
+      uint32_t ring_ph = 0;
+      int cnt[MT] = {}, segs[MT] = {};
+      for (;;) {
+        const int slot = next_segment();
+        if (slot < 0) break;
+        const int n = s_seg[slot].c1 - s_seg[slot].c0, rows = s_seg[slot].rows;
+        release_segment(slot);
+        for (int j = 0; j < n && ok; ++j) {
+          if (!wait(C::FULL + ring, ring_ph)) break;
+          fence_async_proxy();
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            if (m * 128 >= rows) break;
+            const int buf = m * C::kSBufs + cnt[m] % C::kSBufs;
+            if (!wait(C::P_READY + buf, (cnt[m] / C::kSBufs) & 1)) break;
+            if (j == 0 && !wait(C::O_FREE + m, (segs[m]++ & 1) ^ 1)) break;
+            ++cnt[m];
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t pa = tmem_base + C::s_col(m, buf), d = tmem_base + C::o_col(m);
+              const uint64_t vd = v_desc + ring * kTileDesc;
+              // 16 keys = two 8-row groups of V (2048 B) and 8 columns of P
+              if (j == 0)
+                tc_mma_bf16_ta_c<false>(d, pa, vd, kIdescO);
+              else
+                tc_mma_bf16_ta_c<true>(d, pa, vd, kIdescO);
+#pragma unroll
+              for (int k = 1; k < 8; ++k) tc_mma_bf16_ta_c<true>(d, pa + k * 8, vd + (uint64_t)(k * (2048 >> 4)), kIdescO);
+              tc_commit(bar(C::S_FREE + buf));
+              tc_commit(bar(C::PV_DONE + m));
+              mbar_arrive(bar(C::PV_DONE + m));       // carries the copies' `bad` mark to the softmax
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (elect_one()) tc_commit(bar(C::EMPTY + ring));
+          __syncwarp();
+          ring += 2;
+          if (ring >= C::kTiles) {
+            ring -= C::kTiles;
+            ring_ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+      }
+      if (elect_one()) tc_commit(bar(C::DONE_PV));
+      __syncwarp();
+      mbar_wait_bounded(bar(C::DONE_PV), 0, nullptr, kTeardownNs);
+      __syncwarp();
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ segments
+      const int heads = p.t * p.kv_per;
+      auto request = [&](int b) {
+        return tree_request(p.qsl[b], p.qsl[b + 1], p.seq_lens[b], p.T, p.max_query_len, p.max_seq_len, gq, kGroupRows);
+      };
+      auto work = [&](const TreeReq& r) { return (long long)heads * r.groups * r.chunks; };
+      // all requests' chunks; CTA 0 leaves their prefix sums for the merge and reports bad counts
+      long long total = 0;
+      for (int b0 = 0; b0 < p.n_reqs; b0 += 32) {
+        const int b = b0 + lane;
+        long long w = 0;
+        if (b < p.n_reqs) {
+          const TreeReq r = request(b);
+          if (!r.ok && blockIdx.x == 0) atomicExch(p.status, kStatusShape);
+          w = work(r);
+        }
+        long long pre = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long up = __shfl_up_sync(0xffffffffu, pre, o);
+          if (lane >= o) pre += up;
+        }
+        if (blockIdx.x == 0 && b < p.n_reqs) p.prefix[b] = total + pre - w;
+        total += __shfl_sync(0xffffffffu, pre, 31);
+      }
+      const long long per = tree_per(total, gridDim.x);
+      if (blockIdx.x == 0 && lane == 0) p.prefix[p.n_reqs] = total;
+      long long pos = per * blockIdx.x;
+      const long long end = min(total, pos + per);
+      // the request that holds the first chunk
+      int b = 0;
+      long long before = 0;
+      if (pos < end) {
+        for (int b0 = 0; b0 < p.n_reqs; b0 += 32) {
+          const long long w = b0 + lane < p.n_reqs ? work(request(b0 + lane)) : 0;
+          long long pre = w;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, pre, o);
+            if (lane >= o) pre += up;
+          }
+          const unsigned hit = __ballot_sync(0xffffffffu, before + pre > pos);
+          if (hit != 0u) {
+            const int f = __ffs(hit) - 1;
+            b = b0 + f;
+            before += __shfl_sync(0xffffffffu, pre - w, f);
+            break;
+          }
+          before += __shfl_sync(0xffffffffu, pre, 31);
+        }
+      }
+      if (lane == 0) {
+        TreeReq r{};
+        if (pos < end) r = request(b);
+        for (int u = 0;; ++u) {
+          const int slot = u % kUnitSlots;
+          if (!mbar_wait_bounded(bar(C::U_EMPTY + slot), ((u / kUnitSlots) & 1) ^ 1, s_abort, timeout)) {
+            if (!*s_abort) {
+              atomicExch(p.status, kStatusTimeout);
+              *s_abort = 1;
+            }
+            break;
+          }
+          Segment s;
+          s.b = -1;
+          if (pos < end) {
+            while (pos - before >= work(r)) {          // this request is done (or empty)
+              before += work(r);
+              r = request(++b);
+            }
+            const TreeSeg q = tree_segment(pos - before, r.chunks, end - pos, blockIdx.x);
+            const int head = (int)(q.unit / r.groups), grp = (int)(q.unit - (long long)head * r.groups);
+            s.b = b;
+            s.r = head / p.kv_per;
+            s.g = head - s.r * p.kv_per;
+            s.row0 = grp * kGroupRows;
+            s.c0 = q.c0;
+            s.c1 = q.c1;
+            s.q0 = r.q0;
+            s.n = r.n;
+            s.len = r.len;
+            s.part = q.part;
+            s.rows = min(kGroupRows, r.n * gq - s.row0);
+            s.bad = 0;
+            pos += q.c1 - q.c0;
+          }
+          s_seg[slot] = s;
+          mbar_arrive(bar(C::U_FULL + slot));
+          if (s.b < 0) break;
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ copies
+    regs_dec<C::kRegs1>();
+    const int w4 = warp - 4, c16 = lane & 15, half = lane >> 4;
+    // this thread copies 16-byte piece c16 of rows 2 w4 + half + 8 k; lane i of the warp finds the
+    // cache row of row 8 (i / 2) + 2 w4 + i % 2
+    const int row_of = 2 * w4 + half, my_row = 8 * (lane >> 1) + 2 * w4 + (lane & 1);
+    const uint32_t dst0 = (c16 >> 3) * (kTileBytes / 2) + row_of * 128 + (((c16 & 7) ^ (row_of & 7)) << 4);
+    // the cache is read once a call by one item (evicted first) or by its groups of rows
+    const uint64_t pol = p.max_query_len * gq > kGroupRows ? policy_evict_normal() : policy_evict_first();
+    int ring = 0;
+    uint32_t ring_ph = 0;
+    auto advance = [&]() {
+      if (++ring == C::kTiles) {
+        ring = 0;
+        ring_ph ^= 1u;
+      }
+    };
+    for (int seg_no = 0;; ++seg_no) {
+      const int slot = next_segment();
+      if (slot < 0) break;
+      const Segment s = s_seg[slot];
+      const int ctx = s.len - s.n;
+      const int* bt = p.block_tables + (size_t)s.b * p.max_blocks;
+      auto block_of = [&](int c) -> int {            // block id of this lane's key of chunk c
+        const int key = c * kTreeChunk + my_row;
+        return key < s.len ? bt[key / p.block_size] : -1;
+      };
+      int blk = block_of(s.c0);
+      for (int c = s.c0; c < s.c1 && ok; ++c) {
+        const int key = c * kTreeChunk + my_row;
+        int row = -1;                                // cache row of this lane's key (-1: zeros)
+        if (key < s.len) {
+          if (blk >= 0 && blk < p.num_blocks)
+            row = (s.r * p.num_blocks + blk) * p.block_size + key % p.block_size;
+          else
+            atomicExch(p.status, kStatusShape);
+        }
+        if (c + 1 < s.c1) blk = block_of(c + 1);
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          if (!wait(C::EMPTY + ring, ring_ph ^ 1)) break;
+          const __nv_bfloat16* src = (kv ? p.cache_v : p.cache_k) + s.g * kHd + c16 * 8;
+          const uint32_t dst = base + C::kRingOff + ring * kTileBytes + dst0;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int rw = __shfl_sync(0xffffffffu, row, 2 * k + half);
+            cp_async16(dst + k * 1024, src + (size_t)max(rw, 0) * p.kv_per * kHd, rw >= 0 ? 16 : 0, pol);
+          }
+          if (kv == 1 && (c + 1) * kTreeChunk > ctx) {
+            // a chunk with drafted tokens: no value that is not finite stays in V
+            cp_async_wait_all();
+            bool any = false;
+#pragma unroll 1
+            for (int k = 0; k < 16; ++k) {
+              uint4* q = reinterpret_cast<uint4*>(base_ptr + (dst - base) + k * 1024);
+              uint4 v = *q;
+              const bool x = drop_nonfinite(v.x), y = drop_nonfinite(v.y), z = drop_nonfinite(v.z), w = drop_nonfinite(v.w);
+              if (x || y || z || w) {
+                *q = v;
+                any = true;
+              }
+            }
+            if (any) *reinterpret_cast<volatile int*>(&s_seg[slot].bad) = 1;
+            mbar_arrive(bar(C::FULL + ring));
+          } else {
+            cp_async_arrive(bar(C::FULL + ring));
+          }
+          advance();
+        }
+        if (ok && c == s.c0) {
+          // the segment's queries (rows past them zero), once the last one's are no longer read
+          if (!wait(C::Q_EMPTY, (seg_no & 1) ^ 1)) break;
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            if (m * 128 >= s.rows) break;
+#pragma unroll 1
+            for (int k = 0; k < 16; ++k) {
+              const int j = m * 128 + row_of + 8 * k, jr = s.row0 + j;
+              const int tok = jr / gq;
+              const __nv_bfloat16* q = p.qkv;
+              if (j < s.rows)
+                q += (size_t)s.r * p.sstride_in + (size_t)(s.q0 + tok) * p.rstride_in + (s.g * gq + jr - tok * gq) * kHd + c16 * 8;
+              cp_async16(base + m * kTileBytes + dst0 + k * 1024, q, j < s.rows ? 16 : 0, pol);
+            }
+          }
+          cp_async_arrive(bar(C::Q_FULL));
+        }
+      }
+      if (!ok) break;
+      release_segment(slot);
+    }
+    cp_async_wait_all();       // no copy into this CTA's shared memory may outlive it
+  } else {
+    // ------------------------------------------------------------ softmax
+    regs_inc<C::kRegsS>();
+    const int tile = (warp - 8) >> 2, q4 = warp & 3;
+    const int row = tile * 128 + q4 * 32 + lane;      // row of the item; tensor-memory lane row % 128
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(q4 * 32) << 16);
+    const float c = p.scale_log2;
+    int cnt = 0;
+    float s[128];
+    for (;;) {
+      const int slot = next_segment();
+      if (slot < 0) break;
+      const int c0 = s_seg[slot].c0, c1 = s_seg[slot].c1, rows = s_seg[slot].rows;
+      if (tile * 128 >= rows) {
+        release_segment(slot);
+        continue;
+      }
+      const int n = s_seg[slot].n, len = s_seg[slot].len, ctx = len - n, q0 = s_seg[slot].q0;
+      const bool idle = tile * 128 + q4 * 32 >= rows;  // no row of this warp
+      const int jr = s_seg[slot].row0 + row, tok = row < rows ? jr / gq : 0;
+      const int* words = p.mask + (size_t)(q0 + tok) * p.mask_words;
+      float m = -INFINITY, l = 0.f;
+      for (int ck = c0; ck < c1; ++ck) {
+        const int buf = tile * C::kSBufs + cnt % C::kSBufs;
+        if (!wait(C::S_FULL + buf, (cnt / C::kSBufs) & 1)) break;
+        if (!idle) {
+          tc_fence_after();
+          const uint32_t sa = lane_addr + C::s_col(tile, buf);
+          tmem_ld32(sa, s);
+          tmem_ld32(sa + 32, s + 32);
+          tmem_ld32(sa + 64, s + 64);
+          tmem_ld32(sa + 96, s + 96);
+          tc_wait_ld();
+          if ((ck + 1) * kTreeChunk > ctx) {
+            // drafted tokens (or the end) in this chunk: the row's mask
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const unsigned bits = tree_window(words, ck * kTreeChunk + 32 * w, ctx, n);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(bits >> i & 1u)) s[32 * w + i] = -INFINITY;
+            }
+          }
+          float mk[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) mk[j] = fmaxf(s[j], s[8 + j]);
+#pragma unroll
+          for (int k = 16; k < 128; k += 16)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mk[j] = fmax3(mk[j], s[k + j], s[k + 8 + j]);
+          const float mx = c * fmax3(fmax3(mk[0], mk[1], mk[2]), fmax3(mk[3], mk[4], mk[5]), fmaxf(mk[6], mk[7]));
+          if (ck == c0) {
+            m = mx;                                   // the first P V overwrites O
+          } else if (__any_sync(0xffffffffu, mx > m + kRescaleLog2)) {
+            // the warp rescales together, every row by its own factor (1 where the max held);
+            // a row that saw nothing so far (m = -inf) has O = 0 and l = 0
+            float f = 1.0f;
+            if (mx > m + kRescaleLog2) {
+              f = fast_exp2(m - mx);
+              l *= f;
+              m = mx;
+            }
+            if (!wait(C::PV_DONE + tile, (cnt - 1) & 1)) break;
+            tc_fence_after();
+            float o[32];
+#pragma unroll
+            for (int k = 0; k < 128; k += 32) {
+              tmem_ld32(lane_addr + C::o_col(tile) + k, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] *= f;
+              tmem_st32(lane_addr + C::o_col(tile) + k, o);
+            }
+          }
+          // P = 2^(s c - m) as bf16 pairs into the first 64 columns of the buffer (the rounding:
+          // the tensor core's A operand shares V's type; at most 2^-8 of a weight)
+          const float mu = m == -INFINITY ? 0.f : m;  // nothing seen yet: every s is -inf, p = 0
+          const uint64_t c2 = f32x2_pack(c, c), nm2 = f32x2_pack(-mu, -mu);
+          uint64_t lk[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              float x0, x1;
+              f32x2_unpack(f32x2_fma(f32x2_pack(s[h * 64 + 2 * j], s[h * 64 + 2 * j + 1]), c2, nm2), x0, x1);
+              const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+              lk[j & 3] = f32x2_add(lk[j & 3], f32x2_pack(e0, e1));
+              pk[j] = pack_bf16x2(e0, e1);
+            }
+            tmem_st32(sa + h * 32, reinterpret_cast<const float*>(pk));
+          }
+          float la[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f32x2_unpack(lk[j], la[2 * j], la[2 * j + 1]);
+          l += ((la[0] + la[1]) + (la[2] + la[3])) + ((la[4] + la[5]) + (la[6] + la[7]));
+          tc_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::P_READY + buf));
+        ++cnt;
+      }
+      if (!ok) break;
+      if (!wait(C::PV_DONE + tile, (cnt - 1) & 1)) break;
+      if (!idle) {
+        tc_fence_after();
+        const int bad = *reinterpret_cast<volatile int*>(&s_seg[slot].bad);
+        const int r = s_seg[slot].r, g = s_seg[slot].g, b = s_seg[slot].b, part = s_seg[slot].part;
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        __nv_bfloat16* dst = p.out + (size_t)r * p.sstride_out + (size_t)(q0 + tok) * p.rstride_out + (g * gq + jr - tok * gq) * kHd;
+        float* po = part >= 0 ? part_o(p, part) + (size_t)row * kHd : nullptr;
+#pragma unroll 1
+        for (int k = 0; k < 128; k += 32) {
+          __syncwarp();
+          tmem_ld32(lane_addr + C::o_col(tile) + k, s);
+          tc_wait_ld();
+          if (bad) {
+            // V values that were dropped, added to the rows that see their keys
+            const int* bt = p.block_tables + (size_t)b * p.max_blocks;
+            const int k0 = max(c0, ctx / kTreeChunk) * kTreeChunk, k1 = min(c1 * kTreeChunk, len);
+            for (int key = k0; row < rows && key < k1; ++key) {
+              if (!(tree_window(words, key & ~31, ctx, n) >> (key & 31) & 1u)) continue;
+              const int blk = bt[key / p.block_size];
+              if (blk < 0 || blk >= p.num_blocks) continue;
+              const __nv_bfloat16* v = p.cache_v + ((size_t)(r * p.num_blocks + blk) * p.block_size + key % p.block_size) * p.kv_per * kHd + g * kHd + k;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float x = __bfloat162float(v[j]);
+                if (!(fabsf(x) < INFINITY)) s[j] += x;
+              }
+            }
+          }
+          if (row < rows) {
+            if (part >= 0) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 8) st_global_v8(po + k + j, *reinterpret_cast<const uint32_t(*)[8]>(s + j));
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; j += 8) {
+                uint4 v;
+                v.x = pack_bf16x2(s[j] * inv, s[j + 1] * inv);
+                v.y = pack_bf16x2(s[j + 2] * inv, s[j + 3] * inv);
+                v.z = pack_bf16x2(s[j + 4] * inv, s[j + 5] * inv);
+                v.w = pack_bf16x2(s[j + 6] * inv, s[j + 7] * inv);
+                *reinterpret_cast<uint4*>(dst + k + j) = v;
+              }
+            }
+          }
+        }
+        if (row < rows && part >= 0)
+          *reinterpret_cast<float2*>(part_o(p, part) + (size_t)p.part_rows * kHd + 2 * row) = make_float2(m, l);
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::O_FREE + tile));
+      release_segment(slot);
+    }
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+// Joins the parts of the items that more than one CTA computed: a warp per query row, four
+// head dimensions per lane, the parts in the order of their keys (the same bits every time).
+//   o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i
+// Scheduled behind the attention grid's last CTAs (programmatic launch); it reads only after
+// that grid has completed.
+constexpr int kMergeRows = 8;    // rows, and warps, of a CTA
+__global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeAttnParams p, int grid, int group_rows) {
+  const int gq = p.q_per / p.kv_per, heads = p.t * p.kv_per;
+  const int strips = (p.max_query_len * gq + kMergeRows - 1) / kMergeRows;   // of one (request, head)
+  const int strip = blockIdx.x % strips, bh = blockIdx.x / strips;
+  const int head = bh % heads, b = bh / heads;
+  const int jr = strip * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const TreeReq rq = tree_request(p.qsl[b], p.qsl[b + 1], p.seq_lens[b], p.T, p.max_query_len, p.max_seq_len, gq, group_rows);
+  if (jr >= rq.n * gq) return;
+  griddep_wait();
+  const long long per = tree_per(p.prefix[p.n_reqs], grid);
+  const int grp = jr / group_rows, row = jr - grp * group_rows;
+  int first, last;
+  tree_parts(p.prefix[b] + ((long long)head * rq.groups + grp) * rq.chunks, rq.chunks, per, &first, &last);
+  if (first == last) return;                       // whole: written by its CTA
+  auto slot = [&](int c) { return c == first ? 2 * c + 1 : 2 * c; };
+  auto ml = [&](int c) {
+    return *reinterpret_cast<const float2*>(part_o(p, slot(c)) + (size_t)p.part_rows * kHd + 2 * row);
+  };
+  float m = -INFINITY;
+  for (int c = first + lane; c <= last; c += 32) m = fmaxf(m, ml(c).x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = first; c <= last; ++c) {
+    const float2 x = ml(c);
+    const float4 v = *reinterpret_cast<const float4*>(part_o(p, slot(c)) + (size_t)row * kHd + 4 * lane);
+    // a part whose keys the row does not see has o = 0, l = 0 and no max
+    const float w = x.x == -INFINITY ? 0.f : exp2f(x.x - m);
+    if (w != 0.f || x.x != -INFINITY) {
+      l += w * x.y;
+      o.x += w * v.x;
+      o.y += w * v.y;
+      o.z += w * v.z;
+      o.w += w * v.w;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  const int r = head / p.kv_per, g = head - r * p.kv_per, tok = jr / gq;
+  uint2 out;
+  out.x = pack_bf16x2(o.x * inv, o.y * inv);
+  out.y = pack_bf16x2(o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2*>(p.out + (size_t)r * p.sstride_out + (size_t)(rq.q0 + tok) * p.rstride_out +
+                            (g * gq + jr - tok * gq) * kHd + 4 * lane) = out;
 }
 
 cudaError_t launch_tree_mask(int T, int n_reqs, int max_query_len, int words, const int* parents, const int* qsl,
@@ -107,10 +762,46 @@ cudaError_t launch_tree_mask(int T, int n_reqs, int max_query_len, int words, co
   return cudaGetLastError();
 }
 
-cudaError_t launch_tree_attention(const TreeAttnParams& p, cudaStream_t st) {
-  const long long items = (long long)p.n_reqs * p.max_query_len * p.t * p.q_per;
-  tree_attn_kernel<<<(unsigned)((items + 3) / 4), 128, 0, st>>>(p);
+int tree_group_rows(int max_rows) { return max_rows <= 128 ? 128 : 256; }
+
+template <int MT>
+static cudaError_t launch_tree_mt(const TreeAttnParams& p, int grid, cudaStream_t st) {
+  using C = TreeCfg<MT>;
+  static std::atomic<uint64_t> attr_done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(tree_attn_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    // the warpgroups' register budgets (setmaxnreg) come out of the registers of the launch
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, tree_attn_kernel<MT>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs * C::kThreads < 128 * (C::kRegs0 + C::kRegs1 + MT * C::kRegsS)) return cudaErrorInvalidConfiguration;
+    attr_done.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  tree_attn_kernel<MT><<<grid, C::kThreads, C::kSmem, st>>>(p);
   return cudaGetLastError();
+}
+
+cudaError_t launch_tree_attention(const TreeAttnParams& p, int grid, cudaStream_t st) {
+  const int gq = p.q_per / p.kv_per, max_rows = p.max_query_len * gq;
+  const int group_rows = tree_group_rows(max_rows);
+  cudaError_t e = group_rows == 128 ? launch_tree_mt<1>(p, grid, st) : launch_tree_mt<2>(p, grid, st);
+  if (e != cudaSuccess) return e;
+  const long long strips = (max_rows + kMergeRows - 1) / kMergeRows;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(strips * p.n_reqs * p.t * p.kv_per));
+  cfg.blockDim = dim3(32 * kMergeRows);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel, p, grid, group_rows);
 }
 
 }  // namespace tpl

@@ -232,6 +232,20 @@ def test_large_scores_and_equal_bits_on_repetition():
     assert status(ws) == 0
 
 
+def test_workspace_on_a_16_byte_boundary_and_odd_row_counts():
+    # partial slots of 18, 5 and 27 rows, the workspace aligned to 16 bytes only, and nothing written past it
+    for nq, nkv, t, n in ((8, 2, 4, 9), (4, 4, 2, 5), (9, 3, 1, 9)):
+        c = build(nq, nkv, t, [700, 64], [n, 2], 16, seed=n)
+        h = handle(nq, nkv, t)
+        need = h.tree_attention_workspace_size(2, n, 700 + n)
+        buf = torch.zeros(need + 64, dtype=torch.uint8, device="cuda")
+        buf[16 + need:] = 77
+        out, ws = run(h, c, ws=buf[16:16 + need])
+        assert status(ws) == 0
+        assert (buf[16 + need:] == 77).all()
+        check(out, c, nq, nkv, t)
+
+
 def test_long_context_many_requests():
     # more work than one pass of the GPU: splits that start and end inside requests
     nq, nkv, t = 8, 2, 2
