@@ -8,6 +8,7 @@ every call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -128,9 +129,8 @@ def lib() -> ctypes.CDLL:
         "tp_tree_mask": [I64, I32, I32, P, P, P, P, I32, P, P, I64, P],
         "tp_tree_attention_workspace_size": [P, I32, I32, I32, PI64],
         "tp_tree_attention": [P, I64, P, P, P, I32, I32, I32, P, I32, P, I32, P, P, I64, I32, P, P, I64, P],
-        "tp_kv_cache_copy_blocks": [P, P, I32, I32, ctypes.POINTER(P), ctypes.POINTER(P), I64, I32, P, I64, P],
-        "tp_kv_cache_compact": [P, I32, P, P, P, I32, P, P, I32, I32, ctypes.POINTER(P), ctypes.POINTER(P), I64, I32,
-                                P, P, I64, P],
+        "tp_kv_cache_copy_blocks": [P, P, I32, I32, P, P, I64, I32, P, I64, P],
+        "tp_kv_cache_compact": [P, I32, P, P, P, I32, P, P, I32, I32, P, P, I64, I32, P, P, I64, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -157,6 +157,10 @@ def _ptr(t: Optional[torch.Tensor]):
 def _stream(stream=None):
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _stream_ptr(stream=None) -> int:
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 def _bf16(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -358,16 +362,25 @@ class TPLinear:
         return (T, t * w) if self.gathered else (t, T, w)
 
     def _layer_pointers(self, caches_k: Sequence[torch.Tensor], caches_v: Sequence[torch.Tensor]):
-        """HOST pointer arrays of the layers' caches (all of one shape), and that shape's blocks and block size."""
+        """Number of layers, HOST addresses of the arrays of their k and v pointers, blocks and block size of
+        the caches (all of one size), and the object that holds the arrays."""
         if len(caches_k) != len(caches_v) or not caches_k:
             raise ValueError("caches_k and caches_v must list the same layers, one at least")
         shape = caches_k[0].shape
         if len(shape) != 5 or shape != self.kv_cache_shape(shape[1], shape[2]):
             raise ValueError(f"a cache has the shape of kv_cache_shape(), not {tuple(shape)}")
         dev, n = self.w_col.device, len(caches_k)
-        ks = (ctypes.c_void_p * n)(*[_bf16_on(c, "cache_k", dev, shape) for c in caches_k])
-        vs = (ctypes.c_void_p * n)(*[_bf16_on(c, "cache_v", dev, shape) for c in caches_v])
-        return n, ks, vs, shape[1], shape[2]
+        both = [*caches_k, *caches_v]
+        _bf16_on(both[0], "cache_k", dev)
+        # a call names every layer's caches: the same checks of all of them, one attribute at a time
+        T, first = torch.Tensor, both[0]
+        if set(map(T.dtype.__get__, both)) != {torch.bfloat16} or set(map(T.get_device, both)) != {first.get_device()}:
+            raise ValueError(f"every cache must be a bf16 tensor on {dev}")
+        if set(map(T.numel, both)) != {first.numel()} or False in map(T.is_contiguous, both):
+            raise ValueError(f"every cache must be contiguous and of the shape {tuple(shape)}")
+        ptrs = array.array("Q", map(T.data_ptr, both))
+        at = ptrs.buffer_info()[0]
+        return n, at, at + 8 * n, shape[1], shape[2], ptrs
 
     def qk_norm_rope(self, qkv: torch.Tensor, positions: torch.Tensor, rope: "Rope", out: Optional[torch.Tensor] = None,
                      slot_mapping: Optional[torch.Tensor] = None, cache_k: Optional[torch.Tensor] = None,
@@ -406,7 +419,7 @@ class TPLinear:
         if block_pairs.dim() != 2 or block_pairs.shape[1] != 2:
             raise ValueError("block_pairs must be [n, 2]")
         dev = self.w_col.device
-        n, ks, vs, nb, bs = self._layer_pointers(caches_k, caches_v)
+        n, ks, vs, nb, bs, _hold = self._layer_pointers(caches_k, caches_v)
         ws = _workspace(ws, 16, dev)
         _check(lib().tp_kv_cache_copy_blocks(self.handle, _i32(block_pairs, "block_pairs", dev), block_pairs.shape[0],
                                              n, ks, vs, nb, bs, ws.data_ptr(), ws.numel(), _stream(stream)))
@@ -423,7 +436,7 @@ class TPLinear:
         n_reqs = seq_lens.numel()
         if accepted.dim() != 2 or src_tables.dim() != 2 or src_tables.shape != dst_tables.shape:
             raise ValueError("accepted is [n_reqs, m], src_tables and dst_tables [n_reqs, max_blocks]")
-        n, ks, vs, nb, bs = self._layer_pointers(caches_k, caches_v)
+        n, ks, vs, nb, bs, _hold = self._layer_pointers(caches_k, caches_v)
         if out is None:
             out = torch.empty(n_reqs, dtype=torch.int32, device=dev)
         ws = _workspace(ws, 16, dev)

@@ -34,44 +34,75 @@ __global__ void kv_copy_blocks_kernel(const KvLayers layers, const int2* __restr
   for (long long e = threadIdx.x; e < page_vecs; e += blockDim.x) dst[e] = src[e];
 }
 
-// One CTA per (request, shard) and (layer, k or v); a thread moves one 16-byte column of
-// the accepted tokens' rows, in their order. Accepted indices rise, so in place (one page
-// holding both positions) position ctx + j is written only after every token up to j has
-// been read, and the tokens after j come from higher positions: no row is lost.
-__global__ void kv_compact_kernel(const KvLayers layers, const CompactParams p) {
-  const int r = blockIdx.x % p.t, b = blockIdx.x / p.t;
+// A request's rows of all layers, k and v, and shards are one line of 16-byte columns; a CTA
+// takes 256 of them and a thread moves its
+// columns of the accepted tokens in their order, eight rows in flight. The CTA first turns
+// the list into pairs of slots, kept in shared memory.
+// Accepted indices rise, so in place (one page holding both positions) position ctx + j is
+// written only after every token up to j has been read, and the tokens after j come from
+// higher positions: no row is lost.
+constexpr int kCompactThreads = 256;
+__global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const KvLayers layers, const CompactParams p,
+                                                                     int n_layers, int strips) {
+  __shared__ int2 move[kCompactThreads];             // slots (from, to) of a strip of the list
+  __shared__ int s_stop;
+  const int b = blockIdx.x / strips, strip = blockIdx.x - b * strips, tid = threadIdx.x;
   const int q0 = p.qsl[b], n_new = p.qsl[b + 1] - q0, L = p.seq_lens[b], ctx = L - n_new;
-  const bool first = blockIdx.y == 0 && r == 0 && threadIdx.x == 0;
-  if (n_new < 0 || ctx < 0 || (L + p.block_size - 1) / p.block_size > p.max_blocks) {
-    if (first) {
+  if (n_new < 0 || ctx < 0 || L > (long long)p.max_blocks * p.block_size) {
+    if (strip == 0 && tid == 0) {
       atomicExch(p.status, kStatusShape);
       p.new_lens[b] = L;
     }
     return;
   }
-  const int layer = blockIdx.y >> 1;
-  uint4* cache = reinterpret_cast<uint4*>((blockIdx.y & 1) ? layers.v[layer] : layers.k[layer]);
+  // this thread's column: 16 bytes of a (layer, k or v, shard) row
   const int vec = p.kv_per * kHd / 8;
+  const long long col = (long long)strip * kCompactThreads + tid, cols = 2LL * n_layers * p.t * vec;
+  const bool have = col < cols;
+  const int lk = have ? (int)(col / ((long long)p.t * vec)) : 0;
+  const int in = have ? (int)(col - (long long)lk * p.t * vec) : 0, r = in / vec, c = in - r * vec;
+  uint4* cache = reinterpret_cast<uint4*>((lk & 1) ? layers.v[lk >> 1] : layers.k[lk >> 1]) + (size_t)r * p.n_slots * vec + c;
+  const int* acc = p.accepted + (size_t)b * p.max_accepted;
   const int* src_t = p.src_tables + (size_t)b * p.max_blocks;
   const int* dst_t = p.dst_tables + (size_t)b * p.max_blocks;
-  int j = 0;
-  for (int prev = -1; j < p.max_accepted; ++j) {
-    const int a = p.accepted[(size_t)b * p.max_accepted + j];
-    if (a < 0) break;
-    const int so = ctx + a, to = ctx + j;
-    const bool in = a > prev && a < n_new;
-    const int sb = in ? src_t[so / p.block_size] : -1, db = in ? dst_t[to / p.block_size] : -1;
-    if (sb < 0 || db < 0 || sb >= p.num_blocks || db >= p.num_blocks) {
-      if (threadIdx.x == 0) atomicExch(p.status, kStatusShape);
-      break;
+  int kept = 0;
+  for (int j0 = 0; j0 < p.max_accepted; j0 += kCompactThreads) {
+    if (tid == 0) s_stop = kCompactThreads;
+    __syncthreads();
+    const int j = j0 + tid;
+    const int a = j < p.max_accepted ? acc[j] : -1;
+    bool good = a >= 0, error = false;
+    if (good) {
+      const int prev = j > 0 ? acc[j - 1] : -1;
+      const int from = ctx + a, to = ctx + j;
+      error = a <= prev || a >= n_new || a < j;     // rising from 0 on: a >= j, so `to` stays in the table
+      if (!error) {
+        const int sb = src_t[from / p.block_size], db = dst_t[to / p.block_size];
+        error = sb < 0 || db < 0 || sb >= p.num_blocks || db >= p.num_blocks;
+        move[tid] = make_int2(sb * p.block_size + from % p.block_size, db * p.block_size + to % p.block_size);
+      }
+      good = !error;
     }
-    prev = a;
-    const long long s = (long long)sb * p.block_size + so % p.block_size, d = (long long)db * p.block_size + to % p.block_size;
-    if (s == d) continue;
-    for (int c = threadIdx.x; c < vec; c += blockDim.x)
-      cache[((size_t)r * p.n_slots + d) * vec + c] = cache[((size_t)r * p.n_slots + s) * vec + c];
+    if (!good) atomicMin(&s_stop, tid);
+    __syncthreads();
+    const int n = min(s_stop, p.max_accepted - j0);
+    if (error && tid == n && strip == 0) atomicExch(p.status, kStatusShape);   // what ended the list
+    if (have) {
+      for (int k0 = 0; k0 < n; k0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k0 + k < n) v[k] = cache[(size_t)move[k0 + k].x * vec];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k0 + k < n && move[k0 + k].x != move[k0 + k].y) cache[(size_t)move[k0 + k].y * vec] = v[k];
+      }
+    }
+    kept += n;
+    if (n < kCompactThreads) break;
+    __syncthreads();
   }
-  if (first) p.new_lens[b] = ctx + j;
+  if (strip == 0 && tid == 0) p.new_lens[b] = ctx + kept;
 }
 
 cudaError_t launch_kv_copy_blocks(const KvLayers& layers, int n_layers, const int* pairs, int n_pairs,
@@ -84,8 +115,10 @@ cudaError_t launch_kv_copy_blocks(const KvLayers& layers, int n_layers, const in
 }
 
 cudaError_t launch_kv_compact(const KvLayers& layers, int n_layers, const CompactParams& p, int n_reqs, cudaStream_t st) {
-  const dim3 grid((unsigned)((long long)n_reqs * p.t), (unsigned)(2 * n_layers));
-  kv_compact_kernel<<<grid, 64, 0, st>>>(layers, p);
+  const long long cols = 2LL * n_layers * p.t * (p.kv_per * kHd / 8);
+  const int strips = (int)((cols + kCompactThreads - 1) / kCompactThreads);
+  if ((long long)n_reqs * strips > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  kv_compact_kernel<<<(unsigned)((long long)n_reqs * strips), kCompactThreads, 0, st>>>(layers, p, n_layers, strips);
   return cudaGetLastError();
 }
 

@@ -19,6 +19,11 @@ namespace tpl {
 namespace {
 constexpr int kStatusShape = -2;   // TP_ERR_SHAPE
 constexpr int kWarps = 4;
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return reinterpret_cast<const uint32_t&>(v);
+}
 }  // namespace
 
 // Entry (p, i): the angle p * f_i in 64 bits (its fraction of a turn would be lost in
@@ -35,9 +40,12 @@ __global__ void rope_table_kernel(const RopeFreqs f, long long n_pos, int half, 
   }
 }
 
-// One warp per (token, shard, head).
+// The general kernel: one warp per (token, shard, head), the head in shared memory. It takes
+// the half layout with a rotary_dim that is no multiple of 16, whose pairs do not lie in
+// whole 16-byte pieces (4096 tokens of 32 + 16 heads, t = 4: 113 us, where the vector kernel
+// below takes 22).
 __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopeParams p) {
-  __shared__ float xs[kWarps][256];
+  __shared__ float xs[kWarps][kRopeMaxDim];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int heads = p.q_per + 2 * p.kv_per;
   const long long items = (long long)p.T * p.t * heads;
@@ -55,16 +63,15 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopePar
     }
     const size_t at = (size_t)r * p.sstride + (size_t)i * p.rstride + (size_t)h * hd;
     __nv_bfloat16* cache = nullptr;
+    const bool is_v = h >= p.q_per + p.kv_per;
     if (p.slots != nullptr && h >= p.q_per) {
       const long long s = p.slots[i];
-      const bool v = h >= p.q_per + p.kv_per;
       if (s >= p.n_slots) {
         if (lane == 0) atomicExch(p.status, kStatusShape);
       } else if (s >= 0) {
-        cache = (v ? p.cache_v : p.cache_k) + (((size_t)r * p.n_slots + s) * p.kv_per + (h - p.q_per) % p.kv_per) * hd;
+        cache = (is_v ? p.cache_v : p.cache_k) + (((size_t)r * p.n_slots + s) * p.kv_per + (h - p.q_per) % p.kv_per) * hd;
       }
     }
-    const bool is_v = h >= p.q_per + p.kv_per;
     const __nv_bfloat16* gamma = is_v ? nullptr : h < p.q_per ? p.q_gamma : p.k_gamma;
     float ss = 0.f;
     for (int e = lane; e < hd; e += 32) {
@@ -96,6 +103,164 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopePar
   }
 }
 
+// The vector kernel. Bound by HBM: every q, k and v element is read once and written once.
+// A head is held by G lanes, two 16-byte pieces of 8 elements each, chosen so that both
+// elements of every pair are in one lane and no exchange is needed:
+//   half layout         pieces l and l + rd/16 for l < rd/16 (pairs 8 l .. 8 l + 7), the
+//                       unrotated pieces two by two after them
+//   interleaved layout  pieces 2 l and 2 l + 1 (the same pairs 8 l .. 8 l + 7)
+// A warp takes `per_warp` steps of 32 / G heads of ONE token, so a lane's cosines, sines and
+// gammas are loaded once for all its heads; the loads of kUnroll steps are in flight
+// together. Few tokens: one step per warp, many short warps (latency); many: a token per
+// warp.
+template <int G>
+__global__ void __launch_bounds__(256) qk_norm_rope_vec_kernel(const RopeParams p, int per_warp, int parts) {
+  constexpr int kUnroll = 3, HPW = 32 / G;           // heads of a step
+  const int lane = threadIdx.x & 31;
+  const long long wid = blockIdx.x * 8LL + (threadIdx.x >> 5);
+  const int i = (int)(wid / parts), part = (int)(wid - (long long)i * parts);
+  if (i >= p.T) return;
+  const int heads = p.q_per + 2 * p.kv_per, total = p.t * heads;
+  const int sub = lane / G, l = lane % G;
+  // the pieces of this lane (vb < 0 or va < 0: none)
+  const int nv = p.hd >> 3, half = p.rd >> 1;
+  int va, vb, rot;                                   // rot: rotated pairs of this lane (8 l on)
+  if (p.interleaved) {
+    va = 2 * l;
+    vb = 2 * l + 1;
+    rot = min(8, max(0, half - 8 * l));
+  } else {
+    const int np = p.rd >> 4;
+    va = l < np ? l : 2 * l;
+    vb = l < np ? l + np : 2 * l + 1;
+    rot = l < np ? 8 : 0;
+  }
+  if (va >= nv) va = -1;
+  if (vb >= nv) vb = -1;
+  const long long pos = p.pos[i];
+  const int slot = p.slots != nullptr ? p.slots[i] : -1;
+  const int h0 = part * per_warp * HPW + sub, h_end = min(total, (part + 1) * per_warp * HPW);
+  const bool in_place = p.in == p.out;
+  uint4 a[kUnroll], b[kUnroll];
+  auto address = [&](int h, int& head) -> size_t {   // shard-local head and element offset of head h
+    const int r = h / heads;
+    head = h - r * heads;
+    return (size_t)r * p.sstride + (size_t)i * p.rstride + (size_t)head * p.hd;
+  };
+  auto load = [&](int u, int h) {
+    a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (h < h_end) {
+      int head;
+      const __nv_bfloat16* src = p.in + address(h, head);
+      if (in_place && p.slots == nullptr && head >= p.q_per + p.kv_per) return;   // v stays where it is
+      if (va >= 0) a[u] = *reinterpret_cast<const uint4*>(src + va * 8);
+      if (vb >= 0) b[u] = *reinterpret_cast<const uint4*>(src + vb * 8);
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) load(u, h0 + u * HPW);
+  if (pos < 0 || pos >= p.n_pos) {                   // padding token, or past the table: nothing is written
+    if (pos >= 0 && lane == 0) atomicExch(p.status, kStatusShape);
+    return;
+  }
+  if (slot >= p.n_slots && p.slots != nullptr && lane == 0) atomicExch(p.status, kStatusShape);
+  const bool write = slot >= 0 && slot < p.n_slots;
+  float c[8], s[8];
+  const float* tab = p.table + pos * p.rd + 8 * l;
+  if (rot == 8 && (p.rd & 7) == 0) {
+#pragma unroll
+    for (int k = 0; k < 8; k += 4) {
+      *reinterpret_cast<float4*>(c + k) = *reinterpret_cast<const float4*>(tab + k);
+      *reinterpret_cast<float4*>(s + k) = *reinterpret_cast<const float4*>(tab + half + k);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      c[k] = k < rot ? tab[k] : 1.f;
+      s[k] = k < rot ? tab[half + k] : 0.f;
+    }
+  }
+  const float inv_hd = 1.0f / p.hd;
+  for (int hb = h0; hb - sub < h_end; hb += kUnroll * HPW) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int h = hb + u * HPW;
+      int head;
+      const size_t at = address(min(h, total - 1), head);
+      const bool is_v = head >= p.q_per + p.kv_per, is_k = !is_v && head >= p.q_per;
+      uint4 oa = a[u], ob = b[u];
+      const __nv_bfloat16* gamma = is_v ? nullptr : is_k ? p.k_gamma : p.q_gamma;
+      float x[8], y[8];
+      const uint32_t* wa = &a[u].x;
+      const uint32_t* wb = &b[u].x;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[2 * k] = __uint_as_float(wa[k] << 16);
+        x[2 * k + 1] = __uint_as_float(wa[k] & 0xffff0000u);
+        y[2 * k] = __uint_as_float(wb[k] << 16);
+        y[2 * k + 1] = __uint_as_float(wb[k] & 0xffff0000u);
+      }
+      if (p.q_gamma != nullptr || p.k_gamma != nullptr) {   // the whole warp: its heads share the exchange
+        float ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ss += x[k] * x[k] + y[k] * y[k];
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (gamma != nullptr) {
+          const float rs = 1.0f / sqrtf(ss * inv_hd + p.eps);
+          uint4 ga = make_uint4(0u, 0u, 0u, 0u), gb = ga;
+          if (va >= 0) ga = __ldg(reinterpret_cast<const uint4*>(gamma + va * 8));
+          if (vb >= 0) gb = __ldg(reinterpret_cast<const uint4*>(gamma + vb * 8));
+          const uint32_t* wga = &ga.x;
+          const uint32_t* wgb = &gb.x;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x[2 * k] *= rs * __uint_as_float(wga[k] << 16);
+            x[2 * k + 1] *= rs * __uint_as_float(wga[k] & 0xffff0000u);
+            y[2 * k] *= rs * __uint_as_float(wgb[k] << 16);
+            y[2 * k + 1] *= rs * __uint_as_float(wgb[k] & 0xffff0000u);
+          }
+        }
+      }
+      if (!is_v) {
+        if (p.interleaved) {
+          // pairs (x0 x1) (x2 x3) .. of piece a are 8 l .. 8 l + 3, of piece b 8 l + 4 .. 8 l + 7
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float x0 = x[2 * k], x1 = x[2 * k + 1], y0 = y[2 * k], y1 = y[2 * k + 1];
+            x[2 * k] = x0 * c[k] - x1 * s[k];
+            x[2 * k + 1] = x1 * c[k] + x0 * s[k];
+            y[2 * k] = y0 * c[4 + k] - y1 * s[4 + k];
+            y[2 * k + 1] = y1 * c[4 + k] + y0 * s[4 + k];
+          }
+        } else if (rot) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float x0 = x[k];
+            x[k] = x0 * c[k] - y[k] * s[k];
+            y[k] = y[k] * c[k] + x0 * s[k];
+          }
+        }
+        oa = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+        ob = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+      }
+      if (h < h_end) {
+        if (!is_v || !in_place) {
+          if (va >= 0) *reinterpret_cast<uint4*>(p.out + at + va * 8) = oa;
+          if (vb >= 0) *reinterpret_cast<uint4*>(p.out + at + vb * 8) = ob;
+        }
+        if (write && head >= p.q_per) {
+          __nv_bfloat16* dst = (is_v ? p.cache_v : p.cache_k) +
+                               (((size_t)(h / heads) * p.n_slots + slot) * p.kv_per + (head - p.q_per - (is_v ? p.kv_per : 0))) * p.hd;
+          if (va >= 0) *reinterpret_cast<uint4*>(dst + va * 8) = oa;
+          if (vb >= 0) *reinterpret_cast<uint4*>(dst + vb * 8) = ob;
+        }
+      }
+      load(u, h + kUnroll * HPW);                    // this step's place for the one kUnroll steps on
+    }
+  }
+}
+
 cudaError_t launch_rope_table(const RopeFreqs& f, long long n_pos, int rotary_dim, float* table, int nsm, cudaStream_t st) {
   const long long n = n_pos * (rotary_dim / 2);
   const int grid = (int)std::min<long long>((n + 255) / 256, 16LL * nsm);
@@ -103,7 +268,28 @@ cudaError_t launch_rope_table(const RopeFreqs& f, long long n_pos, int rotary_di
   return cudaGetLastError();
 }
 
+template <int G>
+static void launch_vec(const RopeParams& p, int nsm, cudaStream_t st) {
+  // steps of 32 / G heads of a token, shared out so that about 16 warps per SM have work; a
+  // warp that has a whole token loads its cosines once
+  const int steps = (p.t * (p.q_per + 2 * p.kv_per) * G + 31) / 32;
+  const long long want = 16LL * nsm;
+  const int parts = (int)std::max<long long>(1, std::min<long long>(steps, want / std::max(1, p.T)));
+  const int per_warp = (steps + parts - 1) / parts, used = (steps + per_warp - 1) / per_warp;
+  const long long warps = (long long)p.T * used;
+  qk_norm_rope_vec_kernel<G><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(p, per_warp, used);
+}
+
 cudaError_t launch_qk_norm_rope(const RopeParams& p, int nsm, cudaStream_t st) {
+  if (p.interleaved || p.rd % 16 == 0) {
+    const int lanes = (p.hd / 8 + 1) / 2;            // of a head
+    if (lanes <= 1) launch_vec<1>(p, nsm, st);
+    else if (lanes <= 2) launch_vec<2>(p, nsm, st);
+    else if (lanes <= 4) launch_vec<4>(p, nsm, st);
+    else if (lanes <= 8) launch_vec<8>(p, nsm, st);
+    else launch_vec<16>(p, nsm, st);
+    return cudaGetLastError();
+  }
   const long long items = (long long)p.T * p.t * (p.q_per + 2 * p.kv_per);
   const int grid = (int)std::min<long long>((items + kWarps - 1) / kWarps, 16LL * nsm);
   qk_norm_rope_kernel<<<grid, 32 * kWarps, 0, st>>>(p);
