@@ -9,6 +9,22 @@ namespace tpl {
 
 constexpr int kStatusCapacity = -5;
 
+// A launch that may be scheduled before the grid in front of it has completed (programmatic
+// serialisation). Its kernel executes griddepcontrol.wait in every thread that goes on, before
+// it reads or writes anything in global memory, so that results are those of stream order.
+inline cudaLaunchConfig_t programmatic(dim3 grid, int threads, size_t smem, cudaStream_t st, cudaLaunchAttribute* attr) {
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
 // ---------------------------------------------------------------- capture
 constexpr int kCaptureMaxTensors = 8;
 struct CaptureMeta {
@@ -161,6 +177,9 @@ cudaError_t launch_kv_copy_blocks(const KvLayers& layers, int n_layers, const in
 cudaError_t launch_kv_compact(const KvLayers& layers, int n_layers, const CompactParams& p, int n_reqs, cudaStream_t st);
 
 // Attention of drafted token trees over the cache (tree_attention.cu).
+struct TreeItem {
+  int r, g, row0, rows, q0, last, pad0, pad1;   // rows 0: none; last: the last CTA that holds a part
+};
 struct TreeAttnParams {
   const __nv_bfloat16* qkv;          // drafted tokens: shard r, token i at qkv + r * sstride_in + i * rstride_in
   long long sstride_in;
@@ -177,7 +196,7 @@ struct TreeAttnParams {
   int* status;
   int T, n_reqs, t, q_per, kv_per, max_blocks, num_blocks, block_size, max_query_len, max_seq_len, mask_words;
   float scale_log2;                  // log2(e) / sqrt(hd)
-  long long* prefix;                 // [n_reqs + 1] chunks before each request, written for the merge
+  TreeItem* items;                   // [grid] the item each CTA begins and others go on with, for the merge
   float* partials;                   // [2 * grid] slots of part_rows x (128 + 2)
   int part_rows;
   unsigned long long timeout_ns;

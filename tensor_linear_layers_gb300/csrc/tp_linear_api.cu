@@ -1718,7 +1718,7 @@ int tp_tree_mask(int64_t T, int32_t n_reqs, int32_t max_query_len, const int32_t
 }
 
 // Tree attention: at most one CTA per SM, no more than there are chunks of keys. Workspace: the
-// status word, the requests' prefix sums, two partial slots per CTA.
+// status word, the item each CTA leaves unfinished, two partial slots per CTA.
 namespace {
 struct TreePlan {
   int grid, part_rows;
@@ -1730,7 +1730,7 @@ TreePlan tree_plan(const tp_linear* h, int n_reqs, int max_query_len, int max_se
   TreePlan pl{};
   pl.grid = (int)std::min<int64_t>(h->nsm, chunks);
   pl.part_rows = (std::min(rows, max_rows) + 7) / 8 * 8;    // a slot is a multiple of 32 bytes (32-byte stores)
-  pl.partials_off = align256(256 + 8 * ((int64_t)n_reqs + 1));
+  pl.partials_off = align256(256 + (int64_t)sizeof(TreeItem) * pl.grid);
   // the workspace itself is 16-byte aligned: room to start the slots on a 32-byte boundary
   pl.ws_bytes = align256(pl.partials_off + 32 + 2LL * pl.grid * pl.part_rows * (128 + 2) * 4);
   return pl;
@@ -1809,7 +1809,7 @@ int tp_tree_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t*
   p.max_seq_len = max_seq_len;
   p.mask_words = mask_words;
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt(128.0));
-  p.prefix = reinterpret_cast<long long*>(static_cast<char*>(workspace) + 256);
+  p.items = reinterpret_cast<TreeItem*>(static_cast<char*>(workspace) + 256);
   p.partials = reinterpret_cast<float*>(
       (reinterpret_cast<uintptr_t>(workspace) + (uintptr_t)pl.partials_off + 31) & ~uintptr_t(31));
   p.part_rows = pl.part_rows;

@@ -31,6 +31,8 @@ __global__ void __launch_bounds__(kMaxDraft)
                      int* __restrict__ status) {
   __shared__ int par[kMaxDraft];
   const int b = blockIdx.x, i = threadIdx.x;
+  griddep_launch_dependents();
+  griddep_wait();
   const int q0 = qsl[b], n = qsl[b + 1] - q0, ctx = seq_lens[b] - n;
   if (q0 < 0 || n < 0 || n > max_query_len || q0 > T - n || ctx < 0) {
     if (i == 0) atomicExch(status, kStatusShape);
@@ -74,8 +76,11 @@ __global__ void __launch_bounds__(kMaxDraft)
 // CTA per SM; the chunks of all items are one line cut into equal ranges (tree_plan.h), so
 // the CTAs stream the same number of keys whatever the requests' lengths.
 //
-// MT = 1: up to 128 rows per item, S/P in three buffers. MT = 2: up to 256 rows as two tiles
-// on the same K and V, one S/P buffer each (tensor memory holds 512 columns: 2 x (S + O)).
+// MT = 1: up to 128 rows per item; S of a chunk in one of three buffers of 128 columns; two Q
+// buffers, so that the next segment's queries load while this one's are read. MT = 2: up to
+// 256 rows as two tiles on the same K and V. Tensor memory holds 512 columns, 2 x 128 of them
+// O: S goes by halves of a chunk (64 keys), two buffers of 64 columns per tile, so that a
+// tile's next S is ready when its softmax is done with the last.
 //
 //   warp 0      issues S;  warp 1 issues P V (an elected lane of a converged warp);
 //   warp 2      walks the CTA's range and publishes segments; warp 3 idle
@@ -95,31 +100,33 @@ namespace {
 constexpr int kTileBytes = 128 * 128 * 2;      // 128 rows x 128 bf16: two 64-column boxes
 constexpr int kUnitSlots = 4;
 constexpr float kRescaleLog2 = 8.0f;           // rescale O when the row max grows by more than this
-constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128);
 constexpr uint32_t kIdescO = idesc_bf16_f32(128, 128) | kIdescBMnMajor;
 constexpr int kTmemCols = 512;
 
 template <int MT>
 struct TreeCfg {
   static constexpr int kThreads = 256 + 128 * MT;
-  static constexpr int kTiles = MT == 1 ? 6 : 5;           // K/V ring
-  static constexpr int kSBufs = MT == 1 ? 3 : 1;           // S/P buffers of a tile
-  static constexpr int kRingOff = MT * kTileBytes;         // after Q
+  static constexpr int kTiles = 5;                         // K/V ring
+  static constexpr int kQBufs = MT == 1 ? 2 : 1;
+  static constexpr int kSub = MT == 1 ? 128 : 64;          // keys of one S, softmax and P V
+  static constexpr int kSubs = kTreeChunk / kSub;
+  static constexpr int kSBufs = MT == 1 ? 3 : 2;           // S/P buffers of a tile
+  static constexpr uint32_t kIdescS = idesc_bf16_f32(128, kSub);
+  static constexpr int kRingOff = MT * kQBufs * kTileBytes;   // after Q
   static constexpr int kBarOff = kRingOff + kTiles * kTileBytes;
   // registers: issuers, copies, softmax
-  static constexpr int kRegs0 = 56, kRegs1 = MT == 1 ? 120 : 72, kRegsS = MT == 1 ? 232 : 192;
+  static constexpr int kRegs0 = 80, kRegs1 = MT == 1 ? 152 : 96, kRegsS = MT == 1 ? 232 : 168;
   static constexpr int kLaunchRegs = MT == 1 ? 168 : 128;
   static_assert(128 * (kRegs0 + kRegs1 + MT * kRegsS) <= kThreads * kLaunchRegs, "register split within the launch's");
-  // tensor memory: MT = 1: S/P at 0, 128, 256, O at 384; MT = 2: tile m S/P at 256 m, O at 256 m + 128
-  static __device__ __forceinline__ uint32_t s_col(int tile, int buf) { return MT == 1 ? buf * 128 : tile * 256; }
+  // tensor memory: MT = 1: S/P at 0, 128, 256, O at 384; MT = 2: tile m S/P at 256 m and 256 m + 64, O at 256 m + 128
+  static __device__ __forceinline__ uint32_t s_col(int tile, int buf) { return tile * 256 + (buf - tile * kSBufs) * kSub; }
   static __device__ __forceinline__ uint32_t o_col(int tile) { return MT == 1 ? 384 : tile * 256 + 128; }
   enum {
-    Q_FULL = 0, Q_EMPTY, FULL, EMPTY = FULL + kTiles,
+    Q_FULL = 0, Q_EMPTY = Q_FULL + kQBufs, FULL = Q_EMPTY + kQBufs, EMPTY = FULL + kTiles,
     S_FULL = EMPTY + kTiles,          // per S/P buffer of every tile
     P_READY = S_FULL + MT * kSBufs,
-    S_FREE = P_READY + MT * kSBufs,
-    PV_DONE = S_FREE + MT * kSBufs,   // per tile
-    O_FREE = PV_DONE + MT,
+    S_FREE = P_READY + MT * kSBufs,   // its P V has completed
+    O_FREE = S_FREE + MT * kSBufs,    // per tile
     U_FULL = O_FREE + MT, U_EMPTY = U_FULL + kUnitSlots,
     DONE_S = U_EMPTY + kUnitSlots, DONE_PV, NBARS
   };
@@ -185,13 +192,12 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
   Segment* s_seg = reinterpret_cast<Segment*>(base_ptr + C::kUnitOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_launch_dependents();   // the merge grid may be scheduled; it waits for this one to complete
-
   if (threadIdx.x == 0) {
     for (int b = 0; b < C::NBARS; ++b) {
       int count = 1;
-      if (b == C::Q_FULL || (b >= C::FULL && b < C::EMPTY)) count = 128;        // every copying thread
+      if (b < C::Q_EMPTY || (b >= C::FULL && b < C::EMPTY)) count = 128;        // every copying thread
       if (b >= C::P_READY && b < C::S_FREE) count = 4;                          // the tile's softmax warps
-      if (b >= C::PV_DONE && b < C::O_FREE) count = 2;                          // the MMAs, and their issuer
+      if (b >= C::S_FREE && b < C::O_FREE) count = 2;                           // the MMAs, and their issuer
       if (b >= C::O_FREE && b < C::U_FULL) count = 4;
       if (b >= C::U_EMPTY && b < C::DONE_S) count = 2 + 4 + 4 * MT;             // issuers, copy and softmax warps
       mbar_init(bar(b), count);
@@ -203,6 +209,9 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
     tmem_alloc(smem_u32(const_cast<uint32_t*>(s_tmem)), kTmemCols);
     tmem_relinquish();
   }
+  // the set-up above may overlap the grid before (programmatic launch); nothing that grid
+  // wrote is read before this
+  griddep_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -252,34 +261,40 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
         if (slot < 0) break;
         const int n = s_seg[slot].c1 - s_seg[slot].c0, rows = s_seg[slot].rows;
         release_segment(slot);
-        if (!wait(C::Q_FULL, seg_no & 1)) break;
+        const int qb = seg_no % C::kQBufs;
+        if (!wait(C::Q_FULL + qb, (seg_no / C::kQBufs) & 1)) break;
         for (int j = 0; j < n && ok; ++j) {
           if (!wait(C::FULL + ring, ring_ph)) break;
           fence_async_proxy();
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            if (m * 128 >= rows) break;
-            const int buf = m * C::kSBufs + cnt[m] % C::kSBufs;
-            if (!wait(C::S_FREE + buf, ((cnt[m] / C::kSBufs) & 1) ^ 1)) break;
-            ++cnt[m];
-            tc_fence_after();
-            if (elect_one()) {
-              const uint32_t d = tmem_base + C::s_col(m, buf);
-              const uint64_t qd = q_desc + m * kTileDesc, kd = k_desc + ring * kTileDesc;
-              tc_mma_bf16_c<false>(d, qd, kd, kIdescS);
+          for (int h = 0; h < C::kSubs; ++h) {
 #pragma unroll
-              for (int k = 1; k < 8; ++k) {
-                const uint64_t o = (uint64_t)(((k >> 2) * (kTileBytes / 2) + (k & 3) * 32) >> 4);
-                tc_mma_bf16_c<true>(d, qd + o, kd + o, kIdescS);
+            for (int m = 0; m < MT; ++m) {
+              if (m * 128 >= rows) break;
+              const int buf = m * C::kSBufs + cnt[m] % C::kSBufs;
+              if (!wait(C::S_FREE + buf, ((cnt[m] / C::kSBufs) & 1) ^ 1)) break;
+              ++cnt[m];
+              tc_fence_after();
+              if (elect_one()) {
+                const uint32_t d = tmem_base + C::s_col(m, buf);
+                // half h of the chunk: 64 K rows of 128 bytes further
+                const uint64_t qd = q_desc + (qb * MT + m) * kTileDesc, kd = k_desc + ring * kTileDesc + h * ((64 * 128) >> 4);
+                tc_mma_bf16_c<false>(d, qd, kd, C::kIdescS);
+#pragma unroll
+                for (int k = 1; k < 8; ++k) {
+                  const uint64_t o = (uint64_t)(((k >> 2) * (kTileBytes / 2) + (k & 3) * 32) >> 4);
+                  tc_mma_bf16_c<true>(d, qd + o, kd + o, C::kIdescS);
+                }
+                tc_commit(bar(C::S_FULL + buf));
               }
-              tc_commit(bar(C::S_FULL + buf));
+              __syncwarp();
             }
-            __syncwarp();
+            if (!ok) break;
           }
           if (!ok) break;
           if (elect_one()) {
             tc_commit(bar(C::EMPTY + ring));
-            if (j == n - 1) tc_commit(bar(C::Q_EMPTY));
+            if (j == n - 1) tc_commit(bar(C::Q_EMPTY + qb));
           }
           __syncwarp();
           ring += 2;
@@ -310,28 +325,33 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
           if (!wait(C::FULL + ring, ring_ph)) break;
           fence_async_proxy();
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            if (m * 128 >= rows) break;
-            const int buf = m * C::kSBufs + cnt[m] % C::kSBufs;
-            if (!wait(C::P_READY + buf, (cnt[m] / C::kSBufs) & 1)) break;
-            if (j == 0 && !wait(C::O_FREE + m, (segs[m]++ & 1) ^ 1)) break;
-            ++cnt[m];
-            tc_fence_after();
-            if (elect_one()) {
-              const uint32_t pa = tmem_base + C::s_col(m, buf), d = tmem_base + C::o_col(m);
-              const uint64_t vd = v_desc + ring * kTileDesc;
-              // 16 keys = two 8-row groups of V (2048 B) and 8 columns of P
-              if (j == 0)
-                tc_mma_bf16_ta_c<false>(d, pa, vd, kIdescO);
-              else
-                tc_mma_bf16_ta_c<true>(d, pa, vd, kIdescO);
+          for (int h = 0; h < C::kSubs; ++h) {
 #pragma unroll
-              for (int k = 1; k < 8; ++k) tc_mma_bf16_ta_c<true>(d, pa + k * 8, vd + (uint64_t)(k * (2048 >> 4)), kIdescO);
-              tc_commit(bar(C::S_FREE + buf));
-              tc_commit(bar(C::PV_DONE + m));
-              mbar_arrive(bar(C::PV_DONE + m));       // carries the copies' `bad` mark to the softmax
+            for (int m = 0; m < MT; ++m) {
+              if (m * 128 >= rows) break;
+              const int buf = m * C::kSBufs + cnt[m] % C::kSBufs;
+              if (!wait(C::P_READY + buf, (cnt[m] / C::kSBufs) & 1)) break;
+              const bool first = j == 0 && h == 0;
+              if (first && !wait(C::O_FREE + m, (segs[m]++ & 1) ^ 1)) break;
+              ++cnt[m];
+              tc_fence_after();
+              if (elect_one()) {
+                const uint32_t pa = tmem_base + C::s_col(m, buf), d = tmem_base + C::o_col(m);
+                const uint64_t vd = v_desc + ring * kTileDesc + h * ((64 * 128) >> 4);
+                // 16 keys = two 8-row groups of V (2048 B) and 8 columns of P
+                if (first)
+                  tc_mma_bf16_ta_c<false>(d, pa, vd, kIdescO);
+                else
+                  tc_mma_bf16_ta_c<true>(d, pa, vd, kIdescO);
+#pragma unroll
+                for (int k = 1; k < C::kSub / 16; ++k)
+                  tc_mma_bf16_ta_c<true>(d, pa + k * 8, vd + (uint64_t)(k * (2048 >> 4)), kIdescO);
+                tc_commit(bar(C::S_FREE + buf));
+                mbar_arrive(bar(C::S_FREE + buf));    // carries the copies' `bad` mark to the softmax
+              }
+              __syncwarp();
             }
-            __syncwarp();
+            if (!ok) break;
           }
           if (!ok) break;
           if (elect_one()) tc_commit(bar(C::EMPTY + ring));
@@ -355,54 +375,55 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
         return tree_request(p.qsl[b], p.qsl[b + 1], p.seq_lens[b], p.T, p.max_query_len, p.max_seq_len, gq, kGroupRows);
       };
       auto work = [&](const TreeReq& r) { return (long long)heads * r.groups * r.chunks; };
-      // all requests' chunks; CTA 0 leaves their prefix sums for the merge and reports bad counts
-      long long total = 0;
-      for (int b0 = 0; b0 < p.n_reqs; b0 += 32) {
-        const int b = b0 + lane;
-        long long w = 0;
-        if (b < p.n_reqs) {
-          const TreeReq r = request(b);
-          if (!r.ok && blockIdx.x == 0) atomicExch(p.status, kStatusShape);
-          w = work(r);
-        }
-        long long pre = w;
+      // all requests' chunks; CTA 0 reports bad counts. A lane holds request `strip + lane` of the
+      // last strip of 32, so that up to 32 requests are read once.
+      TreeReq mine{};
+      long long total = 0, w = 0, pre = 0;            // pre: the strip's chunks up to and with this lane's
+      auto scan = [&](int b0) {
+        mine = TreeReq{};
+        if (b0 + lane < p.n_reqs) mine = request(b0 + lane);
+        else mine.ok = true;
+        w = pre = work(mine);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const long long up = __shfl_up_sync(0xffffffffu, pre, o);
           if (lane >= o) pre += up;
         }
-        if (blockIdx.x == 0 && b < p.n_reqs) p.prefix[b] = total + pre - w;
+      };
+      for (int b0 = 0; b0 < p.n_reqs; b0 += 32) {
+        scan(b0);
+        if (!mine.ok && blockIdx.x == 0) atomicExch(p.status, kStatusShape);
         total += __shfl_sync(0xffffffffu, pre, 31);
       }
       const long long per = tree_per(total, gridDim.x);
-      if (blockIdx.x == 0 && lane == 0) p.prefix[p.n_reqs] = total;
       long long pos = per * blockIdx.x;
       const long long end = min(total, pos + per);
-      // the request that holds the first chunk
+      // the request that holds the first chunk, and the chunks before it
+      TreeReq r{};
       int b = 0;
       long long before = 0;
       if (pos < end) {
         for (int b0 = 0; b0 < p.n_reqs; b0 += 32) {
-          const long long w = b0 + lane < p.n_reqs ? work(request(b0 + lane)) : 0;
-          long long pre = w;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const long long up = __shfl_up_sync(0xffffffffu, pre, o);
-            if (lane >= o) pre += up;
-          }
+          if (p.n_reqs > 32) scan(b0);
           const unsigned hit = __ballot_sync(0xffffffffu, before + pre > pos);
           if (hit != 0u) {
             const int f = __ffs(hit) - 1;
             b = b0 + f;
             before += __shfl_sync(0xffffffffu, pre - w, f);
+            r.q0 = __shfl_sync(0xffffffffu, mine.q0, f);
+            r.n = __shfl_sync(0xffffffffu, mine.n, f);
+            r.len = __shfl_sync(0xffffffffu, mine.len, f);
+            r.chunks = __shfl_sync(0xffffffffu, mine.chunks, f);
+            r.groups = __shfl_sync(0xffffffffu, mine.groups, f);
             break;
           }
           before += __shfl_sync(0xffffffffu, pre, 31);
         }
       }
+      // no item of this CTA is continued by others, unless a segment says so below
+      if (lane == 0) p.items[blockIdx.x].rows = 0;
+      __syncwarp();
       if (lane == 0) {
-        TreeReq r{};
-        if (pos < end) r = request(b);
         for (int u = 0;; ++u) {
           const int slot = u % kUnitSlots;
           if (!mbar_wait_bounded(bar(C::U_EMPTY + slot), ((u / kUnitSlots) & 1) ^ 1, s_abort, timeout)) {
@@ -433,6 +454,11 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
             s.part = q.part;
             s.rows = min(kGroupRows, r.n * gq - s.row0);
             s.bad = 0;
+            if (q.c0 == 0 && q.part >= 0) {
+              int first, last;
+              tree_parts(before + q.unit * r.chunks, r.chunks, per, &first, &last);
+              p.items[blockIdx.x] = TreeItem{s.r, s.g, s.row0, s.rows, s.q0, last, 0, 0};
+            }
             pos += q.c1 - q.c0;
           }
           s_seg[slot] = s;
@@ -460,6 +486,25 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
         ring_ph ^= 1u;
       }
     };
+    // a segment's queries (rows past them zero), once those that the buffer held are no longer read
+    auto load_q = [&](const Segment& s, int seg_no) {
+      const int qb = seg_no % C::kQBufs;
+      if (!wait(C::Q_EMPTY + qb, ((seg_no / C::kQBufs) & 1) ^ 1)) return;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if (m * 128 >= s.rows) break;
+#pragma unroll 4
+        for (int k = 0; k < 16; ++k) {
+          const int j = m * 128 + row_of + 8 * k, jr = s.row0 + j;
+          const int tok = jr / gq;
+          const __nv_bfloat16* q = p.qkv;
+          if (j < s.rows)
+            q += (size_t)s.r * p.sstride_in + (size_t)(s.q0 + tok) * p.rstride_in + (s.g * gq + jr - tok * gq) * kHd + c16 * 8;
+          cp_async16(base + (qb * MT + m) * kTileBytes + dst0 + k * 1024, q, j < s.rows ? 16 : 0, pol);
+        }
+      }
+      cp_async_arrive(bar(C::Q_FULL + qb));
+    };
     for (int seg_no = 0;; ++seg_no) {
       const int slot = next_segment();
       if (slot < 0) break;
@@ -471,6 +516,7 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
         return key < s.len ? bt[key / p.block_size] : -1;
       };
       int blk = block_of(s.c0);
+      if (C::kQBufs > 1) load_q(s, seg_no);
       for (int c = s.c0; c < s.c1 && ok; ++c) {
         const int key = c * kTreeChunk + my_row;
         int row = -1;                                // cache row of this lane's key (-1: zeros)
@@ -512,24 +558,8 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
           }
           advance();
         }
-        if (ok && c == s.c0) {
-          // the segment's queries (rows past them zero), once the last one's are no longer read
-          if (!wait(C::Q_EMPTY, (seg_no & 1) ^ 1)) break;
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            if (m * 128 >= s.rows) break;
-#pragma unroll 1
-            for (int k = 0; k < 16; ++k) {
-              const int j = m * 128 + row_of + 8 * k, jr = s.row0 + j;
-              const int tok = jr / gq;
-              const __nv_bfloat16* q = p.qkv;
-              if (j < s.rows)
-                q += (size_t)s.r * p.sstride_in + (size_t)(s.q0 + tok) * p.rstride_in + (s.g * gq + jr - tok * gq) * kHd + c16 * 8;
-              cp_async16(base + m * kTileBytes + dst0 + k * 1024, q, j < s.rows ? 16 : 0, pol);
-            }
-          }
-          cp_async_arrive(bar(C::Q_FULL));
-        }
+        // one Q buffer: the last segment's queries may still be read, so K and V go first
+        if (ok && C::kQBufs == 1 && c == s.c0) load_q(s, seg_no);
       }
       if (!ok) break;
       release_segment(slot);
@@ -543,7 +573,12 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(q4 * 32) << 16);
     const float c = p.scale_log2;
     int cnt = 0;
-    float s[128];
+    // The last P V of this tile, known by its own buffer: the issuer arrives there again only
+    // after this warp has written the P that comes kSBufs later.
+    auto wait_last_pv = [&]() -> bool {
+      return wait(C::S_FREE + tile * C::kSBufs + (cnt - 1) % C::kSBufs, ((cnt - 1) / C::kSBufs) & 1);
+    };
+    float s[C::kSub];
     for (;;) {
       const int slot = next_segment();
       if (slot < 0) break;
@@ -557,22 +592,20 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
       const int jr = s_seg[slot].row0 + row, tok = row < rows ? jr / gq : 0;
       const int* words = p.mask + (size_t)(q0 + tok) * p.mask_words;
       float m = -INFINITY, l = 0.f;
-      for (int ck = c0; ck < c1; ++ck) {
+      for (int sc = c0 * C::kSubs; sc < c1 * C::kSubs; ++sc) {
         const int buf = tile * C::kSBufs + cnt % C::kSBufs;
         if (!wait(C::S_FULL + buf, (cnt / C::kSBufs) & 1)) break;
         if (!idle) {
           tc_fence_after();
           const uint32_t sa = lane_addr + C::s_col(tile, buf);
-          tmem_ld32(sa, s);
-          tmem_ld32(sa + 32, s + 32);
-          tmem_ld32(sa + 64, s + 64);
-          tmem_ld32(sa + 96, s + 96);
-          tc_wait_ld();
-          if ((ck + 1) * kTreeChunk > ctx) {
-            // drafted tokens (or the end) in this chunk: the row's mask
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const unsigned bits = tree_window(words, ck * kTreeChunk + 32 * w, ctx, n);
+          for (int k = 0; k < C::kSub; k += 32) tmem_ld32(sa + k, s + k);
+          tc_wait_ld();
+          if ((sc + 1) * C::kSub > ctx) {
+            // drafted tokens (or the end) among these keys: the row's mask
+#pragma unroll
+            for (int w = 0; w < C::kSub / 32; ++w) {
+              const unsigned bits = tree_window(words, sc * C::kSub + 32 * w, ctx, n);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!(bits >> i & 1u)) s[32 * w + i] = -INFINITY;
@@ -582,11 +615,11 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
 #pragma unroll
           for (int j = 0; j < 8; ++j) mk[j] = fmaxf(s[j], s[8 + j]);
 #pragma unroll
-          for (int k = 16; k < 128; k += 16)
+          for (int k = 16; k < C::kSub; k += 16)
 #pragma unroll
             for (int j = 0; j < 8; ++j) mk[j] = fmax3(mk[j], s[k + j], s[k + 8 + j]);
           const float mx = c * fmax3(fmax3(mk[0], mk[1], mk[2]), fmax3(mk[3], mk[4], mk[5]), fmaxf(mk[6], mk[7]));
-          if (ck == c0) {
+          if (sc == c0 * C::kSubs) {
             m = mx;                                   // the first P V overwrites O
           } else if (__any_sync(0xffffffffu, mx > m + kRescaleLog2)) {
             // the warp rescales together, every row by its own factor (1 where the max held);
@@ -597,7 +630,7 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
               l *= f;
               m = mx;
             }
-            if (!wait(C::PV_DONE + tile, (cnt - 1) & 1)) break;
+            if (!wait_last_pv()) break;
             tc_fence_after();
             float o[32];
 #pragma unroll
@@ -609,13 +642,13 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
               tmem_st32(lane_addr + C::o_col(tile) + k, o);
             }
           }
-          // P = 2^(s c - m) as bf16 pairs into the first 64 columns of the buffer (the rounding:
+          // P = 2^(s c - m) as bf16 pairs into the first half of the buffer's columns (the rounding:
           // the tensor core's A operand shares V's type; at most 2^-8 of a weight)
           const float mu = m == -INFINITY ? 0.f : m;  // nothing seen yet: every s is -inf, p = 0
           const uint64_t c2 = f32x2_pack(c, c), nm2 = f32x2_pack(-mu, -mu);
           uint64_t lk[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < C::kSub / 64; ++h) {
             uint32_t pk[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
@@ -639,7 +672,7 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
         ++cnt;
       }
       if (!ok) break;
-      if (!wait(C::PV_DONE + tile, (cnt - 1) & 1)) break;
+      if (!wait_last_pv()) break;
       if (!idle) {
         tc_fence_after();
         const int bad = *reinterpret_cast<volatile int*>(&s_seg[slot].bad);
@@ -702,43 +735,35 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
   }
 }
 
-// Joins the parts of the items that more than one CTA computed: a warp per query row, four
-// head dimensions per lane, the parts in the order of their keys (the same bits every time).
+// Joins the parts of the items that more than one CTA computed. At most one item begins in a
+// CTA and goes on in the next ones: item blockIdx.x (described by that CTA), a warp per query
+// row, four head dimensions per lane, the parts in the order of their keys (the same bits
+// every time).
 //   o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i
 // Scheduled behind the attention grid's last CTAs (programmatic launch); it reads only after
 // that grid has completed.
 constexpr int kMergeRows = 8;    // rows, and warps, of a CTA
-__global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeAttnParams p, int grid, int group_rows) {
-  const int gq = p.q_per / p.kv_per, heads = p.t * p.kv_per;
-  const int strips = (p.max_query_len * gq + kMergeRows - 1) / kMergeRows;   // of one (request, head)
-  const int strip = blockIdx.x % strips, bh = blockIdx.x / strips;
-  const int head = bh % heads, b = bh / heads;
-  const int jr = strip * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const TreeReq rq = tree_request(p.qsl[b], p.qsl[b + 1], p.seq_lens[b], p.T, p.max_query_len, p.max_seq_len, gq, group_rows);
-  if (jr >= rq.n * gq) return;
+__global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeAttnParams p) {
   griddep_wait();
-  const long long per = tree_per(p.prefix[p.n_reqs], grid);
-  const int grp = jr / group_rows, row = jr - grp * group_rows;
-  int first, last;
-  tree_parts(p.prefix[b] + ((long long)head * rq.groups + grp) * rq.chunks, rq.chunks, per, &first, &last);
-  if (first == last) return;                       // whole: written by its CTA
-  auto slot = [&](int c) { return c == first ? 2 * c + 1 : 2 * c; };
+  const int cta = blockIdx.x, row = blockIdx.y * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const TreeItem it = p.items[cta];
+  if (row >= it.rows) return;
+  auto slot = [&](int c) { return c == cta ? 2 * c + 1 : 2 * c; };
   auto ml = [&](int c) {
     return *reinterpret_cast<const float2*>(part_o(p, slot(c)) + (size_t)p.part_rows * kHd + 2 * row);
   };
   float m = -INFINITY;
-  for (int c = first + lane; c <= last; c += 32) m = fmaxf(m, ml(c).x);
+  for (int c = cta + lane; c <= it.last; c += 32) m = fmaxf(m, ml(c).x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int c = first; c <= last; ++c) {
+  for (int c = cta; c <= it.last; ++c) {
     const float2 x = ml(c);
     const float4 v = *reinterpret_cast<const float4*>(part_o(p, slot(c)) + (size_t)row * kHd + 4 * lane);
-    // a part whose keys the row does not see has o = 0, l = 0 and no max
-    const float w = x.x == -INFINITY ? 0.f : exp2f(x.x - m);
-    if (w != 0.f || x.x != -INFINITY) {
+    if (x.x != -INFINITY) {                          // else the row sees no key of that part
+      const float w = exp2f(x.x - m);
       l += w * x.y;
       o.x += w * v.x;
       o.y += w * v.y;
@@ -747,19 +772,19 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeA
     }
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
-  const int r = head / p.kv_per, g = head - r * p.kv_per, tok = jr / gq;
+  const int gq = p.q_per / p.kv_per, jr = it.row0 + row, tok = jr / gq;
   uint2 out;
   out.x = pack_bf16x2(o.x * inv, o.y * inv);
   out.y = pack_bf16x2(o.z * inv, o.w * inv);
-  *reinterpret_cast<uint2*>(p.out + (size_t)r * p.sstride_out + (size_t)(rq.q0 + tok) * p.rstride_out +
-                            (g * gq + jr - tok * gq) * kHd + 4 * lane) = out;
+  *reinterpret_cast<uint2*>(p.out + (size_t)it.r * p.sstride_out + (size_t)(it.q0 + tok) * p.rstride_out +
+                            (it.g * gq + jr - tok * gq) * kHd + 4 * lane) = out;
 }
 
 cudaError_t launch_tree_mask(int T, int n_reqs, int max_query_len, int words, const int* parents, const int* qsl,
                              const int* seq_lens, int* mask, int* positions, int* status, cudaStream_t st) {
-  const int threads = (max_query_len + 31) / 32 * 32;
-  tree_mask_kernel<<<n_reqs, threads, 0, st>>>(T, max_query_len, words, parents, qsl, seq_lens, mask, positions, status);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = programmatic(dim3(n_reqs), (max_query_len + 31) / 32 * 32, 0, st, attr);
+  return cudaLaunchKernelEx(&cfg, tree_mask_kernel, T, max_query_len, words, parents, qsl, seq_lens, mask, positions, status);
 }
 
 int tree_group_rows(int max_rows) { return max_rows <= 128 ? 128 : 256; }
@@ -782,26 +807,18 @@ static cudaError_t launch_tree_mt(const TreeAttnParams& p, int grid, cudaStream_
     if (fa.numRegs * C::kThreads < 128 * (C::kRegs0 + C::kRegs1 + MT * C::kRegsS)) return cudaErrorInvalidConfiguration;
     attr_done.fetch_or(bit, std::memory_order_acq_rel);
   }
-  tree_attn_kernel<MT><<<grid, C::kThreads, C::kSmem, st>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = programmatic(dim3(grid), C::kThreads, C::kSmem, st, attr);
+  return cudaLaunchKernelEx(&cfg, tree_attn_kernel<MT>, p);
 }
 
 cudaError_t launch_tree_attention(const TreeAttnParams& p, int grid, cudaStream_t st) {
-  const int gq = p.q_per / p.kv_per, max_rows = p.max_query_len * gq;
-  const int group_rows = tree_group_rows(max_rows);
-  cudaError_t e = group_rows == 128 ? launch_tree_mt<1>(p, grid, st) : launch_tree_mt<2>(p, grid, st);
+  const int max_rows = p.max_query_len * (p.q_per / p.kv_per);
+  cudaError_t e = tree_group_rows(max_rows) == 128 ? launch_tree_mt<1>(p, grid, st) : launch_tree_mt<2>(p, grid, st);
   if (e != cudaSuccess) return e;
-  const long long strips = (max_rows + kMergeRows - 1) / kMergeRows;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(strips * p.n_reqs * p.t * p.kv_per));
-  cfg.blockDim = dim3(32 * kMergeRows);
-  cfg.stream = st;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel, p, grid, group_rows);
+  const cudaLaunchConfig_t cfg = programmatic(dim3(grid, (p.part_rows + kMergeRows - 1) / kMergeRows), 32 * kMergeRows, 0, st, attr);
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel, p);
 }
 
 }  // namespace tpl
