@@ -13,16 +13,24 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace tpl {
 
 namespace {
 constexpr int kStatusShape = -2;   // TP_ERR_SHAPE
 constexpr int kWarps = 4;
+constexpr int kUnroll = 3, kMinCtas = 3;   // loads of a lane in flight; CTAs of the vector kernel per SM
 
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return reinterpret_cast<const uint32_t&>(v);
+// two bf16 of a word as a pair of fp32, and back (rounded to nearest even)
+__device__ __forceinline__ uint64_t unpack2(uint32_t w) {
+  return f32x2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack2(uint64_t v) {
+  float a, b;
+  f32x2_unpack(v, a, b);
+  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+  return reinterpret_cast<const uint32_t&>(r);
 }
 }  // namespace
 
@@ -109,23 +117,24 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopePar
 //   half layout         pieces l and l + rd/16 for l < rd/16 (pairs 8 l .. 8 l + 7), the
 //                       unrotated pieces two by two after them
 //   interleaved layout  pieces 2 l and 2 l + 1 (the same pairs 8 l .. 8 l + 7)
-// A warp takes `per_warp` steps of 32 / G heads of ONE token, so a lane's cosines, sines and
-// gammas are loaded once for all its heads; the loads of kUnroll steps are in flight
-// together. Few tokens: one step per warp, many short warps (latency); many: a token per
-// warp.
-template <int G>
-__global__ void __launch_bounds__(256) qk_norm_rope_vec_kernel(const RopeParams p, int per_warp, int parts) {
-  constexpr int kUnroll = 3, HPW = 32 / G;           // heads of a step
+// A warp takes up to kUnroll steps of 32 / G heads of ONE token, all loaded at once: a lane's
+// cosines and sines serve all of them. Warps are short and many (a token of 48 heads of 128
+// is four of them), which fills the SMs evenly; few tokens get a step per warp (latency).
+// The arithmetic goes by pairs of fp32 (fma.rn.f32x2): the first form, scalar and with the
+// address of a step worked out twice, was bound by instruction issue (369 a step of 1 KB).
+template <int G, bool INTERLEAVED, bool NORM>
+__global__ void __launch_bounds__(256, kMinCtas) qk_norm_rope_vec_kernel(const RopeParams p, int steps, int parts) {
+  constexpr int HPW = 32 / G;                        // heads of a step
   const int lane = threadIdx.x & 31;
   const long long wid = blockIdx.x * 8LL + (threadIdx.x >> 5);
   const int i = (int)(wid / parts), part = (int)(wid - (long long)i * parts);
   if (i >= p.T) return;
   const int heads = p.q_per + 2 * p.kv_per, total = p.t * heads;
   const int sub = lane / G, l = lane % G;
-  // the pieces of this lane (vb < 0 or va < 0: none)
+  // the pieces of this lane (va, vb < 0: none) and its rotated pairs, 8 l on
   const int nv = p.hd >> 3, half = p.rd >> 1;
-  int va, vb, rot;                                   // rot: rotated pairs of this lane (8 l on)
-  if (p.interleaved) {
+  int va, vb, rot;
+  if (INTERLEAVED) {
     va = 2 * l;
     vb = 2 * l + 1;
     rot = min(8, max(0, half - 8 * l));
@@ -137,28 +146,35 @@ __global__ void __launch_bounds__(256) qk_norm_rope_vec_kernel(const RopeParams 
   }
   if (va >= nv) va = -1;
   if (vb >= nv) vb = -1;
-  const long long pos = p.pos[i];
+  const int pos = p.pos[i];
   const int slot = p.slots != nullptr ? p.slots[i] : -1;
-  const int h0 = part * per_warp * HPW + sub, h_end = min(total, (part + 1) * per_warp * HPW);
+  const int h0 = part * steps * HPW + sub, h_end = min(total, (part + 1) * steps * HPW);
   const bool in_place = p.in == p.out;
   uint4 a[kUnroll], b[kUnroll];
-  auto address = [&](int h, int& head) -> size_t {   // shard-local head and element offset of head h
-    const int r = h / heads;
-    head = h - r * heads;
-    return (size_t)r * p.sstride + (size_t)i * p.rstride + (size_t)head * p.hd;
-  };
-  auto load = [&](int u, int h) {
-    a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (h < h_end) {
-      int head;
-      const __nv_bfloat16* src = p.in + address(h, head);
-      if (in_place && p.slots == nullptr && head >= p.q_per + p.kv_per) return;   // v stays where it is
-      if (va >= 0) a[u] = *reinterpret_cast<const uint4*>(src + va * 8);
-      if (vb >= 0) b[u] = *reinterpret_cast<const uint4*>(src + vb * 8);
-    }
-  };
+  size_t at[kUnroll];                                // element of the head in qkv
+  int kind[kUnroll];                                 // its index among the shard's heads (< 0: none), and the shard
+  int shard[kUnroll];
+  // h / heads as a product: 2^32 / heads rounded up is off by less than 1, and h * heads < 2^32
+  const unsigned magic = 0xffffffffu / (unsigned)heads + 1u;
+  const size_t token = (size_t)i * p.rstride;
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) load(u, h0 + u * HPW);
+  for (int u = 0; u < kUnroll; ++u) {
+    const int h = h0 + u * HPW;
+    a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
+    kind[u] = -1;
+    if (h < h_end) {
+      shard[u] = (int)__umulhi((unsigned)h, magic);
+      kind[u] = h - shard[u] * heads;
+      at[u] = token + (size_t)shard[u] * p.sstride + kind[u] * p.hd;
+      if (in_place && p.slots == nullptr && kind[u] >= p.q_per + p.kv_per) {
+        kind[u] = -1;                                // v stays where it is
+      } else {
+        const __nv_bfloat16* src = p.in + at[u];
+        if (va >= 0) a[u] = *reinterpret_cast<const uint4*>(src + va * 8);
+        if (vb >= 0) b[u] = *reinterpret_cast<const uint4*>(src + vb * 8);
+      }
+    }
+  }
   if (pos < 0 || pos >= p.n_pos) {                   // padding token, or past the table: nothing is written
     if (pos >= 0 && lane == 0) atomicExch(p.status, kStatusShape);
     return;
@@ -166,7 +182,7 @@ __global__ void __launch_bounds__(256) qk_norm_rope_vec_kernel(const RopeParams 
   if (slot >= p.n_slots && p.slots != nullptr && lane == 0) atomicExch(p.status, kStatusShape);
   const bool write = slot >= 0 && slot < p.n_slots;
   float c[8], s[8];
-  const float* tab = p.table + pos * p.rd + 8 * l;
+  const float* tab = p.table + (size_t)pos * p.rd + 8 * l;
   if (rot == 8 && (p.rd & 7) == 0) {
 #pragma unroll
     for (int k = 0; k < 8; k += 4) {
@@ -181,82 +197,87 @@ __global__ void __launch_bounds__(256) qk_norm_rope_vec_kernel(const RopeParams 
     }
   }
   const float inv_hd = 1.0f / p.hd;
-  for (int hb = h0; hb - sub < h_end; hb += kUnroll * HPW) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = hb + u * HPW;
-      int head;
-      const size_t at = address(min(h, total - 1), head);
-      const bool is_v = head >= p.q_per + p.kv_per, is_k = !is_v && head >= p.q_per;
-      uint4 oa = a[u], ob = b[u];
-      const __nv_bfloat16* gamma = is_v ? nullptr : is_k ? p.k_gamma : p.q_gamma;
-      float x[8], y[8];
-      const uint32_t* wa = &a[u].x;
-      const uint32_t* wb = &b[u].x;
+  for (int u = 0; u < kUnroll; ++u) {
+    if (h0 - sub + u * HPW >= h_end) break;          // the whole warp
+    const bool is_v = kind[u] >= p.q_per + p.kv_per, is_q = kind[u] < p.q_per;
+    uint4 oa = a[u], ob = b[u];
+    const uint32_t* wa = &a[u].x;
+    const uint32_t* wb = &b[u].x;
+    uint64_t x[4], y[4];                             // elements 2 k, 2 k + 1 of the two pieces
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[2 * k] = __uint_as_float(wa[k] << 16);
-        x[2 * k + 1] = __uint_as_float(wa[k] & 0xffff0000u);
-        y[2 * k] = __uint_as_float(wb[k] << 16);
-        y[2 * k + 1] = __uint_as_float(wb[k] & 0xffff0000u);
-      }
-      if (p.q_gamma != nullptr || p.k_gamma != nullptr) {   // the whole warp: its heads share the exchange
-        float ss = 0.f;
+    for (int k = 0; k < 4; ++k) {
+      x[k] = unpack2(wa[k]);
+      y[k] = unpack2(wb[k]);
+    }
+    float rs = 1.f;
+    if (NORM) {                                      // the whole warp: its heads share the exchange
+      uint64_t q = 0ull;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) ss += x[k] * x[k] + y[k] * y[k];
+      for (int k = 0; k < 4; ++k) q = f32x2_fma(y[k], y[k], f32x2_fma(x[k], x[k], q));
+      float s0, s1;
+      f32x2_unpack(q, s0, s1);
+      s0 += s1;
 #pragma unroll
-        for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (gamma != nullptr) {
-          const float rs = 1.0f / sqrtf(ss * inv_hd + p.eps);
-          uint4 ga = make_uint4(0u, 0u, 0u, 0u), gb = ga;
-          if (va >= 0) ga = __ldg(reinterpret_cast<const uint4*>(gamma + va * 8));
-          if (vb >= 0) gb = __ldg(reinterpret_cast<const uint4*>(gamma + vb * 8));
-          const uint32_t* wga = &ga.x;
-          const uint32_t* wgb = &gb.x;
+      for (int o = G / 2; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+      const __nv_bfloat16* gamma = is_q ? p.q_gamma : p.k_gamma;
+      if (!is_v && gamma != nullptr) {
+        rs = rsqrtf(s0 * inv_hd + p.eps);            // applied after the rotation, which is linear
+        uint4 ga = make_uint4(0u, 0u, 0u, 0u), gb = ga;
+        if (va >= 0) ga = __ldg(reinterpret_cast<const uint4*>(gamma + va * 8));
+        if (vb >= 0) gb = __ldg(reinterpret_cast<const uint4*>(gamma + vb * 8));
+        const uint32_t* wga = &ga.x;
+        const uint32_t* wgb = &gb.x;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[2 * k] *= rs * __uint_as_float(wga[k] << 16);
-            x[2 * k + 1] *= rs * __uint_as_float(wga[k] & 0xffff0000u);
-            y[2 * k] *= rs * __uint_as_float(wgb[k] << 16);
-            y[2 * k + 1] *= rs * __uint_as_float(wgb[k] & 0xffff0000u);
-          }
+        for (int k = 0; k < 4; ++k) {
+          x[k] = f32x2_mul(x[k], unpack2(wga[k]));
+          y[k] = f32x2_mul(y[k], unpack2(wgb[k]));
         }
       }
-      if (!is_v) {
-        if (p.interleaved) {
-          // pairs (x0 x1) (x2 x3) .. of piece a are 8 l .. 8 l + 3, of piece b 8 l + 4 .. 8 l + 7
+    }
+    if (!is_v) {
+      if (INTERLEAVED) {
+        // the pairs of piece a are 8 l .. 8 l + 3, of piece b 8 l + 4 .. 8 l + 7
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float x0 = x[2 * k], x1 = x[2 * k + 1], y0 = y[2 * k], y1 = y[2 * k + 1];
-            x[2 * k] = x0 * c[k] - x1 * s[k];
-            x[2 * k + 1] = x1 * c[k] + x0 * s[k];
-            y[2 * k] = y0 * c[4 + k] - y1 * s[4 + k];
-            y[2 * k + 1] = y1 * c[4 + k] + y0 * s[4 + k];
-          }
-        } else if (rot) {
+        for (int k = 0; k < 4; ++k) {
+          float x0, x1, y0, y1;
+          f32x2_unpack(x[k], x0, x1);
+          f32x2_unpack(y[k], y0, y1);
+          x[k] = f32x2_pack(x0 * c[k] - x1 * s[k], x1 * c[k] + x0 * s[k]);
+          y[k] = f32x2_pack(y0 * c[4 + k] - y1 * s[4 + k], y1 * c[4 + k] + y0 * s[4 + k]);
+        }
+      } else if (rot) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float x0 = x[k];
-            x[k] = x0 * c[k] - y[k] * s[k];
-            y[k] = y[k] * c[k] + x0 * s[k];
-          }
-        }
-        oa = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
-        ob = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
-      }
-      if (h < h_end) {
-        if (!is_v || !in_place) {
-          if (va >= 0) *reinterpret_cast<uint4*>(p.out + at + va * 8) = oa;
-          if (vb >= 0) *reinterpret_cast<uint4*>(p.out + at + vb * 8) = ob;
-        }
-        if (write && head >= p.q_per) {
-          __nv_bfloat16* dst = (is_v ? p.cache_v : p.cache_k) +
-                               (((size_t)(h / heads) * p.n_slots + slot) * p.kv_per + (head - p.q_per - (is_v ? p.kv_per : 0))) * p.hd;
-          if (va >= 0) *reinterpret_cast<uint4*>(dst + va * 8) = oa;
-          if (vb >= 0) *reinterpret_cast<uint4*>(dst + vb * 8) = ob;
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t c2 = f32x2_pack(c[2 * k], c[2 * k + 1]), s2 = f32x2_pack(s[2 * k], s[2 * k + 1]);
+          const uint64_t n2 = f32x2_pack(-s[2 * k], -s[2 * k + 1]), x0 = x[k];
+          x[k] = f32x2_fma(y[k], n2, f32x2_mul(x0, c2));
+          y[k] = f32x2_fma(x0, s2, f32x2_mul(y[k], c2));
         }
       }
-      load(u, h + kUnroll * HPW);                    // this step's place for the one kUnroll steps on
+      if (NORM) {
+        const uint64_t r2 = f32x2_pack(rs, rs);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[k] = f32x2_mul(x[k], r2);
+          y[k] = f32x2_mul(y[k], r2);
+        }
+      }
+      oa = make_uint4(pack2(x[0]), pack2(x[1]), pack2(x[2]), pack2(x[3]));
+      ob = make_uint4(pack2(y[0]), pack2(y[1]), pack2(y[2]), pack2(y[3]));
+    }
+    if (kind[u] >= 0) {
+      if (!is_v || !in_place) {
+        __nv_bfloat16* dst = p.out + at[u];
+        if (va >= 0) *reinterpret_cast<uint4*>(dst + va * 8) = oa;
+        if (vb >= 0) *reinterpret_cast<uint4*>(dst + vb * 8) = ob;
+      }
+      if (write && !is_q) {
+        __nv_bfloat16* dst = (is_v ? p.cache_v : p.cache_k) +
+                             (((size_t)shard[u] * p.n_slots + slot) * p.kv_per + (kind[u] - p.q_per - (is_v ? p.kv_per : 0))) * p.hd;
+        if (va >= 0) *reinterpret_cast<uint4*>(dst + va * 8) = oa;
+        if (vb >= 0) *reinterpret_cast<uint4*>(dst + vb * 8) = ob;
+      }
     }
   }
 }
@@ -270,14 +291,20 @@ cudaError_t launch_rope_table(const RopeFreqs& f, long long n_pos, int rotary_di
 
 template <int G>
 static void launch_vec(const RopeParams& p, int nsm, cudaStream_t st) {
-  // steps of 32 / G heads of a token, shared out so that about 16 warps per SM have work; a
-  // warp that has a whole token loads its cosines once
-  const int steps = (p.t * (p.q_per + 2 * p.kv_per) * G + 31) / 32;
-  const long long want = 16LL * nsm;
-  const int parts = (int)std::max<long long>(1, std::min<long long>(steps, want / std::max(1, p.T)));
-  const int per_warp = (steps + parts - 1) / parts, used = (steps + per_warp - 1) / per_warp;
-  const long long warps = (long long)p.T * used;
-  qk_norm_rope_vec_kernel<G><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(p, per_warp, used);
+  // steps of 32 / G heads of a token: kUnroll per warp, fewer where that leaves SMs without work
+  const int total = (p.t * (p.q_per + 2 * p.kv_per) * G + 31) / 32;
+  int steps = kUnroll;
+  while (steps > 1 && (long long)p.T * ((total + steps - 1) / steps) < 16LL * nsm) --steps;
+  const int parts = (total + steps - 1) / steps;
+  const long long warps = (long long)p.T * parts;
+  const unsigned grid = (unsigned)((warps + 7) / 8);
+  const bool norm = p.q_gamma != nullptr || p.k_gamma != nullptr;
+  if (p.interleaved)
+    norm ? qk_norm_rope_vec_kernel<G, true, true><<<grid, 256, 0, st>>>(p, steps, parts)
+         : qk_norm_rope_vec_kernel<G, true, false><<<grid, 256, 0, st>>>(p, steps, parts);
+  else
+    norm ? qk_norm_rope_vec_kernel<G, false, true><<<grid, 256, 0, st>>>(p, steps, parts)
+         : qk_norm_rope_vec_kernel<G, false, false><<<grid, 256, 0, st>>>(p, steps, parts);
 }
 
 cudaError_t launch_qk_norm_rope(const RopeParams& p, int nsm, cudaStream_t st) {

@@ -23,13 +23,17 @@ constexpr int kStatusShape = -2;   // TP_ERR_SHAPE
 constexpr int kMaxDraft = 256;     // TP_TREE_MAX_DRAFT
 }  // namespace
 
-// One CTA per request, a thread per drafted token: it walks up its ancestors (a parent
-// comes before its children, so the walk ends) and sets a bit for each and for itself.
+// One CTA per request, a thread per drafted token. By pointer jumping: a token's row starts
+// as its own bit and its parent's index; each round adds the row of the token it points to
+// and points to where that one points, so a chain of d ancestors takes log2(d) + 1 rounds
+// (a chain of 64: 7; walking up it took 64 dependent reads). Latency bounds it: a few KB.
 __global__ void __launch_bounds__(kMaxDraft)
     tree_mask_kernel(int T, int max_query_len, int words, const int* __restrict__ parents, const int* __restrict__ qsl,
                      const int* __restrict__ seq_lens, int* __restrict__ mask, int* __restrict__ positions,
                      int* __restrict__ status) {
-  __shared__ int par[kMaxDraft];
+  constexpr int kWords = kMaxDraft / 32;
+  __shared__ unsigned rows[2][kWords][kMaxDraft];
+  __shared__ int up[2][kMaxDraft];                   // >= 0: the next ancestor; -1: none left; -2: a bad parent above
   const int b = blockIdx.x, i = threadIdx.x;
   griddep_launch_dependents();
   griddep_wait();
@@ -38,30 +42,45 @@ __global__ void __launch_bounds__(kMaxDraft)
     if (i == 0) atomicExch(status, kStatusShape);
     return;
   }
-  if (i < n) par[i] = parents[q0 + i];
-  __syncthreads();
-  if (i >= n) return;
-  unsigned bits[kMaxDraft / 32];
+  const int used = (n + 31) / 32;
+  int to = -1;
+  unsigned bits[kWords];
 #pragma unroll
-  for (int w = 0; w < kMaxDraft / 32; ++w) bits[w] = 0u;
-  int at = i, depth = -1;
-  bool ok = true;
-  while (at >= 0) {
-#pragma unroll
-    for (int w = 0; w < kMaxDraft / 32; ++w)
-      if (w == at >> 5) bits[w] |= 1u << (at & 31);
-    const int up = par[at];
-    if (up < -1 || up >= at) {
-      ok = false;
-      break;
+  for (int w = 0; w < kWords; ++w) bits[w] = 0u;
+  if (i < n) {
+    to = parents[q0 + i];
+    if (to < -1 || to >= i) {
+      to = -2;
+      atomicExch(status, kStatusShape);
     }
-    at = up;
-    ++depth;
-  }
-  if (!ok) atomicExch(status, kStatusShape);
 #pragma unroll
-  for (int w = 0; w < kMaxDraft / 32; ++w)
+    for (int w = 0; w < kWords; ++w)
+      if (w == i >> 5) bits[w] = 1u << (i & 31);
+  }
+  int buf = 0;
+  for (int round = 0; round < 10; ++round) {         // 256 tokens: at most 9
+    up[buf][i] = to;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w)
+      if (w < used) rows[buf][w][i] = bits[w];
+    if (!__syncthreads_or(to >= 0)) break;
+    if (to >= 0) {
+#pragma unroll
+      for (int w = 0; w < kWords; ++w)
+        if (w < used) bits[w] |= rows[buf][w][to];
+      to = up[buf][to];
+    }
+    buf ^= 1;
+  }
+  if (i >= n) return;
+  const bool ok = to == -1;
+  int depth = -1;
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) depth += __popc(bits[w]);
+#pragma unroll
+  for (int w = 0; w < kWords; ++w)
     if (w < words) mask[(size_t)(q0 + i) * words + w] = ok ? (int)bits[w] : 0;
+  for (int w = kWords; w < words; ++w) mask[(size_t)(q0 + i) * words + w] = 0;
   if (positions != nullptr) positions[q0 + i] = ok ? ctx + depth : -1;
 }
 
@@ -192,8 +211,8 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
   Segment* s_seg = reinterpret_cast<Segment*>(base_ptr + C::kUnitOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_launch_dependents();   // the merge grid may be scheduled; it waits for this one to complete
-  if (threadIdx.x == 0) {
-    for (int b = 0; b < C::NBARS; ++b) {
+  if (warp == 0) {
+    for (int b = lane; b < C::NBARS; b += 32) {
       int count = 1;
       if (b < C::Q_EMPTY || (b >= C::FULL && b < C::EMPTY)) count = 128;        // every copying thread
       if (b >= C::P_READY && b < C::S_FREE) count = 4;                          // the tile's softmax warps
@@ -202,7 +221,7 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
       if (b >= C::U_EMPTY && b < C::DONE_S) count = 2 + 4 + 4 * MT;             // issuers, copy and softmax warps
       mbar_init(bar(b), count);
     }
-    *s_abort = 0;
+    if (lane == 0) *s_abort = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -212,13 +231,22 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
   // the set-up above may overlap the grid before (programmatic launch); nothing that grid
   // wrote is read before this
   griddep_wait();
+  const int gq = p.q_per / p.kv_per;                // q heads of a kv head
+  constexpr int kGroupRows = 128 * MT;
+  auto request = [&](int b) {
+    return tree_request(p.qsl[b], p.qsl[b + 1], p.seq_lens[b], p.T, p.max_query_len, p.max_seq_len, gq, kGroupRows);
+  };
+  TreeReq mine{};                                   // warp 2: request `lane` of a strip of 32; the first strip loads here
+  mine.ok = true;
+  if (warp == 2 && lane < p.n_reqs) mine = request(lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
   const unsigned long long timeout = p.timeout_ns;
-  const int gq = p.q_per / p.kv_per;                // q heads of a kv head
-  constexpr int kGroupRows = 128 * MT;
+  // row / gq as a product: 2^32 / gq rounded up is off by less than 1, and row * gq < 2^32
+  const unsigned gq_magic = 0xffffffffu / (unsigned)gq + 1u;
+  auto token_of = [&](int row) { return gq == 1 ? row : (int)__umulhi((unsigned)row, gq_magic); };
   bool ok = true;
   // a wait of a whole warp
   auto wait = [&](int b, uint32_t ph) -> bool {
@@ -371,18 +399,18 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
     } else if (warp == 2) {
       // ------------------------------------------------------------ segments
       const int heads = p.t * p.kv_per;
-      auto request = [&](int b) {
-        return tree_request(p.qsl[b], p.qsl[b + 1], p.seq_lens[b], p.T, p.max_query_len, p.max_seq_len, gq, kGroupRows);
-      };
-      auto work = [&](const TreeReq& r) { return (long long)heads * r.groups * r.chunks; };
-      // all requests' chunks; CTA 0 reports bad counts. A lane holds request `strip + lane` of the
+      auto work = [&](const TreeReq& r) { return (long long)heads * r.groups * tree_item(r.chunks); };
+      // all requests' work; CTA 0 reports bad counts. A lane holds request `strip + lane` of the
       // last strip of 32, so that up to 32 requests are read once.
-      TreeReq mine{};
-      long long total = 0, w = 0, pre = 0;            // pre: the strip's chunks up to and with this lane's
+      long long total = 0, w = 0, pre = 0;            // pre: the strip's work up to and with this lane's
+      int strip = 0;                                  // that `mine` holds
       auto scan = [&](int b0) {
-        mine = TreeReq{};
-        if (b0 + lane < p.n_reqs) mine = request(b0 + lane);
-        else mine.ok = true;
+        if (b0 != strip) {
+          mine = TreeReq{};
+          mine.ok = true;
+          if (b0 + lane < p.n_reqs) mine = request(b0 + lane);
+          strip = b0;
+        }
         w = pre = work(mine);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -398,7 +426,7 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
       const long long per = tree_per(total, gridDim.x);
       long long pos = per * blockIdx.x;
       const long long end = min(total, pos + per);
-      // the request that holds the first chunk, and the chunks before it
+      // the request that holds the first place, and the places before it
       TreeReq r{};
       int b = 0;
       long long before = 0;
@@ -435,12 +463,14 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
           }
           Segment s;
           s.b = -1;
-          if (pos < end) {
+          while (pos < end) {
             while (pos - before >= work(r)) {          // this request is done (or empty)
               before += work(r);
               r = request(++b);
             }
             const TreeSeg q = tree_segment(pos - before, r.chunks, end - pos, blockIdx.x);
+            pos += q.places;
+            if (q.c0 == q.c1) continue;                // the CTA's range ends within an item's first places
             const int head = (int)(q.unit / r.groups), grp = (int)(q.unit - (long long)head * r.groups);
             s.b = b;
             s.r = head / p.kv_per;
@@ -455,11 +485,10 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
             s.rows = min(kGroupRows, r.n * gq - s.row0);
             s.bad = 0;
             if (q.c0 == 0 && q.part >= 0) {
-              int first, last;
-              tree_parts(before + q.unit * r.chunks, r.chunks, per, &first, &last);
+              const int last = tree_last(before + q.unit * tree_item(r.chunks), r.chunks, per);
               p.items[blockIdx.x] = TreeItem{s.r, s.g, s.row0, s.rows, s.q0, last, 0, 0};
             }
-            pos += q.c1 - q.c0;
+            break;
           }
           s_seg[slot] = s;
           mbar_arrive(bar(C::U_FULL + slot));
@@ -486,21 +515,23 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
         ring_ph ^= 1u;
       }
     };
-    // a segment's queries (rows past them zero), once those that the buffer held are no longer read
+    // a segment's queries, once those that the buffer held are no longer read
     auto load_q = [&](const Segment& s, int seg_no) {
       const int qb = seg_no % C::kQBufs;
       if (!wait(C::Q_EMPTY + qb, ((seg_no / C::kQBufs) & 1) ^ 1)) return;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         if (m * 128 >= s.rows) break;
-#pragma unroll 4
+        // rows past the item's keep what the buffer held: they only reach their own rows of S and O
+        const __nv_bfloat16* q = p.qkv + (size_t)s.r * p.sstride_in + s.g * gq * kHd + c16 * 8;
+#pragma unroll 1
         for (int k = 0; k < 16; ++k) {
-          const int j = m * 128 + row_of + 8 * k, jr = s.row0 + j;
-          const int tok = jr / gq;
-          const __nv_bfloat16* q = p.qkv;
+          const int j = m * 128 + row_of + 8 * k;
+          if (m * 128 + 2 * w4 + 8 * k >= s.rows) break;   // the whole warp
+          const int jr = s.row0 + j, tok = token_of(jr);
           if (j < s.rows)
-            q += (size_t)s.r * p.sstride_in + (size_t)(s.q0 + tok) * p.rstride_in + (s.g * gq + jr - tok * gq) * kHd + c16 * 8;
-          cp_async16(base + (qb * MT + m) * kTileBytes + dst0 + k * 1024, q, j < s.rows ? 16 : 0, pol);
+            cp_async16(base + (qb * MT + m) * kTileBytes + dst0 + k * 1024,
+                       q + (size_t)(s.q0 + tok) * p.rstride_in + (jr - tok * gq) * kHd, 16, pol);
         }
       }
       cp_async_arrive(bar(C::Q_FULL + qb));
@@ -589,7 +620,7 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
       }
       const int n = s_seg[slot].n, len = s_seg[slot].len, ctx = len - n, q0 = s_seg[slot].q0;
       const bool idle = tile * 128 + q4 * 32 >= rows;  // no row of this warp
-      const int jr = s_seg[slot].row0 + row, tok = row < rows ? jr / gq : 0;
+      const int jr = s_seg[slot].row0 + row, tok = row < rows ? token_of(jr) : 0;
       const int* words = p.mask + (size_t)(q0 + tok) * p.mask_words;
       float m = -INFINITY, l = 0.f;
       for (int sc = c0 * C::kSubs; sc < c1 * C::kSubs; ++sc) {
@@ -681,9 +712,10 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
         __nv_bfloat16* dst = p.out + (size_t)r * p.sstride_out + (size_t)(q0 + tok) * p.rstride_out + (g * gq + jr - tok * gq) * kHd;
         float* po = part >= 0 ? part_o(p, part) + (size_t)row * kHd : nullptr;
 #pragma unroll 1
-        for (int k = 0; k < 128; k += 32) {
+        for (int k = 0; k < 128; k += C::kSub) {
           __syncwarp();
-          tmem_ld32(lane_addr + C::o_col(tile) + k, s);
+#pragma unroll
+          for (int j = 0; j < C::kSub; j += 32) tmem_ld32(lane_addr + C::o_col(tile) + k + j, s + j);
           tc_wait_ld();
           if (bad) {
             // V values that were dropped, added to the rows that see their keys
@@ -695,7 +727,7 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
               if (blk < 0 || blk >= p.num_blocks) continue;
               const __nv_bfloat16* v = p.cache_v + ((size_t)(r * p.num_blocks + blk) * p.block_size + key % p.block_size) * p.kv_per * kHd + g * kHd + k;
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
+              for (int j = 0; j < C::kSub; ++j) {
                 const float x = __bfloat162float(v[j]);
                 if (!(fabsf(x) < INFINITY)) s[j] += x;
               }
@@ -704,10 +736,10 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
           if (row < rows) {
             if (part >= 0) {
 #pragma unroll
-              for (int j = 0; j < 32; j += 8) st_global_v8(po + k + j, *reinterpret_cast<const uint32_t(*)[8]>(s + j));
+              for (int j = 0; j < C::kSub; j += 8) st_global_v8(po + k + j, *reinterpret_cast<const uint32_t(*)[8]>(s + j));
             } else {
 #pragma unroll
-              for (int j = 0; j < 32; j += 8) {
+              for (int j = 0; j < C::kSub; j += 8) {
                 uint4 v;
                 v.x = pack_bf16x2(s[j] * inv, s[j + 1] * inv);
                 v.y = pack_bf16x2(s[j + 2] * inv, s[j + 3] * inv);

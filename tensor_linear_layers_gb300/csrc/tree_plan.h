@@ -1,12 +1,13 @@
 // Work split of the tree attention, shared by its kernels and a host test.
 //
-// The work is counted in chunks of 128 keys: request b has units(b) = t * kv_per * groups
-// items (a kv head of a shard and a group of query rows), each of chunks(b) = ceil(L / 128)
-// chunks, numbered item by item, requests in order. CTA c of the grid takes chunks
-// [c * per, (c + 1) * per) of that line, so every CTA streams the same number of keys
-// whatever the lengths. An item that crosses a boundary is computed in parts: CTA c writes
-// the part that continues an item begun by an earlier CTA to slot 2 c, the part that begins
-// one it does not finish to slot 2 c + 1, and the merge kernel joins them in chunk order.
+// Request b has units(b) = t * kv_per * groups items (a kv head of a shard and a group of query
+// rows), each of chunks(b) = ceil(L / 128) chunks of 128 keys. An item takes its chunks' places
+// on a line, after kTreeItemCost more for what it costs besides them (its queries, the first
+// products, its output); items and requests follow each other in order. CTA c of the grid
+// takes places [c * per, (c + 1) * per), so the CTAs have the same work whatever the lengths.
+// An item that crosses a boundary is computed in parts: CTA c writes the part that continues
+// an item begun by an earlier CTA to slot 2 c, the part that begins one it does not finish to
+// slot 2 c + 1, and the merge kernel joins them in chunk order.
 #pragma once
 
 #ifdef __CUDACC__
@@ -36,29 +37,36 @@ TPL_HD TreeReq tree_request(int q0, int q1, int len, int T, int max_query_len, i
   return r;
 }
 
-// Chunks per CTA.
+// Places of an item.
+constexpr int kTreeItemCost = 1;
+TPL_HD long long tree_item(int chunks) { return chunks > 0 ? chunks + kTreeItemCost : 0; }
+
+// Places per CTA.
 TPL_HD long long tree_per(long long total, int grid) { return total > 0 ? (total + grid - 1) / grid : 1; }
 
 struct TreeSeg {
   long long unit;                 // item within the request
-  int c0, c1;                     // its chunks [c0, c1)
+  long long places;               // taken from the line
+  int c0, c1;                     // its chunks [c0, c1); none where the places are the item's first ones alone
   int part;                       // slot of the partial result, or -1: the item is whole
 };
-// The segment of CTA cta that starts at chunk `at` of its request, `left` chunks before the CTA's end.
+// The segment of CTA cta that starts at place `at` of its request, `left` places before the CTA's end.
 TPL_HD TreeSeg tree_segment(long long at, int chunks, long long left, int cta) {
   TreeSeg s;
-  s.unit = at / chunks;
-  s.c0 = (int)(at - s.unit * chunks);
-  s.c1 = chunks - s.c0 < left ? chunks : s.c0 + (int)left;
+  const long long item = tree_item(chunks);
+  s.unit = at / item;
+  const int p0 = (int)(at - s.unit * item);
+  s.places = item - p0 < left ? item - p0 : left;
+  const int p1 = p0 + (int)s.places;
+  s.c0 = p0 > kTreeItemCost ? p0 - kTreeItemCost : 0;
+  s.c1 = p1 > kTreeItemCost ? p1 - kTreeItemCost : 0;
   s.part = s.c0 > 0 ? 2 * cta : s.c1 < chunks ? 2 * cta + 1 : -1;
   return s;
 }
 
-// CTAs [first, last] that hold the item whose chunks are [begin, begin + chunks) of the line.
-TPL_HD void tree_parts(long long begin, int chunks, long long per, int* first, int* last) {
-  *first = (int)(begin / per);
-  *last = (int)((begin + chunks - 1) / per);
-}
+// The CTAs that hold the first and the last chunk of the item that begins at place `begin`.
+TPL_HD int tree_first(long long begin, long long per) { return (int)((begin + kTreeItemCost) / per); }
+TPL_HD int tree_last(long long begin, int chunks, long long per) { return (int)((begin + kTreeItemCost + chunks - 1) / per); }
 
 // Visibility of the 32 keys from position key on, as bits, to a drafted token with mask row
 // `words`: cached positions (before ctx) always, the n drafted ones by their bits, none after.

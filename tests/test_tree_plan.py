@@ -20,6 +20,8 @@ def lib(tmp_path_factory):
     L = ctypes.CDLL(so)
     L.plan_per.restype = ctypes.c_longlong
     L.plan_per.argtypes = [ctypes.c_longlong, ctypes.c_int]
+    L.plan_item.restype = ctypes.c_longlong
+    L.plan_item.argtypes = [ctypes.c_int]
     L.plan_segment.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p]
     L.plan_parts.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p]
     L.plan_window.restype = ctypes.c_uint
@@ -51,25 +53,29 @@ def test_every_chunk_once_and_parts_where_the_merge_looks(lib, seed):
     n = rng.integers(0, 65, reqs)
     lens = n + rng.integers(0, int(rng.choice([50, 3000])), reqs)
     info = [request(lib, 0, int(k), int(L), 64, gq=gq, rows=rows) for k, L in zip(n, lens)]
-    base = np.concatenate([[0], np.cumsum([heads * g * c for _, _, c, g in info])])
+    base = np.concatenate([[0], np.cumsum([heads * g * lib.plan_item(c) for _, _, c, g in info])])
+    chunks = sum(heads * g * c for _, _, c, g in info)
     total = int(base[-1])
     per = lib.plan_per(total, grid)
     assert per * grid >= total
-    seen, slots = {}, {}
-    out = (ctypes.c_longlong * 4)()
+    seen, slots, unfinished = set(), {}, {}
+    out = (ctypes.c_longlong * 5)()
     for cta in range(grid):
         pos, end = cta * per, min(total, (cta + 1) * per)
-        segs = 0
         while pos < end:
             b = int(np.searchsorted(base, pos, side="right")) - 1
             lib.plan_segment(pos - int(base[b]), info[b][2], end - pos, cta, out)
-            unit, c0, c1, part = [int(x) for x in out]
-            assert 0 <= unit < heads * info[b][3] and 0 <= c0 < c1 <= info[b][2] and c1 - c0 <= end - pos
+            unit, c0, c1, part, places = [int(x) for x in out]
+            assert 0 <= unit < heads * info[b][3] and 0 <= c0 <= c1 <= info[b][2] and 0 < places <= end - pos
+            pos += places
+            if c0 == c1:
+                assert pos == end                          # the range ends before the item's first chunk
+                continue
             for c in range(c0, c1):
-                assert seen.setdefault((b, unit, c), cta) == cta and (b, unit, c, "x") not in seen
-                seen[(b, unit, c, "x")] = 1
+                assert (b, unit, c) not in seen
+                seen.add((b, unit, c))
             parts = (ctypes.c_int * 2)()
-            lib.plan_parts(int(base[b]) + unit * info[b][2], info[b][2], per, parts)
+            lib.plan_parts(int(base[b]) + unit * lib.plan_item(info[b][2]), info[b][2], per, parts)
             first, last = parts
             assert first <= cta <= last < grid
             if part < 0:
@@ -77,9 +83,14 @@ def test_every_chunk_once_and_parts_where_the_merge_looks(lib, seed):
             else:
                 assert first < last and part not in slots and part == (2 * cta + 1 if cta == first else 2 * cta)
                 slots[part] = (b, unit)
-            pos += c1 - c0
-            segs += 1
-    assert len(seen) == 2 * total
+                if c0 == 0:
+                    assert cta == first and cta not in unfinished      # one item per CTA for the merge
+                    unfinished[cta] = (b, unit, last)
+    assert len(seen) == chunks
+    for cta, (b, unit, last) in unfinished.items():
+        for c in range(cta, last + 1):
+            assert slots[2 * c + 1 if c == cta else 2 * c] == (b, unit)
+    assert len(slots) == sum(last - cta + 1 for cta, (_, _, last) in unfinished.items())
 
 
 @pytest.mark.parametrize("seed", range(6))

@@ -9,6 +9,7 @@ int plan_request(int q0, int q1, int len, int T, int max_q, int max_len, int gq,
   out[2] = r.groups;
   return r.ok ? 1 : 0;
 }
+long long plan_item(int chunks) { return tpl::tree_item(chunks); }
 long long plan_per(long long total, int grid) { return tpl::tree_per(total, grid); }
 void plan_segment(long long at, int chunks, long long left, int cta, long long* out) {
   const tpl::TreeSeg s = tpl::tree_segment(at, chunks, left, cta);
@@ -16,7 +17,11 @@ void plan_segment(long long at, int chunks, long long left, int cta, long long* 
   out[1] = s.c0;
   out[2] = s.c1;
   out[3] = s.part;
+  out[4] = s.places;
 }
-void plan_parts(long long begin, int chunks, long long per, int* out) { tpl::tree_parts(begin, chunks, per, out, out + 1); }
+void plan_parts(long long begin, int chunks, long long per, int* out) {
+  out[0] = tpl::tree_first(begin, per);
+  out[1] = tpl::tree_last(begin, chunks, per);
+}
 unsigned plan_window(const int* words, int key, int ctx, int n) { return tpl::tree_window(words, key, ctx, n); }
 }
