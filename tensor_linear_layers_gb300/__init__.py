@@ -159,8 +159,16 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+# torch's own call for the current stream's handle: a stream object made for every call costs 3 us
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_ptr(stream=None) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _bf16(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -243,6 +251,13 @@ class TPLinear:
         self.handle = h
         self._ws = None
         self._ws_sizes = {}
+        self._dev = dev
+        if cfg.kind == TP_BLOCK_ATTN_PROJ:     # per-shard head counts and row widths of qkv and of the attention output
+            self._kv_per = 1 if cfg.t >= cfg.n_kv_heads else cfg.n_kv_heads // cfg.t
+            q_per = cfg.n_q_heads // cfg.t
+            self._qkv_width, self._attn_width = (q_per + 2 * self._kv_per) * cfg.head_dim, q_per * cfg.head_dim
+            self._gathered = bool(cfg.flags & TP_FLAG_GATHERED)
+            self._shape = (cfg.t, self._kv_per, cfg.head_dim)
 
     def close(self):
         if getattr(self, "handle", None) is not None and self.handle.value:
@@ -351,27 +366,37 @@ class TPLinear:
         kv_per = 1 if c.t >= c.n_kv_heads else c.n_kv_heads // c.t
         return (c.t, num_blocks, block_size, kv_per, c.head_dim)
 
-    @property
-    def _qkv_width(self) -> int:
-        c = self.cfg
-        kv_per = 1 if c.t >= c.n_kv_heads else c.n_kv_heads // c.t
-        return (c.n_q_heads // c.t + 2 * kv_per) * c.head_dim
+    def _attention_handle(self) -> None:
+        if self.cfg.kind != TP_BLOCK_ATTN_PROJ:
+            raise ValueError("not an attention handle")
 
-    def _qkv_shape(self, T: int):
-        w, t = self._qkv_width, self.cfg.t
-        return (T, t * w) if self.gathered else (t, T, w)
+    def _rows(self, x: torch.Tensor, width: int):
+        """Tokens of a shard-major [t][T][width] or gathered [T][t * width] tensor, and the shape it must have."""
+        t = self._shape[0]
+        if self._gathered:
+            return x.shape[0], (x.shape[0], t * width)
+        if x.dim() != 3:
+            raise ValueError(f"expected [t, T, {width}], got {tuple(x.shape)}")
+        return x.shape[1], (t, x.shape[1], width)
+
+    def _cache_shape(self, cache: torch.Tensor):
+        """The shape a cache with as many blocks of that size must have."""
+        if cache.dim() != 5:
+            raise ValueError("a cache has the shape of kv_cache_shape()")
+        _, nb, bs, _, _ = cache.shape
+        t, kv_per, hd = self._shape
+        return nb, bs, (t, nb, bs, kv_per, hd)
 
     def _layer_pointers(self, caches_k: Sequence[torch.Tensor], caches_v: Sequence[torch.Tensor]):
         """Number of layers, HOST addresses of the arrays of their k and v pointers, blocks and block size of
         the caches (all of one size), and the object that holds the arrays."""
         if len(caches_k) != len(caches_v) or not caches_k:
             raise ValueError("caches_k and caches_v must list the same layers, one at least")
-        shape = caches_k[0].shape
-        if len(shape) != 5 or shape != self.kv_cache_shape(shape[1], shape[2]):
-            raise ValueError(f"a cache has the shape of kv_cache_shape(), not {tuple(shape)}")
-        dev, n = self.w_col.device, len(caches_k)
+        self._attention_handle()
+        nb, bs, shape = self._cache_shape(caches_k[0])
+        dev, n = self._dev, len(caches_k)
         both = [*caches_k, *caches_v]
-        _bf16_on(both[0], "cache_k", dev)
+        _bf16_on(both[0], "cache_k", dev, shape)
         # a call names every layer's caches: the same checks of all of them, one attribute at a time
         T, first = torch.Tensor, both[0]
         if set(map(T.dtype.__get__, both)) != {torch.bfloat16} or set(map(T.get_device, both)) != {first.get_device()}:
@@ -380,7 +405,7 @@ class TPLinear:
             raise ValueError(f"every cache must be contiguous and of the shape {tuple(shape)}")
         ptrs = array.array("Q", map(T.data_ptr, both))
         at = ptrs.buffer_info()[0]
-        return n, at, at + 8 * n, shape[1], shape[2], ptrs
+        return n, at, at + 8 * n, nb, bs, ptrs
 
     def qk_norm_rope(self, qkv: torch.Tensor, positions: torch.Tensor, rope: "Rope", out: Optional[torch.Tensor] = None,
                      slot_mapping: Optional[torch.Tensor] = None, cache_k: Optional[torch.Tensor] = None,
@@ -389,9 +414,10 @@ class TPLinear:
         negative = padding); out: a new tensor of qkv's shape, or qkv itself (in place). With slot_mapping
         (int32 [T], negative = none) k and v also go to their cache slots. Returns (out, 16-byte workspace
         whose first word is the status)."""
-        dev = self.w_col.device
-        T = qkv.shape[0] if self.gathered else qkv.shape[1]
-        src = _bf16_on(qkv, "qkv", dev, self._qkv_shape(T))
+        self._attention_handle()
+        dev = self._dev
+        T, shape = self._rows(qkv, self._qkv_width)
+        src = _bf16_on(qkv, "qkv", dev, shape)
         if out is None:
             out = torch.empty_like(qkv)
         ws = _workspace(ws, 16, dev)
@@ -401,14 +427,13 @@ class TPLinear:
             if cache_k is None or cache_v is None:
                 raise ValueError("slot_mapping needs cache_k and cache_v")
             slots = _i32(slot_mapping, "slot_mapping", dev, T)
-            nb, bs = cache_k.shape[1], cache_k.shape[2]
-            shape = self.kv_cache_shape(nb, bs)
-            ck, cv = _bf16_on(cache_k, "cache_k", dev, shape), _bf16_on(cache_v, "cache_v", dev, shape)
+            nb, bs, cshape = self._cache_shape(cache_k)
+            ck, cv = _bf16_on(cache_k, "cache_k", dev, cshape), _bf16_on(cache_v, "cache_v", dev, cshape)
         if rope.table.device != dev:
             raise ValueError(f"the rope table is on {rope.table.device}, not {dev}")
-        _check(lib().tp_qk_norm_rope(self.handle, T, src, _bf16_on(out, "out", dev, qkv.shape),
+        _check(lib().tp_qk_norm_rope(self.handle, T, src, _bf16_on(out, "out", dev, shape),
                                      _i32(positions, "positions", dev, T), rope.args, slots, ck, cv, nb, bs,
-                                     ws.data_ptr(), ws.numel(), _stream(stream)))
+                                     ws.data_ptr(), ws.numel(), _stream_ptr(stream)))
         return out, ws
 
     def kv_cache_copy_blocks(self, block_pairs: torch.Tensor, caches_k: Sequence[torch.Tensor],
@@ -418,11 +443,11 @@ class TPLinear:
         in the caches of all listed layers. Returns the workspace whose first word is the status."""
         if block_pairs.dim() != 2 or block_pairs.shape[1] != 2:
             raise ValueError("block_pairs must be [n, 2]")
-        dev = self.w_col.device
+        dev = self._dev
         n, ks, vs, nb, bs, _hold = self._layer_pointers(caches_k, caches_v)
         ws = _workspace(ws, 16, dev)
         _check(lib().tp_kv_cache_copy_blocks(self.handle, _i32(block_pairs, "block_pairs", dev), block_pairs.shape[0],
-                                             n, ks, vs, nb, bs, ws.data_ptr(), ws.numel(), _stream(stream)))
+                                             n, ks, vs, nb, bs, ws.data_ptr(), ws.numel(), _stream_ptr(stream)))
         return ws
 
     def kv_cache_compact(self, query_start_loc: torch.Tensor, seq_lens: torch.Tensor, accepted: torch.Tensor,
@@ -432,7 +457,7 @@ class TPLinear:
         """Move the accepted drafted tokens of every request (accepted int32 [n_reqs, m], rising draft
         indices, ended by -1) from src_tables' pages to the positions after the cached tokens in dst_tables'
         (the same tensor: in place), in the caches of all listed layers. Returns (new lengths, workspace)."""
-        dev = self.w_col.device
+        dev = self._dev
         n_reqs = seq_lens.numel()
         if accepted.dim() != 2 or src_tables.dim() != 2 or src_tables.shape != dst_tables.shape:
             raise ValueError("accepted is [n_reqs, m], src_tables and dst_tables [n_reqs, max_blocks]")
@@ -445,7 +470,7 @@ class TPLinear:
             self.handle, n_reqs, _i32(query_start_loc, "query_start_loc", dev, n_reqs + 1),
             _i32(seq_lens, "seq_lens", dev), _i32(accepted, "accepted", dev, n_reqs * accepted.shape[1]),
             accepted.shape[1], _i32(src_tables, "src_tables", dev, n_reqs * mb), _i32(dst_tables, "dst_tables", dev),
-            mb, n, ks, vs, nb, bs, _i32(out, "out", dev, n_reqs), ws.data_ptr(), ws.numel(), _stream(stream)))
+            mb, n, ks, vs, nb, bs, _i32(out, "out", dev, n_reqs), ws.data_ptr(), ws.numel(), _stream_ptr(stream)))
         return out, ws
 
     def tree_attention_workspace_size(self, n_reqs: int, max_query_len: int, max_seq_len: int) -> int:
@@ -460,13 +485,12 @@ class TPLinear:
         """Attention of every request's drafted tokens (rows of qkv, already in the cache as its last
         positions) over its cached tokens and over the drafted ones that their mask rows (tree_mask) name.
         Returns (attn in the attention core's output layout, workspace)."""
-        c, dev = self.cfg, self.w_col.device
-        T = qkv.shape[0] if self.gathered else qkv.shape[1]
-        n_reqs = seq_lens.numel()
-        nb, bs = cache_k.shape[1], cache_k.shape[2]
-        shape = self.kv_cache_shape(nb, bs)
-        w = c.n_q_heads // c.t * c.head_dim
-        out_shape = (T, c.t * w) if self.gathered else (c.t, T, w)
+        self._attention_handle()
+        dev, n_reqs = self._dev, seq_lens.numel()
+        T, shape = self._rows(qkv, self._qkv_width)
+        nb, bs, cshape = self._cache_shape(cache_k)
+        t, w = self._shape[0], self._attn_width
+        out_shape = (T, t * w) if self._gathered else (t, T, w)
         if out is None:
             out = torch.empty(out_shape, dtype=torch.bfloat16, device=dev)
         if ws is None:
@@ -474,13 +498,14 @@ class TPLinear:
                              dtype=torch.uint8, device=dev)
         if block_tables.dim() != 2 or mask.dim() != 2:
             raise ValueError("block_tables is [n_reqs, max_blocks], mask [T, words]")
+        max_blocks, words = block_tables.shape[1], mask.shape[1]
         _check(lib().tp_tree_attention(
-            self.handle, T, _bf16_on(qkv, "qkv", dev, self._qkv_shape(T)),
+            self.handle, T, _bf16_on(qkv, "qkv", dev, shape),
             _i32(query_start_loc, "query_start_loc", dev, n_reqs + 1), _i32(seq_lens, "seq_lens", dev), n_reqs,
-            max_query_len, max_seq_len, _i32(block_tables, "block_tables", dev, n_reqs * block_tables.shape[1]),
-            block_tables.shape[1], _i32(mask, "mask", dev, T * mask.shape[1]), mask.shape[1],
-            _bf16_on(cache_k, "cache_k", dev, shape), _bf16_on(cache_v, "cache_v", dev, shape), nb, bs,
-            _bf16_on(out, "out", dev, out_shape), _workspace(ws, 0, dev).data_ptr(), ws.numel(), _stream(stream)))
+            max_query_len, max_seq_len, _i32(block_tables, "block_tables", dev, n_reqs * max_blocks), max_blocks,
+            _i32(mask, "mask", dev, T * words), words, _bf16_on(cache_k, "cache_k", dev, cshape),
+            _bf16_on(cache_v, "cache_v", dev, cshape), nb, bs, _bf16_on(out, "out", dev, out_shape),
+            _workspace(ws, 0, dev).data_ptr(), ws.numel(), _stream_ptr(stream)))
         return out, ws
 
     def kv_cache_write(self, qkv: torch.Tensor, slot_mapping: torch.Tensor, cache_k: torch.Tensor,
@@ -712,7 +737,7 @@ def tree_mask(parents: torch.Tensor, query_start_loc: torch.Tensor, seq_lens: to
                               _i32(query_start_loc, "query_start_loc", dev, n_reqs + 1),
                               _i32(seq_lens, "seq_lens", dev), _i32(mask, "mask", dev), words,
                               None if positions is None else _i32(positions, "positions", dev, T), ws.data_ptr(),
-                              ws.numel(), _stream(stream)))
+                              ws.numel(), _stream_ptr(stream)))
     return mask, positions, ws
 
 

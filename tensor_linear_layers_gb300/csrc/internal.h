@@ -199,6 +199,7 @@ struct TreeAttnParams {
   TreeItem* items;                   // [grid] the item each CTA begins and others go on with, for the merge
   float* partials;                   // [2 * grid] slots of part_rows x (128 + 2)
   int part_rows;
+  int out_align32;                   // out is 32-byte aligned (rows are then written with 32-byte stores)
   unsigned long long timeout_ns;
 };
 int tree_group_rows(int max_rows);   // query rows of one item: 128 or 256

@@ -1813,6 +1813,7 @@ int tp_tree_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t*
   p.partials = reinterpret_cast<float*>(
       (reinterpret_cast<uintptr_t>(workspace) + (uintptr_t)pl.partials_off + 31) & ~uintptr_t(31));
   p.part_rows = pl.part_rows;
+  p.out_align32 = (reinterpret_cast<uintptr_t>(attn_out) & 31u) == 0 ? 1 : 0;
   p.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
   const cudaError_t e = launch_tree_attention(p, pl.grid, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");

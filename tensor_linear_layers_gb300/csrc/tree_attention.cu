@@ -192,10 +192,15 @@ __device__ __forceinline__ bool drop_nonfinite(uint32_t& w) {
 }
 }  // namespace
 
-// Partial results of a slot: [rows][128] fp32 O, then [rows][2] (max in the exp2 domain, sum).
-// part_rows is a multiple of 8 and the first slot 32-byte aligned: every row starts on 32 bytes.
-__device__ __forceinline__ float* part_o(const TreeAttnParams& p, int slot) {
-  return p.partials + (size_t)slot * p.part_rows * (kHd + 2);
+// Partial results of a slot: O as [16][rows][8] fp32 (pieces of eight dimensions, so that the
+// 32 rows of a warp write 1 KB on end; rows written whole, 512 bytes apart, took 2.5 us for 256
+// of them and held up the copies behind them), then [rows][2] (max in the exp2 domain, sum).
+// part_rows is a multiple of 8 and the first slot 32-byte aligned: every piece starts on 32 bytes.
+__device__ __forceinline__ float* part_o(const TreeAttnParams& p, int slot, int row, int d) {
+  return p.partials + (size_t)slot * p.part_rows * (kHd + 2) + ((size_t)(d >> 3) * p.part_rows + row) * 8 + (d & 7);
+}
+__device__ __forceinline__ float2* part_ml(const TreeAttnParams& p, int slot, int row) {
+  return reinterpret_cast<float2*>(p.partials + (size_t)slot * p.part_rows * (kHd + 2) + (size_t)p.part_rows * kHd) + row;
 }
 
 template <int MT>
@@ -399,30 +404,33 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
     } else if (warp == 2) {
       // ------------------------------------------------------------ segments
       const int heads = p.t * p.kv_per;
-      auto work = [&](const TreeReq& r) { return (long long)heads * r.groups * tree_item(r.chunks); };
-      // all requests' work; CTA 0 reports bad counts. A lane holds request `strip + lane` of the
-      // last strip of 32, so that up to 32 requests are read once.
-      long long total = 0, w = 0, pre = 0;            // pre: the strip's work up to and with this lane's
-      int strip = 0;                                  // that `mine` holds
-      auto scan = [&](int b0) {
-        if (b0 != strip) {
-          mine = TreeReq{};
-          mine.ok = true;
-          if (b0 + lane < p.n_reqs) mine = request(b0 + lane);
-          strip = b0;
-        }
-        w = pre = work(mine);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long up = __shfl_up_sync(0xffffffffu, pre, o);
-          if (lane >= o) pre += up;
-        }
+      int cost = 0;
+      auto work = [&](const TreeReq& r) { return heads * tree_head(r, cost); };
+      // A lane holds request `strip + lane` of a strip of 32, so that up to 32 requests are read once.
+      int strip = 0;
+      auto hold = [&](int b0) {
+        if (b0 == strip) return;
+        mine = TreeReq{};
+        mine.ok = true;
+        if (b0 + lane < p.n_reqs) mine = request(b0 + lane);
+        strip = b0;
       };
+      auto sum = [&](long long v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+      };
+      // all requests' chunks and heads' places with an item cost of 0 and of 1 apart; CTA 0 reports bad counts
+      long long chunks = 0, places = 0, items = 0;
       for (int b0 = 0; b0 < p.n_reqs; b0 += 32) {
-        scan(b0);
+        hold(b0);
         if (!mine.ok && blockIdx.x == 0) atomicExch(p.status, kStatusShape);
-        total += __shfl_sync(0xffffffffu, pre, 31);
+        chunks += (long long)mine.groups * mine.chunks;
+        places += tree_head(mine, 0);
+        items += mine.groups;
       }
+      cost = tree_cost(heads * sum(chunks), gridDim.x);
+      const long long total = heads * sum(places + cost * items);
       const long long per = tree_per(total, gridDim.x);
       long long pos = per * blockIdx.x;
       const long long end = min(total, pos + per);
@@ -432,7 +440,14 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
       long long before = 0;
       if (pos < end) {
         for (int b0 = 0; b0 < p.n_reqs; b0 += 32) {
-          if (p.n_reqs > 32) scan(b0);
+          hold(b0);
+          const long long w = work(mine);
+          long long pre = w;                          // the strip's places up to and with this lane's
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, pre, o);
+            if (lane >= o) pre += up;
+          }
           const unsigned hit = __ballot_sync(0xffffffffu, before + pre > pos);
           if (hit != 0u) {
             const int f = __ffs(hit) - 1;
@@ -443,6 +458,8 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
             r.len = __shfl_sync(0xffffffffu, mine.len, f);
             r.chunks = __shfl_sync(0xffffffffu, mine.chunks, f);
             r.groups = __shfl_sync(0xffffffffu, mine.groups, f);
+            r.full = __shfl_sync(0xffffffffu, mine.full, f);
+            r.last = __shfl_sync(0xffffffffu, mine.last, f);
             break;
           }
           before += __shfl_sync(0xffffffffu, pre, 31);
@@ -468,14 +485,13 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
               before += work(r);
               r = request(++b);
             }
-            const TreeSeg q = tree_segment(pos - before, r.chunks, end - pos, blockIdx.x);
+            const TreeSeg q = tree_segment(r, cost, pos - before, end - pos, blockIdx.x);
             pos += q.places;
-            if (q.c0 == q.c1) continue;                // the CTA's range ends within an item's first places
-            const int head = (int)(q.unit / r.groups), grp = (int)(q.unit - (long long)head * r.groups);
+            if (q.c0 == q.c1) continue;                // no chunk begins in these places
             s.b = b;
-            s.r = head / p.kv_per;
-            s.g = head - s.r * p.kv_per;
-            s.row0 = grp * kGroupRows;
+            s.r = q.head / p.kv_per;
+            s.g = q.head - s.r * p.kv_per;
+            s.row0 = q.group * kGroupRows;
             s.c0 = q.c0;
             s.c1 = q.c1;
             s.q0 = r.q0;
@@ -485,7 +501,7 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
             s.rows = min(kGroupRows, r.n * gq - s.row0);
             s.bad = 0;
             if (q.c0 == 0 && q.part >= 0) {
-              const int last = tree_last(before + q.unit * tree_item(r.chunks), r.chunks, per);
+              const int last = tree_last(r, q.group, before + q.begin, cost, per);
               p.items[blockIdx.x] = TreeItem{s.r, s.g, s.row0, s.rows, s.q0, last, 0, 0};
             }
             break;
@@ -547,7 +563,8 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
         return key < s.len ? bt[key / p.block_size] : -1;
       };
       int blk = block_of(s.c0);
-      if (C::kQBufs > 1) load_q(s, seg_no);
+      const bool q_first = C::kQBufs > 1 || seg_no == 0;
+      if (q_first) load_q(s, seg_no);
       for (int c = s.c0; c < s.c1 && ok; ++c) {
         const int key = c * kTreeChunk + my_row;
         int row = -1;                                // cache row of this lane's key (-1: zeros)
@@ -590,7 +607,7 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
           advance();
         }
         // one Q buffer: the last segment's queries may still be read, so K and V go first
-        if (ok && C::kQBufs == 1 && c == s.c0) load_q(s, seg_no);
+        if (ok && !q_first && c == s.c0) load_q(s, seg_no);
       }
       if (!ok) break;
       release_segment(slot);
@@ -710,7 +727,6 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
         const int r = s_seg[slot].r, g = s_seg[slot].g, b = s_seg[slot].b, part = s_seg[slot].part;
         const float inv = l == 0.f ? 0.f : 1.0f / l;
         __nv_bfloat16* dst = p.out + (size_t)r * p.sstride_out + (size_t)(q0 + tok) * p.rstride_out + (g * gq + jr - tok * gq) * kHd;
-        float* po = part >= 0 ? part_o(p, part) + (size_t)row * kHd : nullptr;
 #pragma unroll 1
         for (int k = 0; k < 128; k += C::kSub) {
           __syncwarp();
@@ -736,22 +752,25 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
           if (row < rows) {
             if (part >= 0) {
 #pragma unroll
-              for (int j = 0; j < C::kSub; j += 8) st_global_v8(po + k + j, *reinterpret_cast<const uint32_t(*)[8]>(s + j));
+              for (int j = 0; j < C::kSub; j += 8)
+                st_global_v8(part_o(p, part, row, k + j), *reinterpret_cast<const uint32_t(*)[8]>(s + j));
             } else {
 #pragma unroll
-              for (int j = 0; j < C::kSub; j += 8) {
-                uint4 v;
-                v.x = pack_bf16x2(s[j] * inv, s[j + 1] * inv);
-                v.y = pack_bf16x2(s[j + 2] * inv, s[j + 3] * inv);
-                v.z = pack_bf16x2(s[j + 4] * inv, s[j + 5] * inv);
-                v.w = pack_bf16x2(s[j + 6] * inv, s[j + 7] * inv);
-                *reinterpret_cast<uint4*>(dst + k + j) = v;
+              for (int j = 0; j < C::kSub; j += 16) {
+                uint32_t v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = pack_bf16x2(s[j + 2 * i] * inv, s[j + 2 * i + 1] * inv);
+                if (p.out_align32) {
+                  st_global_v8(dst + k + j, v);
+                } else {
+                  *reinterpret_cast<uint4*>(dst + k + j) = make_uint4(v[0], v[1], v[2], v[3]);
+                  *reinterpret_cast<uint4*>(dst + k + j + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+                }
               }
             }
           }
         }
-        if (row < rows && part >= 0)
-          *reinterpret_cast<float2*>(part_o(p, part) + (size_t)p.part_rows * kHd + 2 * row) = make_float2(m, l);
+        if (row < rows && part >= 0) *part_ml(p, part, row) = make_float2(m, l);
         tc_fence_before();
       }
       __syncwarp();
@@ -781,9 +800,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeA
   const TreeItem it = p.items[cta];
   if (row >= it.rows) return;
   auto slot = [&](int c) { return c == cta ? 2 * c + 1 : 2 * c; };
-  auto ml = [&](int c) {
-    return *reinterpret_cast<const float2*>(part_o(p, slot(c)) + (size_t)p.part_rows * kHd + 2 * row);
-  };
+  auto ml = [&](int c) { return *part_ml(p, slot(c), row); };
   float m = -INFINITY;
   for (int c = cta + lane; c <= it.last; c += 32) m = fmaxf(m, ml(c).x);
 #pragma unroll
@@ -793,7 +810,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) tree_merge_kernel(const TreeA
 #pragma unroll 4
   for (int c = cta; c <= it.last; ++c) {
     const float2 x = ml(c);
-    const float4 v = *reinterpret_cast<const float4*>(part_o(p, slot(c)) + (size_t)row * kHd + 4 * lane);
+    const float4 v = *reinterpret_cast<const float4*>(part_o(p, slot(c), row, 4 * lane));
     if (x.x != -INFINITY) {                          // else the row sees no key of that part
       const float w = exp2f(x.x - m);
       l += w * x.y;

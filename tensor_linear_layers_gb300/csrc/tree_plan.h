@@ -1,13 +1,17 @@
 // Work split of the tree attention, shared by its kernels and a host test.
 //
-// Request b has units(b) = t * kv_per * groups items (a kv head of a shard and a group of query
-// rows), each of chunks(b) = ceil(L / 128) chunks of 128 keys. An item takes its chunks' places
-// on a line, after kTreeItemCost more for what it costs besides them (its queries, the first
-// products, its output); items and requests follow each other in order. CTA c of the grid
-// takes places [c * per, (c + 1) * per), so the CTAs have the same work whatever the lengths.
-// An item that crosses a boundary is computed in parts: CTA c writes the part that continues
-// an item begun by an earlier CTA to slot 2 c, the part that begins one it does not finish to
-// slot 2 c + 1, and the merge kernel joins them in chunk order.
+// Request b has t * kv_per * groups items: a kv head of a shard and a group of query rows,
+// up to 128 or 256 of them in one or two tiles of 128. Every item takes its chunks of 128 keys,
+// ceil(L / 128). Items lie on a line, head by head and group by group, requests in order. A
+// chunk takes 2 + tiles places (the second tile's products and softmax against the copies,
+// which both share: 1.6 us against 1.2 us), and an item kTreeItemCost more before its first
+// chunk for what it costs besides them (its queries, the first products, its output). CTA c
+// of the grid takes the chunks whose first place is in [c * per, (c + 1) * per), so the CTAs
+// have the same work whatever the lengths. Where there is little work (fewer than four chunks
+// per CTA) an item costs nothing besides its chunks: they are spread over as many CTAs as
+// there are. An item that crosses a boundary is computed in parts: CTA c writes the part that
+// continues an item begun by an earlier CTA to slot 2 c, the part that begins one it does not
+// finish to slot 2 c + 1, and the merge kernel joins them in chunk order.
 #pragma once
 
 #ifdef __CUDACC__
@@ -20,8 +24,11 @@ namespace tpl {
 
 constexpr int kTreeChunk = 128;   // keys of one chunk
 
+constexpr int kTreeItemCost = 4;  // places
+
 struct TreeReq {
   int q0, n, len, chunks, groups;
+  int full, last;                 // places of a chunk in a full group and in the last one
   bool ok;                        // the counts fit the call (a request without drafts does too, and has no work)
 };
 // rows_per_group: query rows (tokens x q heads of one kv head) of one item.
@@ -34,39 +41,51 @@ TPL_HD TreeReq tree_request(int q0, int q1, int len, int T, int max_query_len, i
   r.n = r.ok ? q1 - q0 : 0;
   r.chunks = r.n > 0 ? (len + kTreeChunk - 1) / kTreeChunk : 0;
   r.groups = r.n > 0 ? (r.n * gq + rows_per_group - 1) / rows_per_group : 0;
+  r.full = 2 + rows_per_group / 128;
+  r.last = 2 + (r.n * gq - (r.groups - 1) * rows_per_group + 127) / 128;
   return r;
 }
 
-// Places of an item.
-constexpr int kTreeItemCost = 1;
-TPL_HD long long tree_item(int chunks) { return chunks > 0 ? chunks + kTreeItemCost : 0; }
+// Places of one head's items. cost: kTreeItemCost, or 0.
+TPL_HD long long tree_head(const TreeReq& r, int cost) {
+  return r.groups > 0 ? (long long)(r.groups - 1) * (cost + r.chunks * r.full) + cost + r.chunks * r.last : 0;
+}
 
-// Places per CTA.
+// What an item costs besides its chunks, and the places per CTA.
+TPL_HD int tree_cost(long long chunks, int grid) { return chunks >= 4LL * grid ? kTreeItemCost : 0; }
 TPL_HD long long tree_per(long long total, int grid) { return total > 0 ? (total + grid - 1) / grid : 1; }
 
 struct TreeSeg {
-  long long unit;                 // item within the request
+  int head, group;
   long long places;               // taken from the line
-  int c0, c1;                     // its chunks [c0, c1); none where the places are the item's first ones alone
+  int c0, c1;                     // the item's chunks [c0, c1); none where no chunk begins in the places
   int part;                       // slot of the partial result, or -1: the item is whole
+  long long begin;                // the item's first place in its request
 };
 // The segment of CTA cta that starts at place `at` of its request, `left` places before the CTA's end.
-TPL_HD TreeSeg tree_segment(long long at, int chunks, long long left, int cta) {
+TPL_HD TreeSeg tree_segment(const TreeReq& r, int cost, long long at, long long left, int cta) {
   TreeSeg s;
-  const long long item = tree_item(chunks);
-  s.unit = at / item;
-  const int p0 = (int)(at - s.unit * item);
+  const long long head = tree_head(r, cost);
+  const int item_full = cost + r.chunks * r.full;
+  s.head = (int)(at / head);
+  const int in = (int)(at - s.head * head);
+  s.group = in / item_full < r.groups - 1 ? in / item_full : r.groups - 1;
+  const int p0 = in - s.group * item_full, w = s.group < r.groups - 1 ? r.full : r.last;
+  s.begin = s.head * head + (long long)s.group * item_full;
+  const int item = cost + r.chunks * w;
   s.places = item - p0 < left ? item - p0 : left;
   const int p1 = p0 + (int)s.places;
-  s.c0 = p0 > kTreeItemCost ? p0 - kTreeItemCost : 0;
-  s.c1 = p1 > kTreeItemCost ? p1 - kTreeItemCost : 0;
-  s.part = s.c0 > 0 ? 2 * cta : s.c1 < chunks ? 2 * cta + 1 : -1;
+  s.c0 = p0 > cost ? (p0 - cost + w - 1) / w : 0;
+  s.c1 = p1 > cost ? (p1 - cost + w - 1) / w : 0;
+  s.part = s.c0 > 0 ? 2 * cta : s.c1 < r.chunks ? 2 * cta + 1 : -1;
   return s;
 }
 
-// The CTAs that hold the first and the last chunk of the item that begins at place `begin`.
-TPL_HD int tree_first(long long begin, long long per) { return (int)((begin + kTreeItemCost) / per); }
-TPL_HD int tree_last(long long begin, int chunks, long long per) { return (int)((begin + kTreeItemCost + chunks - 1) / per); }
+// The CTAs that hold the first and the last chunk of the item of group `group` that begins at place `begin` of the line.
+TPL_HD int tree_first(long long begin, int cost, long long per) { return (int)((begin + cost) / per); }
+TPL_HD int tree_last(const TreeReq& r, int group, long long begin, int cost, long long per) {
+  return (int)((begin + cost + (long long)(r.chunks - 1) * (group < r.groups - 1 ? r.full : r.last)) / per);
+}
 
 // Visibility of the 32 keys from position key on, as bits, to a drafted token with mask row
 // `words`: cached positions (before ctx) always, the n drafted ones by their bits, none after.

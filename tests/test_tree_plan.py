@@ -20,10 +20,10 @@ def lib(tmp_path_factory):
     L = ctypes.CDLL(so)
     L.plan_per.restype = ctypes.c_longlong
     L.plan_per.argtypes = [ctypes.c_longlong, ctypes.c_int]
-    L.plan_item.restype = ctypes.c_longlong
-    L.plan_item.argtypes = [ctypes.c_int]
-    L.plan_segment.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p]
-    L.plan_parts.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p]
+    L.plan_cost.argtypes = [ctypes.c_longlong, ctypes.c_int]
+    L.plan_head.restype = ctypes.c_longlong
+    L.plan_segment.argtypes = [ctypes.c_int, ctypes.c_longlong, ctypes.c_longlong, ctypes.c_int, ctypes.c_void_p]
+    L.plan_parts.argtypes = [ctypes.c_int, ctypes.c_longlong, ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p]
     L.plan_window.restype = ctypes.c_uint
     return L
 
@@ -52,45 +52,53 @@ def test_every_chunk_once_and_parts_where_the_merge_looks(lib, seed):
     reqs = int(rng.integers(1, 20))
     n = rng.integers(0, 65, reqs)
     lens = n + rng.integers(0, int(rng.choice([50, 3000])), reqs)
-    info = [request(lib, 0, int(k), int(L), 64, gq=gq, rows=rows) for k, L in zip(n, lens)]
-    base = np.concatenate([[0], np.cumsum([heads * g * lib.plan_item(c) for _, _, c, g in info])])
+    args = [(0, int(k), int(L), 64, 256, 1 << 20, gq, rows) for k, L in zip(n, lens)]
+    info = [request(lib, *a) for a in args]
     chunks = sum(heads * g * c for _, _, c, g in info)
+    cost = lib.plan_cost(chunks, grid)
+    heads_at = []
+    for a in args:
+        request(lib, *a)
+        heads_at.append(heads * lib.plan_head(cost))
+    base = np.concatenate([[0], np.cumsum(heads_at)])
     total = int(base[-1])
     per = lib.plan_per(total, grid)
     assert per * grid >= total
-    seen, slots, unfinished = set(), {}, {}
-    out = (ctypes.c_longlong * 5)()
+    seen, slots, unfinished, load = set(), {}, {}, []
+    out = (ctypes.c_longlong * 7)()
     for cta in range(grid):
         pos, end = cta * per, min(total, (cta + 1) * per)
         while pos < end:
             b = int(np.searchsorted(base, pos, side="right")) - 1
-            lib.plan_segment(pos - int(base[b]), info[b][2], end - pos, cta, out)
-            unit, c0, c1, part, places = [int(x) for x in out]
-            assert 0 <= unit < heads * info[b][3] and 0 <= c0 <= c1 <= info[b][2] and 0 < places <= end - pos
+            request(lib, *args[b])
+            n_chunks, groups = info[b][2:]
+            lib.plan_segment(cost, pos - int(base[b]), end - pos, cta, out)
+            head, group, c0, c1, part, places, begin = [int(x) for x in out]
+            assert 0 <= head < heads and 0 <= group < groups
+            assert 0 <= c0 <= c1 <= n_chunks and 0 < places <= end - pos
             pos += places
             if c0 == c1:
-                assert pos == end                          # the range ends before the item's first chunk
                 continue
             for c in range(c0, c1):
-                assert (b, unit, c) not in seen
-                seen.add((b, unit, c))
+                assert (b, head, group, c) not in seen
+                seen.add((b, head, group, c))
             parts = (ctypes.c_int * 2)()
-            lib.plan_parts(int(base[b]) + unit * lib.plan_item(info[b][2]), info[b][2], per, parts)
+            lib.plan_parts(group, int(base[b]) + begin, cost, per, parts)
             first, last = parts
             assert first <= cta <= last < grid
             if part < 0:
-                assert first == last and (c0, c1) == (0, info[b][2])
+                assert first == last and (c0, c1) == (0, n_chunks)
             else:
                 assert first < last and part not in slots and part == (2 * cta + 1 if cta == first else 2 * cta)
-                slots[part] = (b, unit)
+                slots[part] = (b, head, group)
                 if c0 == 0:
                     assert cta == first and cta not in unfinished      # one item per CTA for the merge
-                    unfinished[cta] = (b, unit, last)
+                    unfinished[cta] = (b, head, group, last)
     assert len(seen) == chunks
-    for cta, (b, unit, last) in unfinished.items():
+    for cta, (b, head, group, last) in unfinished.items():
         for c in range(cta, last + 1):
-            assert slots[2 * c + 1 if c == cta else 2 * c] == (b, unit)
-    assert len(slots) == sum(last - cta + 1 for cta, (_, _, last) in unfinished.items())
+            assert slots[2 * c + 1 if c == cta else 2 * c] == (b, head, group)
+    assert len(slots) == sum(u[3] - cta + 1 for cta, u in unfinished.items())
 
 
 @pytest.mark.parametrize("seed", range(6))
