@@ -102,16 +102,19 @@ __global__ void __launch_bounds__(kMaxDraft)
 // tile's next S is ready when its softmax is done with the last.
 //
 //   warp 0      issues S;  warp 1 issues P V (an elected lane of a converged warp);
-//   warp 2      walks the CTA's range and publishes segments; warp 3 idle
+//   warp 2      walks the CTA's range and publishes segments
+//   warp 3      looks over the V rows of drafted tokens (below)
 //   warps 4-7   copies: K and V rows through the block table with 16-byte cp.async into
 //               128-byte-swizzled tiles (any block size: a key's row is found on its own),
 //               a ring of tiles K0 V0 K1 V1 ...; Q rows of a segment
 //   warps 8-    softmax, a row per thread, four warps per tile; at a segment's end O / l to
 //               global memory, or the unnormalised O with (m, l) to a partial slot
 //
-// A row's mask applies to the chunks that hold drafted tokens alone. There, V values that
-// are not finite are set to zero in shared memory, so that 0 * v of a token that does not
-// see the key stays 0, and the rows that do see it get the value added at the end.
+// A row's mask applies to the chunks that hold drafted tokens alone. There, values of a drafted
+// token's V that are not finite are set to zero in shared memory, so that 0 * v of a token that
+// does not see the key stays 0, and the rows that do see it get the value added at the end.
+// Warp 3 does that between the copy and the product (the copying threads themselves would have
+// to wait for their copies, which left the ring empty at every item's end: up to 5 us of 35).
 //
 // Bound by HBM up to 256 rows: a chunk is 64 KB, 1.47 us of one SM's share of the measured
 // bandwidth; its products take 1024 tensor cycles (0.55 us) per tile.
@@ -146,7 +149,8 @@ struct TreeCfg {
     P_READY = S_FULL + MT * kSBufs,
     S_FREE = P_READY + MT * kSBufs,   // its P V has completed
     O_FREE = S_FREE + MT * kSBufs,    // per tile
-    U_FULL = O_FREE + MT, U_EMPTY = U_FULL + kUnitSlots,
+    LANDED = O_FREE + MT,             // a V tile with drafted tokens, per ring tile: to be looked over
+    U_FULL = LANDED + kTiles, U_EMPTY = U_FULL + kUnitSlots,
     DONE_S = U_EMPTY + kUnitSlots, DONE_PV, NBARS
   };
   static constexpr int kMiscOff = kBarOff + 8 * NBARS;     // tensor memory address, abort flag
@@ -172,6 +176,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int sr
 // One arrival on bar once all cp.async of this thread so far have landed (counted in the barrier's own count).
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Shared memory written by ordinary copies and stores, seen by this thread through a barrier,
@@ -222,8 +229,9 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
       if (b < C::Q_EMPTY || (b >= C::FULL && b < C::EMPTY)) count = 128;        // every copying thread
       if (b >= C::P_READY && b < C::S_FREE) count = 4;                          // the tile's softmax warps
       if (b >= C::S_FREE && b < C::O_FREE) count = 2;                           // the MMAs, and their issuer
-      if (b >= C::O_FREE && b < C::U_FULL) count = 4;
-      if (b >= C::U_EMPTY && b < C::DONE_S) count = 2 + 4 + 4 * MT;             // issuers, copy and softmax warps
+      if (b >= C::O_FREE && b < C::LANDED) count = 4;
+      if (b >= C::LANDED && b < C::U_FULL) count = 128;
+      if (b >= C::U_EMPTY && b < C::DONE_S) count = 3 + 4 + 4 * MT;             // issuers, warp 3, copy and softmax warps
       mbar_init(bar(b), count);
     }
     if (lane == 0) *s_abort = 0;
@@ -512,6 +520,44 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
         }
       }
       __syncwarp();
+    } else {
+      // ------------------------------------------------------------ V of drafted tokens
+      int ring = 1;                                   // tile of the next V
+      uint32_t phases = 0;                            // bit i: phase of LANDED + i
+      for (;;) {
+        const int slot = next_segment();
+        if (slot < 0) break;
+        const int c0 = s_seg[slot].c0, c1 = s_seg[slot].c1, len = s_seg[slot].len, ctx = len - s_seg[slot].n;
+        bool bad = false;
+        for (int c = c0; c < c1; ++c) {
+          if ((c + 1) * kTreeChunk > ctx) {
+            if (!wait(C::LANDED + ring, phases >> ring & 1u)) break;
+            phases ^= 1u << ring;
+            // rows of drafted tokens; a row is 8 pieces of 16 bytes in each of two boxes, in any order
+            const int r1 = min(len - c * kTreeChunk, kTreeChunk), box = (lane >> 3) & 1, piece = lane & 7;
+            uint8_t* v = base_ptr + C::kRingOff + ring * kTileBytes + box * (kTileBytes / 2) + piece * 16;
+#pragma unroll 4
+            for (int row = max(ctx - c * kTreeChunk, 0) + (lane >> 4); row < r1; row += 2) {
+              uint4* q = reinterpret_cast<uint4*>(v + row * 128);
+              uint4 d = *q;
+              const bool x = drop_nonfinite(d.x), y = drop_nonfinite(d.y), z = drop_nonfinite(d.z), w = drop_nonfinite(d.w);
+              if (x || y || z || w) {
+                *q = d;
+                bad = true;
+              }
+            }
+            bad = __any_sync(0xffffffffu, bad);
+            if (lane == 0) {
+              if (bad) *reinterpret_cast<volatile int*>(&s_seg[slot].bad) = 1;
+              mbar_arrive_n(bar(C::FULL + ring), 128);   // for the copying threads
+            }
+          }
+          ring += 2;
+          if (ring >= C::kTiles) ring -= C::kTiles;
+        }
+        if (!ok) break;
+        release_segment(slot);
+      }
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ copies
@@ -563,6 +609,7 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
         return key < s.len ? bt[key / p.block_size] : -1;
       };
       int blk = block_of(s.c0);
+      // with one Q buffer the last segment's queries may still be read: the first K tile goes before
       const bool q_first = C::kQBufs > 1 || seg_no == 0;
       if (q_first) load_q(s, seg_no);
       for (int c = s.c0; c < s.c1 && ok; ++c) {
@@ -585,29 +632,11 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
             const int rw = __shfl_sync(0xffffffffu, row, 2 * k + half);
             cp_async16(dst + k * 1024, src + (size_t)max(rw, 0) * p.kv_per * kHd, rw >= 0 ? 16 : 0, pol);
           }
-          if (kv == 1 && (c + 1) * kTreeChunk > ctx) {
-            // a chunk with drafted tokens: no value that is not finite stays in V
-            cp_async_wait_all();
-            bool any = false;
-#pragma unroll 1
-            for (int k = 0; k < 16; ++k) {
-              uint4* q = reinterpret_cast<uint4*>(base_ptr + (dst - base) + k * 1024);
-              uint4 v = *q;
-              const bool x = drop_nonfinite(v.x), y = drop_nonfinite(v.y), z = drop_nonfinite(v.z), w = drop_nonfinite(v.w);
-              if (x || y || z || w) {
-                *q = v;
-                any = true;
-              }
-            }
-            if (any) *reinterpret_cast<volatile int*>(&s_seg[slot].bad) = 1;
-            mbar_arrive(bar(C::FULL + ring));
-          } else {
-            cp_async_arrive(bar(C::FULL + ring));
-          }
+          cp_async_arrive(bar((kv == 1 && (c + 1) * kTreeChunk > ctx ? C::LANDED : C::FULL) + ring));
           advance();
+          if (kv == 0 && c == s.c0 && !q_first) load_q(s, seg_no);
+          if (!ok) break;
         }
-        // one Q buffer: the last segment's queries may still be read, so K and V go first
-        if (ok && !q_first && c == s.c0) load_q(s, seg_no);
       }
       if (!ok) break;
       release_segment(slot);
@@ -736,7 +765,7 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
           if (bad) {
             // V values that were dropped, added to the rows that see their keys
             const int* bt = p.block_tables + (size_t)b * p.max_blocks;
-            const int k0 = max(c0, ctx / kTreeChunk) * kTreeChunk, k1 = min(c1 * kTreeChunk, len);
+            const int k0 = max(c0 * kTreeChunk, ctx), k1 = min(c1 * kTreeChunk, len);
             for (int key = k0; row < rows && key < k1; ++key) {
               if (!(tree_window(words, key & ~31, ctx, n) >> (key & 31) & 1u)) continue;
               const int blk = bt[key / p.block_size];
