@@ -397,12 +397,13 @@ class TPLinear:
         dev, n = self._dev, len(caches_k)
         both = [*caches_k, *caches_v]
         _bf16_on(both[0], "cache_k", dev, shape)
-        # a call names every layer's caches: the same checks of all of them, one attribute at a time
+        # A call names every layer's caches, 64 tensors for 32 layers: the same checks of all of them, one
+        # attribute at a time (a copy takes bits, so the size in bytes stands for shape and type).
         T, first = torch.Tensor, both[0]
-        if set(map(T.dtype.__get__, both)) != {torch.bfloat16} or set(map(T.get_device, both)) != {first.get_device()}:
-            raise ValueError(f"every cache must be a bf16 tensor on {dev}")
-        if set(map(T.numel, both)) != {first.numel()} or False in map(T.is_contiguous, both):
-            raise ValueError(f"every cache must be contiguous and of the shape {tuple(shape)}")
+        if set(map(T.nbytes.__get__, both)) != {first.nbytes} or False in map(T.is_contiguous, both):
+            raise ValueError(f"every cache must be a contiguous bf16 tensor of the shape {tuple(shape)}")
+        if set(map(T.get_device, both)) != {first.get_device()}:
+            raise ValueError(f"every cache must be on {dev}")
         ptrs = array.array("Q", map(T.data_ptr, both))
         at = ptrs.buffer_info()[0]
         return n, at, at + 8 * n, nb, bs, ptrs
