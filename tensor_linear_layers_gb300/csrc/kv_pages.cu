@@ -9,6 +9,7 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace tpl {
 
@@ -20,6 +21,8 @@ constexpr int kStatusShape = -2;   // TP_ERR_SHAPE
 // One CTA per (pair, shard) and (layer, k or v): dst page = src page.
 __global__ void kv_copy_blocks_kernel(const KvLayers layers, const int2* __restrict__ pairs, long long num_blocks,
                                       long long page_vecs, int t, int* __restrict__ status) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int r = blockIdx.x % t;
   const int2 pr = pairs[blockIdx.x / t];
   if (pr.x < 0) return;                              // padding entry
@@ -46,6 +49,8 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const KvLay
                                                                      int n_layers, int strips) {
   __shared__ int2 move[kCompactThreads];             // slots (from, to) of a strip of the list
   __shared__ int s_stop;
+  griddep_launch_dependents();
+  griddep_wait();
   const int b = blockIdx.x / strips, strip = blockIdx.x - b * strips, tid = threadIdx.x;
   const int q0 = p.qsl[b], n_new = p.qsl[b + 1] - q0, L = p.seq_lens[b], ctx = L - n_new;
   if (n_new < 0 || ctx < 0 || L > (long long)p.max_blocks * p.block_size) {
@@ -108,18 +113,20 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const KvLay
 cudaError_t launch_kv_copy_blocks(const KvLayers& layers, int n_layers, const int* pairs, int n_pairs,
                                   long long num_blocks, int block_size, int kv_per, int t, int* status,
                                   cudaStream_t st) {
-  const dim3 grid((unsigned)((long long)n_pairs * t), (unsigned)(2 * n_layers));
-  kv_copy_blocks_kernel<<<grid, 256, 0, st>>>(layers, reinterpret_cast<const int2*>(pairs), num_blocks,
-                                              (long long)block_size * kv_per * kHd / 8, t, status);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg =
+      programmatic(dim3((unsigned)((long long)n_pairs * t), (unsigned)(2 * n_layers)), 256, 0, st, attr);
+  return cudaLaunchKernelEx(&cfg, kv_copy_blocks_kernel, layers, reinterpret_cast<const int2*>(pairs), num_blocks,
+                            (long long)block_size * kv_per * kHd / 8, t, status);
 }
 
 cudaError_t launch_kv_compact(const KvLayers& layers, int n_layers, const CompactParams& p, int n_reqs, cudaStream_t st) {
   const long long cols = 2LL * n_layers * p.t * (p.kv_per * kHd / 8);
   const int strips = (int)((cols + kCompactThreads - 1) / kCompactThreads);
   if ((long long)n_reqs * strips > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  kv_compact_kernel<<<(unsigned)((long long)n_reqs * strips), kCompactThreads, 0, st>>>(layers, p, n_layers, strips);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = programmatic(dim3((unsigned)((long long)n_reqs * strips)), kCompactThreads, 0, st, attr);
+  return cudaLaunchKernelEx(&cfg, kv_compact_kernel, layers, p, n_layers, strips);
 }
 
 }  // namespace tpl

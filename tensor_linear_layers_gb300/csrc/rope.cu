@@ -125,6 +125,8 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopePar
 template <int G, bool INTERLEAVED, bool NORM>
 __global__ void __launch_bounds__(256, kMinCtas) qk_norm_rope_vec_kernel(const RopeParams p, int steps, int parts) {
   constexpr int HPW = 32 / G;                        // heads of a step
+  griddep_launch_dependents();
+  griddep_wait();
   const int lane = threadIdx.x & 31;
   const long long wid = blockIdx.x * 8LL + (threadIdx.x >> 5);
   const int i = (int)(wid / parts), part = (int)(wid - (long long)i * parts);
@@ -290,32 +292,28 @@ cudaError_t launch_rope_table(const RopeFreqs& f, long long n_pos, int rotary_di
 }
 
 template <int G>
-static void launch_vec(const RopeParams& p, int nsm, cudaStream_t st) {
+static cudaError_t launch_vec(const RopeParams& p, int nsm, cudaStream_t st) {
   // steps of 32 / G heads of a token: kUnroll per warp, fewer where that leaves SMs without work
   const int total = (p.t * (p.q_per + 2 * p.kv_per) * G + 31) / 32;
   int steps = kUnroll;
   while (steps > 1 && (long long)p.T * ((total + steps - 1) / steps) < 16LL * nsm) --steps;
   const int parts = (total + steps - 1) / steps;
   const long long warps = (long long)p.T * parts;
-  const unsigned grid = (unsigned)((warps + 7) / 8);
   const bool norm = p.q_gamma != nullptr || p.k_gamma != nullptr;
-  if (p.interleaved)
-    norm ? qk_norm_rope_vec_kernel<G, true, true><<<grid, 256, 0, st>>>(p, steps, parts)
-         : qk_norm_rope_vec_kernel<G, true, false><<<grid, 256, 0, st>>>(p, steps, parts);
-  else
-    norm ? qk_norm_rope_vec_kernel<G, false, true><<<grid, 256, 0, st>>>(p, steps, parts)
-         : qk_norm_rope_vec_kernel<G, false, false><<<grid, 256, 0, st>>>(p, steps, parts);
+  auto kernel = p.interleaved ? (norm ? qk_norm_rope_vec_kernel<G, true, true> : qk_norm_rope_vec_kernel<G, true, false>)
+                              : (norm ? qk_norm_rope_vec_kernel<G, false, true> : qk_norm_rope_vec_kernel<G, false, false>);
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = programmatic(dim3((unsigned)((warps + 7) / 8)), 256, 0, st, attr);
+  return cudaLaunchKernelEx(&cfg, kernel, p, steps, parts);
 }
 
 cudaError_t launch_qk_norm_rope(const RopeParams& p, int nsm, cudaStream_t st) {
   if (p.interleaved || p.rd % 16 == 0) {
     const int lanes = (p.hd / 8 + 1) / 2;            // of a head
-    if (lanes <= 1) launch_vec<1>(p, nsm, st);
-    else if (lanes <= 2) launch_vec<2>(p, nsm, st);
-    else if (lanes <= 4) launch_vec<4>(p, nsm, st);
-    else if (lanes <= 8) launch_vec<8>(p, nsm, st);
-    else launch_vec<16>(p, nsm, st);
-    return cudaGetLastError();
+    if (lanes <= 1) return launch_vec<1>(p, nsm, st);
+    if (lanes <= 2) return launch_vec<2>(p, nsm, st);
+    if (lanes <= 4) return launch_vec<4>(p, nsm, st);
+    return lanes <= 8 ? launch_vec<8>(p, nsm, st) : launch_vec<16>(p, nsm, st);
   }
   const long long items = (long long)p.T * p.t * (p.q_per + 2 * p.kv_per);
   const int grid = (int)std::min<long long>((items + kWarps - 1) / kWarps, 16LL * nsm);
