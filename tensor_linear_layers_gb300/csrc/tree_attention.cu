@@ -586,10 +586,9 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
         if (m * 128 >= s.rows) break;
         // rows past the item's keep what the buffer held: they only reach their own rows of S and O
         const __nv_bfloat16* q = p.qkv + (size_t)s.r * p.sstride_in + s.g * gq * kHd + c16 * 8;
-#pragma unroll 1
+#pragma unroll 4
         for (int k = 0; k < 16; ++k) {
           const int j = m * 128 + row_of + 8 * k;
-          if (m * 128 + 2 * w4 + 8 * k >= s.rows) break;   // the whole warp
           const int jr = s.row0 + j, tok = token_of(jr);
           if (j < s.rows)
             cp_async16(base + (qb * MT + m) * kTileBytes + dst0 + k * 1024,
@@ -610,8 +609,17 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
       };
       int blk = block_of(s.c0);
       // with one Q buffer the last segment's queries may still be read: the first K tile goes before
+      // (and the queries' rows, 256 bytes each, start for L2: their copy is what S waits for)
       const bool q_first = C::kQBufs > 1 || seg_no == 0;
-      if (q_first) load_q(s, seg_no);
+      if (q_first) {
+        load_q(s, seg_no);
+      } else {
+        for (int j = threadIdx.x - 128; j < 2 * s.rows; j += 128) {
+          const int jr = s.row0 + (j >> 1), tok = token_of(jr);
+          prefetch_l2(p.qkv + (size_t)s.r * p.sstride_in + (size_t)(s.q0 + tok) * p.rstride_in +
+                      (s.g * gq + jr - tok * gq) * kHd + (j & 1) * 64);
+        }
+      }
       for (int c = s.c0; c < s.c1 && ok; ++c) {
         const int key = c * kTreeChunk + my_row;
         int row = -1;                                // cache row of this lane's key (-1: zeros)
