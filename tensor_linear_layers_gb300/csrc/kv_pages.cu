@@ -21,8 +21,8 @@ constexpr int kStatusShape = -2;   // TP_ERR_SHAPE
 // One CTA per (pair, shard) and (layer, k or v): dst page = src page.
 __global__ void kv_copy_blocks_kernel(const KvLayers layers, const int2* __restrict__ pairs, long long num_blocks,
                                       long long page_vecs, int t, int* __restrict__ status) {
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   const int r = blockIdx.x % t;
   const int2 pr = pairs[blockIdx.x / t];
   if (pr.x < 0) return;                              // padding entry
@@ -49,8 +49,8 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const KvLay
                                                                      int n_layers, int strips) {
   __shared__ int2 move[kCompactThreads];             // slots (from, to) of a strip of the list
   __shared__ int s_stop;
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   const int b = blockIdx.x / strips, strip = blockIdx.x - b * strips, tid = threadIdx.x;
   const int q0 = p.qsl[b], n_new = p.qsl[b + 1] - q0, L = p.seq_lens[b], ctx = L - n_new;
   if (n_new < 0 || ctx < 0 || L > (long long)p.max_blocks * p.block_size) {

@@ -125,8 +125,8 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopePar
 template <int G, bool INTERLEAVED, bool NORM>
 __global__ void __launch_bounds__(256, kMinCtas) qk_norm_rope_vec_kernel(const RopeParams p, int steps, int parts) {
   constexpr int HPW = 32 / G;                        // heads of a step
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
   const long long wid = blockIdx.x * 8LL + (threadIdx.x >> 5);
   const int i = (int)(wid / parts), part = (int)(wid - (long long)i * parts);

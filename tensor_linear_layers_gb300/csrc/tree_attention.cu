@@ -35,8 +35,8 @@ __global__ void __launch_bounds__(kMaxDraft)
   __shared__ unsigned rows[2][kWords][kMaxDraft];
   __shared__ int up[2][kMaxDraft];                   // >= 0: the next ancestor; -1: none left; -2: a bad parent above
   const int b = blockIdx.x, i = threadIdx.x;
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   const int q0 = qsl[b], n = qsl[b + 1] - q0, ctx = seq_lens[b] - n;
   if (q0 < 0 || n < 0 || n > max_query_len || q0 > T - n || ctx < 0) {
     if (i == 0) atomicExch(status, kStatusShape);
@@ -249,9 +249,22 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
   auto request = [&](int b) {
     return tree_request(p.qsl[b], p.qsl[b + 1], p.seq_lens[b], p.T, p.max_query_len, p.max_seq_len, gq, kGroupRows);
   };
-  TreeReq mine{};                                   // warp 2: request `lane` of a strip of 32; the first strip loads here
-  mine.ok = true;
-  if (warp == 2 && lane < p.n_reqs) mine = request(lane);
+  // warp 2: requests `lane`, `lane` + 32, .. of a batch of 128 (first row, drafted tokens, tokens; -1: bad
+  // counts), loaded together; the first batch here, beside the set-up
+  constexpr int kStrips = 4;
+  int3 mine[kStrips];
+  auto load_batch = [&](int b0) {
+#pragma unroll
+    for (int i = 0; i < kStrips; ++i) {
+      mine[i] = make_int3(0, 0, 0);
+      const int b = b0 + 32 * i + lane;
+      if (b < p.n_reqs) {
+        const TreeReq r = request(b);
+        mine[i] = make_int3(r.q0, r.ok ? r.n : -1, r.len);
+      }
+    }
+  };
+  if (warp == 2) load_batch(0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -414,14 +427,12 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
       const int heads = p.t * p.kv_per;
       int cost = 0;
       auto work = [&](const TreeReq& r) { return heads * tree_head(r, cost); };
-      // A lane holds request `strip + lane` of a strip of 32, so that up to 32 requests are read once.
-      int strip = 0;
-      auto hold = [&](int b0) {
-        if (b0 == strip) return;
-        mine = TreeReq{};
-        mine.ok = true;
-        if (b0 + lane < p.n_reqs) mine = request(b0 + lane);
-        strip = b0;
+      auto counted = [&](int3 m) {                    // the request of its counts (none where they are bad)
+        return tree_request(m.x, m.x + max(m.y, 0), m.z, p.T, p.max_query_len, p.max_seq_len, gq, kGroupRows);
+      };
+      auto broadcast = [&](int3 m, int from) {
+        return counted(make_int3(__shfl_sync(0xffffffffu, m.x, from), __shfl_sync(0xffffffffu, m.y, from),
+                                 __shfl_sync(0xffffffffu, m.z, from)));
       };
       auto sum = [&](long long v) {
 #pragma unroll
@@ -430,12 +441,16 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
       };
       // all requests' chunks and heads' places with an item cost of 0 and of 1 apart; CTA 0 reports bad counts
       long long chunks = 0, places = 0, items = 0;
-      for (int b0 = 0; b0 < p.n_reqs; b0 += 32) {
-        hold(b0);
-        if (!mine.ok && blockIdx.x == 0) atomicExch(p.status, kStatusShape);
-        chunks += (long long)mine.groups * mine.chunks;
-        places += tree_head(mine, 0);
-        items += mine.groups;
+      for (int b0 = 0; b0 < p.n_reqs; b0 += 32 * kStrips) {
+        if (b0 > 0) load_batch(b0);
+#pragma unroll
+        for (int i = 0; i < kStrips; ++i) {
+          if (mine[i].y < 0 && blockIdx.x == 0) atomicExch(p.status, kStatusShape);
+          const TreeReq q = counted(mine[i]);
+          chunks += (long long)q.groups * q.chunks;
+          places += tree_head(q, 0);
+          items += q.groups;
+        }
       }
       cost = tree_cost(heads * sum(chunks), gridDim.x);
       const long long total = heads * sum(places + cost * items);
@@ -447,79 +462,95 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
       int b = 0;
       long long before = 0;
       if (pos < end) {
-        for (int b0 = 0; b0 < p.n_reqs; b0 += 32) {
-          hold(b0);
-          const long long w = work(mine);
-          long long pre = w;                          // the strip's places up to and with this lane's
+        bool found = false;
+        for (int b0 = 0; b0 < p.n_reqs && !found; b0 += 32 * kStrips) {
+          if (p.n_reqs > 32 * kStrips) load_batch(b0);
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const long long up = __shfl_up_sync(0xffffffffu, pre, o);
-            if (lane >= o) pre += up;
+          for (int i = 0; i < kStrips; ++i) {
+            if (found) break;
+            const TreeReq q = counted(mine[i]);
+            const long long w = work(q);
+            long long pre = w;                        // the strip's places up to and with this lane's
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const long long up = __shfl_up_sync(0xffffffffu, pre, o);
+              if (lane >= o) pre += up;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, before + pre > pos);
+            if (hit != 0u) {
+              const int f = __ffs(hit) - 1;
+              b = b0 + 32 * i + f;
+              before += __shfl_sync(0xffffffffu, pre - w, f);
+              r = broadcast(mine[i], f);
+              found = true;
+            } else {
+              before += __shfl_sync(0xffffffffu, pre, 31);
+            }
           }
-          const unsigned hit = __ballot_sync(0xffffffffu, before + pre > pos);
-          if (hit != 0u) {
-            const int f = __ffs(hit) - 1;
-            b = b0 + f;
-            before += __shfl_sync(0xffffffffu, pre - w, f);
-            r.q0 = __shfl_sync(0xffffffffu, mine.q0, f);
-            r.n = __shfl_sync(0xffffffffu, mine.n, f);
-            r.len = __shfl_sync(0xffffffffu, mine.len, f);
-            r.chunks = __shfl_sync(0xffffffffu, mine.chunks, f);
-            r.groups = __shfl_sync(0xffffffffu, mine.groups, f);
-            r.full = __shfl_sync(0xffffffffu, mine.full, f);
-            r.last = __shfl_sync(0xffffffffu, mine.last, f);
-            break;
-          }
-          before += __shfl_sync(0xffffffffu, pre, 31);
         }
       }
       // no item of this CTA is continued by others, unless a segment says so below
       if (lane == 0) p.items[blockIdx.x].rows = 0;
       __syncwarp();
-      if (lane == 0) {
-        for (int u = 0;; ++u) {
-          const int slot = u % kUnitSlots;
-          if (!mbar_wait_bounded(bar(C::U_EMPTY + slot), ((u / kUnitSlots) & 1) ^ 1, s_abort, timeout)) {
-            if (!*s_abort) {
-              atomicExch(p.status, kStatusTimeout);
-              *s_abort = 1;
+      for (int u = 0;; ++u) {
+        const int slot = u % kUnitSlots;
+        if (!wait(C::U_EMPTY + slot, ((u / kUnitSlots) & 1) ^ 1)) break;
+        Segment s;
+        s.b = -1;
+        while (pos < end) {
+          while (pos - before >= work(r)) {            // this request is done: on to the next one with work
+            before += work(r);
+            for (;; b += 32) {
+              const int next = b + 1 + lane;
+              int3 m = make_int3(0, 0, 0);
+              if (next < p.n_reqs) {
+                const TreeReq q = request(next);
+                m = make_int3(q.q0, q.n, q.len);
+              }
+              const unsigned hit = __ballot_sync(0xffffffffu, m.y > 0);
+              if (hit != 0u) {
+                const int f = __ffs(hit) - 1;
+                b += 1 + f;
+                r = broadcast(m, f);
+                break;
+              }
+              if (b + 32 >= p.n_reqs) {                // cannot be: a place before `end` belongs to a request
+                pos = end;
+                r = TreeReq{};
+                break;
+              }
             }
-            break;
+            if (pos >= end) break;
           }
-          Segment s;
-          s.b = -1;
-          while (pos < end) {
-            while (pos - before >= work(r)) {          // this request is done (or empty)
-              before += work(r);
-              r = request(++b);
-            }
-            const TreeSeg q = tree_segment(r, cost, pos - before, end - pos, blockIdx.x);
-            pos += q.places;
-            if (q.c0 == q.c1) continue;                // no chunk begins in these places
-            s.b = b;
-            s.r = q.head / p.kv_per;
-            s.g = q.head - s.r * p.kv_per;
-            s.row0 = q.group * kGroupRows;
-            s.c0 = q.c0;
-            s.c1 = q.c1;
-            s.q0 = r.q0;
-            s.n = r.n;
-            s.len = r.len;
-            s.part = q.part;
-            s.rows = min(kGroupRows, r.n * gq - s.row0);
-            s.bad = 0;
-            if (q.c0 == 0 && q.part >= 0) {
-              const int last = tree_last(r, q.group, before + q.begin, cost, per);
-              p.items[blockIdx.x] = TreeItem{s.r, s.g, s.row0, s.rows, s.q0, last, 0, 0};
-            }
-            break;
+          if (pos >= end) break;
+          const TreeSeg q = tree_segment(r, cost, pos - before, end - pos, blockIdx.x);
+          pos += q.places;
+          if (q.c0 == q.c1) continue;                  // no chunk begins in these places
+          s.b = b;
+          s.r = q.head / p.kv_per;
+          s.g = q.head - s.r * p.kv_per;
+          s.row0 = q.group * kGroupRows;
+          s.c0 = q.c0;
+          s.c1 = q.c1;
+          s.q0 = r.q0;
+          s.n = r.n;
+          s.len = r.len;
+          s.part = q.part;
+          s.rows = min(kGroupRows, r.n * gq - s.row0);
+          s.bad = 0;
+          if (q.c0 == 0 && q.part >= 0 && lane == 0) {
+            const int last = tree_last(r, q.group, before + q.begin, cost, per);
+            p.items[blockIdx.x] = TreeItem{s.r, s.g, s.row0, s.rows, s.q0, last, 0, 0};
           }
+          break;
+        }
+        if (lane == 0) {
           s_seg[slot] = s;
           mbar_arrive(bar(C::U_FULL + slot));
-          if (s.b < 0) break;
         }
+        __syncwarp();
+        if (s.b < 0) break;
       }
-      __syncwarp();
     } else {
       // ------------------------------------------------------------ V of drafted tokens
       int ring = 1;                                   // tile of the next V

@@ -259,6 +259,57 @@ def test_long_context_many_requests():
     check(out, c, nq, nkv, t)
 
 
+def test_more_requests_than_one_batch_and_long_runs_of_empty_ones():
+    # 300 requests, most of them without drafted tokens (a padded batch), work at both ends and between
+    nq, nkv, t = 4, 2, 1
+    n, ctx = [0] * 300, [0] * 300
+    rng = np.random.default_rng(9)
+    for b in (0, 31, 32, 127, 128, 200, 299):
+        n[b], ctx[b] = int(rng.integers(1, 6)), int(rng.integers(0, 400))
+    for b in range(250, 298):
+        ctx[b] = 17                                         # cached tokens, nothing drafted
+    c = build(nq, nkv, t, ctx, n, 16, seed=50)
+    out, ws = run(handle(nq, nkv, t), c)
+    assert status(ws) == 0
+    check(out, c, nq, nkv, t)
+    # nobody has a drafted token: nothing is computed, nothing written
+    d = dict(c, qsl=np.zeros(301, dtype=np.int64), lens=ctx)
+    keep = torch.full_like(out, 5.0)
+    mask = torch.zeros(c["T"], 1, dtype=torch.int32, device="cuda")
+    _, ws = run(handle(nq, nkv, t), d, mask=mask, out=keep, max_q=5, max_len=max(c["lens"]))
+    assert status(ws) == 0 and (keep == 5.0).all()
+
+
+def test_wait_limit_runs_out_and_context_survives():
+    # 24 requests that share one document's pages (read only): some 100 us of work for every SM, in which
+    # the warp that looks at the drafted tokens' values waits for the last chunk of its item
+    nq = nkv = 8
+    reqs, ctx, n = 24, 8192, 2
+    c = build(nq, nkv, 1, [ctx], [n], 16, seed=60)
+    h = handle(nq, nkv, 1)
+    many = dict(c, tables=np.repeat(c["tables"], reqs, 0), lens=[ctx + n] * reqs, qsl=np.arange(reqs + 1) * n,
+                n=[n] * reqs, T=reqs * n, qkv=c["qkv"].repeat(1, reqs, 1), parents=c["parents"] * reqs)
+    good, ws = run(h, many)
+    good = good.clone()
+    assert status(ws) == 0
+    tl.set_wait_timeout(1)                                  # waits of more than one suspended try (20 us) run out
+    try:
+        _, ws = run(h, many, ws=ws)
+        st = status(ws)                                     # returns: nothing hung, nothing faulted
+    finally:
+        tl.set_wait_timeout(2_000_000_000)
+    assert st == tl.TP_ERR_TIMEOUT
+    ws.zero_()
+    out, ws = run(h, many, ws=ws)
+    assert status(ws) == 0 and torch.equal(out, good)
+    # requests 0 and 17 against the oracle
+    ref = oracle.tree_attention(c["qkv"], [0, n], [ctx + n], c["tables"], [oracle.tree_sees(c["parents"][0])], c["ck"],
+                                c["cv"], nq, nkv, 128, 1, 16)
+    for b in (0, 17):
+        g = f64(out[:, b * n:(b + 1) * n].cpu())
+        assert np.abs(g - ref).max() <= 2e-2 * np.abs(ref).max()
+
+
 def test_chain_agrees_with_paged_attention():
     # a chain of drafted tokens is the causal case that tp_paged_attention computes
     nq, nkv, t = 8, 2, 2
