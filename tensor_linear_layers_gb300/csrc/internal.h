@@ -11,7 +11,9 @@ constexpr int kStatusCapacity = -5;
 
 // A launch that may be scheduled before the grid in front of it has completed (programmatic
 // serialisation). Its kernel executes griddepcontrol.wait in every thread that goes on, before
-// it reads or writes anything in global memory, so that results are those of stream order.
+// it reads or writes anything in global memory, so that results are those of stream order, and
+// reads what other kernels wrote with coherent loads: one through a const __restrict__ pointer
+// or __ldg counts as invariant and may be moved above the wait.
 inline cudaLaunchConfig_t programmatic(dim3 grid, int threads, size_t smem, cudaStream_t st, cudaLaunchAttribute* attr) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -19,8 +19,8 @@ constexpr int kStatusShape = -2;   // TP_ERR_SHAPE
 }  // namespace
 
 // One CTA per (pair, shard) and (layer, k or v): dst page = src page.
-__global__ void kv_copy_blocks_kernel(const KvLayers layers, const int2* __restrict__ pairs, long long num_blocks,
-                                      long long page_vecs, int t, int* __restrict__ status) {
+__global__ void kv_copy_blocks_kernel(const KvLayers layers, const int2* pairs, long long num_blocks, long long page_vecs,
+                                      int t, int* status) {
   griddep_wait();
   griddep_launch_dependents();
   const int r = blockIdx.x % t;

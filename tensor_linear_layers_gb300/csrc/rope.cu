@@ -35,7 +35,7 @@ __device__ __forceinline__ uint32_t pack2(uint64_t v) {
 
 // Entry (p, i): the angle p * f_i in 64 bits (its fraction of a turn would be lost in
 // 32 bits at far positions), its cosine and sine rounded to fp32. Built once per model.
-__global__ void rope_table_kernel(const RopeFreqs f, long long n_pos, int half, float* __restrict__ table) {
+__global__ void rope_table_kernel(const RopeFreqs f, long long n_pos, int half, float* table) {
   const long long n = n_pos * half;
   for (long long e = blockIdx.x * (long long)blockDim.x + threadIdx.x; e < n; e += (long long)gridDim.x * blockDim.x) {
     const long long p = e / half;
@@ -124,8 +124,8 @@ __device__ __forceinline__ void turn(uint4& a, uint4& b, const Pieces& q, const 
     if (gamma != nullptr) {
       rs = rsqrtf(s0 * inv_hd + eps);                // applied after the rotation, which is linear
       uint4 ga = make_uint4(0u, 0u, 0u, 0u), gb = ga;
-      if (q.va >= 0) ga = __ldg(reinterpret_cast<const uint4*>(gamma + q.va * 8));
-      if (q.vb >= 0) gb = __ldg(reinterpret_cast<const uint4*>(gamma + q.vb * 8));
+      if (q.va >= 0) ga = *reinterpret_cast<const uint4*>(gamma + q.va * 8);
+      if (q.vb >= 0) gb = *reinterpret_cast<const uint4*>(gamma + q.vb * 8);
       const uint32_t* wga = &ga.x;
       const uint32_t* wgb = &gb.x;
 #pragma unroll

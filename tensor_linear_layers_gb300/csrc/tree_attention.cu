@@ -28,9 +28,8 @@ constexpr int kMaxDraft = 256;     // TP_TREE_MAX_DRAFT
 // and points to where that one points, so a chain of d ancestors takes log2(d) + 1 rounds
 // (a chain of 64: 7; walking up it took 64 dependent reads). Latency bounds it: a few KB.
 __global__ void __launch_bounds__(kMaxDraft)
-    tree_mask_kernel(int T, int max_query_len, int words, const int* __restrict__ parents, const int* __restrict__ qsl,
-                     const int* __restrict__ seq_lens, int* __restrict__ mask, int* __restrict__ positions,
-                     int* __restrict__ status) {
+    tree_mask_kernel(int T, int max_query_len, int words, const int* parents, const int* qsl, const int* seq_lens,
+                     int* mask, int* positions, int* status) {
   constexpr int kWords = kMaxDraft / 32;
   __shared__ unsigned rows[2][kWords][kMaxDraft];
   __shared__ int up[2][kMaxDraft];                   // >= 0: the next ancestor; -1: none left; -2: a bad parent above
