@@ -115,8 +115,11 @@ __global__ void __launch_bounds__(kMaxDraft)
 // Warp 3 does that between the copy and the product (the copying threads themselves would have
 // to wait for their copies, which left the ring empty at every item's end: up to 5 us of 35).
 //
-// Bound by HBM up to 256 rows: a chunk is 64 KB, 1.47 us of one SM's share of the measured
-// bandwidth; its products take 1024 tensor cycles (0.55 us) per tile.
+// Up to 128 rows HBM bounds it: a chunk is 64 KB, 1.47 us of one SM's share of the measured copy
+// bandwidth, and takes 1.52 us (2 x 131072 keys, 8 drafts of 64 q heads: 167 us, 0.94). With two
+// tiles it is the chain S, softmax, P V of a tile through its two buffers: 1.85 us per chunk of
+// 256 rows (26 drafts: 211 us, 0.75), against 1.33 us of tensor pipe; without the exponentials
+// or the row maximum it takes as long.
 namespace {
 constexpr int kTileBytes = 128 * 128 * 2;      // 128 rows x 128 bf16: two 64-column boxes
 constexpr int kUnitSlots = 4;
