@@ -177,6 +177,65 @@ def test_steps_follow_each_other(graph):
             sv.check(s, PARENTS)
 
 
+FIRST_CALLS_CAPTURED = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+from tests import test_gpu_draft_step as m
+import tensor_linear_layers_gb300 as tl
+h = m.handle(m.NQ, m.NKV, m.T)
+rope = tl.Rope(512, 128)
+blocks, n, ctx = 16, 5, 40
+ck = [torch.randn(h.kv_cache_shape(blocks, m.BS), device="cuda").to(torch.bfloat16) for _ in range(2)]
+cv = [torch.randn(h.kv_cache_shape(blocks, m.BS), device="cuda").to(torch.bfloat16) for _ in range(2)]
+src = torch.randn(m.T, n, m.W, device="cuda").to(torch.bfloat16)
+qkv, rot = torch.zeros_like(src), torch.zeros_like(src)
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+parents, qsl, lens, tab = i32([-1, 0, 0, 1, 2]), i32([0, n]), i32([ctx + n]), i32([[3, 1, 4, 9]])
+pairs, acc, new = i32([[4, 12]]), i32([[0, 2, 4]]), i32([0])
+slots = i32([(ctx + j) % 16 + 16 * [3, 1, 4, 9][(ctx + j) // 16] for j in range(n)])
+mask, pos = torch.zeros(n, 1, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+out = torch.zeros(m.T, n, m.NQ // m.T * 128, dtype=torch.bfloat16, device="cuda")
+ws = torch.zeros(h.tree_attention_workspace_size(1, n, 64), dtype=torch.uint8, device="cuda")
+
+def step():
+    qkv.copy_(src)                       # a copy node in front of a programmatic launch
+    h.kv_cache_copy_blocks(pairs, ck, cv, ws=ws)
+    tl.tree_mask(parents, qsl, lens, n, out=(mask, pos), ws=ws)
+    h.qk_norm_rope(qkv, pos, rope, out=rot, slot_mapping=slots, cache_k=ck[0], cache_v=cv[0], ws=ws)
+    out.zero_()                          # a memset node
+    h.tree_attention(rot, qsl, lens, tab, mask, ck[0], cv[0], n, 64, out=out, ws=ws)
+    h.kv_cache_compact(qsl, lens, acc, tab, tab, ck, cv, out=new, ws=ws)
+
+keep = [x.clone() for x in ck + cv]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+g.replay()
+torch.cuda.synchronize()
+assert int(ws[:4].view(torch.int32)) == 0 and new.tolist() == [ctx + 3]
+a = [out.clone(), rot.clone(), mask.clone(), pos.clone()] + [x.clone() for x in ck + cv]
+for x, k in zip(ck + cv, keep):
+    x.copy_(k)
+step()
+torch.cuda.synchronize()
+for x, y in zip(a, [out, rot, mask, pos] + ck + cv):
+    assert torch.equal(x, y)
+print("captured first: ok")
+"""
+
+
+def test_calls_captured_before_they_ever_ran_and_after_copies():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS_CAPTURED.format(root=root)], cwd=root, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "captured first: ok" in r.stdout, r.stdout + r.stderr
+
+
 def test_two_streams_with_their_own_workspaces():
     a, b = Server([37, 16], N, ACCEPTED, seed=3), Server([50, 90], N, ACCEPTED, seed=4)
     sa, sb = a.buffers(PARENTS), b.buffers(PARENTS)

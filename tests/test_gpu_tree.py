@@ -144,6 +144,7 @@ def test_tree_mask_bad_parents_and_counts():
     (4, 4, 1, [500], [64], 128),                          # one q head per kv head
     (8, 1, 2, [260], [70], 5),                            # 280 rows a shard: three tiles of rows
     (8, 2, 2, [50, 60], [0, 4], 16),                      # a request without drafted tokens
+    (64, 1, 1, [100, 260], [5, 3], 16),                   # one kv head for 64 q heads
 ])
 @pytest.mark.parametrize("gathered", [False, True])
 def test_tree_attention_matches_oracle(nq, nkv, t, ctx, n, bs, gathered):
