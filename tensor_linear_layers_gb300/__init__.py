@@ -177,29 +177,32 @@ def _bf16(t: torch.Tensor, name: str) -> torch.Tensor:
     return t
 
 
-def _i32(t: torch.Tensor, name: str, device: torch.device, numel: int = -1) -> int:
-    """Device pointer of a contiguous int32 tensor on `device` (of `numel` elements at least)."""
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous int32 tensor on {device}")
+_INT32, _BF16 = torch.int32, torch.bfloat16
+
+
+def _i32(t: torch.Tensor, name: str, index: int, numel: int = -1) -> int:
+    """Device pointer of a contiguous int32 tensor on CUDA device `index` (of `numel` elements at least)."""
+    if t.dtype is not _INT32 or t.get_device() != index or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 tensor on cuda:{index}")
     if t.numel() < numel:
         raise ValueError(f"{name} has {t.numel()} elements, {numel} needed")
     return t.data_ptr()
 
 
-def _bf16_on(t: torch.Tensor, name: str, device: torch.device, shape=None) -> int:
-    """Device pointer of a contiguous bf16 tensor on `device` (of this shape)."""
-    if t.dtype != torch.bfloat16 or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous bf16 tensor on {device}")
+def _bf16_on(t: torch.Tensor, name: str, index: int, shape=None) -> int:
+    """Device pointer of a contiguous bf16 tensor on CUDA device `index` (of this shape)."""
+    if t.dtype is not _BF16 or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous bf16 tensor on cuda:{index}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     return t.data_ptr()
 
 
-def _workspace(ws: Optional[torch.Tensor], need: int, device: torch.device) -> torch.Tensor:
+def _workspace(ws: Optional[torch.Tensor], need: int, index: int) -> torch.Tensor:
     if ws is None:
-        return torch.zeros(need, dtype=torch.uint8, device=device)
-    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
+        return torch.zeros(need, dtype=torch.uint8, device=torch.device("cuda", index))
+    if ws.dtype is not torch.uint8 or ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on cuda:{index}")
     return ws
 
 
@@ -251,7 +254,7 @@ class TPLinear:
         self.handle = h
         self._ws = None
         self._ws_sizes = {}
-        self._dev = dev
+        self._dev, self._index = dev, dev.index
         if cfg.kind == TP_BLOCK_ATTN_PROJ:     # per-shard head counts and row widths of qkv and of the attention output
             self._kv_per = 1 if cfg.t >= cfg.n_kv_heads else cfg.n_kv_heads // cfg.t
             q_per = cfg.n_q_heads // cfg.t
@@ -394,7 +397,7 @@ class TPLinear:
             raise ValueError("caches_k and caches_v must list the same layers, one at least")
         self._attention_handle()
         nb, bs, shape = self._cache_shape(caches_k[0])
-        dev, n = self._dev, len(caches_k)
+        dev, n = self._index, len(caches_k)
         both = [*caches_k, *caches_v]
         _bf16_on(both[0], "cache_k", dev, shape)
         # A call names every layer's caches, 64 tensors for 32 layers: the same checks of all of them, one
@@ -403,7 +406,7 @@ class TPLinear:
         if set(map(T.nbytes.__get__, both)) != {first.nbytes} or False in map(T.is_contiguous, both):
             raise ValueError(f"every cache must be a contiguous bf16 tensor of the shape {tuple(shape)}")
         if set(map(T.get_device, both)) != {first.get_device()}:
-            raise ValueError(f"every cache must be on {dev}")
+            raise ValueError(f"every cache must be on cuda:{dev}")
         ptrs = array.array("Q", map(T.data_ptr, both))
         at = ptrs.buffer_info()[0]
         return n, at, at + 8 * n, nb, bs, ptrs
@@ -416,7 +419,7 @@ class TPLinear:
         (int32 [T], negative = none) k and v also go to their cache slots. Returns (out, 16-byte workspace
         whose first word is the status)."""
         self._attention_handle()
-        dev = self._dev
+        dev = self._index
         T, shape = self._rows(qkv, self._qkv_width)
         src = _bf16_on(qkv, "qkv", dev, shape)
         if out is None:
@@ -430,8 +433,7 @@ class TPLinear:
             slots = _i32(slot_mapping, "slot_mapping", dev, T)
             nb, bs, cshape = self._cache_shape(cache_k)
             ck, cv = _bf16_on(cache_k, "cache_k", dev, cshape), _bf16_on(cache_v, "cache_v", dev, cshape)
-        if rope.table.device != dev:
-            raise ValueError(f"the rope table is on {rope.table.device}, not {dev}")
+        rope.check(dev, self._shape[2])
         _check(lib().tp_qk_norm_rope(self.handle, T, src, _bf16_on(out, "out", dev, shape),
                                      _i32(positions, "positions", dev, T), rope.args, slots, ck, cv, nb, bs,
                                      ws.data_ptr(), ws.numel(), _stream_ptr(stream)))
@@ -444,7 +446,7 @@ class TPLinear:
         in the caches of all listed layers. Returns the workspace whose first word is the status."""
         if block_pairs.dim() != 2 or block_pairs.shape[1] != 2:
             raise ValueError("block_pairs must be [n, 2]")
-        dev = self._dev
+        dev = self._index
         n, ks, vs, nb, bs, _hold = self._layer_pointers(caches_k, caches_v)
         ws = _workspace(ws, 16, dev)
         _check(lib().tp_kv_cache_copy_blocks(self.handle, _i32(block_pairs, "block_pairs", dev), block_pairs.shape[0],
@@ -458,13 +460,13 @@ class TPLinear:
         """Move the accepted drafted tokens of every request (accepted int32 [n_reqs, m], rising draft
         indices, ended by -1) from src_tables' pages to the positions after the cached tokens in dst_tables'
         (the same tensor: in place), in the caches of all listed layers. Returns (new lengths, workspace)."""
-        dev = self._dev
+        dev = self._index
         n_reqs = seq_lens.numel()
         if accepted.dim() != 2 or src_tables.dim() != 2 or src_tables.shape != dst_tables.shape:
             raise ValueError("accepted is [n_reqs, m], src_tables and dst_tables [n_reqs, max_blocks]")
         n, ks, vs, nb, bs, _hold = self._layer_pointers(caches_k, caches_v)
         if out is None:
-            out = torch.empty(n_reqs, dtype=torch.int32, device=dev)
+            out = torch.empty(n_reqs, dtype=torch.int32, device=self._dev)
         ws = _workspace(ws, 16, dev)
         mb = src_tables.shape[1]
         _check(lib().tp_kv_cache_compact(
@@ -487,16 +489,16 @@ class TPLinear:
         positions) over its cached tokens and over the drafted ones that their mask rows (tree_mask) name.
         Returns (attn in the attention core's output layout, workspace)."""
         self._attention_handle()
-        dev, n_reqs = self._dev, seq_lens.numel()
+        dev, n_reqs = self._index, seq_lens.numel()
         T, shape = self._rows(qkv, self._qkv_width)
         nb, bs, cshape = self._cache_shape(cache_k)
         t, w = self._shape[0], self._attn_width
         out_shape = (T, t * w) if self._gathered else (t, T, w)
         if out is None:
-            out = torch.empty(out_shape, dtype=torch.bfloat16, device=dev)
+            out = torch.empty(out_shape, dtype=torch.bfloat16, device=self._dev)
         if ws is None:
             ws = torch.zeros(self.tree_attention_workspace_size(n_reqs, max_query_len, max_seq_len),
-                             dtype=torch.uint8, device=dev)
+                             dtype=torch.uint8, device=self._dev)
         if block_tables.dim() != 2 or mask.dim() != 2:
             raise ValueError("block_tables is [n_reqs, max_blocks], mask [T, words]")
         max_blocks, words = block_tables.shape[1], mask.shape[1]
@@ -647,9 +649,10 @@ class TPLayer:
         if rope is None:
             _check(lib().tp_layer_set_rope(self.handle, None, None))
         else:
-            dev = self.attn.w_col.device
-            if positions is None or rope.table.device != dev:
-                raise ValueError(f"set_rope needs positions, and the rope table on {dev}")
+            dev = self.attn._index
+            if positions is None:
+                raise ValueError("set_rope needs positions")
+            rope.check(dev, self.attn.cfg.head_dim)
             _check(lib().tp_layer_set_rope(self.handle, rope.args, _i32(positions, "positions", dev, self.max_tokens)))
         self._rope = (rope, positions)     # borrowed by the handle
 
@@ -690,6 +693,13 @@ class Rope:
     scaling: "none", "linear", "ntk", "bands" or "yarn" (see include/tp_linear.h for the formulas).
     """
 
+    def check(self, index: int, head_dim: int) -> None:
+        """Refuse a use on CUDA device `index` or with heads of `head_dim` elements that it does not fit."""
+        if self.index != index:
+            raise ValueError(f"the rope table is on cuda:{self.index}, not cuda:{index}")
+        if self.gamma_dim not in (0, head_dim):
+            raise ValueError(f"the norms' weights have {self.gamma_dim} elements, heads {head_dim}")
+
     def __init__(self, n_pos: int, rotary_dim: int, base: float = 10000.0, layout: int = TP_ROPE_HALF,
                  scaling: str = "none", factor: float = 1.0, original_max_position: int = 0,
                  low_freq_factor: float = 1.0, high_freq_factor: float = 4.0, beta_slow: float = 1.0,
@@ -706,10 +716,14 @@ class Rope:
                                  device=torch.device("cuda", torch.cuda.current_device()) if device is None else device)
         with torch.cuda.device(self.table.device):
             _check(lib().tp_rope_table(ctypes.byref(self.config), n_pos, self.table.data_ptr(), _stream(stream)))
+        self.index = self.table.get_device()
         for name, g in (("q_gamma", q_gamma), ("k_gamma", k_gamma)):
             if g is not None:
-                _bf16_on(g, name, self.table.device)
-        self.gammas = (q_gamma, k_gamma)
+                _bf16_on(g, name, self.index)
+        dims = {g.numel() for g in (q_gamma, k_gamma) if g is not None}
+        if len(dims) > 1:
+            raise ValueError("q_gamma and k_gamma have different lengths")
+        self.gammas, self.gamma_dim = (q_gamma, k_gamma), dims.pop() if dims else 0
         self.args = RopeArgs(self.table.data_ptr(), n_pos, rotary_dim, layout,
                              None if q_gamma is None else q_gamma.data_ptr(),
                              None if k_gamma is None else k_gamma.data_ptr(), eps)
@@ -720,13 +734,13 @@ def tree_mask(parents: torch.Tensor, query_start_loc: torch.Tensor, seq_lens: to
     """Mask rows and positions of drafted token trees: parents int32 [T], each token's parent among its
     request's drafted tokens (before it) or -1. Returns (mask int32 [T, words], positions int32 [T],
     workspace whose first word is the status); out: (mask, positions) to write instead of new tensors."""
-    dev, T = parents.device, parents.numel()
-    if not parents.is_cuda or dev.index != torch.cuda.current_device():
+    dev, T = parents.get_device(), parents.numel()
+    if dev != torch.cuda.current_device():
         raise TypeError("parents must be a tensor on the current CUDA device")
     words = (max_query_len + 31) // 32
     if out is None:
-        mask = torch.empty(T, words, dtype=torch.int32, device=dev)
-        positions = torch.empty(T, dtype=torch.int32, device=dev)
+        mask = torch.empty(T, words, dtype=torch.int32, device=parents.device)
+        positions = torch.empty(T, dtype=torch.int32, device=parents.device)
     else:
         mask, positions = out
         if mask.dim() != 2 or mask.shape[0] != T:

@@ -252,4 +252,12 @@ def test_refusals():
         h.qk_norm_rope(qkv, pos, r, slot_mapping=pos)
     with pytest.raises(ValueError):
         tl.Rope(64, 128, scaling="spiral")
+    with pytest.raises(ValueError):
+        tl.Rope(64, 128, q_gamma=gamma(128, 0).cuda(), k_gamma=gamma(64, 0).cuda())
+    with pytest.raises(ValueError):                                             # weights of other heads
+        h.qk_norm_rope(qkv, pos, tl.Rope(64, 64, k_gamma=gamma(64, 0).cuda()))
+    with pytest.raises(ValueError):
+        h.qk_norm_rope(qkv, pos, r, out=torch.zeros(1, 4, 7 * 128, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        mlp.qk_norm_rope(qkv, pos, r)
     torch.cuda.synchronize()
