@@ -18,7 +18,9 @@ constexpr int kHd = 128;
 constexpr int kStatusShape = -2;   // TP_ERR_SHAPE
 }  // namespace
 
-// One CTA per (pair, shard) and (layer, k or v): dst page = src page.
+// One CTA per (pair, shard) and (layer, k or v): dst page = src page, 16 bytes a thread. Bound by
+// HBM: 96 pages of 16 tokens, 8 kv heads, 32 layers (403 MB moved) in 61 to 63 us, 0.95 to 0.98
+// of the copy bandwidth; four pages 4.2 us, the launch.
 __global__ void kv_copy_blocks_kernel(const KvLayers layers, const int2* pairs, long long num_blocks, long long page_vecs,
                                       int t, int* status) {
   griddep_wait();
@@ -38,9 +40,11 @@ __global__ void kv_copy_blocks_kernel(const KvLayers layers, const int2* pairs, 
 }
 
 // A request's rows of all layers, k and v, and shards are one line of 16-byte columns; a CTA
-// takes 256 of them and a thread moves its
-// columns of the accepted tokens in their order, eight rows in flight. The CTA first turns
-// the list into pairs of slots, kept in shared memory.
+// takes 256 of them, and a thread moves its column of the accepted tokens in their order, eight
+// rows in flight. The CTA first turns the list into pairs of slots, kept in shared memory.
+// (One CTA per request, layer, k or v and shard: 16 to 32 threads with work, and each read the
+// list for itself; 64 requests of up to 9 tokens, 32 layers, 64 us, this 14 to 18: 74 MB, 0.6 of
+// the copy bandwidth. One request: 3.5 us, the launch and four dependent loads.)
 // Accepted indices rise, so in place (one page holding both positions) position ctx + j is
 // written only after every token up to j has been read, and the tokens after j come from
 // higher positions: no row is lost.

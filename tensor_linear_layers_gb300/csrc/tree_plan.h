@@ -7,9 +7,10 @@
 // which both share: 1.6 us against 1.2 us), and an item kTreeItemCost more before its first
 // chunk for what it costs besides them (its queries, the first products, its output). CTA c
 // of the grid takes the chunks whose first place is in [c * per, (c + 1) * per), so the CTAs
-// have the same work whatever the lengths. Where there is little work (fewer than four chunks
-// per CTA) an item costs nothing besides its chunks: they are spread over as many CTAs as
-// there are. An item that crosses a boundary is computed in parts: CTA c writes the part that
+// have the same work whatever the lengths (32 requests of 256 to 4096 keys: 56.1 us, 59.8 with
+// chunks alone counted). Where there is little work (fewer than four chunks per CTA) an item
+// costs nothing besides its chunks: they are spread over as many CTAs as there are (one request
+// of 508 keys: 13.0 us, 13.7 with the cost). An item that crosses a boundary is computed in parts: CTA c writes the part that
 // continues an item begun by an earlier CTA to slot 2 c, the part that begins one it does not
 // finish to slot 2 c + 1, and the merge kernel joins them in chunk order.
 #pragma once
