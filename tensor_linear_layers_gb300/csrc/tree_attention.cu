@@ -117,9 +117,10 @@ __global__ void __launch_bounds__(kMaxDraft)
 //
 // Up to 128 rows HBM bounds it: a chunk is 64 KB, 1.47 us of one SM's share of the measured copy
 // bandwidth, and takes 1.52 us (2 x 131072 keys, 8 drafts of 64 q heads: 167 us, 0.94). With two
-// tiles it is the chain S, softmax, P V of a tile through its two buffers: 1.85 us per chunk of
-// 256 rows (26 drafts: 211 us, 0.75), against 1.33 us of tensor pipe; without the exponentials
-// or the row maximum it takes as long.
+// tiles shared memory does, 256 KB read by the products (Q again for each half of S) and 64 KB
+// written per chunk, 1.3 us, with the chain S, softmax, P V of a tile through its two buffers:
+// 1.85 us per chunk (26 drafts: 211 us, 0.75); without the exponentials or the row maximum it
+// takes as long.
 namespace {
 constexpr int kTileBytes = 128 * 128 * 2;      // 128 rows x 128 bf16: two 64-column boxes
 constexpr int kUnitSlots = 4;
