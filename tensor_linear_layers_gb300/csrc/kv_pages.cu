@@ -40,15 +40,16 @@ __global__ void kv_copy_blocks_kernel(const KvLayers layers, const int2* pairs, 
 }
 
 // A request's rows of all layers, k and v, and shards are one line of 16-byte columns; a CTA
-// takes 256 of them, and a thread moves its column of the accepted tokens in their order, eight
-// rows in flight. The CTA first turns the list into pairs of slots, kept in shared memory.
+// takes 256 of them, and a thread moves its column of the accepted tokens in their order, four
+// or eight rows in flight. The CTA first turns the list into pairs of slots, kept in shared memory.
 // (One CTA per request, layer, k or v and shard: 16 to 32 threads with work, and each read the
-// list for itself; 64 requests of up to 9 tokens, 32 layers, 64 us, this 14 to 18: 74 MB, 0.6 of
+// list for itself; 64 requests of up to 9 tokens, 32 layers, 64 us, this 17: 74 MB, 0.64 of
 // the copy bandwidth. One request: 3.5 us, the launch and four dependent loads.)
 // Accepted indices rise, so in place (one page holding both positions) position ctx + j is
 // written only after every token up to j has been read, and the tokens after j come from
 // higher positions: no row is lost.
 constexpr int kCompactThreads = 256;
+template <int ROWS>
 __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const KvLayers layers, const CompactParams p,
                                                                      int n_layers, int strips) {
   __shared__ int2 move[kCompactThreads];             // slots (from, to) of a strip of the list
@@ -97,13 +98,13 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const KvLay
     const int n = min(s_stop, p.max_accepted - j0);
     if (error && tid == n && strip == 0) atomicExch(p.status, kStatusShape);   // what ended the list
     if (have) {
-      for (int k0 = 0; k0 < n; k0 += 8) {
-        uint4 v[8];
+      for (int k0 = 0; k0 < n; k0 += ROWS) {
+        uint4 v[ROWS];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < ROWS; ++k)
           if (k0 + k < n) v[k] = cache[(size_t)move[k0 + k].x * vec];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < ROWS; ++k)
           if (k0 + k < n && move[k0 + k].x != move[k0 + k].y) cache[(size_t)move[k0 + k].y * vec] = v[k];
       }
     }
@@ -130,7 +131,12 @@ cudaError_t launch_kv_compact(const KvLayers& layers, int n_layers, const Compac
   if ((long long)n_reqs * strips > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = programmatic(dim3((unsigned)((long long)n_reqs * strips)), kCompactThreads, 0, st, attr);
-  return cudaLaunchKernelEx(&cfg, kv_compact_kernel, layers, p, n_layers, strips);
+  // Eight rows in flight hide the latency while every block is resident (59 registers: four blocks per
+  // SM; 20 requests of 32 layers and up to 9 tokens 6.3 us, with four rows 6.7). Well beyond one wave the
+  // other blocks hide it, and four rows leave room for six (24 such requests 7.6 us, with eight rows
+  // 8.3; 64: 17.1 and 18.3; 64 of up to 3 tokens 8.3 and 10.3; 64 of up to 32: 46.5 and 45.7).
+  const bool many = (long long)n_reqs * strips > 5 * 152;
+  return cudaLaunchKernelEx(&cfg, many ? kv_compact_kernel<4> : kv_compact_kernel<8>, layers, p, n_layers, strips);
 }
 
 }  // namespace tpl

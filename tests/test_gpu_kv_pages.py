@@ -129,6 +129,21 @@ def test_compact(nq, nkv, t, ctx, n, accepted, bs, layers, m, in_place):
         np.testing.assert_array_equal(bits(b), oracle.compact(a, ctx, accepted, c["src"], c["dst"], bs))
 
 
+@pytest.mark.parametrize("in_place", [True, False])
+def test_compact_of_more_blocks_than_one_wave(in_place):
+    h, layers, bs = handle(8, 8, 8), 128, 8   # 128 strips of columns for each of 7 requests
+    rng = np.random.default_rng(71)
+    ctx, n = [0, 3, 8, 13, 29, 40, 1], [9, 12, 8, 20, 17, 0, 5]
+    accepted = [sorted(rng.permutation(k)[:min(k, m)].tolist()) for k, m in zip(n, [4, 5, 8, 17, 0, 3, 1])]
+    c = compact_case(h, ctx, n, accepted, bs, layers, 71, in_place, 20)
+    before = [bits(x) for x in c["ck"] + c["cv"]]
+    new, ws = run_compact(h, c)
+    assert status(ws) == 0
+    assert new.tolist() == [x + len(a) for x, a in zip(ctx, accepted)]
+    for a, b in zip(before, c["ck"] + c["cv"]):
+        np.testing.assert_array_equal(bits(b), oracle.compact(a, ctx, accepted, c["src"], c["dst"], bs))
+
+
 def test_compact_bad_lists_end_there():
     h, bs, ctx = handle(8, 2, 2), 16, [5, 20, 7, 3, 2]
     good = [[0, 2], [1, 3], [0], [1], []]
