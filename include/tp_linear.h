@@ -355,7 +355,8 @@ int tp_paged_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t
  * mask row: bit j % 32 of word tree_mask[i][j / 32] (int32 [T][mask_words], 32 * mask_words
  * >= max_query_len). Any mask is legal, not only a tree's; a token that sees nothing gets 0.
  * What it does not see has no effect on it, NaN and infinities included. Other arguments,
- * layouts, bounds and errors as for tp_paged_attention; max_query_len <= TP_TREE_MAX_DRAFT.
+ * layouts, bounds and errors as for tp_paged_attention; max_query_len <= TP_TREE_MAX_DRAFT,
+ * max_seq_len <= 2^26, attn_out apart from qkv.
  * Rows of attn_out that belong to no request are left as they were. Scores, softmax and
  * sums in fp32, P rounded to bf16 for the P V product, output rounded to bf16. The
  * workspace (tp_tree_attention_workspace_size; caller-owned, ZERO-FILLED before first use)
@@ -386,7 +387,7 @@ int tp_tree_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t*
 /*
  * Pages moved inside the cache, in the caches of n_layers layers (1..TP_KV_MAX_LAYERS) in
  * one launch. caches_k, caches_v: HOST arrays of n_layers device pointers, each a cache of
- * the layout above. Copies, bit-exact. head_dim 128. Status: workspace bytes [0, 4); 16 bytes.
+ * the layout above; no two overlap (layers that share a cache list it once). Copies, bit-exact. head_dim 128. Status: workspace bytes [0, 4); 16 bytes.
  *
  * tp_kv_cache_copy_blocks: for every pair (src, dst) of block_pairs (device int32
  *   [n_pairs][2], 8-byte aligned) block dst = block src, k and v of every shard and layer
@@ -398,7 +399,7 @@ int tp_tree_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t*
  *   [n_reqs][max_accepted]) lists rising draft indices, ended by a negative one or the row's
  *   end. k and v at position ctx + accepted[b][j] of block table src_tables[b] go to position
  *   ctx + j of dst_tables[b] (both int32 [n_reqs][max_blocks_per_req], device), and
- *   new_seq_lens[b] = ctx + the number kept (may not be seq_lens itself). The tables may be
+ *   new_seq_lens[b] = ctx + the number kept (no array that the call reads). The tables may be
  *   the same array (in place); where they differ, a slot that is written is read by no entry
  *   of the call but one that moves within its own request's pages. An index that does not
  *   rise, is past the request's drafts or whose block id is out of range writes TP_ERR_SHAPE

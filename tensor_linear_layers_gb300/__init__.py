@@ -401,11 +401,12 @@ class TPLinear:
         both = [*caches_k, *caches_v]
         _bf16_on(both[0], "cache_k", dev, shape)
         # A call names every layer's caches, 64 tensors for 32 layers: the same checks of all of them, one
-        # attribute at a time (a copy takes bits, so the size in bytes stands for shape and type).
-        T, first = torch.Tensor, both[0]
-        if set(map(T.nbytes.__get__, both)) != {first.nbytes} or False in map(T.is_contiguous, both):
+        # attribute at a time.
+        T = torch.Tensor
+        if (list(map(T.size, both)).count(shape) != len(both) or False in map(T.is_contiguous, both)
+                or set(map(T.dtype.__get__, both)) != {_BF16}):
             raise ValueError(f"every cache must be a contiguous bf16 tensor of the shape {tuple(shape)}")
-        if set(map(T.get_device, both)) != {first.get_device()}:
+        if set(map(T.get_device, both)) != {dev}:
             raise ValueError(f"every cache must be on cuda:{dev}")
         ptrs = array.array("Q", map(T.data_ptr, both))
         at = ptrs.buffer_info()[0]

@@ -1709,6 +1709,16 @@ int tp_tree_mask(int64_t T, int32_t n_reqs, int32_t max_query_len, const int32_t
       return fail(TP_ERR_ARG, "parents, query_start_loc, seq_lens and tree_mask must be 4-byte aligned device arrays");
   if ((reinterpret_cast<uintptr_t>(positions) & 3u) != 0)
     return fail(TP_ERR_ARG, "positions must be null or a 4-byte aligned device array");
+  // requests are read while others are written
+  const int64_t mask_bytes = T * mask_words * 4;
+  const struct { const void* at; int64_t bytes; } in[] = {{parents, 4 * T}, {query_start_loc, 4LL * n_reqs + 4},
+                                                          {seq_lens, 4LL * n_reqs}};
+  for (const auto& x : in)
+    if (ranges_overlap(x.at, x.bytes, tree_mask, mask_bytes) ||
+        (positions != nullptr && ranges_overlap(x.at, x.bytes, positions, 4 * T)))
+      return fail(TP_ERR_ARG, "tree_mask or positions overlaps parents, query_start_loc or seq_lens");
+  if (positions != nullptr && ranges_overlap(tree_mask, mask_bytes, positions, 4 * T))
+    return fail(TP_ERR_ARG, "positions overlaps tree_mask");
   if ((rc = check_status_ws(workspace, workspace_bytes))) return rc;
   const cudaError_t e = launch_tree_mask((int)T, n_reqs, max_query_len, mask_words, parents, query_start_loc, seq_lens,
                                          tree_mask, positions, reinterpret_cast<int*>(workspace),
@@ -1717,9 +1727,12 @@ int tp_tree_mask(int64_t T, int32_t n_reqs, int32_t max_query_len, const int32_t
   return ok();
 }
 
-// Tree attention: at most one CTA per SM, no more than there are chunks of keys. Workspace: the
+// Tree attention: at most one CTA per SM, no more than there are chunks of keys. The places of a
+// head's items (up to 256 tokens x the group's q heads in groups of 256 rows) are counted in 32
+// bits, so a request has at most 2^26 tokens. Workspace: the
 // status word, the item each CTA leaves unfinished, two partial slots per CTA.
 namespace {
+constexpr int kTreeMaxSeq = 1 << 26;
 struct TreePlan {
   int grid, part_rows;
   int64_t partials_off, ws_bytes;
@@ -1746,6 +1759,7 @@ int tp_tree_attention_workspace_size(const tp_linear_t* h, int32_t n_reqs, int32
     return fail(TP_ERR_SHAPE, "need n_reqs >= 1 and 1 <= max_query_len <= max_seq_len");
   if (max_query_len > TP_TREE_MAX_DRAFT)
     return fail(TP_ERR_UNSUPPORTED, "more than %d drafted tokens per request", TP_TREE_MAX_DRAFT);
+  if (max_seq_len > kTreeMaxSeq) return fail(TP_ERR_UNSUPPORTED, "more than %d tokens per request", kTreeMaxSeq);
   *bytes = tree_plan(h, n_reqs, max_query_len, max_seq_len).ws_bytes;
   return ok();
 }
@@ -1763,6 +1777,7 @@ int tp_tree_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t*
     return fail(TP_ERR_SHAPE, "need n_reqs >= 1 and 1 <= max_query_len <= max_seq_len");
   if (max_query_len > TP_TREE_MAX_DRAFT)
     return fail(TP_ERR_UNSUPPORTED, "more than %d drafted tokens per request", TP_TREE_MAX_DRAFT);
+  if (max_seq_len > kTreeMaxSeq) return fail(TP_ERR_UNSUPPORTED, "more than %d tokens per request", kTreeMaxSeq);
   if (mask_words < 1 || mask_words > 65536 || (int64_t)mask_words * 32 < max_query_len)
     return fail(TP_ERR_SHAPE, "mask_words does not cover max_query_len bits");
   if ((rc = check_cache_size(h, num_blocks, block_size))) return rc;
@@ -1781,6 +1796,8 @@ int tp_tree_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t*
   if (workspace_bytes < pl.ws_bytes)
     return fail(TP_ERR_ARG, "workspace too small: %lld bytes, %lld needed", (long long)workspace_bytes,
                 (long long)pl.ws_bytes);
+  if (ranges_overlap(qkv, h->cfg.t * T * h->ws_qkv * 2, attn_out, h->cfg.t * T * h->Ks * 2))
+    return fail(TP_ERR_ARG, "attn_out overlaps qkv");
   if ((rc = check_device(h))) return rc;
   const bool gath = gathered(h);
   TreeAttnParams p{};
@@ -1821,16 +1838,25 @@ int tp_tree_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t*
 }
 
 // ============================================================================ pages of the cache
-static int gather_layers(int32_t n_layers, void* const* caches_k, void* const* caches_v, KvLayers* out) {
+static int gather_layers(const tp_linear_t* h, int32_t n_layers, void* const* caches_k, void* const* caches_v,
+                         int64_t num_blocks, int32_t block_size, KvLayers* out) {
   if (n_layers < 1) return fail(TP_ERR_SHAPE, "n_layers must be >= 1");
   if (n_layers > TP_KV_MAX_LAYERS) return fail(TP_ERR_UNSUPPORTED, "more than %d layers in one call", TP_KV_MAX_LAYERS);
   if (caches_k == nullptr || caches_v == nullptr) return fail(TP_ERR_ARG, "caches_k or caches_v is null");
+  uintptr_t at[2 * TP_KV_MAX_LAYERS];
   for (int i = 0; i < n_layers; ++i) {
     TP_CHECK_PTR(caches_k[i], "caches_k[i]");
     TP_CHECK_PTR(caches_v[i], "caches_v[i]");
     out->k[i] = caches_k[i];
     out->v[i] = caches_v[i];
+    at[2 * i] = reinterpret_cast<uintptr_t>(caches_k[i]);
+    at[2 * i + 1] = reinterpret_cast<uintptr_t>(caches_v[i]);
   }
+  // A cache listed twice would have its rows moved by two CTAs at once, one reading what the other wrote.
+  std::sort(at, at + 2 * n_layers);
+  const uintptr_t bytes = (uintptr_t)(h->cfg.t * num_blocks * block_size * h->kv_per) * 128 * 2;
+  for (int i = 1; i < 2 * n_layers; ++i)
+    if (at[i] - at[i - 1] < bytes) return fail(TP_ERR_ARG, "two of the caches overlap");
   return TP_OK;
 }
 
@@ -1844,7 +1870,7 @@ int tp_kv_cache_copy_blocks(tp_linear_t* h, const int32_t* block_pairs, int32_t 
   if ((rc = check_cache_size(h, num_blocks, block_size))) return rc;
   if (n_pairs == 0) return ok();
   KvLayers layers{};
-  if ((rc = gather_layers(n_layers, caches_k, caches_v, &layers))) return rc;
+  if ((rc = gather_layers(h, n_layers, caches_k, caches_v, num_blocks, block_size, &layers))) return rc;
   if (block_pairs == nullptr || (reinterpret_cast<uintptr_t>(block_pairs) & 7u) != 0)
     return fail(TP_ERR_ARG, "block_pairs is null or not 8-byte aligned");
   if ((rc = check_status_ws(workspace, workspace_bytes)) || (rc = check_device(h))) return rc;
@@ -1868,13 +1894,18 @@ int tp_kv_cache_compact(tp_linear_t* h, int32_t n_reqs, const int32_t* query_sta
   if ((rc = check_cache_size(h, num_blocks, block_size))) return rc;
   if (n_reqs == 0) return ok();
   KvLayers layers{};
-  if ((rc = gather_layers(n_layers, caches_k, caches_v, &layers))) return rc;
+  if ((rc = gather_layers(h, n_layers, caches_k, caches_v, num_blocks, block_size, &layers))) return rc;
   for (const int32_t* q : {query_start_loc, seq_lens, accepted, src_tables, dst_tables, (const int32_t*)new_seq_lens})
     if (!aligned4(q))
       return fail(TP_ERR_ARG, "query_start_loc, seq_lens, accepted, src_tables, dst_tables and new_seq_lens must be "
                               "4-byte aligned device arrays");
-  if (ranges_overlap(seq_lens, 4LL * n_reqs, new_seq_lens, 4LL * n_reqs))
-    return fail(TP_ERR_ARG, "new_seq_lens overlaps seq_lens");
+  const int64_t accepted_bytes = 4LL * n_reqs * max_accepted, table_bytes = 4LL * n_reqs * max_blocks_per_req;
+  const struct { const void* at; int64_t bytes; } in[] = {{query_start_loc, 4LL * n_reqs + 4}, {seq_lens, 4LL * n_reqs},
+                                                          {accepted, accepted_bytes}, {src_tables, table_bytes},
+                                                          {dst_tables, table_bytes}};
+  for (const auto& x : in)
+    if (ranges_overlap(x.at, x.bytes, new_seq_lens, 4LL * n_reqs))
+      return fail(TP_ERR_ARG, "new_seq_lens overlaps an array that the call reads");
   if ((rc = check_status_ws(workspace, workspace_bytes)) || (rc = check_device(h))) return rc;
   CompactParams p{};
   p.qsl = query_start_loc;

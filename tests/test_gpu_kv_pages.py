@@ -217,3 +217,35 @@ def test_refusals():
         h.kv_cache_copy_blocks(dev([(0, 1)]), [ck[0], ck[1][:, :2]], cv)
     with pytest.raises(TypeError):
         h.kv_cache_copy_blocks(dev([(0, 1)]).long(), ck, cv)
+
+
+def test_refusals_of_caches_that_differ_or_overlap():
+    h, L, p = handle(8, 2, 2), tl.lib(), ctypes.c_void_p(0x10000)
+    size = 2 * 8 * 16 * 1 * 128 * 2                          # bytes of a cache: t, blocks, block size, kv heads, hd
+
+    def arr(*at):
+        return (ctypes.c_void_p * len(at))(*at)
+
+    def both(ck, cv, new=0x20000):
+        copy = L.tp_kv_cache_copy_blocks(h.handle, p, 1, len(ck), ck, cv, 8, 16, p, 16, None)
+        comp = L.tp_kv_cache_compact(h.handle, 1, p, p, p, 4, p, p, 4, len(ck), ck, cv, 8, 16, ctypes.c_void_p(new), p, 16,
+                                     None)
+        return copy, comp
+    a = 1 << 24
+    for ck, cv in [(arr(a), arr(a)), (arr(a, a), arr(a + size, a + 2 * size)),
+                   (arr(a, a + 4 * size), arr(a + 2 * size, a + size - 16)), (arr(a + size - 16), arr(a))]:
+        assert both(ck, cv) == (tl.TP_ERR_ARG,) * 2 and b"overlap" in L.tp_last_error()
+    for new in (0x10000, 0x10004):                           # inside what the call reads
+        comp = L.tp_kv_cache_compact(h.handle, 1, ctypes.c_void_p(0x10000), ctypes.c_void_p(0x30000), ctypes.c_void_p(0x40000),
+                                     4, ctypes.c_void_p(0x50000), ctypes.c_void_p(0x60000), 4, 1, arr(a), arr(a + size), 8,
+                                     16, ctypes.c_void_p(new), p, 16, None)
+        assert comp == tl.TP_ERR_ARG and b"new_seq_lens" in L.tp_last_error()
+    ck, cv = caches(h, 2, 4, 16, 1)
+    pairs = dev([(0, 1)])
+    same_bytes = torch.zeros(h.kv_cache_shape(8, 8), dtype=torch.bfloat16, device="cuda")
+    for other in (same_bytes, ck[1].view(torch.float16), ck[1].view(torch.int16), ck[1].transpose(1, 2), ck[1].cpu()):
+        for k, v in (([ck[0], other], cv), (ck, [cv[0], other])):
+            with pytest.raises(ValueError):
+                h.kv_cache_copy_blocks(pairs, k, v)
+    with pytest.raises(tl.TPError):
+        h.kv_cache_copy_blocks(pairs, [ck[0], ck[0]], cv)

@@ -378,3 +378,28 @@ def test_refusals():
         run(h, c, mask=torch.zeros(2, 1, dtype=torch.int32, device="cuda"))
     with pytest.raises(ValueError):
         run(h, dict(c, ck=c["ck"][:, :, :, :, :64]))
+
+
+def test_refusals_of_outputs_over_inputs_and_of_long_requests():
+    h, L, n = handle(8, 2, 2), tl.lib(), ctypes.c_int64()
+
+    def at(x):
+        return ctypes.c_void_p(x)
+    p, ws_bytes = at(0x10000), 1 << 40
+    width = h.kv_cache_shape(1, 1)[0] * 8 * (4 + 2) * 128 * 2    # an upper bound on the bytes of 8 rows of qkv
+
+    def attention(out, ml=64, mb=4, bs=16):
+        return L.tp_tree_attention(h.handle, 8, at(1 << 24), p, p, 2, 4, ml, p, mb, p, 1, p, p, 8, bs, at(out), p, ws_bytes,
+                                   None)
+    for out in (1 << 24, (1 << 24) + 256, (1 << 24) - 256):
+        assert width > 256 and attention(out) == tl.TP_ERR_ARG and b"overlaps" in L.tp_last_error()
+    long = (1 << 26) + 1
+    assert attention(1 << 20, ml=long, mb=1 << 23) == tl.TP_ERR_UNSUPPORTED
+    assert L.tp_tree_attention_workspace_size(h.handle, 1, 1, long, ctypes.byref(n)) == tl.TP_ERR_UNSUPPORTED
+    assert L.tp_tree_attention_workspace_size(h.handle, 1, 1, long - 1, ctypes.byref(n)) == tl.TP_OK
+
+    def mask(parents=0x10000, qsl=0x20000, lens=0x30000, out=0x40000, pos=0x50000):
+        return L.tp_tree_mask(8, 2, 4, at(parents), at(qsl), at(lens), at(out), 1, at(pos), at(0x60000), 16, None)
+    for k, v in (("out", 0x10000), ("out", 0x20008), ("out", 0x30004), ("pos", 0x10004), ("pos", 0x20008),
+                 ("pos", 0x2fffc), ("pos", 0x40010)):
+        assert mask(**{k: v}) == tl.TP_ERR_ARG and b"overlaps" in L.tp_last_error()
