@@ -19,9 +19,9 @@ namespace tpl {
 
 namespace {
 constexpr int kStatusShape = -2;   // TP_ERR_SHAPE
-// steps of a warp in flight, its CTAs per SM: 3, 3 is within 2 % of the best of (2, 3), (2, 4),
-// (3, 2), (4, 2) with norm, without it, and with half the head rotated
-constexpr int kUnroll = 3, kMinCtas = 3;
+// steps of a warp in flight, warps per SM (80 registers): 4096 tokens of 48 heads with norm 23.5 us;
+// (2, 32) 27.3, (4, 20) 24.0, (4, 24) 24.5, (6, 16) 26.0
+constexpr int kUnroll = 3, kMinCtas = 25;
 
 // two bf16 of a word as a pair of fp32, and back (rounded to nearest even)
 __device__ __forceinline__ uint64_t unpack2(uint32_t w) {
@@ -202,19 +202,18 @@ __device__ __forceinline__ void store_pieces(__nv_bfloat16* dst, const Pieces& q
 // in steps of 32 / G, first the q heads of all shards, then the k heads, then the v heads, so
 // that a step is of one kind (steps that mixed them ran both ways: 27.4 against 24.6 us for
 // 4096 tokens of 48 heads with norm). A warp takes up to kUnroll steps of one token, loaded together:
-// a lane's cosines, sines and weights serve all of them. Warps are short and many, which fills
-// the SMs evenly; few tokens get a step per warp (latency). Tried and dropped: persistent warps
-// with a ring of bulk copies in shared memory (8192 tokens of 80 heads 65.9 against 64.4 us,
-// 2048 tokens 19.0 against 15.7).
+// a lane's cosines, sines and weights serve all of them. A warp is a CTA: each ends and makes room
+// for the next by itself (4096 tokens of 48 heads with norm 23.5 us, 25.6 with eight warps to a CTA,
+// 25.2 with four or two; 8192 tokens of 80 heads 61.5, 64.4, 62.8, 62.1), 0.75 and 0.90 of HBM. Tried
+// and dropped: persistent warps with a ring of bulk copies in shared memory (8192 tokens of 80 heads
+// 65.9 us, 2048 tokens of 48 heads 19.0 against 13.8).
 template <int G, int MODE, bool NORM>
-__global__ void __launch_bounds__(256, kMinCtas) qk_norm_rope_kernel(const RopeParams p, int steps, int parts) {
+__global__ void __launch_bounds__(32, kMinCtas) qk_norm_rope_kernel(const RopeParams p, int steps, int parts) {
   constexpr int HPW = 32 / G;                        // heads of a step
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const unsigned wid = blockIdx.x * 8u + (threadIdx.x >> 5);
-  const int i = (int)(wid / (unsigned)parts), part = (int)(wid - (unsigned)i * (unsigned)parts);
-  if (i >= p.T) return;
+  const int lane = threadIdx.x;
+  const int i = (int)(blockIdx.x / (unsigned)parts), part = (int)(blockIdx.x - (unsigned)i * (unsigned)parts);
   const int sub = lane / G, l = lane % G;
   const Pieces q = pieces_of<MODE>(l, p.hd, p.rd);
   const int pos = p.pos[i];
@@ -253,8 +252,8 @@ __global__ void __launch_bounds__(256, kMinCtas) qk_norm_rope_kernel(const RopeP
   }
   if (slot >= p.n_slots && p.slots != nullptr && lane == 0) atomicExch(p.status, kStatusShape);
   const bool write = slot >= 0 && slot < p.n_slots;
-  __shared__ float heads_s[MODE == kHalfAny ? 8 : 1][MODE == kHalfAny ? 512 : 1];   // a warp's heads: 16 elements a lane
-  float* xs = MODE == kHalfAny ? heads_s[threadIdx.x >> 5] + 16 * G * sub : nullptr;
+  __shared__ float heads_s[MODE == kHalfAny ? 512 : 1];   // 16 elements a lane
+  float* xs = MODE == kHalfAny ? heads_s + 16 * G * sub : nullptr;
   const float* tab = p.table + (size_t)pos * p.rd;
   float c[8], s[8];
   if (MODE != kHalfAny) load_angles(c, s, tab + 8 * l, p.rd, q.rot);
@@ -284,13 +283,13 @@ cudaError_t launch_rope_table(const RopeFreqs& f, long long n_pos, int rotary_di
 template <int G>
 static cudaError_t launch_heads(const RopeParams& p, int nsm, cudaStream_t st) {
   constexpr int HPW = 32 / G;
-  // the steps of a token: kUnroll per warp, fewer where that leaves SMs without work (48 heads
-  // with norm: 32 tokens 3.1 us with one step, 4.2 with three; 512 tokens 4.8 with two, 5.5
-  // either way; 4096 tokens 25.3 with three, 34.2 with one)
+  // the steps of a token: kUnroll per warp, fewer where that leaves SMs without work, until there are
+  // eight warps for each (64 tokens of 80 heads 2.8 us, with a bound of four 3.4; 384 tokens of 48 heads
+  // with norm 4.8, with 16 6.2; 512 tokens 5.1, with 28 7.6; 1024 tokens 6.9, with 48 13.7)
   const int q_steps = (p.t * p.q_per + HPW - 1) / HPW, kv_steps = (p.t * p.kv_per + HPW - 1) / HPW;
   const int total = q_steps + (p.in == p.out && p.slots == nullptr ? 1 : 2) * kv_steps;
   int steps = kUnroll;
-  while (steps > 1 && (long long)p.T * ((total + steps - 1) / steps) < 16LL * nsm) --steps;
+  while (steps > 1 && (long long)p.T * ((total + steps - 1) / steps) < 8LL * nsm) --steps;
   const int parts = (total + steps - 1) / steps;
   const long long warps = (long long)p.T * parts;
   if (warps > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
@@ -299,7 +298,7 @@ static cudaError_t launch_heads(const RopeParams& p, int nsm, cudaStream_t st) {
                 : p.rd % 16 == 0 ? (norm ? qk_norm_rope_kernel<G, kHalf, true> : qk_norm_rope_kernel<G, kHalf, false>)
                                  : (norm ? qk_norm_rope_kernel<G, kHalfAny, true> : qk_norm_rope_kernel<G, kHalfAny, false>);
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = programmatic(dim3((unsigned)((warps + 7) / 8)), 256, 0, st, attr);
+  const cudaLaunchConfig_t cfg = programmatic(dim3((unsigned)warps), 32, 0, st, attr);
   return cudaLaunchKernelEx(&cfg, kernel, p, steps, parts);
 }
 
