@@ -16,6 +16,7 @@
 
 #include "gemm_tc.cuh"
 #include "internal.h"
+#include "tree_plan.h"
 #include "tp_linear.h"
 
 namespace tpl {
@@ -1739,9 +1740,8 @@ struct TreePlan {
 };
 TreePlan tree_plan(const tp_linear* h, int n_reqs, int max_query_len, int max_seq_len) {
   const int max_rows = max_query_len * (h->q_per / h->kv_per), rows = tree_group_rows(max_rows);
-  const int64_t chunks = (int64_t)n_reqs * h->cfg.t * h->kv_per * ceil_div(max_rows, rows) * ceil_div(max_seq_len, 128);
   TreePlan pl{};
-  pl.grid = (int)std::min<int64_t>(h->nsm, chunks);
+  pl.grid = tree_grid(h->nsm, n_reqs, h->cfg.t * h->kv_per, max_rows, rows, max_seq_len);
   pl.part_rows = (std::min(rows, max_rows) + 7) / 8 * 8;    // a slot is a multiple of 32 bytes (32-byte stores)
   pl.partials_off = align256(256 + (int64_t)sizeof(TreeItem) * pl.grid);
   // the workspace itself is 16-byte aligned: room to start the slots on a 32-byte boundary

@@ -444,6 +444,7 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
       };
       // all requests' chunks and heads' places with an item cost of 0 and of 1 apart; CTA 0 reports bad counts
       long long chunks = 0, places = 0, items = 0;
+      int widest = 1;
       for (int b0 = 0; b0 < p.n_reqs; b0 += 32 * kStrips) {
         if (b0 > 0) load_batch(b0);
 #pragma unroll
@@ -453,11 +454,12 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
           chunks += (long long)q.groups * q.chunks;
           places += tree_head(q, 0);
           items += q.groups;
+          widest = max(widest, tree_widest(q));
         }
       }
       cost = tree_cost(heads * sum(chunks), gridDim.x);
       const long long total = heads * sum(places + cost * items);
-      const long long per = tree_per(total, gridDim.x);
+      const long long per = tree_per(total, gridDim.x, __reduce_max_sync(0xffffffffu, widest));
       long long pos = per * blockIdx.x;
       const long long end = min(total, pos + per);
       // the request that holds the first place, and the places before it

@@ -8,12 +8,16 @@
 // chunk for what it costs besides them (its queries, the first products, its output). CTA c
 // of the grid takes the chunks whose first place is in [c * per, (c + 1) * per), so the CTAs
 // have the same work whatever the lengths (32 requests of 256 to 4096 keys: 56.1 us, 59.8 with
-// chunks alone counted). Where there is little work (fewer than four chunks per CTA) an item
+// chunks alone counted). A CTA has at least the places of the call's widest chunk: with fewer,
+// a CTA inside an item could hold no chunk's first place, and so leave its slot unwritten for
+// the merge, which reads the slots of all CTAs from an item's first to its last. Where there is little work (fewer than four chunks per CTA) an item
 // costs nothing besides its chunks: they are spread over as many CTAs as there are (one request
 // of 508 keys: 13.0 us, 13.7 with the cost). An item that crosses a boundary is computed in parts: CTA c writes the part that
 // continues an item begun by an earlier CTA to slot 2 c, the part that begins one it does not
 // finish to slot 2 c + 1, and the merge kernel joins them in chunk order.
 #pragma once
+
+#include <algorithm>
 
 #ifdef __CUDACC__
 #define TPL_HD __host__ __device__ __forceinline__
@@ -26,6 +30,15 @@ namespace tpl {
 constexpr int kTreeChunk = 128;   // keys of one chunk
 
 constexpr int kTreeItemCost = 4;  // places
+constexpr int kTreeWidest = 4;    // places of the widest chunk there is (two tiles of rows)
+
+// CTAs of the grid: one per SM, no more than a call of these bounds has chunks. heads: kv heads over
+// all shards; max_rows: query rows of one of them; rows_per_group: those of one item.
+inline int tree_grid(int nsm, int n_reqs, int heads, int max_rows, int rows_per_group, int max_seq_len) {
+  const long long groups = (max_rows + rows_per_group - 1) / rows_per_group;
+  const long long chunks = (long long)n_reqs * heads * groups * ((max_seq_len + kTreeChunk - 1) / kTreeChunk);
+  return (int)std::min<long long>(nsm, chunks);
+}
 
 struct TreeReq {
   int q0, n, len, chunks, groups;
@@ -52,9 +65,18 @@ TPL_HD long long tree_head(const TreeReq& r, int cost) {
   return r.groups > 0 ? (long long)(r.groups - 1) * (cost + r.chunks * r.full) + cost + r.chunks * r.last : 0;
 }
 
+// Places of the widest chunk of a request (0: no work).
+TPL_HD int tree_widest(const TreeReq& r) { return r.groups > 1 ? r.full : r.groups > 0 ? r.last : 0; }
+
 // What an item costs besides its chunks, and the places per CTA.
 TPL_HD int tree_cost(long long chunks, int grid) { return chunks >= 4LL * grid ? kTreeItemCost : 0; }
-TPL_HD long long tree_per(long long total, int grid) { return total > 0 ? (total + grid - 1) / grid : 1; }
+// widest: the most places that a chunk of any request takes (tree_widest). Where all chunks take as
+// many, each still has a CTA of its own when there are CTAs enough; held to the widest chunk there
+// is, chunks of three places would go two to some CTAs.
+TPL_HD long long tree_per(long long total, int grid, int widest = kTreeWidest) {
+  const long long even = (total + grid - 1) / grid;
+  return even > widest ? even : widest;
+}
 
 struct TreeSeg {
   int head, group;
