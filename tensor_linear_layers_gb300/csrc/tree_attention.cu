@@ -583,6 +583,7 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
               }
             }
             bad = __any_sync(0xffffffffu, bad);
+            __syncwarp();                             // every lane's stores, before lane 0 hands the tile on
             if (lane == 0) {
               if (bad) *reinterpret_cast<volatile int*>(&s_seg[slot].bad) = 1;
               mbar_arrive_n(bar(C::FULL + ring), 128);   // for the copying threads
