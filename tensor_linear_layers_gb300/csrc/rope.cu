@@ -163,14 +163,20 @@ __device__ __forceinline__ void turn(uint4& a, uint4& b, const Pieces& q, const 
     }
     __syncwarp();                                    // read before the next step writes
   } else if (MODE == kInterleaved) {
-    // the pairs of piece a are 8 l .. 8 l + 3, of piece b 8 l + 4 .. 8 l + 7
+    // the pairs of piece a are 8 l .. 8 l + 3, of piece b 8 l + 4 .. 8 l + 7; those past the rotated
+    // ones stay as they are (turned by an angle of 0, an infinite element would make its partner NaN).
+    // Both results and a selection: 2043 tokens of 36 heads with norm, half of each rotated, 10.0 us;
+    // branches on the lane's rotated pairs 10.1, everything turned 9.8
+    auto turned = [&](uint64_t v, int k) {
+      float e0, e1;
+      f32x2_unpack(v, e0, e1);
+      return f32x2_pack(e0 * c[k] - e1 * s[k], e1 * c[k] + e0 * s[k]);
+    };
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      float x0, x1, y0, y1;
-      f32x2_unpack(x[k], x0, x1);
-      f32x2_unpack(y[k], y0, y1);
-      x[k] = f32x2_pack(x0 * c[k] - x1 * s[k], x1 * c[k] + x0 * s[k]);
-      y[k] = f32x2_pack(y0 * c[4 + k] - y1 * s[4 + k], y1 * c[4 + k] + y0 * s[4 + k]);
+      const uint64_t tx = turned(x[k], k), ty = turned(y[k], 4 + k);
+      x[k] = k < q.rot ? tx : x[k];
+      y[k] = 4 + k < q.rot ? ty : y[k];
     }
   } else if (q.rot) {
 #pragma unroll
