@@ -198,9 +198,22 @@ def _bf16_on(t: torch.Tensor, name: str, index: int, shape=None) -> int:
     return t.data_ptr()
 
 
-def _workspace(ws: Optional[torch.Tensor], need: int, index: int) -> torch.Tensor:
+def _new(shape, dtype: torch.dtype, device, stream, zero: bool = False) -> torch.Tensor:
+    """A tensor for work on `stream` (None: the current one), allocated and zeroed in that stream's order: a fill
+    on another stream could come after the kernels, and its memory go to other work while they run. The caller
+    has it on the current stream, so its memory is not given away before what runs there either."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        x = make(shape, dtype=dtype, device=device)
+    x.record_stream(torch.cuda.current_stream(device))
+    return x
+
+
+def _workspace(ws: Optional[torch.Tensor], need: int, index: int, stream) -> torch.Tensor:
     if ws is None:
-        return torch.zeros(need, dtype=torch.uint8, device=torch.device("cuda", index))
+        return _new(need, torch.uint8, torch.device("cuda", index), stream, zero=True)
     if ws.dtype is not torch.uint8 or ws.get_device() != index or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous uint8 tensor on cuda:{index}")
     return ws
@@ -424,8 +437,8 @@ class TPLinear:
         T, shape = self._rows(qkv, self._qkv_width)
         src = _bf16_on(qkv, "qkv", dev, shape)
         if out is None:
-            out = torch.empty_like(qkv)
-        ws = _workspace(ws, 16, dev)
+            out = _new(qkv.shape, qkv.dtype, self._dev, stream)
+        ws = _workspace(ws, 16, dev, stream)
         ck = cv = slots = None
         nb = bs = 0
         if slot_mapping is not None:
@@ -449,7 +462,7 @@ class TPLinear:
             raise ValueError("block_pairs must be [n, 2]")
         dev = self._index
         n, ks, vs, nb, bs, _hold = self._layer_pointers(caches_k, caches_v)
-        ws = _workspace(ws, 16, dev)
+        ws = _workspace(ws, 16, dev, stream)
         _check(lib().tp_kv_cache_copy_blocks(self.handle, _i32(block_pairs, "block_pairs", dev), block_pairs.shape[0],
                                              n, ks, vs, nb, bs, ws.data_ptr(), ws.numel(), _stream_ptr(stream)))
         return ws
@@ -467,8 +480,8 @@ class TPLinear:
             raise ValueError("accepted is [n_reqs, m], src_tables and dst_tables [n_reqs, max_blocks]")
         n, ks, vs, nb, bs, _hold = self._layer_pointers(caches_k, caches_v)
         if out is None:
-            out = torch.empty(n_reqs, dtype=torch.int32, device=self._dev)
-        ws = _workspace(ws, 16, dev)
+            out = _new(n_reqs, torch.int32, self._dev, stream)
+        ws = _workspace(ws, 16, dev, stream)
         mb = src_tables.shape[1]
         _check(lib().tp_kv_cache_compact(
             self.handle, n_reqs, _i32(query_start_loc, "query_start_loc", dev, n_reqs + 1),
@@ -496,10 +509,9 @@ class TPLinear:
         t, w = self._shape[0], self._attn_width
         out_shape = (T, t * w) if self._gathered else (t, T, w)
         if out is None:
-            out = torch.empty(out_shape, dtype=torch.bfloat16, device=self._dev)
-        if ws is None:
-            ws = torch.zeros(self.tree_attention_workspace_size(n_reqs, max_query_len, max_seq_len),
-                             dtype=torch.uint8, device=self._dev)
+            out = _new(out_shape, torch.bfloat16, self._dev, stream)
+        need = self.tree_attention_workspace_size(n_reqs, max_query_len, max_seq_len) if ws is None else 0
+        ws = _workspace(ws, need, dev, stream)
         if block_tables.dim() != 2 or mask.dim() != 2:
             raise ValueError("block_tables is [n_reqs, max_blocks], mask [T, words]")
         max_blocks, words = block_tables.shape[1], mask.shape[1]
@@ -509,7 +521,7 @@ class TPLinear:
             max_query_len, max_seq_len, _i32(block_tables, "block_tables", dev, n_reqs * max_blocks), max_blocks,
             _i32(mask, "mask", dev, T * words), words, _bf16_on(cache_k, "cache_k", dev, cshape),
             _bf16_on(cache_v, "cache_v", dev, cshape), nb, bs, _bf16_on(out, "out", dev, out_shape),
-            _workspace(ws, 0, dev).data_ptr(), ws.numel(), _stream_ptr(stream)))
+            ws.data_ptr(), ws.numel(), _stream_ptr(stream)))
         return out, ws
 
     def kv_cache_write(self, qkv: torch.Tensor, slot_mapping: torch.Tensor, cache_k: torch.Tensor,
@@ -692,6 +704,7 @@ class Rope:
     layout of the rotated pairs and the gammas of the q and k heads' norms (bf16 [head_dim] or None).
 
     scaling: "none", "linear", "ntk", "bands" or "yarn" (see include/tp_linear.h for the formulas).
+    stream: where the table is built; uses on other streams come after that.
     """
 
     def check(self, index: int, head_dim: int) -> None:
@@ -713,8 +726,9 @@ class Rope:
         rope_frequencies(self.config)      # refuses a bad configuration before anything is allocated
         if n_pos < 1:
             raise ValueError("n_pos must be >= 1")
-        self.table = torch.empty(n_pos, rotary_dim, dtype=torch.float32,
-                                 device=torch.device("cuda", torch.cuda.current_device()) if device is None else device)
+        if device is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        self.table = _new((n_pos, rotary_dim), torch.float32, device, stream)
         with torch.cuda.device(self.table.device):
             _check(lib().tp_rope_table(ctypes.byref(self.config), n_pos, self.table.data_ptr(), _stream(stream)))
         self.index = self.table.get_device()
@@ -740,15 +754,15 @@ def tree_mask(parents: torch.Tensor, query_start_loc: torch.Tensor, seq_lens: to
         raise TypeError("parents must be a tensor on the current CUDA device")
     words = (max_query_len + 31) // 32
     if out is None:
-        mask = torch.empty(T, words, dtype=torch.int32, device=parents.device)
-        positions = torch.empty(T, dtype=torch.int32, device=parents.device)
+        mask = _new((T, words), torch.int32, parents.device, stream)
+        positions = _new(T, torch.int32, parents.device, stream)
     else:
         mask, positions = out
         if mask.dim() != 2 or mask.shape[0] != T:
             raise ValueError("the mask is [T, words]")
         words = mask.shape[1]
     n_reqs = seq_lens.numel()
-    ws = _workspace(ws, 16, dev)
+    ws = _workspace(ws, 16, dev, stream)
     _check(lib().tp_tree_mask(T, n_reqs, max_query_len, _i32(parents, "parents", dev),
                               _i32(query_start_loc, "query_start_loc", dev, n_reqs + 1),
                               _i32(seq_lens, "seq_lens", dev), _i32(mask, "mask", dev), words,

@@ -1,0 +1,114 @@
+"""The tensors that a call makes for itself (outputs, workspaces, tables) belong to the stream that it was given.
+
+On the CPU, with the library and torch's streams replaced: each is allocated, and where need be zeroed, with the
+call's stream current, so that neither the fill nor other work in the same memory can meet the kernels; and each is
+marked as used by the stream the caller is on.
+"""
+import contextlib
+
+import pytest
+import torch
+
+import tensor_linear_layers_gb300 as tl
+
+CALLER = "the caller's stream"
+
+
+class FakeStream:
+    cuda_stream = 0x1234
+
+
+class FakeLib:
+    def __getattr__(self, name):
+        def call(*args):
+            if name.endswith(("workspace_size", "packed_weight_bytes")):
+                for a in args:
+                    if hasattr(a, "_obj"):
+                        a._obj.value = 64
+            return 0
+        return call
+
+
+@pytest.fixture
+def made(monkeypatch):
+    """[(stream current at the allocation, streams recorded on the tensor)] of what the calls make."""
+    log, current, recorded = [], [CALLER], {}
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, current[0] = current[0], stream
+        yield
+        current[0] = before
+
+    def wrap(real):
+        def make(*a, device=None, **kw):
+            x = real(*a, **kw)
+            log.append((current[0], recorded.setdefault(id(x), []), x))
+            return x
+        return make
+    for name in ("zeros", "empty", "empty_like"):
+        monkeypatch.setattr(torch, name, wrap(getattr(torch, name)))
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current[0])
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", lambda device: contextlib.nullcontext())
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda self: True))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, s: recorded.setdefault(id(self), []).append(s))
+    monkeypatch.setattr(tl, "lib", lambda: FakeLib())
+    monkeypatch.setattr(tl, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(tl, "_stream", lambda stream=None: 0)
+    return log
+
+
+def bf16(*shape):
+    return torch.ones(shape, dtype=torch.bfloat16)
+
+
+def i32(*shape):
+    return torch.ones(shape, dtype=torch.int32)
+
+
+def handle(log):
+    h = tl.TPLinear(tl.make_config(tl.TP_BLOCK_ATTN_PROJ, 1, 64, n_q_heads=2, n_kv_heads=1, head_dim=128),
+                    [bf16(256, 64), bf16(128, 64), bf16(128, 64), bf16(64, 256)])
+    h._dev, h._index = torch.device("cpu"), 0
+    log.clear()
+    return h
+
+
+CACHE = (1, 4, 16, 1, 128)
+CALLS = {
+    "qk_norm_rope": lambda h, s: h.qk_norm_rope(bf16(1, 3, 512), i32(3), ROPE, stream=s),
+    "kv_cache_copy_blocks": lambda h, s: h.kv_cache_copy_blocks(i32(1, 2), [bf16(*CACHE)], [bf16(*CACHE)], stream=s),
+    "kv_cache_compact": lambda h, s: h.kv_cache_compact(i32(2), i32(1), i32(1, 3), i32(1, 4), i32(1, 4), [bf16(*CACHE)],
+                                                        [bf16(*CACHE)], stream=s),
+    "tree_attention": lambda h, s: h.tree_attention(bf16(1, 3, 512), i32(2), i32(1), i32(1, 4), i32(3, 1), bf16(*CACHE),
+                                                    bf16(*CACHE), 3, 64, stream=s),
+    "tree_mask": lambda h, s: tl.tree_mask(i32(3), i32(2), i32(1), 3, stream=s),
+    "Rope": lambda h, s: tl.Rope(16, 128, stream=s),
+}
+MADE = {"qk_norm_rope": 2, "kv_cache_copy_blocks": 1, "kv_cache_compact": 2, "tree_attention": 2, "tree_mask": 3, "Rope": 1}
+
+
+class ROPE:
+    args = None
+
+    @staticmethod
+    def check(index, head_dim):
+        pass
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_made_on_the_calls_stream(made, name):
+    h, st = handle(made), FakeStream()
+    keep = CALLS[name](h, st)
+    assert keep is not None
+    assert [on is st for on, _, _ in made] == [True] * MADE[name]
+    assert all(recorded == [CALLER] for _, recorded, _ in made)
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_made_on_the_current_stream_without_one(made, name):
+    CALLS[name](handle(made), None)
+    assert [(on, recorded) for on, recorded, _ in made] == [(CALLER, [])] * MADE[name]
