@@ -256,8 +256,8 @@ class TPLinear:
         self.cfg = cfg
         col, row = packed_weight_bytes(cfg)
         dev = weights[0].device
-        self.w_col = torch.empty(col // 2, dtype=torch.bfloat16, device=dev)
-        self.w_row = torch.empty(row // 2, dtype=torch.bfloat16, device=dev)
+        self.w_col = _new(col // 2, torch.bfloat16, dev, stream)
+        self.w_row = _new(row // 2, torch.bfloat16, dev, stream)
         self.gamma = None if gamma is None else _bf16(gamma, "gamma")
         ws = [_bf16(w, "weight") for w in weights]
         arr = (ctypes.c_void_p * len(ws))(*[w.data_ptr() for w in ws])
@@ -295,11 +295,14 @@ class TPLinear:
             got = self._ws_sizes[max_tokens] = b.value
         return got
 
-    def workspace(self, max_tokens: int) -> torch.Tensor:
-        """A zero-filled workspace for calls of up to max_tokens tokens (cached, grows on demand)."""
+    def workspace(self, max_tokens: int, stream=None) -> torch.Tensor:
+        """A zero-filled workspace for calls of up to max_tokens tokens on `stream` (cached, grows on demand).
+        It is one for all streams: calls that overlap need workspaces of their own."""
         need = self.workspace_size(max_tokens)
         if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.zeros(need, dtype=torch.uint8, device=self.w_col.device)
+            self._ws = _new(need, torch.uint8, self.w_col.device, stream, zero=True)
+        elif stream is not None:
+            self._ws.record_stream(stream)     # a larger one may take its place while this call runs
         return self._ws
 
     def plan(self, T: int):
@@ -315,12 +318,12 @@ class TPLinear:
         norm = bool(self.cfg.flags & TP_FLAG_HAS_NORM)
         o = out if out is not None else {}
         if "mlp_out" not in o:
-            o["mlp_out"] = torch.empty_like(x)
+            o["mlp_out"] = _new(x.shape, x.dtype, x.device, stream)
         if norm and "residual_out" not in o:
-            o["residual_out"] = torch.empty_like(x)
+            o["residual_out"] = _new(x.shape, x.dtype, x.device, stream)
         if residual_stream and residual is not None and "residual_stream" not in o:
-            o["residual_stream"] = torch.empty_like(x)
-        ws = self.workspace(T) if ws is None else ws
+            o["residual_stream"] = _new(x.shape, x.dtype, x.device, stream)
+        ws = self.workspace(T, stream) if ws is None else ws
         _check(lib().tp_mlp_forward(self.handle, T, _ptr(_bf16(x, "x")), _ptr(residual), _ptr(o.get("residual_out")),
                                     _ptr(o["mlp_out"]), _ptr(o.get("residual_stream")), _ptr(ws), ws.numel(),
                                     _stream(stream)))
@@ -334,11 +337,11 @@ class TPLinear:
         norm = bool(self.cfg.flags & TP_FLAG_HAS_NORM)
         o = out if out is not None else {}
         if "mlp_out" not in o:
-            o["mlp_out"] = torch.empty_like(x)
+            o["mlp_out"] = _new(x.shape, x.dtype, x.device, stream)
         if norm and "residual_out" not in o:
-            o["residual_out"] = torch.empty_like(x)
+            o["residual_out"] = _new(x.shape, x.dtype, x.device, stream)
         if residual_stream and residual is not None and "residual_stream" not in o:
-            o["residual_stream"] = torch.empty_like(x)
+            o["residual_stream"] = _new(x.shape, x.dtype, x.device, stream)
         if status is not None and (status.dtype != torch.int32 or not status.is_cuda or status.numel() < 1
                                    or status.device != self.w_col.device):
             raise ValueError("status must be an int32 CUDA tensor of at least one element on the block's device")
@@ -357,8 +360,8 @@ class TPLinear:
         t, Is = self.cfg.t, self.cfg.intermediate // self.cfg.t
         if h_out is None:
             shape = (T, t * Is) if self.gathered else (t, T, Is)
-            h_out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-        ws = self.workspace(T) if ws is None else ws
+            h_out = _new(shape, torch.bfloat16, x.device, stream)
+        ws = self.workspace(T, stream) if ws is None else ws
         _check(lib().tp_gate_up_forward(self.handle, T, _ptr(_bf16(x, "x")), _ptr(h_out), _ptr(ws), ws.numel(),
                                         _stream(stream)))
         return h_out
@@ -367,10 +370,10 @@ class TPLinear:
              ws=None, stream=None):
         T = h_in.shape[0] if self.gathered else h_in.shape[1]
         H = self.cfg.hidden
-        out = torch.empty(T, H, dtype=torch.bfloat16, device=h_in.device) if out is None else out
+        out = _new((T, H), torch.bfloat16, h_in.device, stream) if out is None else out
         if residual is not None and stream_out is None:
-            stream_out = torch.empty_like(out)
-        ws = self.workspace(T) if ws is None else ws
+            stream_out = _new((T, H), torch.bfloat16, h_in.device, stream)
+        ws = self.workspace(T, stream) if ws is None else ws
         _check(lib().tp_down_forward(self.handle, T, _ptr(_bf16(h_in, "h_in")), _ptr(residual), _ptr(out),
                                      _ptr(stream_out), _ptr(ws), ws.numel(), _stream(stream)))
         return out, stream_out
@@ -530,7 +533,7 @@ class TPLinear:
         Returns the 16-byte workspace whose first word is the status."""
         T = qkv.shape[0] if self.gathered else qkv.shape[1]
         _, nb, bs, _, _ = cache_k.shape
-        ws = torch.zeros(16, dtype=torch.uint8, device=qkv.device) if ws is None else ws
+        ws = _new(16, torch.uint8, qkv.device, stream, zero=True) if ws is None else ws
         _check(lib().tp_kv_cache_write(self.handle, T, _ptr(_bf16(qkv, "qkv")), _ptr(slot_mapping),
                                        _ptr(_bf16(cache_k, "cache_k")), _ptr(_bf16(cache_v, "cache_v")), nb, bs,
                                        _ptr(ws), ws.numel(), _stream(stream)))
@@ -554,10 +557,10 @@ class TPLinear:
         _, nb, bs, _, _ = cache_k.shape
         if out is None:
             shape = (T, c.n_q_heads * c.head_dim) if self.gathered else (c.t, T, c.n_q_heads // c.t * c.head_dim)
-            out = torch.empty(shape, dtype=torch.bfloat16, device=qkv.device)
+            out = _new(shape, torch.bfloat16, qkv.device, stream)
         if ws is None:
-            ws = torch.zeros(self.paged_attention_workspace_size(n_reqs, max_query_len, max_seq_len),
-                             dtype=torch.uint8, device=qkv.device)
+            ws = _new(self.paged_attention_workspace_size(n_reqs, max_query_len, max_seq_len), torch.uint8, qkv.device,
+                      stream, zero=True)
         for name, a in (("query_start_loc", query_start_loc), ("seq_lens", seq_lens), ("block_tables", block_tables),
                         ("slot_mapping", slot_mapping)):
             if a is None and name == "slot_mapping":
@@ -579,8 +582,8 @@ class TPLinear:
         T, k = expert_ids.shape
         if expert_ids.dtype != torch.int32 or gates.dtype != torch.float32 or not expert_ids.is_cuda:
             raise TypeError("expert_ids must be int32 and gates float32 CUDA tensors")
-        out = torch.empty_like(x) if out is None else out
-        ws = self.workspace(T * k) if ws is None else ws
+        out = _new(x.shape, x.dtype, x.device, stream) if out is None else out
+        ws = self.workspace(T * k, stream) if ws is None else ws
         _check(lib().tp_moe_forward(self.handle, T, k, _ptr(_bf16(x, "x")), _ptr(expert_ids.contiguous()),
                                     _ptr(gates.contiguous()), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
         return out
@@ -596,10 +599,10 @@ class TPLinear:
         dev = self.w_col.device
         if x is not None and qkv_out is None:
             shape = (T, c.t * w_s) if self.gathered else (c.t, T, w_s)
-            qkv_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            qkv_out = _new(shape, torch.bfloat16, dev, stream)
         if attn_in is not None and o_out is None:
-            o_out = torch.empty(T, c.hidden, dtype=torch.bfloat16, device=dev)
-        ws = self.workspace(T) if ws is None else ws
+            o_out = _new((T, c.hidden), torch.bfloat16, dev, stream)
+        ws = self.workspace(T, stream) if ws is None else ws
         _check(lib().tp_attn_proj_forward(self.handle, T, _ptr(x), _ptr(qkv_out if x is not None else None),
                                           _ptr(attn_in), _ptr(o_out if attn_in is not None else None),
                                           _ptr(ws), ws.numel(), _stream(stream)))
@@ -617,8 +620,8 @@ class TPLinear:
             raise TypeError("cu_seqlens must be an int32 CUDA tensor")
         if out is None:
             shape = (T, c.n_q_heads * c.head_dim) if self.gathered else (c.t, T, c.n_q_heads // c.t * c.head_dim)
-            out = torch.empty(shape, dtype=torch.bfloat16, device=qkv.device)
-        ws = self.workspace(T) if ws is None else ws
+            out = _new(shape, torch.bfloat16, qkv.device, stream)
+        ws = self.workspace(T, stream) if ws is None else ws
         _check(lib().tp_attention_forward(self.handle, T, _ptr(_bf16(qkv, "qkv")), _ptr(cu_seqlens),
                                           cu_seqlens.numel() - 1, int(max_seqlen), _ptr(out), _ptr(ws),
                                           ws.numel(), _stream(stream)))
@@ -651,9 +654,11 @@ class TPLayer:
         except Exception:
             pass
 
-    def workspace(self) -> torch.Tensor:
+    def workspace(self, stream=None) -> torch.Tensor:
         if self._ws is None:
-            self._ws = torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=self.attn.w_col.device)
+            self._ws = _new(self.workspace_bytes, torch.uint8, self.attn.w_col.device, stream, zero=True)
+        elif stream is not None:
+            self._ws.record_stream(stream)
         return self._ws
 
     def set_rope(self, rope: Optional["Rope"], positions: Optional[torch.Tensor] = None) -> None:
@@ -680,13 +685,13 @@ class TPLayer:
         for k in ("residual_attn", "attn_out", "residual_mlp", "mlp_out") + (
                 ("residual_stream",) if residual_stream else ()):
             if k not in o:
-                o[k] = torch.empty_like(hidden)
+                o[k] = _new(hidden.shape, hidden.dtype, hidden.device, stream)
         io = LayerIO(_bf16(hidden, "hidden").data_ptr(),
                      None if residual is None else _bf16(residual, "residual").data_ptr(),
                      cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, int(max_seqlen),
                      o["residual_attn"].data_ptr(), o["attn_out"].data_ptr(), o["residual_mlp"].data_ptr(),
                      o["mlp_out"].data_ptr(), o["residual_stream"].data_ptr() if "residual_stream" in o else None)
-        ws = self.workspace() if ws is None else ws
+        ws = self.workspace(stream) if ws is None else ws
         _check(lib().tp_decoder_layer_forward(self.handle, T, ctypes.byref(io), _ptr(ws), ws.numel(),
                                               _stream(stream)))
         return o
@@ -774,8 +779,8 @@ def tree_mask(parents: torch.Tensor, query_start_loc: torch.Tensor, seq_lens: to
 def add_rms_norm(a: torch.Tensor, residual: Optional[torch.Tensor], gamma: torch.Tensor, eps: float,
                  residual_out=None, x_out=None, stream=None):
     T, H = a.shape
-    residual_out = torch.empty_like(a) if residual_out is None else residual_out
-    x_out = torch.empty_like(a) if x_out is None else x_out
+    residual_out = _new(a.shape, a.dtype, a.device, stream) if residual_out is None else residual_out
+    x_out = _new(a.shape, a.dtype, a.device, stream) if x_out is None else x_out
     _check(lib().tp_add_rms_norm(T, H, _ptr(_bf16(a, "a")), None if residual is None else _ptr(_bf16(residual, "residual")),
                                  _ptr(_bf16(gamma, "gamma")), eps, _ptr(residual_out), _ptr(x_out),
                                  _stream(stream)))
@@ -797,11 +802,11 @@ def capture_rows(row_req: torch.Tensor, row_pos: torch.Tensor, sel_keys: torch.T
                 or n_out.dtype != torch.int64 or n_out.numel() < 1):
             raise ValueError("capture out tensors: int32 [capacity, 6], bf16 [capacity, H], int64 [1]")
     else:
-        hdr = torch.empty(max(capacity, 1), 6, dtype=torch.int32, device=dev)
-        rows = torch.empty(max(capacity, 1), H, dtype=torch.bfloat16, device=dev)
-        n_out = torch.zeros(1, dtype=torch.int64, device=dev)
+        hdr = _new((max(capacity, 1), 6), torch.int32, dev, stream)
+        rows = _new((max(capacity, 1), H), torch.bfloat16, dev, stream)
+        n_out = _new(1, torch.int64, dev, stream, zero=True)
     need = capture_workspace_size(T, sel_keys.numel())
-    ws = torch.zeros(need, dtype=torch.uint8, device=dev) if ws is None else ws
+    ws = _new(need, torch.uint8, dev, stream, zero=True) if ws is None else ws
     arr = (ctypes.c_void_p * len(tensors))(*[_bf16(t, "tensor").data_ptr() for t in tensors])
     types = (ctypes.c_int32 * len(tensors))(*tensor_types)
     _check(lib().tp_capture_rows(T, H, _ptr(row_req), _ptr(row_pos), _ptr(sel_keys), sel_keys.numel(),

@@ -5,6 +5,7 @@ later changes them. (On the CPU: test_streams.py.)
 import pytest
 import torch
 
+import workloads
 import tensor_linear_layers_gb300 as tl
 from test_gpu_tree import build, built, check, dev, handle, status  # noqa: F401 (built: the module's fixture)
 
@@ -88,3 +89,30 @@ def test_captured_on_the_given_stream():
         torch.cuda.synchronize()
         assert status(ws) == 0 and status(mws) == 0
         check(out, c, NQ, NKV, SHARDS)
+
+
+def test_blocks_made_and_run_beside_a_busy_stream(busy):
+    st, H, inter, T = torch.cuda.Stream(), 256, 512, 40
+    w = [workloads.draw(s, 160, i).cuda() for i, s in enumerate([(inter, H), (inter, H), (H, inter)])]
+    x = workloads.draw((T, H), 161, 0).cuda()
+    cfg = tl.make_config(tl.TP_BLOCK_MLP, 2, H, inter)
+    want = tl.TPLinear(cfg, w).mlp_forward(x)["mlp_out"]
+    busy()
+    blk = tl.TPLinear(cfg, w, stream=st)
+    outs = [blk.mlp_forward(x, stream=st)["mlp_out"] for _ in range(3)]
+    st.synchronize()
+    torch.cuda.synchronize()
+    assert status(blk.workspace(T)) == 0 and all(torch.equal(o, want) for o in outs)
+
+
+def test_paged_attention_beside_a_busy_stream(busy):
+    h, st = handle(NQ, NKV, SHARDS), torch.cuda.Stream()
+    c = build(NQ, NKV, SHARDS, [1500, 300], [1, 1], 16, seed=152)
+    qsl, lens, tables = dev(c["qsl"]), dev(c["lens"]), dev(c["tables"].clip(0))
+    qkv, ck, cv = c["qkv"].cuda(), c["ck"].cuda(), c["cv"].cuda()
+    busy()
+    out, ws = h.paged_attention(qkv, qsl, lens, tables, ck, cv, 1, 1520, stream=st)
+    st.synchronize()
+    torch.cuda.synchronize()
+    assert status(ws) == 0
+    check(out, c, NQ, NKV, SHARDS)

@@ -112,3 +112,61 @@ def test_made_on_the_calls_stream(made, name):
 def test_made_on_the_current_stream_without_one(made, name):
     CALLS[name](handle(made), None)
     assert [(on, recorded) for on, recorded, _ in made] == [(CALLER, [])] * MADE[name]
+
+
+# ------------------------------------------------------------------ the blocks, the layer, the cache and the captures
+def block(kind, flags=0, n_experts=0):
+    w = {tl.TP_BLOCK_MLP: [bf16(128, 64), bf16(128, 64), bf16(64, 128)],
+         tl.TP_BLOCK_ATTN_PROJ: [bf16(256, 64), bf16(128, 64), bf16(128, 64), bf16(64, 256)],
+         tl.TP_BLOCK_MOE: [bf16(2, 128, 64), bf16(2, 128, 64), bf16(2, 64, 128)]}[kind]
+    cfg = tl.make_config(kind, 1, 64, 128, 2, 1, 128, flags=flags, n_experts=n_experts)
+    return tl.TPLinear(cfg, w, bf16(64) if flags else None)
+
+
+def mlp():
+    return block(tl.TP_BLOCK_MLP, tl.TP_FLAG_HAS_NORM)
+
+
+def attn():
+    return block(tl.TP_BLOCK_ATTN_PROJ, tl.TP_FLAG_HAS_NORM)
+
+
+BLOCK_CALLS = {  # handle, call, tensors made
+    "weights": (lambda: None, lambda h, s: tl.TPLinear(tl.make_config(tl.TP_BLOCK_MLP, 1, 64, 128),
+                                                       [bf16(128, 64), bf16(128, 64), bf16(64, 128)], stream=s), 2),
+    "mlp_forward": (mlp, lambda h, s: h.mlp_forward(bf16(3, 64), bf16(3, 64), stream=s), 4),
+    "mlp_forward_no_alloc": (mlp, lambda h, s: h.mlp_forward_no_alloc(bf16(3, 64), bf16(3, 64), stream=s), 3),
+    "gate_up": (mlp, lambda h, s: h.gate_up(bf16(3, 64), stream=s), 2),
+    "down": (mlp, lambda h, s: h.down(bf16(1, 3, 128), bf16(3, 64), stream=s), 3),
+    "moe_forward": (lambda: block(tl.TP_BLOCK_MOE, n_experts=2),
+                    lambda h, s: h.moe_forward(bf16(3, 64), i32(3, 2), torch.ones(3, 2), stream=s), 2),
+    "attn_proj_forward": (attn, lambda h, s: h.attn_proj_forward(bf16(3, 64), bf16(1, 3, 256), stream=s), 3),
+    "attention_forward": (attn, lambda h, s: h.attention_forward(bf16(1, 3, 512), i32(2), 3, stream=s), 2),
+    "kv_cache_write": (attn, lambda h, s: h.kv_cache_write(bf16(1, 3, 512), i32(3), bf16(*CACHE), bf16(*CACHE), stream=s), 1),
+    "paged_attention": (attn, lambda h, s: h.paged_attention(bf16(1, 3, 512), i32(2), i32(1), i32(1, 4), bf16(*CACHE),
+                                                             bf16(*CACHE), 3, 64, stream=s), 2),
+    "layer": (lambda: tl.TPLayer(attn(), mlp(), 8), lambda h, s: h.forward(bf16(3, 64), None, i32(2), 3, stream=s), 6),
+    "add_rms_norm": (lambda: None, lambda h, s: tl.add_rms_norm(bf16(3, 64), None, bf16(64), 1e-5, stream=s), 2),
+    "capture_rows": (lambda: None, lambda h, s: tl.capture_rows(i32(3), i32(3), torch.ones(2, dtype=torch.int64),
+                                                                [bf16(3, 64)], [0], 0, 4, stream=s), 4),
+}
+
+
+@pytest.mark.parametrize("name", BLOCK_CALLS)
+@pytest.mark.parametrize("given", [True, False])
+def test_the_blocks_calls(made, name, given):
+    make, call, n = BLOCK_CALLS[name]
+    h, st = make(), FakeStream() if given else None
+    made.clear()
+    keep = call(h, st)
+    assert keep is not None
+    assert [on for on, _, _ in made] == [st if given else CALLER] * n
+    assert all(recorded == ([CALLER] if given else []) for _, recorded, _ in made)
+
+
+def test_a_cached_workspace_outlives_the_calls_of_other_streams(made):
+    h, a, b = mlp(), FakeStream(), FakeStream()
+    ws = h.workspace(8, a)
+    h.mlp_forward(bf16(3, 64), stream=b)
+    (recorded,) = [r for _, r, x in made if x is ws]
+    assert h.workspace(8) is ws and recorded == [CALLER, b]
