@@ -211,6 +211,14 @@ def _new(shape, dtype: torch.dtype, device, stream, zero: bool = False) -> torch
     return x
 
 
+def _contiguous(x: torch.Tensor, stream) -> torch.Tensor:
+    """x, or a contiguous copy of it made on `stream`; to be held until the kernels that read it are launched."""
+    if stream is None or x.is_contiguous():
+        return x.contiguous()
+    with torch.cuda.stream(stream):
+        return x.contiguous()
+
+
 def _workspace(ws: Optional[torch.Tensor], need: int, index: int, stream) -> torch.Tensor:
     if ws is None:
         return _new(need, torch.uint8, torch.device("cuda", index), stream, zero=True)
@@ -582,10 +590,11 @@ class TPLinear:
         T, k = expert_ids.shape
         if expert_ids.dtype != torch.int32 or gates.dtype != torch.float32 or not expert_ids.is_cuda:
             raise TypeError("expert_ids must be int32 and gates float32 CUDA tensors")
+        ids, gates = _contiguous(expert_ids, stream), _contiguous(gates, stream)
         out = _new(x.shape, x.dtype, x.device, stream) if out is None else out
         ws = self.workspace(T * k, stream) if ws is None else ws
-        _check(lib().tp_moe_forward(self.handle, T, k, _ptr(_bf16(x, "x")), _ptr(expert_ids.contiguous()),
-                                    _ptr(gates.contiguous()), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+        _check(lib().tp_moe_forward(self.handle, T, k, _ptr(_bf16(x, "x")), _ptr(ids), _ptr(gates), _ptr(out),
+                                    _ptr(ws), ws.numel(), _stream(stream)))
         return out
 
     # ------------------------------------------------------------------ attention projections

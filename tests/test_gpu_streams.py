@@ -116,3 +116,21 @@ def test_paged_attention_beside_a_busy_stream(busy):
     torch.cuda.synchronize()
     assert status(ws) == 0
     check(out, c, NQ, NKV, SHARDS)
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_moe_routing_arrays_of_other_strides(busy, given):
+    T, H, inter, E, k = 37, 256, 512, 4, 2
+    w = [workloads.draw(s, 170, i).cuda() for i, s in enumerate([(inter, H), (inter, H), (H, inter)] * E)]
+    blk = tl.TPLinear(tl.make_config(tl.TP_BLOCK_MOE, 2, H, inter, n_experts=E), w)
+    x = workloads.draw((T, H), 171, 0).cuda()
+    rows = torch.arange(T, device="cuda")
+    ids = torch.stack([rows % E, (rows // E + 1 + rows) % E]).to(torch.int32)               # [k, T]
+    gates = torch.stack([rows.float() / T, 1 - rows.float() / T])
+    want = blk.moe_forward(x, ids.t().contiguous(), gates.t().contiguous())
+    assert status(blk.workspace(T * k)) == 0
+    st = torch.cuda.Stream() if given else None
+    busy()
+    got = blk.moe_forward(x, ids.t(), gates.t(), stream=st)
+    torch.cuda.synchronize()
+    assert status(blk.workspace(T * k)) == 0 and torch.equal(got, want)

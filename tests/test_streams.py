@@ -170,3 +170,26 @@ def test_a_cached_workspace_outlives_the_calls_of_other_streams(made):
     h.mlp_forward(bf16(3, 64), stream=b)
     (recorded,) = [r for _, r, x in made if x is ws]
     assert h.workspace(8) is ws and recorded == [CALLER, b]
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_routing_arrays_of_other_strides_last_until_the_launch(made, monkeypatch, given):
+    # copies made of ids and gates that are not contiguous: both alive, and whole, when the library reads them
+    import ctypes
+    seen = {}
+
+    class Reads(FakeLib):
+        @staticmethod
+        def tp_moe_forward(h, T, k, x, ids, gates, *rest):
+            seen["ids"] = list((ctypes.c_int32 * (T * k)).from_address(ids.value))
+            seen["gates"] = list((ctypes.c_float * (T * k)).from_address(gates.value))
+            return 0
+    monkeypatch.setattr(tl, "lib", lambda: Reads())
+    copies, real, st = [], torch.Tensor.contiguous, FakeStream() if given else None
+    monkeypatch.setattr(torch.Tensor, "contiguous", lambda self: copies.append(torch.cuda.current_stream()) or real(self))
+    h, T = block(tl.TP_BLOCK_MOE, n_experts=2), 37
+    ids, gates = torch.arange(2 * T, dtype=torch.int32).view(2, T).t(), torch.arange(2 * T).float().view(2, T).t() + 0.5
+    for _ in range(20):
+        h.moe_forward(bf16(T, 64), ids, gates, stream=st)
+        assert seen == {"ids": ids.flatten().tolist(), "gates": gates.flatten().tolist()}
+    assert set(copies) == {st if given else CALLER}
