@@ -176,7 +176,8 @@ struct CompactParams {
 };
 cudaError_t launch_kv_copy_blocks(const KvLayers& layers, int n_layers, const int* pairs, int n_pairs,
                                   long long num_blocks, int block_size, int kv_per, int t, int* status, cudaStream_t st);
-cudaError_t launch_kv_compact(const KvLayers& layers, int n_layers, const CompactParams& p, int n_reqs, cudaStream_t st);
+cudaError_t launch_kv_compact(const KvLayers& layers, int n_layers, const CompactParams& p, int n_reqs, int nsm,
+                              cudaStream_t st);
 
 // Attention of drafted token trees over the cache (tree_attention.cu).
 struct TreeItem {

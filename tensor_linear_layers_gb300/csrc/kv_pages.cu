@@ -125,7 +125,8 @@ cudaError_t launch_kv_copy_blocks(const KvLayers& layers, int n_layers, const in
                             (long long)block_size * kv_per * kHd / 8, t, status);
 }
 
-cudaError_t launch_kv_compact(const KvLayers& layers, int n_layers, const CompactParams& p, int n_reqs, cudaStream_t st) {
+cudaError_t launch_kv_compact(const KvLayers& layers, int n_layers, const CompactParams& p, int n_reqs, int nsm,
+                              cudaStream_t st) {
   const long long cols = 2LL * n_layers * p.t * (p.kv_per * kHd / 8);
   const int strips = (int)((cols + kCompactThreads - 1) / kCompactThreads);
   if ((long long)n_reqs * strips > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
@@ -135,7 +136,7 @@ cudaError_t launch_kv_compact(const KvLayers& layers, int n_layers, const Compac
   // SM; 20 requests of 32 layers and up to 9 tokens 6.3 us, with four rows 6.7). Well beyond one wave the
   // other blocks hide it, and four rows leave room for six (24 such requests 7.6 us, with eight rows
   // 8.3; 64: 17.1 and 18.3; 64 of up to 3 tokens 8.3 and 10.3; 64 of up to 32: 46.5 and 45.7).
-  const bool many = (long long)n_reqs * strips > 5 * 152;
+  const bool many = (long long)n_reqs * strips > 5LL * nsm;
   return cudaLaunchKernelEx(&cfg, many ? kv_compact_kernel<4> : kv_compact_kernel<8>, layers, p, n_layers, strips);
 }
 

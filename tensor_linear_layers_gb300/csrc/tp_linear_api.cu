@@ -1922,7 +1922,7 @@ int tp_kv_cache_compact(tp_linear_t* h, int32_t n_reqs, const int32_t* query_sta
   p.num_blocks = (int)num_blocks;
   p.block_size = block_size;
   p.max_accepted = max_accepted;
-  const cudaError_t e = launch_kv_compact(layers, n_layers, p, n_reqs, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_kv_compact(layers, n_layers, p, n_reqs, h->nsm, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "KV cache compaction launch");
   return ok();
 }
