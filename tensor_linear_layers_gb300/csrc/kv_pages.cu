@@ -57,14 +57,17 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(const KvLay
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.x / strips, strip = blockIdx.x - b * strips, tid = threadIdx.x;
-  const int q0 = p.qsl[b], n_new = p.qsl[b + 1] - q0, L = p.seq_lens[b], ctx = L - n_new;
-  if (n_new < 0 || ctx < 0 || L > (long long)p.max_blocks * p.block_size) {
+  // counts of any value are compared in 64 bits: a difference that wrapped would pass for one that fits
+  const long long n_drafts = (long long)p.qsl[b + 1] - p.qsl[b];
+  const int L = p.seq_lens[b];
+  if (n_drafts < 0 || L < n_drafts || L > (long long)p.max_blocks * p.block_size) {
     if (strip == 0 && tid == 0) {
       atomicExch(p.status, kStatusShape);
       p.new_lens[b] = L;
     }
     return;
   }
+  const int n_new = (int)n_drafts, ctx = L - n_new;
   // this thread's column: 16 bytes of a (layer, k or v, shard) row
   const int vec = p.kv_per * kHd / 8;
   const long long col = (long long)strip * kCompactThreads + tid, cols = 2LL * n_layers * p.t * vec;

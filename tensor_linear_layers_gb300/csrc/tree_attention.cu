@@ -36,11 +36,12 @@ __global__ void __launch_bounds__(kMaxDraft)
   const int b = blockIdx.x, i = threadIdx.x;
   griddep_wait();
   griddep_launch_dependents();
-  const int q0 = qsl[b], n = qsl[b + 1] - q0, ctx = seq_lens[b] - n;
-  if (q0 < 0 || n < 0 || n > max_query_len || q0 > T - n || ctx < 0) {
+  const int q0 = qsl[b], q1 = qsl[b + 1], len = seq_lens[b];
+  if (q0 < 0 || q1 < q0 || q1 > T || q1 - q0 > max_query_len || len < q1 - q0) {   // no difference that wraps
     if (i == 0) atomicExch(status, kStatusShape);
     return;
   }
+  const int n = q1 - q0, ctx = len - n;
   const int used = (n + 31) / 32;
   int to = -1;
   unsigned bits[kWords];
