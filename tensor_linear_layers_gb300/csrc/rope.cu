@@ -19,7 +19,7 @@ namespace tpl {
 
 namespace {
 constexpr int kStatusShape = -2;   // TP_ERR_SHAPE
-// steps of a warp in flight, warps per SM (80 registers): 4096 tokens of 48 heads with norm 23.5 us;
+// steps of a warp in flight, warps per SM (72 registers): 4096 tokens of 48 heads with norm 23.5 us;
 // (2, 32) 27.3, (4, 20) 24.0, (4, 24) 24.5, (6, 16) 26.0
 constexpr int kUnroll = 3, kMinCtas = 25;
 
