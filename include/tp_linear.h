@@ -385,6 +385,59 @@ int tp_tree_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t*
                       tp_stream_t stream);
 
 /*
+ * A paged cache in 8 bits. Codes and scales, per shard r: codes_k[r], codes_v[r] are
+ * [num_blocks][block_size][kv_per][128] e4m3 (one byte), scales_k[r], scales_v[r]
+ * [num_blocks][block_size][kv_per] bytes; slots as for the bf16 cache. A head row x of 128
+ * elements is held as
+ *   e = the smallest integer with max|x| <= 448 * 2^e, within [-100, 118];  scale = e + 127
+ *   code_i = e4m3(x_i * 2^-e), to nearest, ties to even, at most 448 in size
+ * and stands for code_i * 2^e, exactly a bf16 number. A row with a NaN or an infinity gets scale
+ * 255 and codes 0 and stands for NaN. Codes that are NaN (0x7f, 0xff), which no call here writes,
+ * must not be in slots that are read. num_blocks, block_size: bounds as for tp_paged_attention;
+ * codes 16-byte aligned, scales at any address. Status: workspace bytes [0, 4);
+ * 16 bytes.
+ *
+ * tp_kv_quant_write: for every token i of qkv with slot_mapping[i] >= 0, the k and v heads of
+ *   every shard quantised into that slot. A slot past the cache writes TP_ERR_SHAPE and is
+ *   skipped; negative = padding; no slot twice in a call.
+ * tp_kv_quant_read: k_out[r][i], v_out[r][i] (bf16 [t][n][kv_per][128], 16-byte aligned) = what
+ *   the heads in slots[i] stand for (exact); a negative slot gives zeros, one past the cache too,
+ *   with TP_ERR_SHAPE. Slots may repeat. n <= 2^24.
+ */
+int tp_kv_quant_write(tp_linear_t* h, int64_t T, const void* qkv, const int32_t* slot_mapping, void* codes_k,
+                      void* codes_v, void* scales_k, void* scales_v, int64_t num_blocks, int32_t block_size,
+                      void* workspace, int64_t workspace_bytes, tp_stream_t stream);
+int tp_kv_quant_read(tp_linear_t* h, int64_t n, const int32_t* slots, const void* codes_k, const void* codes_v,
+                     const void* scales_k, const void* scales_v, int64_t num_blocks, int32_t block_size, void* k_out,
+                     void* v_out, void* workspace, int64_t workspace_bytes, tp_stream_t stream);
+
+/*
+ * Attention of chunks of new tokens over a paged cache, in bf16 (scales NULL) or in 8 bits: for
+ * decoding requests (one new token), chunks of prompts and both in one call. The new tokens of
+ * request b are rows [query_start_loc[b], query_start_loc[b+1]) of qkv and the last positions of
+ * its seq_lens[b] tokens; their k and v are in the cache (tp_kv_cache_write, tp_qk_norm_rope,
+ * tp_kv_quant_write). The token at position p sees position j <= p if window = 0, j > p - window
+ * (its own and the window - 1 before it) or j < sinks (first tokens that stay visible; without a
+ * window they have no effect). What a token does not see has no effect on it, NaN and infinities
+ * included; pages that no token sees are not read, and their block table entries not looked at.
+ * Other arguments, layouts, bounds and errors as for tp_paged_attention; max_seq_len <= 2^26, at
+ * most 256 q heads per kv head; attn_out and the workspace apart from what the call reads. Rows of
+ * attn_out that belong to no request are left as they were. Scores, softmax and sums in fp32
+ * (values of v under 2^137 / L, L the tokens seen, do not overflow), P rounded to bf16 for the
+ * P V product, output rounded to bf16. The workspace (tp_chunk_attention_workspace_size;
+ * caller-owned, ZERO-FILLED before first use) holds the status word and partial results; one of
+ * larger bounds serves too, and calls of any bounds that it serves may follow one another in it.
+ */
+int tp_chunk_attention_workspace_size(const tp_linear_t* h, int32_t n_reqs, int32_t max_query_len,
+                                      int32_t max_seq_len, int64_t* bytes);
+int tp_chunk_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t* query_start_loc,
+                       const int32_t* seq_lens, int32_t n_reqs, int32_t max_query_len, int32_t max_seq_len,
+                       const int32_t* block_tables, int32_t max_blocks_per_req, int32_t window, int32_t sinks,
+                       const void* cache_k, const void* cache_v, const void* scales_k, const void* scales_v,
+                       int64_t num_blocks, int32_t block_size, void* attn_out, void* workspace,
+                       int64_t workspace_bytes, tp_stream_t stream);
+
+/*
  * Pages moved inside the cache, in the caches of n_layers layers (1..TP_KV_MAX_LAYERS) in
  * one launch. caches_k, caches_v: HOST arrays of n_layers device pointers, each a cache of
  * the layout above; no two overlap (layers that share a cache list it once). Copies, bit-exact. head_dim 128. Status: workspace bytes [0, 4); 16 bytes.

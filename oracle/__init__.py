@@ -32,8 +32,9 @@ pattern (within-expert tensor parallelism); its routing is an input.
 values to its slot, and attention of new tokens over their requests' cached
 keys through the block tables. ``rope.py`` rotates q and k by their positions
 (and norms their heads); ``drafts.py`` is attention of drafted token trees over
-the paged cache and the moves of pages inside it. The pages define neither:
-both are the published formulas.
+the paged cache and the moves of pages inside it. ``kv_quant.py`` is the paged
+cache in 8 bits and attention of chunks of new tokens with a sliding window.
+The pages define none of the three: they are the published formulas.
 
 Every function computes in float64 from bf16 inputs converted exactly. Where
 the block has a plain definition (the unsharded Y = XW, SiLU, RMSNorm, row
@@ -58,3 +59,4 @@ from .moe import moe_block, moe_block_tp  # noqa: F401
 from .kv_cache import kv_cache_write, paged_attention, slot_of  # noqa: F401
 from .rope import rope_frequencies, qk_norm_rope  # noqa: F401
 from .drafts import tree_sees, mask_words, tree_attention, copy_blocks, compact  # noqa: F401
+from .kv_quant import e4m3_values, round_e4m3, quantise, values, chunk_attention  # noqa: F401

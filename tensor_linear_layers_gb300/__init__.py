@@ -38,6 +38,7 @@ ABI_SYMBOLS = (
     "tp_moe_forward", "tp_kv_cache_write", "tp_paged_attention_workspace_size", "tp_paged_attention",
     "tp_rope_frequencies", "tp_rope_table", "tp_qk_norm_rope", "tp_layer_set_rope", "tp_tree_mask",
     "tp_tree_attention_workspace_size", "tp_tree_attention", "tp_kv_cache_copy_blocks", "tp_kv_cache_compact",
+    "tp_kv_quant_write", "tp_kv_quant_read", "tp_chunk_attention_workspace_size", "tp_chunk_attention",
 )
 
 
@@ -129,6 +130,10 @@ def lib() -> ctypes.CDLL:
         "tp_tree_mask": [I64, I32, I32, P, P, P, P, I32, P, P, I64, P],
         "tp_tree_attention_workspace_size": [P, I32, I32, I32, PI64],
         "tp_tree_attention": [P, I64, P, P, P, I32, I32, I32, P, I32, P, I32, P, P, I64, I32, P, P, I64, P],
+        "tp_kv_quant_write": [P, I64, P, P, P, P, P, P, I64, I32, P, I64, P],
+        "tp_kv_quant_read": [P, I64, P, P, P, P, P, I64, I32, P, P, P, I64, P],
+        "tp_chunk_attention_workspace_size": [P, I32, I32, I32, PI64],
+        "tp_chunk_attention": [P, I64, P, P, P, I32, I32, I32, P, I32, I32, I32, P, P, P, P, I64, I32, P, P, I64, P],
         "tp_kv_cache_copy_blocks": [P, P, I32, I32, P, P, I64, I32, P, I64, P],
         "tp_kv_cache_compact": [P, I32, P, P, P, I32, P, P, I32, I32, P, P, I64, I32, P, P, I64, P],
     }
@@ -177,7 +182,7 @@ def _bf16(t: torch.Tensor, name: str) -> torch.Tensor:
     return t
 
 
-_INT32, _BF16 = torch.int32, torch.bfloat16
+_INT32, _BF16, _E4M3 = torch.int32, torch.bfloat16, torch.float8_e4m3fn
 
 
 def _i32(t: torch.Tensor, name: str, index: int, numel: int = -1) -> int:
@@ -533,6 +538,99 @@ class TPLinear:
             _i32(mask, "mask", dev, T * words), words, _bf16_on(cache_k, "cache_k", dev, cshape),
             _bf16_on(cache_v, "cache_v", dev, cshape), nb, bs, _bf16_on(out, "out", dev, out_shape),
             ws.data_ptr(), ws.numel(), _stream_ptr(stream)))
+        return out, ws
+
+    def kv_quant_cache(self, num_blocks: int, block_size: int, stream=None):
+        """A new, zero-filled cache in 8 bits: (codes_k, codes_v float8_e4m3fn [t, blocks, block_size, kv heads
+        of the shard, 128], scales_k, scales_v uint8 [t, blocks, block_size, kv heads of the shard])."""
+        shape = self.kv_cache_shape(num_blocks, block_size)
+        codes = [_new(shape, torch.uint8, self._dev, stream, zero=True).view(_E4M3) for _ in range(2)]
+        return (*codes, *(_new(shape[:-1], torch.uint8, self._dev, stream, zero=True) for _ in range(2)))
+
+    def _quant(self, codes_k: torch.Tensor, codes_v: torch.Tensor, scales_k: torch.Tensor, scales_v: torch.Tensor):
+        """(blocks, block size, the four device pointers) of a cache in 8 bits on this handle's device."""
+        nb, bs, shape = self._cache_shape(codes_k)
+        dev = self._index
+        for name, x, dtype, want in (("codes_k", codes_k, _E4M3, shape), ("codes_v", codes_v, _E4M3, shape),
+                                     ("scales_k", scales_k, torch.uint8, shape[:-1]),
+                                     ("scales_v", scales_v, torch.uint8, shape[:-1])):
+            if x.dtype is not dtype or x.get_device() != dev or not x.is_contiguous() or x.shape != want:
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(want)} on cuda:{dev}")
+        return nb, bs, codes_k.data_ptr(), codes_v.data_ptr(), scales_k.data_ptr(), scales_v.data_ptr()
+
+    def kv_quant_write(self, qkv: torch.Tensor, slot_mapping: torch.Tensor, codes_k: torch.Tensor,
+                       codes_v: torch.Tensor, scales_k: torch.Tensor, scales_v: torch.Tensor,
+                       ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Quantise every token's k and v heads into its slot of a cache in 8 bits (slot_mapping int32 [T],
+        negative = skip). Returns the 16-byte workspace whose first word is the status."""
+        self._attention_handle()
+        dev = self._index
+        T, shape = self._rows(qkv, self._qkv_width)
+        nb, bs, ck, cv, sk, sv = self._quant(codes_k, codes_v, scales_k, scales_v)
+        ws = _workspace(ws, 16, dev, stream)
+        _check(lib().tp_kv_quant_write(self.handle, T, _bf16_on(qkv, "qkv", dev, shape),
+                                       _i32(slot_mapping, "slot_mapping", dev, T), ck, cv, sk, sv, nb, bs,
+                                       ws.data_ptr(), ws.numel(), _stream_ptr(stream)))
+        return ws
+
+    def kv_quant_read(self, slots: torch.Tensor, codes_k: torch.Tensor, codes_v: torch.Tensor,
+                      scales_k: torch.Tensor, scales_v: torch.Tensor, out=None, ws: Optional[torch.Tensor] = None,
+                      stream=None):
+        """What the heads in these slots (int32 [n], negative = zeros) of a cache in 8 bits stand for: (k, v bf16
+        [t, n, kv heads of the shard, 128], workspace whose first word is the status); out: (k, v) to write
+        instead of new tensors."""
+        self._attention_handle()
+        dev, n = self._index, slots.numel()
+        nb, bs, ck, cv, sk, sv = self._quant(codes_k, codes_v, scales_k, scales_v)
+        t, kv_per, hd = self._shape
+        shape = (t, n, kv_per, hd)
+        k, v = (_new(shape, torch.bfloat16, self._dev, stream) for _ in range(2)) if out is None else out
+        ws = _workspace(ws, 16, dev, stream)
+        _check(lib().tp_kv_quant_read(self.handle, n, _i32(slots, "slots", dev), ck, cv, sk, sv, nb, bs,
+                                      _bf16_on(k, "out[0]", dev, shape), _bf16_on(v, "out[1]", dev, shape),
+                                      ws.data_ptr(), ws.numel(), _stream_ptr(stream)))
+        return k, v, ws
+
+    def chunk_attention_workspace_size(self, n_reqs: int, max_query_len: int, max_seq_len: int) -> int:
+        b = ctypes.c_int64()
+        _check(lib().tp_chunk_attention_workspace_size(self.handle, n_reqs, max_query_len, max_seq_len,
+                                                       ctypes.byref(b)))
+        return b.value
+
+    def chunk_attention(self, qkv: torch.Tensor, query_start_loc: torch.Tensor, seq_lens: torch.Tensor,
+                        block_tables: torch.Tensor, cache_k: torch.Tensor, cache_v: torch.Tensor, max_query_len: int,
+                        max_seq_len: int, window: int = 0, sinks: int = 0, scales_k: Optional[torch.Tensor] = None,
+                        scales_v: Optional[torch.Tensor] = None, out=None, ws=None, stream=None):
+        """Attention of every request's new tokens (rows of qkv, already in the cache as its last positions)
+        over its cached tokens, causal: with a window, over the last `window` of them and the first `sinks`.
+        The caches are bf16, or e4m3 codes with their scales (kv_quant_write). Returns (attn in the
+        attention core's output layout, workspace whose first word is the status)."""
+        self._attention_handle()
+        dev, n_reqs = self._index, seq_lens.numel()
+        T, shape = self._rows(qkv, self._qkv_width)
+        if (scales_k is None) != (scales_v is None):
+            raise ValueError("scales_k and scales_v: both (a cache in 8 bits) or neither (in bf16)")
+        if scales_k is not None:
+            nb, bs, ck, cv, sk, sv = self._quant(cache_k, cache_v, scales_k, scales_v)
+        else:
+            nb, bs, cshape = self._cache_shape(cache_k)
+            ck, cv = _bf16_on(cache_k, "cache_k", dev, cshape), _bf16_on(cache_v, "cache_v", dev, cshape)
+            sk = sv = None
+        t, w = self._shape[0], self._attn_width
+        out_shape = (T, t * w) if self._gathered else (t, T, w)
+        if out is None:
+            out = _new(out_shape, torch.bfloat16, self._dev, stream)
+        need = self.chunk_attention_workspace_size(n_reqs, max_query_len, max_seq_len) if ws is None else 0
+        ws = _workspace(ws, need, dev, stream)
+        if block_tables.dim() != 2:
+            raise ValueError("block_tables is [n_reqs, max_blocks]")
+        max_blocks = block_tables.shape[1]
+        _check(lib().tp_chunk_attention(
+            self.handle, T, _bf16_on(qkv, "qkv", dev, shape),
+            _i32(query_start_loc, "query_start_loc", dev, n_reqs + 1), _i32(seq_lens, "seq_lens", dev), n_reqs,
+            max_query_len, max_seq_len, _i32(block_tables, "block_tables", dev, n_reqs * max_blocks), max_blocks,
+            window, sinks, ck, cv, sk, sv, nb, bs, _bf16_on(out, "out", dev, out_shape), ws.data_ptr(), ws.numel(),
+            _stream_ptr(stream)))
         return out, ws
 
     def kv_cache_write(self, qkv: torch.Tensor, slot_mapping: torch.Tensor, cache_k: torch.Tensor,

@@ -1,0 +1,1112 @@
+// Attention of chunks of new tokens over the paged KV cache, the cache in bf16 or in 8 bits, with
+// an optional sliding window and a few first tokens that stay visible.
+//
+// Request b has ctx cached tokens and n new ones at positions ctx .. ctx + n - 1, all in the
+// cache. The token at position p sees key j if j <= p and (no window, or j > p - window, or
+// j < sinks):
+//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp((q . k_j - m) / sqrt(hd))
+// An 8-bit cache stands for k = code * 2^(scale - 127) (kv_quant.cu), each exactly a bf16.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "chunk_plan.h"
+#include "gemm_tc.cuh"
+#include "internal.h"
+#include "paged_tiles.cuh"
+
+namespace tpl {
+
+// ---------------------------------------------------------------- kernel
+// The queries of a group of whole tokens (tokens x the q heads of one kv head) are the rows of
+// 128-row tensor-core tiles; the keys that any of them sees go by in chunks of 128, read once
+// from the cache for all of them:
+//   S = Q K^T  (tcgen05, fp32 in tensor memory)
+//   P = 2^(s c - m) as bf16, written over S (tensor memory, the A operand of P V)
+//   O += P V   (tcgen05, O in tensor memory)
+// with the running max m and sum l of every row in its thread's registers. Persistent, one CTA
+// per SM; the chunks of all items are one line cut into equal ranges (chunk_plan.h), so decoding
+// requests and chunks of prompts share a call, and few long requests still fill the GPU.
+//
+// MT = 1: up to 128 rows per item; S of a chunk in one of three buffers of 128 columns; two Q
+// buffers. MT = 2: up to 256 rows as two tiles on the same K and V. Tensor memory holds 512
+// columns, 2 x 128 of them O: S goes by halves of a chunk (64 keys), two buffers of 64 columns
+// per tile.
+//
+//   warp 0      issues S;  warp 1 issues P V (an elected lane of a converged warp);
+//   warp 2      walks the CTA's range and publishes segments
+//   warp 3      bf16: looks over the V rows that only some rows of the item see (below);
+//               8 bits: copies the queries
+//   warps 4-7   bf16: copies K and V rows through the block table with 16-byte cp.async into
+//               128-byte-swizzled tiles (any block size: a key's row is found on its own), and Q.
+//               8 bits: the same copies bring the codes to buffers of their own, two chunks
+//               ahead; each thread turns the codes that it copied into bf16 and stores those
+//   warps 8-    softmax, a row per thread, four warps per tile; at a segment's end O / l to
+//               global memory, or the unnormalised O with (m, l) to a partial slot
+//
+// Keys that no row of the item sees are filled with zeros, not read. In chunks with keys that
+// some of its rows see and others do not (the new tokens themselves, and the keys that leave the
+// window between the first and the last of them), values of V that are not finite become zero in
+// shared memory, so that 0 * v stays 0 for the rows that do not see the key; the rows that see it
+// get the value added at the end.
+//
+// Codes become bf16 with integer operations and one product: e4m3 is s eeee mmm with bias 7, and
+// those bits put at s 0000eeee mmm0000 of a bf16 (bias 127) are the value times 2^-120, subnormal
+// numbers too; a product with 2^120 and the head's scale, exact, gives the value.
+namespace {
+constexpr int kHd = 128;
+constexpr int kStatusShape = -2;               // TP_ERR_SHAPE
+constexpr int kTileBytes = 128 * 128 * 2;      // 128 rows x 128 bf16: two 64-column boxes
+constexpr int kCodeBytes = 128 * 128;          // codes of 128 keys
+constexpr int kUnitSlots = 4;
+constexpr float kRescaleLog2 = 8.0f;           // rescale O when the row max grows by more than this
+// m is the row max and this much more, so that weights are at most 2^(8 - 17): a sum of 512 weighted
+// bf16 numbers fits fp32 (any v < 2^137 / L does for L keys), and so do products with v of 2^-100
+constexpr float kHeadroomLog2 = 17.0f;
+constexpr uint32_t kIdescO = idesc_bf16_f32(128, 128) | kIdescBMnMajor;
+constexpr int kTmemCols = 512;
+
+template <int MT, bool Q8>
+struct ChunkCfg {
+  static constexpr int kThreads = 256 + 128 * MT;
+  static constexpr int kTiles = Q8 ? 3 : 5;                // K/V ring
+  static constexpr int kAhead = 4;                         // tiles of codes in flight
+  static constexpr int kQBufs = MT == 1 ? 2 : 1;
+  static constexpr int kSub = MT == 1 ? 128 : 64;          // keys of one S, softmax and P V
+  static constexpr int kSubs = kChunkKeys / kSub;
+  static constexpr int kSBufs = MT == 1 ? 3 : 2;           // S/P buffers of a tile
+  static constexpr uint32_t kIdescS = idesc_bf16_f32(128, kSub);
+  static constexpr int kRingOff = MT * kQBufs * kTileBytes;   // after Q
+  static constexpr int kCodeOff = kRingOff + kTiles * kTileBytes;
+  static constexpr int kBarOff = kCodeOff + (Q8 ? kAhead * kCodeBytes : 0);
+  // registers: issuers, copies, softmax
+  static constexpr int kRegs0 = 80, kRegs1 = MT == 1 ? 152 : 96, kRegsS = MT == 1 ? 232 : 168;
+  static constexpr int kLaunchRegs = MT == 1 ? 168 : 128;
+  static_assert(128 * (kRegs0 + kRegs1 + MT * kRegsS) <= kThreads * kLaunchRegs, "register split within the launch's");
+  // tensor memory: MT = 1: S/P at 0, 128, 256, O at 384; MT = 2: tile m S/P at 256 m and 256 m + 64, O at 256 m + 128
+  static __device__ __forceinline__ uint32_t s_col(int tile, int buf) { return tile * 256 + (buf - tile * kSBufs) * kSub; }
+  static __device__ __forceinline__ uint32_t o_col(int tile) { return MT == 1 ? 384 : tile * 256 + 128; }
+  enum {
+    Q_FULL = 0, Q_EMPTY = Q_FULL + kQBufs, FULL = Q_EMPTY + kQBufs, EMPTY = FULL + kTiles,
+    S_FULL = EMPTY + kTiles,          // per S/P buffer of every tile
+    P_READY = S_FULL + MT * kSBufs,
+    S_FREE = P_READY + MT * kSBufs,   // its P V has completed
+    O_FREE = S_FREE + MT * kSBufs,    // per tile
+    LANDED = O_FREE + MT,             // bf16: a V tile to be looked over, per ring tile
+    U_FULL = LANDED + kTiles, U_EMPTY = U_FULL + kUnitSlots,
+    DONE_S = U_EMPTY + kUnitSlots, DONE_PV, NBARS
+  };
+  static constexpr int kMiscOff = kBarOff + 8 * NBARS;     // tensor memory address, abort flag
+  static constexpr int kUnitOff = (kMiscOff + 8 + 15) / 16 * 16;
+  static constexpr int kSmem = 1024 + kUnitOff + kUnitSlots * 64;
+  static_assert(kSmem <= 232448, "shared memory of one CTA");
+};
+
+// A segment: chunks [c0, c1) of one item. b < 0: no more.
+struct __align__(16) ChunkSegment {
+  int b, r, g, tok0;                 // request, shard, kv head of the shard, first new token of the group
+  int c0, c1, q0, ctx;               // chunks; row of the request's first new token; cached tokens
+  int part, rows, bad, skip;         // partial slot or -1; query rows; V not finite; key chunks left out from sc on
+  int p0, p1, pad0, pad1;            // positions of the group's first and last token
+};
+static_assert(sizeof(ChunkSegment) == 64, "unit slots");
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Codes 2 h and 2 h + 1 of a word as bf16, 2^-120 of their values.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int h) {
+  const uint32_t r = __byte_perm(w, 0u, h == 0 ? 0x1404 : 0x3424);
+  return (r & 0x80008000u) | ((r >> 4) & 0x07f007f0u);
+}
+// 2^(s - 127 + 120) of a scale byte twice as bf16; past the largest power the rest is in the second
+// factor. kDropRow: 0.
+constexpr uint32_t kScaleNan = 255u, kDropRow = 256u;
+__device__ __forceinline__ uint32_t scale_factor(uint32_t s) {
+  return (s == kDropRow ? 0u : s == kScaleNan ? 0x7fc0u : min(s + 120u, 254u) << 7) * 0x10001u;
+}
+__device__ __forceinline__ uint32_t scale_rest(uint32_t s) {
+  return (s > 134u && s < kScaleNan ? s - 7u << 7 : 0x3f80u) * 0x10001u;
+}
+// Key chunk of chunk j of an item.
+__device__ __forceinline__ int key_chunk(int j, int sc, int skip) { return j + (j >= sc ? skip : 0); }
+}  // namespace
+
+// Partial results of a slot: O as [16][rows][8] fp32 (pieces of eight dimensions, so that the
+// 32 rows of a warp write 1 KB on end), then [rows][2] (max in the exp2 domain, sum).
+// part_rows is a multiple of 8 and the first slot 32-byte aligned: every piece starts on 32 bytes.
+__device__ __forceinline__ float* chunk_part_o(const ChunkAttnParams& p, int slot, int row, int d) {
+  return p.partials + (size_t)slot * p.part_rows * (kHd + 2) + ((size_t)(d >> 3) * p.part_rows + row) * 8 + (d & 7);
+}
+__device__ __forceinline__ float2* chunk_part_ml(const ChunkAttnParams& p, int slot, int row) {
+  return reinterpret_cast<float2*>(p.partials + (size_t)slot * p.part_rows * (kHd + 2) + (size_t)p.part_rows * kHd) + row;
+}
+
+template <int MT, bool Q8>
+__global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kernel(const ChunkAttnParams p) {
+  using C = ChunkCfg<MT, Q8>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  uint8_t* base_ptr = smem_raw + (base - raw_addr);
+  auto bar = [&](int b) { return base + C::kBarOff + 8u * b; };
+  volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(base_ptr + C::kMiscOff);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(base_ptr + C::kMiscOff + 4);
+  ChunkSegment* s_seg = reinterpret_cast<ChunkSegment*>(base_ptr + C::kUnitOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  griddep_launch_dependents();   // the merge grid may be scheduled; it waits for this one to complete
+  if (warp == 0) {
+    for (int b = lane; b < C::NBARS; b += 32) {
+      int count = 1;
+      if (b < C::Q_EMPTY) count = Q8 ? 32 : 128;                                // every thread that copies queries
+      if (b >= C::FULL && b < C::EMPTY) count = 128;                            // every copying thread
+      if (b >= C::P_READY && b < C::S_FREE) count = 4;                          // the tile's softmax warps
+      if (b >= C::S_FREE && b < C::O_FREE) count = 2;                           // the MMAs, and their issuer
+      if (b >= C::O_FREE && b < C::LANDED) count = 4;
+      if (b >= C::LANDED && b < C::U_FULL) count = 128;
+      if (b >= C::U_EMPTY && b < C::DONE_S) count = 3 + 4 + 4 * MT;             // issuers, warp 3, copy and softmax warps
+      mbar_init(bar(b), count);
+    }
+    if (lane == 0) *s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(const_cast<uint32_t*>(s_tmem)), kTmemCols);
+    tmem_relinquish();
+  }
+  // the set-up above may overlap the grid before (programmatic launch); nothing that grid
+  // wrote is read before this
+  griddep_wait();
+  const int gq = p.call.gq;                         // q heads of a kv head
+  const int sc = chunk_sinks(p.call), window = p.call.window, sinks = p.call.sinks;
+  // warp 2: requests `lane`, `lane` + 32, .. of a batch of 128 (row of the first new token, new tokens, all
+  // tokens; -1: bad counts), loaded together; the first batch here, beside the set-up
+  constexpr int kStrips = 4;
+  int3 mine[kStrips];
+  auto counts = [&](int b) {
+    const ChunkReq r = chunk_request(p.call, p.qsl[b], p.qsl[b + 1], p.seq_lens[b]);
+    return make_int3(r.q0, r.ok ? r.n : -1, r.ctx + r.n);
+  };
+  auto load_batch = [&](int b0) {
+#pragma unroll
+    for (int i = 0; i < kStrips; ++i) {
+      const int b = b0 + 32 * i + lane;
+      mine[i] = b < p.n_reqs ? counts(b) : make_int3(0, 0, 0);
+    }
+  };
+  if (warp == 2) load_batch(0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+  const unsigned long long timeout = p.timeout_ns;
+  // row / gq as a product: 2^32 / gq rounded up is off by less than 1, and row * gq < 2^32
+  const unsigned gq_magic = 0xffffffffu / (unsigned)gq + 1u;
+  auto token_of = [&](int row) { return gq == 1 ? row : (int)__umulhi((unsigned)row, gq_magic); };
+  bool ok = true;
+  // a wait of a whole warp
+  auto wait = [&](int b, uint32_t ph) -> bool {
+    bool w = mbar_wait_bounded(bar(b), ph, s_abort, timeout);
+    w = __all_sync(0xffffffffu, w);
+    if (!w) {
+      if (lane == 0 && !*s_abort) {
+        atomicExch(p.status, kStatusTimeout);
+        *s_abort = 1;
+      }
+      ok = false;
+    }
+    return w;
+  };
+  // the next segment's slot, or -1 at the end
+  int nu = 0;
+  auto next_segment = [&]() -> int {
+    const int slot = nu % kUnitSlots;
+    if (!wait(C::U_FULL + slot, (nu / kUnitSlots) & 1)) return -1;
+    ++nu;
+    return s_seg[slot].b < 0 ? -1 : slot;
+  };
+  auto release_segment = [&](int slot) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::U_EMPTY + slot));
+  };
+  // a key that some tokens of the item see and others do not, of those that any sees
+  auto partly_seen = [&](int key, int p0, int p1) {
+    return key > p0 || (window > 0 && key <= p1 - window && key >= sinks);
+  };
+  // whether key chunk kc has such keys
+  auto mixed_chunk = [&](int kc, int p0, int p1) {
+    const int k0 = kc * kChunkKeys, k1 = k0 + kChunkKeys - 1;
+    return p1 > p0 && (k1 > p0 || (window > 0 && k0 <= p1 - window && k1 > p0 - window && k1 >= sinks));
+  };
+  // whether any token of the item sees the key
+  auto any_sees = [&](int key, int p0, int p1) {
+    return key <= p1 && (window == 0 || key > p0 - window || key < sinks);
+  };
+  // cache row of a key of request b for shard r: a head's elements are at (row * kv_per + g) * hd; -1 on a bad block
+  auto cache_row = [&](int r, int blk, int key) {
+    return blk >= 0 && blk < p.num_blocks ? (r * p.num_blocks + blk) * p.block_size + key % p.block_size : -1;
+  };
+
+  if (warp < 4) {
+    regs_dec<C::kRegs0>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ S = Q K^T
+      const uint64_t q_desc = smem_desc_k128(base);
+      const uint64_t k_desc = smem_desc_k128(base + C::kRingOff);
+      constexpr uint64_t kTileDesc = kTileBytes >> 4;
+      int ring = 0;                                   // tile of the next K
+      uint32_t ring_ph = 0;
+      int cnt[MT] = {};                               // S of each tile so far
+      for (int seg_no = 0;; ++seg_no) {
+        const int slot = next_segment();
+        if (slot < 0) break;
+        const int n = s_seg[slot].c1 - s_seg[slot].c0, rows = s_seg[slot].rows;
+        release_segment(slot);
+        const int qb = seg_no % C::kQBufs;
+        if (!wait(C::Q_FULL + qb, (seg_no / C::kQBufs) & 1)) break;
+        for (int j = 0; j < n && ok; ++j) {
+          // The first S of the chunk waits for its buffer before it waits for K: that P V is done, so the
+          // V that the ring's tile held before, handed on late by warp 3, has been counted, and the next
+          // phase of the tile's barrier is this K's (two phases ahead would look like the one before).
+          if (!wait(C::S_FREE + cnt[0] % C::kSBufs, ((cnt[0] / C::kSBufs) & 1) ^ 1)) break;
+          if (!wait(C::FULL + ring, ring_ph)) break;
+          fence_async_proxy();
+#pragma unroll
+          for (int h = 0; h < C::kSubs; ++h) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              if (m * 128 >= rows) break;
+              const int buf = m * C::kSBufs + cnt[m] % C::kSBufs;
+              if ((h > 0 || m > 0) && !wait(C::S_FREE + buf, ((cnt[m] / C::kSBufs) & 1) ^ 1)) break;
+              ++cnt[m];
+              tc_fence_after();
+              if (elect_one()) {
+                const uint32_t d = tmem_base + C::s_col(m, buf);
+                // half h of the chunk: 64 K rows of 128 bytes further
+                const uint64_t qd = q_desc + (qb * MT + m) * kTileDesc, kd = k_desc + ring * kTileDesc + h * ((64 * 128) >> 4);
+                tc_mma_bf16_c<false>(d, qd, kd, C::kIdescS);
+#pragma unroll
+                for (int k = 1; k < 8; ++k) {
+                  const uint64_t o = (uint64_t)(((k >> 2) * (kTileBytes / 2) + (k & 3) * 32) >> 4);
+                  tc_mma_bf16_c<true>(d, qd + o, kd + o, C::kIdescS);
+                }
+                tc_commit(bar(C::S_FULL + buf));
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+          }
+          if (!ok) break;
+          if (elect_one()) {
+            tc_commit(bar(C::EMPTY + ring));
+            if (j == n - 1) tc_commit(bar(C::Q_EMPTY + qb));
+          }
+          __syncwarp();
+          ring += 2;
+          if (ring >= C::kTiles) {
+            ring -= C::kTiles;
+            ring_ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+      }
+      if (elect_one()) tc_commit(bar(C::DONE_S));
+      __syncwarp();
+      mbar_wait_bounded(bar(C::DONE_S), 0, nullptr, kTeardownNs);
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ O += P V
+      const uint64_t v_desc = smem_desc_mn128(base + C::kRingOff, kTileBytes / 2);
+      constexpr uint64_t kTileDesc = kTileBytes >> 4;
+      int ring = 1;                                   // tile of the next V
+      uint32_t ring_ph = 0;
+      int cnt[MT] = {}, segs[MT] = {};
+      for (;;) {
+        const int slot = next_segment();
+        if (slot < 0) break;
+        const int n = s_seg[slot].c1 - s_seg[slot].c0, rows = s_seg[slot].rows;
+        release_segment(slot);
+        for (int j = 0; j < n && ok; ++j) {
+          if (!wait(C::FULL + ring, ring_ph)) break;
+          fence_async_proxy();
+#pragma unroll
+          for (int h = 0; h < C::kSubs; ++h) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              if (m * 128 >= rows) break;
+              const int buf = m * C::kSBufs + cnt[m] % C::kSBufs;
+              if (!wait(C::P_READY + buf, (cnt[m] / C::kSBufs) & 1)) break;
+              const bool first = j == 0 && h == 0;
+              if (first && !wait(C::O_FREE + m, (segs[m]++ & 1) ^ 1)) break;
+              ++cnt[m];
+              tc_fence_after();
+              if (elect_one()) {
+                const uint32_t pa = tmem_base + C::s_col(m, buf), d = tmem_base + C::o_col(m);
+                const uint64_t vd = v_desc + ring * kTileDesc + h * ((64 * 128) >> 4);
+                // 16 keys = two 8-row groups of V (2048 B) and 8 columns of P
+                if (first)
+                  tc_mma_bf16_ta_c<false>(d, pa, vd, kIdescO);
+                else
+                  tc_mma_bf16_ta_c<true>(d, pa, vd, kIdescO);
+#pragma unroll
+                for (int k = 1; k < C::kSub / 16; ++k)
+                  tc_mma_bf16_ta_c<true>(d, pa + k * 8, vd + (uint64_t)(k * (2048 >> 4)), kIdescO);
+                tc_commit(bar(C::S_FREE + buf));
+                mbar_arrive(bar(C::S_FREE + buf));    // carries the `bad` mark to the softmax
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+          }
+          if (!ok) break;
+          if (elect_one()) tc_commit(bar(C::EMPTY + ring));
+          __syncwarp();
+          ring += 2;
+          if (ring >= C::kTiles) {
+            ring -= C::kTiles;
+            ring_ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+      }
+      if (elect_one()) tc_commit(bar(C::DONE_PV));
+      __syncwarp();
+      mbar_wait_bounded(bar(C::DONE_PV), 0, nullptr, kTeardownNs);
+      __syncwarp();
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ segments
+      const int heads = p.t * p.kv_per;
+      auto request = [&](int3 m) {                    // the request of its counts (none where they are bad)
+        return chunk_request(p.call, m.x, m.x + max(m.y, 0), m.z);
+      };
+      auto broadcast = [&](int3 m, int from) {
+        return request(make_int3(__shfl_sync(0xffffffffu, m.x, from), __shfl_sync(0xffffffffu, m.y, from),
+                                 __shfl_sync(0xffffffffu, m.z, from)));
+      };
+      auto sum = [&](long long v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+      };
+      // a head's places of all requests with an item cost of 0 and its items; CTA 0 reports bad counts.
+      // A batch's places are kept: they are looked up again for the CTA's first request.
+      long long places = 0, items = 0, kept[kStrips];
+      int widest = 1;
+      for (int b0 = 0; b0 < p.n_reqs; b0 += 32 * kStrips) {
+        if (b0 > 0) load_batch(b0);
+#pragma unroll
+        for (int i = 0; i < kStrips; ++i) {
+          if (mine[i].y < 0 && blockIdx.x == 0) atomicExch(p.status, kStatusShape);
+          const ChunkReq q = request(mine[i]);
+          kept[i] = chunk_head(p.call, q, 0);
+          places += kept[i];
+          items += q.groups;
+          widest = max(widest, chunk_widest(p.call, q));
+        }
+      }
+      places = heads * sum(places);
+      const int cost = chunk_cost(places, p.call.full, gridDim.x);
+      const long long total = places + heads * cost * sum(items);
+      const long long per = chunk_per(total, gridDim.x, __reduce_max_sync(0xffffffffu, widest));
+      long long pos = per * blockIdx.x;
+      const long long end = min(total, pos + per);
+      // the request that holds the first place, and the places before it
+      ChunkReq r{};
+      int b = 0;
+      long long before = 0, head_places = 0;
+      if (pos < end) {
+        bool found = false;
+        for (int b0 = 0; b0 < p.n_reqs && !found; b0 += 32 * kStrips) {
+          const bool again = p.n_reqs > 32 * kStrips;
+          if (again) load_batch(b0);
+#pragma unroll
+          for (int i = 0; i < kStrips; ++i) {
+            if (found) break;
+            const ChunkReq q = request(mine[i]);
+            const long long one = (again ? chunk_head(p.call, q, 0) : kept[i]) + (long long)cost * q.groups, w = heads * one;
+            long long pre = w;                        // the strip's places up to and with this lane's
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const long long up = __shfl_up_sync(0xffffffffu, pre, o);
+              if (lane >= o) pre += up;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, before + pre > pos);
+            if (hit != 0u) {
+              const int f = __ffs(hit) - 1;
+              b = b0 + 32 * i + f;
+              before += __shfl_sync(0xffffffffu, pre - w, f);
+              head_places = __shfl_sync(0xffffffffu, one, f);
+              r = broadcast(mine[i], f);
+              found = true;
+            } else {
+              before += __shfl_sync(0xffffffffu, pre, 31);
+            }
+          }
+        }
+      }
+      // the item that holds the first place: head, group and its own first place on the line
+      int head = 0, group = 0;
+      long long begin = 0;
+      if (pos < end) {
+        head = (int)((pos - before) / head_places);
+        const long long at = pos - before - head * head_places;
+        // the last group whose prefix is not past `at`: 32 candidates at a time
+        int lo = 0, n = r.groups;
+        while (n > 1) {
+          const int step = (n + 31) / 32, g = lo + lane * step;
+          const bool in = g < lo + n && chunk_prefix(p.call, r, g, cost) <= at;
+          const int last = 31 - __clz(__ballot_sync(0xffffffffu, in));
+          n = min(step, lo + n - (lo + last * step));
+          lo += last * step;
+        }
+        group = lo;
+        begin = before + head * head_places + chunk_prefix(p.call, r, group, cost);
+      }
+      // no item of this CTA is continued by others, unless a segment says so below
+      if (lane == 0) p.items[blockIdx.x].rows = 0;
+      __syncwarp();
+      for (int u = 0;; ++u) {
+        const int slot = u % kUnitSlots;
+        if (!wait(C::U_EMPTY + slot, ((u / kUnitSlots) & 1) ^ 1)) break;
+        ChunkSegment s;
+        s.b = -1;
+        while (pos < end) {
+          const ChunkKeys keys = chunk_item_keys(p.call, r, group);
+          const int width = chunk_width(p.call, r, group);
+          const long long item = cost + (long long)keys.count * width, p1 = min(item, end - begin);
+          const ChunkPart q = chunk_part(pos - begin, p1, cost, width, keys.count, blockIdx.x);
+          const int it_head = head, it_group = group, it_b = b;
+          const ChunkReq it = r;
+          const long long it_begin = begin;
+          pos = begin + p1;
+          if (p1 == item && pos < end) {               // on to the next item
+            begin = pos;
+            if (++group == r.groups) {
+              group = 0;
+              if (++head == heads) {
+                head = 0;
+                for (;; b += 32) {                     // the next request with new tokens
+                  const int next = b + 1 + lane;
+                  const int3 m = next < p.n_reqs ? counts(next) : make_int3(0, 0, 0);
+                  const unsigned hit = __ballot_sync(0xffffffffu, m.y > 0);
+                  if (hit != 0u) {
+                    const int f = __ffs(hit) - 1;
+                    b += 1 + f;
+                    r = broadcast(m, f);
+                    break;
+                  }
+                  if (b + 32 >= p.n_reqs) {            // cannot be: a place before `end` belongs to a request
+                    pos = end;
+                    break;
+                  }
+                }
+              }
+            }
+          }
+          if (q.c0 == q.c1) continue;                  // no chunk begins in these places
+          s.b = it_b;
+          s.r = it_head / p.kv_per;
+          s.g = it_head - s.r * p.kv_per;
+          s.tok0 = it_group * p.call.tg;
+          s.c0 = q.c0;
+          s.c1 = q.c1;
+          s.q0 = it.q0;
+          s.ctx = it.ctx;
+          s.part = q.slot;
+          const int tokens = min(p.call.tg, it.n - s.tok0);
+          s.rows = tokens * gq;
+          s.bad = 0;
+          s.skip = keys.skip;
+          s.p0 = it.ctx + s.tok0;
+          s.p1 = s.p0 + tokens - 1;
+          s.pad0 = s.pad1 = 0;
+          if (q.c0 == 0 && q.slot >= 0 && lane == 0) {
+            const int last = chunk_last(it_begin, cost, width, keys.count, per);
+            p.items[blockIdx.x] = TreeItem{s.r, s.g, 0, s.rows, s.q0 + s.tok0, last, 0, 0};
+          }
+          break;
+        }
+        if (lane == 0) {
+          s_seg[slot] = s;
+          mbar_arrive(bar(C::U_FULL + slot));
+        }
+        __syncwarp();
+        if (s.b < 0) break;
+      }
+    } else if (Q8) {
+      // ------------------------------------------------------------ queries
+      const uint64_t pol = policy_evict_normal();
+      const int c16 = lane & 15, half = lane >> 4;
+      for (int seg_no = 0;; ++seg_no) {
+        const int slot = next_segment();
+        if (slot < 0) break;
+        const int rows = s_seg[slot].rows, r = s_seg[slot].r, g = s_seg[slot].g, q0 = s_seg[slot].q0 + s_seg[slot].tok0;
+        release_segment(slot);
+        const int qb = seg_no % C::kQBufs;
+        if (!wait(C::Q_EMPTY + qb, ((seg_no / C::kQBufs) & 1) ^ 1)) break;
+        const __nv_bfloat16* q = p.qkv + (size_t)r * p.sstride_in + (size_t)q0 * p.rstride_in + g * gq * kHd + c16 * 8;
+        const uint32_t dst = base + qb * MT * kTileBytes + (c16 >> 3) * (kTileBytes / 2);
+        // rows past the item's keep what the buffer held: they only reach their own rows of S and O
+#pragma unroll 4
+        for (int j = half; j < rows; j += 2) {
+          const int tok = token_of(j);
+          cp_async16(dst + (j >> 7) * kTileBytes + (j & 127) * 128 + (((c16 & 7) ^ (j & 7)) << 4),
+                     q + (size_t)tok * p.rstride_in + (j - tok * gq) * kHd, 16, pol);
+        }
+        cp_async_arrive(bar(C::Q_FULL + qb));
+      }
+      cp_async_wait_all();     // no copy into this CTA's shared memory may outlive it
+    } else {
+      // ------------------------------------------------------------ V that only some rows see
+      int ring = 1;                                   // tile of the next V
+      uint32_t phases = 0;                            // bit i: phase of LANDED + i
+      for (;;) {
+        const int slot = next_segment();
+        if (slot < 0) break;
+        const int c0 = s_seg[slot].c0, c1 = s_seg[slot].c1, p0 = s_seg[slot].p0, p1 = s_seg[slot].p1, skip = s_seg[slot].skip;
+        bool bad = false;
+        for (int c = c0; c < c1; ++c) {
+          const int kc = key_chunk(c, sc, skip);
+          if (mixed_chunk(kc, p0, p1)) {
+            if (!wait(C::LANDED + ring, phases >> ring & 1u)) break;
+            phases ^= 1u << ring;
+            // a row is 8 pieces of 16 bytes in each of two boxes, in any order
+            const int k0 = kc * kChunkKeys, box = (lane >> 3) & 1, piece = lane & 7;
+            uint8_t* v = base_ptr + C::kRingOff + ring * kTileBytes + box * (kTileBytes / 2) + piece * 16;
+#pragma unroll 4
+            for (int row = lane >> 4; row < kChunkKeys; row += 2) {
+              if (!partly_seen(k0 + row, p0, p1)) continue;
+              uint4* q = reinterpret_cast<uint4*>(v + row * 128);
+              uint4 d = *q;
+              const bool x = drop_nonfinite(d.x), y = drop_nonfinite(d.y), z = drop_nonfinite(d.z), w = drop_nonfinite(d.w);
+              if (x || y || z || w) {
+                *q = d;
+                bad = true;
+              }
+            }
+            bad = __any_sync(0xffffffffu, bad);
+            __syncwarp();                             // every lane's stores, before lane 0 hands the tile on
+            if (lane == 0) {
+              if (bad) *reinterpret_cast<volatile int*>(&s_seg[slot].bad) = 1;
+              mbar_arrive_n(bar(C::FULL + ring), 128);   // for the copying threads
+            }
+          }
+          ring += 2;
+          if (ring >= C::kTiles) ring -= C::kTiles;
+        }
+        if (!ok) break;
+        release_segment(slot);
+      }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ copies
+    regs_dec<C::kRegs1>();
+    const int w4 = warp - 4;
+    // the cache is read once a call by one item (evicted first) or by its groups of rows
+    const uint64_t pol = p.call.max_query_len > p.call.tg ? policy_evict_normal() : policy_evict_first();
+    int ring = 0;
+    uint32_t ring_ph = 0;
+    auto advance = [&]() {
+      if (++ring == C::kTiles) {
+        ring = 0;
+        ring_ph ^= 1u;
+      }
+    };
+    if constexpr (!Q8) {
+      const int c16 = lane & 15, half = lane >> 4;
+      // this thread copies 16-byte piece c16 of rows 2 w4 + half + 8 k; lane i of the warp finds the
+      // cache row of row 8 (i / 2) + 2 w4 + i % 2
+      const int row_of = 2 * w4 + half, my_row = 8 * (lane >> 1) + 2 * w4 + (lane & 1);
+      const uint32_t dst0 = (c16 >> 3) * (kTileBytes / 2) + row_of * 128 + (((c16 & 7) ^ (row_of & 7)) << 4);
+      const __nv_bfloat16* cache_k = static_cast<const __nv_bfloat16*>(p.cache_k);
+      const __nv_bfloat16* cache_v = static_cast<const __nv_bfloat16*>(p.cache_v);
+      // a segment's queries, once those that the buffer held are no longer read
+      auto load_q = [&](const ChunkSegment& s, int seg_no) {
+        const int qb = seg_no % C::kQBufs;
+        if (!wait(C::Q_EMPTY + qb, ((seg_no / C::kQBufs) & 1) ^ 1)) return;
+        const __nv_bfloat16* q = p.qkv + (size_t)s.r * p.sstride_in + (size_t)(s.q0 + s.tok0) * p.rstride_in + s.g * gq * kHd + c16 * 8;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if (m * 128 >= s.rows) break;
+          // rows past the item's keep what the buffer held: they only reach their own rows of S and O
+#pragma unroll 4
+          for (int k = 0; k < 16; ++k) {
+            const int j = m * 128 + row_of + 8 * k, tok = token_of(j);
+            if (j < s.rows)
+              cp_async16(base + (qb * MT + m) * kTileBytes + dst0 + k * 1024,
+                         q + (size_t)tok * p.rstride_in + (j - tok * gq) * kHd, 16, pol);
+          }
+        }
+        cp_async_arrive(bar(C::Q_FULL + qb));
+      };
+      for (int seg_no = 0;; ++seg_no) {
+        const int slot = next_segment();
+        if (slot < 0) break;
+        const ChunkSegment s = s_seg[slot];
+        const int* bt = p.block_tables + (size_t)s.b * p.max_blocks;
+        auto block_of = [&](int c) -> int {            // block id of this lane's key of chunk c
+          const int key = key_chunk(c, sc, s.skip) * kChunkKeys + my_row;
+          return any_sees(key, s.p0, s.p1) ? bt[key / p.block_size] : 0;
+        };
+        int blk = block_of(s.c0);
+        // with one Q buffer the last segment's queries may still be read: the first K tile goes before
+        // (and the queries' rows, 256 bytes each, start for L2: their copy is what S waits for)
+        const bool q_first = C::kQBufs > 1 || seg_no == 0;
+        if (q_first) {
+          load_q(s, seg_no);
+        } else {
+          for (int j = threadIdx.x - 128; j < 2 * s.rows; j += 128) {
+            const int tok = token_of(j >> 1);
+            prefetch_l2(p.qkv + (size_t)s.r * p.sstride_in + (size_t)(s.q0 + s.tok0 + tok) * p.rstride_in +
+                        (s.g * gq + (j >> 1) - tok * gq) * kHd + (j & 1) * 64);
+          }
+        }
+        for (int c = s.c0; c < s.c1 && ok; ++c) {
+          const int kc = key_chunk(c, sc, s.skip), key = kc * kChunkKeys + my_row;
+          int row = -1;                                // cache row of this lane's key (-1: zeros)
+          if (any_sees(key, s.p0, s.p1)) {
+            row = cache_row(s.r, blk, key);
+            if (row < 0) atomicExch(p.status, kStatusShape);
+          }
+          if (c + 1 < s.c1) blk = block_of(c + 1);
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!wait(C::EMPTY + ring, ring_ph ^ 1)) break;
+            const __nv_bfloat16* src = (kv ? cache_v : cache_k) + s.g * kHd + c16 * 8;
+            const uint32_t dst = base + C::kRingOff + ring * kTileBytes + dst0;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int rw = __shfl_sync(0xffffffffu, row, 2 * k + half);
+              cp_async16(dst + k * 1024, src + (size_t)max(rw, 0) * p.kv_per * kHd, rw >= 0 ? 16 : 0, pol);
+            }
+            cp_async_arrive(bar((kv == 1 && mixed_chunk(kc, s.p0, s.p1) ? C::LANDED : C::FULL) + ring));
+            advance();
+            if (kv == 0 && c == s.c0 && !q_first) load_q(s, seg_no);
+            if (!ok) break;
+          }
+        }
+        if (!ok) break;
+        release_segment(slot);
+      }
+    } else {
+      // this warp has rows 32 w4 + (0 .. 31) of a tile; the thread copies and converts 16-byte piece
+      // c8 of rows 32 w4 + 4 k + sub, and finds the cache row of row 32 w4 + lane
+      const int c8 = lane & 7, sub = lane >> 3;
+      const uint8_t* cache_k = static_cast<const uint8_t*>(p.cache_k);
+      const uint8_t* cache_v = static_cast<const uint8_t*>(p.cache_v);
+      const uint32_t raw = base + C::kCodeOff + (threadIdx.x - 128) * 16;    // + tile, + 2048 k: read by this thread alone
+      int issued = 0, converted = 0;                  // tiles so far: their buffers of codes
+      // the two cursors: chunks are issued two ahead of those converted
+      int a_slot = -1, a_c = 0, a_c1 = 0, blk = 0;
+      bool a_end = false;
+      ChunkSegment s{};                               // the issuing cursor's segment
+      // a chunk in flight: its scale bytes for this lane's row; V of that row is only partly seen
+      struct Flight { uint32_t k, v; bool part; };
+      auto block_of = [&](int c) -> int {
+        const int key = key_chunk(c, sc, s.skip) * kChunkKeys + 32 * w4 + lane;
+        return any_sees(key, s.p0, s.p1) ? p.block_tables[(size_t)s.b * p.max_blocks + key / p.block_size] : 0;
+      };
+      int row = -1;
+      // moves the issuing cursor to its next chunk: `row` and the scale bytes of that; false at the end
+      auto next_chunk = [&](Flight& f) -> bool {
+        if (a_end) return false;
+        if (a_c == a_c1) {
+          a_slot = next_segment();
+          if (a_slot < 0) {
+            a_end = true;
+            return false;
+          }
+          s = s_seg[a_slot];
+          a_c = s.c0;
+          a_c1 = s.c1;
+          blk = block_of(a_c);
+        }
+        const int key = key_chunk(a_c, sc, s.skip) * kChunkKeys + 32 * w4 + lane;
+        row = -1;
+        f.k = f.v = 127u;
+        f.part = false;
+        if (any_sees(key, s.p0, s.p1)) {
+          row = cache_row(s.r, blk, key);
+          if (row < 0) atomicExch(p.status, kStatusShape);
+          f.part = partly_seen(key, s.p0, s.p1);
+        }
+        if (row >= 0) {
+          const size_t at = (size_t)row * p.kv_per + s.g;
+          f.k = p.scales_k[at];
+          f.v = p.scales_v[at];
+        }
+        ++a_c;
+        if (a_c < a_c1) blk = block_of(a_c);
+        return true;
+      };
+      auto issue = [&](const uint8_t* cache) {
+        const uint8_t* src = cache + s.g * kHd + c8 * 16;
+        const uint32_t dst = raw + (issued % C::kAhead) * kCodeBytes;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int rw = __shfl_sync(0xffffffffu, row, 4 * k + sub);
+          cp_async16(dst + k * 2048, src + (size_t)max(rw, 0) * p.kv_per * kHd, rw >= 0 ? 16 : 0, pol);
+        }
+      };
+      // codes of the oldest tile in flight to the next tile of the ring; scale: of this lane's row
+      auto convert = [&](uint32_t scale) -> bool {
+        cp_async_wait<C::kAhead - 1>();
+        if (!wait(C::EMPTY + ring, ring_ph ^ 1)) return false;
+        const uint32_t src = raw + (converted % C::kAhead) * kCodeBytes;
+        const uint32_t fac = scale_factor(scale), rest = scale_rest(scale);
+        const bool large = __any_sync(0xffffffffu, rest != 0x3f803f80u);
+        // the piece's two 16-byte halves: chunks 2 c8 and 2 c8 + 1 of the row's sixteen; in the second
+        // box the odd one is written first, so that eight lanes write eight different banks groups
+        const int swap = c8 >> 2;
+        const uint32_t dst = base + C::kRingOff + ring * kTileBytes + (c8 >> 2) * (kTileBytes / 2) + (32 * w4 + sub) * 128;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint4 w = lds128(src + k * 2048);
+          const uint32_t f = __shfl_sync(0xffffffffu, fac, 4 * k + sub);
+          uint32_t x[8] = {code_pair(w.x, 0), code_pair(w.x, 1), code_pair(w.y, 0), code_pair(w.y, 1),
+                           code_pair(w.z, 0), code_pair(w.z, 1), code_pair(w.w, 0), code_pair(w.w, 1)};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = mul_bf16x2(x[i], f);
+          if (large) {
+            const uint32_t f2 = __shfl_sync(0xffffffffu, rest, 4 * k + sub);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = mul_bf16x2(x[i], f2);
+          }
+          const int rr = (4 * k + sub) & 7;           // row & 7
+          const uint32_t even = ((2 * (c8 & 3)) ^ rr) << 4, odd = ((2 * (c8 & 3) + 1) ^ rr) << 4;
+          const uint32_t at = dst + 4 * k * 128;
+          if (swap) {
+            sts128(at + odd, x[4], x[5], x[6], x[7]);
+            sts128(at + even, x[0], x[1], x[2], x[3]);
+          } else {
+            sts128(at + even, x[0], x[1], x[2], x[3]);
+            sts128(at + odd, x[4], x[5], x[6], x[7]);
+          }
+        }
+        fence_async_proxy();
+        ++converted;
+        return true;
+      };
+      Flight f0{}, f1{}, f2{};
+      // one chunk for each of the two places ahead; an empty group where there is none
+      auto prime = [&](Flight& f) {
+        const bool more = next_chunk(f);
+        if (more) issue(cache_k);
+        cp_async_commit();
+        ++issued;
+        if (more) issue(cache_v);
+        cp_async_commit();
+        ++issued;
+      };
+      prime(f0);
+      prime(f1);
+      for (int b_no = 0; ok; ++b_no) {
+        // the converting cursor's segment: published, as the issuing one has read it or the end
+        const int slot = b_no % kUnitSlots;
+        if (!wait(C::U_FULL + slot, (b_no / kUnitSlots) & 1)) break;
+        if (s_seg[slot].b < 0) break;
+        const int n = s_seg[slot].c1 - s_seg[slot].c0;
+        for (int j = 0; j < n && ok; ++j) {
+          const bool more = next_chunk(f2);
+          if (!ok || !convert(f0.k)) break;
+          mbar_arrive(bar(C::FULL + ring));
+          advance();
+          if (more) issue(cache_k);
+          cp_async_commit();
+          ++issued;
+          // a V row that is not finite and only partly seen: zeros, and the mark
+          const bool drop = f0.part && f0.v == kScaleNan;
+          if (drop) *reinterpret_cast<volatile int*>(&s_seg[slot].bad) = 1;
+          if (!convert(drop ? kDropRow : f0.v)) break;
+          mbar_arrive(bar(C::FULL + ring));
+          advance();
+          if (more) issue(cache_v);
+          cp_async_commit();
+          ++issued;
+          f0 = f1;
+          f1 = f2;
+        }
+        if (!ok) break;
+        release_segment(slot);
+      }
+    }
+    cp_async_wait_all();       // no copy into this CTA's shared memory may outlive it
+  } else {
+    // ------------------------------------------------------------ softmax
+    regs_inc<C::kRegsS>();
+    const int tile = (warp - 8) >> 2, q4 = warp & 3;
+    const int row = tile * 128 + q4 * 32 + lane;      // row of the item; tensor-memory lane row % 128
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(q4 * 32) << 16);
+    const float c = p.scale_log2;
+    int cnt = 0;
+    // The last P V of this tile, known by its own buffer: the issuer arrives there again only
+    // after this warp has written the P that comes kSBufs later.
+    auto wait_last_pv = [&]() -> bool {
+      return wait(C::S_FREE + tile * C::kSBufs + (cnt - 1) % C::kSBufs, ((cnt - 1) / C::kSBufs) & 1);
+    };
+    float s[C::kSub];
+    for (;;) {
+      const int slot = next_segment();
+      if (slot < 0) break;
+      const int c0 = s_seg[slot].c0, c1 = s_seg[slot].c1, rows = s_seg[slot].rows;
+      if (tile * 128 >= rows) {
+        release_segment(slot);
+        continue;
+      }
+      const int p0 = s_seg[slot].p0, p1 = s_seg[slot].p1, skip = s_seg[slot].skip;
+      const bool idle = tile * 128 + q4 * 32 >= rows;  // no row of this warp
+      const int tok = token_of(min(row, rows - 1)), pos = p0 + tok;
+      float m = -INFINITY, l = 0.f;
+      for (int j = c0 * C::kSubs; j < c1 * C::kSubs; ++j) {
+        const int buf = tile * C::kSBufs + cnt % C::kSBufs;
+        if (!wait(C::S_FULL + buf, (cnt / C::kSBufs) & 1)) break;
+        if (!idle) {
+          tc_fence_after();
+          const uint32_t sa = lane_addr + C::s_col(tile, buf);
+#pragma unroll
+          for (int k = 0; k < C::kSub; k += 32) tmem_ld32(sa + k, s + k);
+          tc_wait_ld();
+          const int key = key_chunk(j / C::kSubs, sc, skip) * kChunkKeys + (j % C::kSubs) * C::kSub;
+          // keys that not all of the item's tokens see: the row's mask
+          if (key + C::kSub - 1 > p0 || (window > 0 && key <= p1 - window && key + C::kSub > sinks)) {
+#pragma unroll
+            for (int w = 0; w < C::kSub / 32; ++w) {
+              const unsigned bits = chunk_sees(key + 32 * w, pos, window, sinks);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(bits >> i & 1u)) s[32 * w + i] = -INFINITY;
+            }
+          }
+          float mk[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mk[i] = fmaxf(s[i], s[8 + i]);
+#pragma unroll
+          for (int k = 16; k < C::kSub; k += 16)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mk[i] = fmax3(mk[i], s[k + i], s[k + 8 + i]);
+          const float mx = fmaf(c, fmax3(fmax3(mk[0], mk[1], mk[2]), fmax3(mk[3], mk[4], mk[5]), fmaxf(mk[6], mk[7])), kHeadroomLog2);
+          if (j == c0 * C::kSubs) {
+            m = mx;                                   // the first P V overwrites O
+          } else if (__any_sync(0xffffffffu, mx > m + kRescaleLog2)) {
+            // the warp rescales together, every row by its own factor (1 where the max held);
+            // a row that saw nothing so far (m = -inf) has O = 0 and l = 0
+            float f = 1.0f;
+            if (mx > m + kRescaleLog2) {
+              f = fast_exp2(m - mx);
+              l *= f;
+              m = mx;
+            }
+            if (!wait_last_pv()) break;
+            tc_fence_after();
+            float o[32];
+#pragma unroll
+            for (int k = 0; k < 128; k += 32) {
+              tmem_ld32(lane_addr + C::o_col(tile) + k, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= f;
+              tmem_st32(lane_addr + C::o_col(tile) + k, o);
+            }
+          }
+          // P = 2^(s c - m) as bf16 pairs into the first half of the buffer's columns (the rounding:
+          // the tensor core's A operand shares V's type; at most 2^-8 of a weight)
+          const float mu = m == -INFINITY ? 0.f : m;  // nothing seen yet: every s is -inf, p = 0
+          const uint64_t c2 = f32x2_pack(c, c), nm2 = f32x2_pack(-mu, -mu);
+          uint64_t lk[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int h = 0; h < C::kSub / 64; ++h) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float x0, x1;
+              f32x2_unpack(f32x2_fma(f32x2_pack(s[h * 64 + 2 * i], s[h * 64 + 2 * i + 1]), c2, nm2), x0, x1);
+              const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+              lk[i & 3] = f32x2_add(lk[i & 3], f32x2_pack(e0, e1));
+              pk[i] = pack_bf16x2(e0, e1);
+            }
+            tmem_st32(sa + h * 32, reinterpret_cast<const float*>(pk));
+          }
+          float la[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f32x2_unpack(lk[i], la[2 * i], la[2 * i + 1]);
+          l += ((la[0] + la[1]) + (la[2] + la[3])) + ((la[4] + la[5]) + (la[6] + la[7]));
+          tc_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::P_READY + buf));
+        ++cnt;
+      }
+      if (!ok) break;
+      if (!wait_last_pv()) break;
+      if (!idle) {
+        tc_fence_after();
+        const int bad = *reinterpret_cast<volatile int*>(&s_seg[slot].bad);
+        const int r = s_seg[slot].r, g = s_seg[slot].g, b = s_seg[slot].b, part = s_seg[slot].part;
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        __nv_bfloat16* dst = p.out + (size_t)r * p.sstride_out +
+                             (size_t)(s_seg[slot].q0 + s_seg[slot].tok0 + tok) * p.rstride_out + (g * gq + row - tok * gq) * kHd;
+#pragma unroll 1
+        for (int k = 0; k < 128; k += C::kSub) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < C::kSub; i += 32) tmem_ld32(lane_addr + C::o_col(tile) + k + i, s + i);
+          tc_wait_ld();
+          if (bad && row < rows) {
+            // V values that were dropped, added to the rows that see their keys
+            const int* bt = p.block_tables + (size_t)b * p.max_blocks;
+            for (int j = c0; j < c1; ++j) {
+              const int kc = key_chunk(j, sc, skip);
+              if (!mixed_chunk(kc, p0, p1)) continue;
+              for (int key = kc * kChunkKeys; key < (kc + 1) * kChunkKeys; ++key) {
+                if (!partly_seen(key, p0, p1) || !(chunk_sees(key & ~31, pos, window, sinks) >> (key & 31) & 1u)) continue;
+                const int rw = cache_row(r, bt[key / p.block_size], key);
+                if (rw < 0) continue;
+                const size_t at = (size_t)rw * p.kv_per + g;
+                if constexpr (Q8) {
+                  if (p.scales_v[at] != kScaleNan) continue;
+#pragma unroll
+                  for (int i = 0; i < C::kSub; ++i) s[i] = __int_as_float(0x7fffffff);
+                } else {
+                  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.cache_v) + at * kHd + k;
+#pragma unroll
+                  for (int i = 0; i < C::kSub; ++i) {
+                    const float x = __bfloat162float(v[i]);
+                    if (!(fabsf(x) < INFINITY)) s[i] += x;
+                  }
+                }
+              }
+            }
+          }
+          if (row < rows) {
+            if (part >= 0) {
+#pragma unroll
+              for (int i = 0; i < C::kSub; i += 8)
+                st_global_v8(chunk_part_o(p, part, row, k + i), *reinterpret_cast<const uint32_t(*)[8]>(s + i));
+            } else {
+#pragma unroll
+              for (int i = 0; i < C::kSub; i += 16) {
+                uint32_t v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = pack_bf16x2(s[i + 2 * e] * inv, s[i + 2 * e + 1] * inv);
+                if (p.out_align32) {
+                  st_global_v8(dst + k + i, v);
+                } else {
+                  *reinterpret_cast<uint4*>(dst + k + i) = make_uint4(v[0], v[1], v[2], v[3]);
+                  *reinterpret_cast<uint4*>(dst + k + i + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+                }
+              }
+            }
+          }
+        }
+        if (row < rows && part >= 0) *chunk_part_ml(p, part, row) = make_float2(m, l);
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::O_FREE + tile));
+      release_segment(slot);
+    }
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+// Joins the parts of the items that more than one CTA computed. At most one item begins in a
+// CTA and goes on in the next ones: item blockIdx.x (described by that CTA), a warp per query
+// row, four head dimensions per lane, the parts in the order of their keys (the same bits
+// every time).
+//   o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i
+// Scheduled behind the attention grid's last CTAs (programmatic launch); it reads only after
+// that grid has completed.
+constexpr int kMergeRows = 8;    // rows, and warps, of a CTA
+__global__ void __launch_bounds__(32 * kMergeRows) chunk_merge_kernel(const ChunkAttnParams p) {
+  griddep_wait();
+  const int cta = blockIdx.x, row = blockIdx.y * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const TreeItem it = p.items[cta];
+  if (row >= it.rows) return;
+  auto slot = [&](int c) { return c == cta ? 2 * c + 1 : 2 * c; };
+  auto ml = [&](int c) { return *chunk_part_ml(p, slot(c), row); };
+  float m = -INFINITY;
+  for (int c = cta + lane; c <= it.last; c += 32) m = fmaxf(m, ml(c).x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = cta; c <= it.last; ++c) {
+    const float2 x = ml(c);
+    const float4 v = *reinterpret_cast<const float4*>(chunk_part_o(p, slot(c), row, 4 * lane));
+    if (x.x != -INFINITY) {                          // else the row sees no key of that part
+      const float w = exp2f(x.x - m);
+      l += w * x.y;
+      o.x += w * v.x;
+      o.y += w * v.y;
+      o.z += w * v.z;
+      o.w += w * v.w;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  const int gq = p.call.gq, tok = row / gq;
+  uint2 out;
+  out.x = pack_bf16x2(o.x * inv, o.y * inv);
+  out.y = pack_bf16x2(o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2*>(p.out + (size_t)it.r * p.sstride_out + (size_t)(it.q0 + tok) * p.rstride_out +
+                            (it.g * gq + row - tok * gq) * kHd + 4 * lane) = out;
+}
+
+int chunk_group_rows(int max_rows) { return max_rows <= 128 ? 128 : 256; }
+
+template <int MT, bool Q8>
+static cudaError_t launch_chunk(const ChunkAttnParams& p, int grid, cudaStream_t st) {
+  using C = ChunkCfg<MT, Q8>;
+  static std::atomic<uint64_t> attr_done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(chunk_attn_kernel<MT, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    // the warpgroups' register budgets (setmaxnreg) come out of the registers of the launch
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, chunk_attn_kernel<MT, Q8>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs * C::kThreads < 128 * (C::kRegs0 + C::kRegs1 + MT * C::kRegsS)) return cudaErrorInvalidConfiguration;
+    attr_done.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = programmatic(dim3(grid), C::kThreads, C::kSmem, st, attr);
+  return cudaLaunchKernelEx(&cfg, chunk_attn_kernel<MT, Q8>, p);
+}
+
+cudaError_t launch_chunk_attention(const ChunkAttnParams& p, int grid, cudaStream_t st) {
+  const bool one = p.call.full == 3, q8 = p.scales_k != nullptr;
+  cudaError_t e = one ? (q8 ? launch_chunk<1, true>(p, grid, st) : launch_chunk<1, false>(p, grid, st))
+                      : (q8 ? launch_chunk<2, true>(p, grid, st) : launch_chunk<2, false>(p, grid, st));
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = programmatic(dim3(grid, (p.part_rows + kMergeRows - 1) / kMergeRows), 32 * kMergeRows, 0, st, attr);
+  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel, p);
+}
+
+}  // namespace tpl

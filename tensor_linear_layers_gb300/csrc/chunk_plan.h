@@ -1,0 +1,166 @@
+// Work split of the attention of chunks of new tokens, shared by its kernel and a host test.
+//
+// Request b has t * kv_per * groups items: a kv head of a shard and a group of up to `tg` whole
+// tokens, whose tg * gq query rows (gq: q heads of the kv head) fill one or two tiles of 128. The
+// tokens of group G are those from tg * G on, the first at position p0 and the last at p1; of the
+// keys, chunks of 128, the item takes
+//   the chunks of the first `sinks` tokens    [0, sc),  sc = ceil(sinks / 128)   (with a window)
+//   and those of its window up to its end     [lo, hi), lo = (p0 - window + 1) / 128, hi = p1 / 128 + 1
+// in order: chunk j of the item is key chunk j, or j + skip from j = sc on, skip = max(0, lo - sc).
+//
+// Items lie on a line, requests in order, head by head and group by group. A chunk takes
+// 2 + tiles places, an item `cost` more before its first chunk for what it costs besides them.
+// CTA c of the grid takes the chunks whose first place is in [c * per, (c + 1) * per), so the CTAs
+// have the same work whatever the lengths, windows and numbers of new tokens. No CTA has fewer places than the
+// call's widest chunk: inside an item every CTA then holds some chunk's first place and writes
+// its slot. An item that crosses a boundary is computed in parts: CTA c writes the part that
+// continues an item begun by an earlier CTA to slot 2 c, the part that begins one it does not
+// finish to slot 2 c + 1, and the merge kernel joins them in order.
+#pragma once
+
+#include <algorithm>
+
+#ifndef TPL_HD
+#ifdef __CUDACC__
+#define TPL_HD __host__ __device__ __forceinline__
+#else
+#define TPL_HD inline
+#endif
+#endif
+
+namespace tpl {
+
+constexpr int kChunkKeys = 128;
+constexpr int kChunkItemCost = 4;   // places
+
+// sum of floor((a i + b) / m) over i = 0 .. n - 1; n a + b < 2^31, all >= 0, m > 0: by Euclid's
+// steps on (a, m), each of which exchanges the axes of the lattice points under the line
+TPL_HD long long chunk_floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+  long long s = 0;
+  for (;;) {
+    s += (long long)(a / m) * ((long long)n * (n - 1LL) / 2) + (long long)(b / m) * n;
+    a %= m;
+    b %= m;
+    const unsigned top = a * n + b;
+    if (top < m) return s;
+    n = top / m;
+    b = top % m;
+    const unsigned x = a;
+    a = m;
+    m = x;
+  }
+}
+
+// What the groups of a call have in common.
+struct ChunkCall {
+  int T, max_query_len, max_seq_len;
+  int gq, tg;                       // q heads of a kv head; whole tokens of a group
+  int window, sinks;                // 0: none
+  int full;                         // places of a chunk of a full group: 2 + its tiles
+};
+// rows_per_group: 128 or 256, at least gq
+TPL_HD int chunk_group_tokens(int gq, int rows_per_group) { return rows_per_group / gq; }
+
+struct ChunkReq {
+  int q0, n, ctx, groups;
+  int last;                         // places of a chunk of the last group
+  bool ok;                          // the counts fit the call
+};
+TPL_HD ChunkReq chunk_request(const ChunkCall& c, int q0, int q1, int len) {
+  ChunkReq r;
+  r.q0 = q0;
+  r.ok = q0 >= 0 && q1 >= q0 && q1 <= c.T && q1 - q0 <= c.max_query_len && len >= q1 - q0 && len <= c.max_seq_len;
+  r.n = r.ok ? q1 - q0 : 0;
+  r.ctx = r.ok ? len - r.n : 0;
+  r.groups = (r.n + c.tg - 1) / c.tg;
+  r.last = 2 + ((r.n - (r.groups - 1) * c.tg) * c.gq + 127) / 128;
+  return r;
+}
+
+// The key chunks of one item.
+struct ChunkKeys {
+  int count, sc, skip;              // chunks of the item; chunk j >= sc is key chunk j + skip
+};
+TPL_HD int chunk_sinks(const ChunkCall& c) {
+  return c.window > 0 ? (int)(((unsigned)c.sinks + kChunkKeys - 1u) / kChunkKeys) : 0;
+}
+TPL_HD ChunkKeys chunk_keys(const ChunkCall& c, int p0, int p1) {
+  ChunkKeys k;
+  k.sc = chunk_sinks(c);
+  const int lo = c.window > 0 && p0 >= c.window ? (p0 - c.window + 1) / kChunkKeys : 0;
+  k.skip = lo > k.sc ? lo - k.sc : 0;
+  k.count = p1 / kChunkKeys + 1 - k.skip;
+  return k;
+}
+TPL_HD ChunkKeys chunk_item_keys(const ChunkCall& c, const ChunkReq& r, int group) {
+  const int t0 = group * c.tg, t1 = t0 + c.tg < r.n ? t0 + c.tg : r.n;
+  return chunk_keys(c, r.ctx + t0, r.ctx + t1 - 1);
+}
+TPL_HD int chunk_width(const ChunkCall& c, const ChunkReq& r, int group) { return group < r.groups - 1 ? c.full : r.last; }
+// Places of one item.
+TPL_HD long long chunk_item(const ChunkCall& c, const ChunkReq& r, int group, int cost) {
+  return cost + (long long)chunk_item_keys(c, r, group).count * chunk_width(c, r, group);
+}
+// Places of a head's first m items, all of them full groups (m < groups).
+TPL_HD long long chunk_prefix(const ChunkCall& c, const ChunkReq& r, int m, int cost) {
+  if (m <= 0) return 0;
+  // hi - skip over the groups, in closed form: both are quotients of lines by 128
+  long long n = m + chunk_floor_sum(m, kChunkKeys, c.tg, r.ctx + c.tg - 1);
+  if (c.window > 0) {
+    // skip > 0 from the first group on whose window starts at key 128 (sc + 1) or later
+    const int sc = chunk_sinks(c);
+    const long long at = (sc + 1LL) * kChunkKeys + c.window - 1 - r.ctx;
+    const long long g0 = at > 0 ? (at + c.tg - 1) / c.tg : 0;
+    if (g0 < m) {
+      const int rest = (int)(m - g0), b = (int)(r.ctx + g0 * c.tg - c.window + 1);
+      n -= chunk_floor_sum(rest, kChunkKeys, c.tg, b) - (long long)rest * sc;
+    }
+  }
+  return (long long)m * cost + n * c.full;
+}
+// Places of all items of one head.
+TPL_HD long long chunk_head(const ChunkCall& c, const ChunkReq& r, int cost) {
+  return r.groups > 0 ? chunk_prefix(c, r, r.groups - 1, cost) + chunk_item(c, r, r.groups - 1, cost) : 0;
+}
+TPL_HD int chunk_widest(const ChunkCall& c, const ChunkReq& r) { return r.groups > 1 ? c.full : r.groups > 0 ? r.last : 0; }
+
+// Few chunks per CTA: they are spread over as many CTAs as there are, so an item costs nothing besides them.
+TPL_HD int chunk_cost(long long places, int full, int grid) { return places >= 4LL * full * grid ? kChunkItemCost : 0; }
+TPL_HD long long chunk_per(long long total, int grid, int widest) {
+  const long long even = (total + grid - 1) / grid;
+  return even > widest ? even : widest;
+}
+
+// Part of the item whose places are [0, cost + keys.count * width): those from p0 on that lie before p1.
+struct ChunkPart {
+  int c0, c1;                       // the item's chunks that begin there
+  int slot;                         // slot of the partial result, or -1: the item is whole
+};
+TPL_HD ChunkPart chunk_part(long long p0, long long p1, int cost, int width, int count, int cta) {
+  ChunkPart s;
+  s.c0 = p0 > cost ? (int)((p0 - cost + width - 1) / width) : 0;
+  s.c1 = p1 > cost ? (int)((p1 - cost + width - 1) / width) : 0;
+  s.slot = s.c0 > 0 ? 2 * cta : s.c1 < count ? 2 * cta + 1 : -1;
+  return s;
+}
+// The CTA that holds the last chunk of the item that begins at place `begin` of the line.
+TPL_HD int chunk_last(long long begin, int cost, int width, int count, long long per) {
+  return (int)((begin + cost + (long long)(count - 1) * width) / per);
+}
+
+// CTAs of the grid: one per SM, no more than a call of these bounds has chunks.
+inline int chunk_grid(int nsm, int n_reqs, int heads, int max_query_len, int tg, int max_seq_len) {
+  const double groups = (max_query_len + tg - 1) / tg;
+  const double chunks = (double)n_reqs * heads * groups * ((max_seq_len + kChunkKeys - 1) / kChunkKeys);
+  return chunks < nsm ? (int)chunks : nsm;
+}
+
+// Visibility of the 32 keys from `key` on to a token at position pos, as bits.
+TPL_HD unsigned chunk_low(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+TPL_HD unsigned chunk_sees(int key, int pos, int window, int sinks) {
+  unsigned bits = chunk_low(pos - key + 1);
+  if (window > 0) bits &= ~chunk_low(pos - window + 1 - key) | chunk_low(sinks - key);
+  return bits;
+}
+
+}  // namespace tpl

@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "chunk_plan.h"
+
 namespace tpl {
 
 constexpr int kStatusCapacity = -5;
@@ -209,6 +211,50 @@ int tree_group_rows(int max_rows);   // query rows of one item: 128 or 256
 cudaError_t launch_tree_mask(int T, int n_reqs, int max_query_len, int words, const int* parents, const int* qsl,
                              const int* seq_lens, int* mask, int* positions, int* status, cudaStream_t st);
 cudaError_t launch_tree_attention(const TreeAttnParams& p, int grid, cudaStream_t st);
+
+// Attention of chunks of new tokens over the cache (chunk_attention.cu).
+struct ChunkAttnParams {
+  ChunkCall call;                    // bounds, groups, window and sinks
+  const __nv_bfloat16* qkv;          // new tokens: shard r, token i at qkv + r * sstride_in + i * rstride_in
+  long long sstride_in;
+  int rstride_in;
+  const int* qsl;                    // [n_reqs + 1]
+  const int* seq_lens;               // [n_reqs], new tokens included
+  const int* block_tables;           // [n_reqs][max_blocks]
+  const void* cache_k;               // [t][num_blocks][block_size][kv_per][128] bf16, or e4m3 codes
+  const void* cache_v;
+  const uint8_t* scales_k;           // [t][num_blocks][block_size][kv_per] of codes; null: the caches are bf16
+  const uint8_t* scales_v;
+  __nv_bfloat16* out;                // shard r, token i at out + r * sstride_out + i * rstride_out
+  long long sstride_out;
+  int rstride_out;
+  int* status;
+  int n_reqs, t, kv_per, max_blocks, num_blocks, block_size;
+  float scale_log2;                  // log2(e) / sqrt(hd)
+  TreeItem* items;                   // [grid] the item each CTA begins and others go on with, for the merge
+  float* partials;                   // [2 * grid] slots of part_rows x (128 + 2)
+  int part_rows;
+  int out_align32;                   // out is 32-byte aligned (rows are then written with 32-byte stores)
+  unsigned long long timeout_ns;
+};
+int chunk_group_rows(int max_rows);  // query rows of one item: up to 128 or 256
+cudaError_t launch_chunk_attention(const ChunkAttnParams& p, int grid, cudaStream_t st);
+
+// A cache in 8 bits (kv_quant.cu).
+struct KvQuantParams {
+  const __nv_bfloat16* qkv;          // write: shard r, token i at qkv + r * sstride + i * rstride
+  long long sstride;
+  int rstride;
+  const int* slots;                  // [n]
+  long long n_slots;                 // num_blocks * block_size
+  uint8_t* codes[2];                 // k, v: [t][n_slots][kv_per][128] e4m3
+  uint8_t* scales[2];                // [t][n_slots][kv_per]
+  __nv_bfloat16* out[2];             // read: [t][n][kv_per][128]
+  int* status;
+  int n, t, q_per, kv_per;
+};
+cudaError_t launch_kv_quant_write(const KvQuantParams& p, int nsm, cudaStream_t st);
+cudaError_t launch_kv_quant_read(const KvQuantParams& p, int nsm, cudaStream_t st);
 
 // Mixture of experts (moe.cu): routing sort, row gather, weighted combine.
 cudaError_t launch_moe_route(const int* ids, int n_entries, int k, int E, int max_rows, int* rank, int* perm_row,

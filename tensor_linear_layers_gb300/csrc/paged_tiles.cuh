@@ -1,0 +1,38 @@
+// Pieces shared by the kernels that stage keys and values of the paged cache in shared memory
+// for the tensor cores.
+#pragma once
+#include <cstdint>
+
+namespace tpl {
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int src_bytes, uint64_t pol) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(src_bytes),
+               "l"(pol)
+               : "memory");
+}
+// One arrival on bar once all cp.async of this thread so far have landed (counted in the barrier's own count).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Shared memory written by ordinary copies and stores, seen by this thread through a barrier,
+// is ordered before the tensor core's reads that it issues next.
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// bf16 pairs of a 32-bit word whose exponent is all ones become zero; true if one was
+__device__ __forceinline__ bool drop_nonfinite(uint32_t& w) {
+  bool any = false;
+  if ((w & 0x7f80u) == 0x7f80u) {
+    w &= 0xffff0000u;
+    any = true;
+  }
+  if ((w & 0x7f800000u) == 0x7f800000u) {
+    w &= 0x0000ffffu;
+    any = true;
+  }
+  return any;
+}
+
+}  // namespace tpl

@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <initializer_list>
 #include <atomic>
 #include <cstdlib>
 #include <cstdarg>
@@ -1834,6 +1835,224 @@ int tp_tree_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t*
   p.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
   const cudaError_t e = launch_tree_attention(p, pl.grid, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
+  return ok();
+}
+
+// ============================================================================ cache in 8 bits, chunks of new tokens
+// Arrays that a call writes lie apart from each other and from those that it reads.
+namespace {
+struct Range {
+  const void* at;
+  int64_t bytes;
+  const char* name;
+};
+int check_apart(std::initializer_list<Range> written, std::initializer_list<Range> read) {
+  for (const Range* w = written.begin(); w != written.end(); ++w) {
+    for (const Range* o = written.begin(); o != w; ++o)
+      if (ranges_overlap(w->at, w->bytes, o->at, o->bytes)) return fail(TP_ERR_ARG, "%s overlaps %s", w->name, o->name);
+    for (const Range& o : read)
+      if (ranges_overlap(w->at, w->bytes, o.at, o.bytes)) return fail(TP_ERR_ARG, "%s overlaps %s", w->name, o.name);
+  }
+  return TP_OK;
+}
+// What both calls of the 8-bit cache check before their own arguments.
+int check_quant(const tp_linear* h, int64_t n, const int32_t* slots, const void* codes_k, const void* codes_v,
+                const void* scales_k, const void* scales_v, int64_t num_blocks, int32_t block_size) {
+  int rc;
+  if ((rc = check_cache_size(h, num_blocks, block_size))) return rc;
+  if (2LL * h->cfg.t * h->kv_per * n >= (int64_t(1) << 31))
+    return fail(TP_ERR_UNSUPPORTED, "2^31 or more head rows in one call");
+  TP_CHECK_PTR(codes_k, "codes_k");
+  TP_CHECK_PTR(codes_v, "codes_v");
+  if (scales_k == nullptr || scales_v == nullptr) return fail(TP_ERR_ARG, "scales_k or scales_v is null");
+  if (!aligned4(slots)) return fail(TP_ERR_ARG, "the slots must be a 4-byte aligned device array");
+  return TP_OK;
+}
+KvQuantParams quant_params(const tp_linear* h, int64_t n, const int32_t* slots, void* codes_k, void* codes_v,
+                           void* scales_k, void* scales_v, int64_t num_blocks, int32_t block_size, void* workspace) {
+  KvQuantParams p{};
+  p.slots = slots;
+  p.n_slots = num_blocks * (int64_t)block_size;
+  p.codes[0] = static_cast<uint8_t*>(codes_k);
+  p.codes[1] = static_cast<uint8_t*>(codes_v);
+  p.scales[0] = static_cast<uint8_t*>(scales_k);
+  p.scales[1] = static_cast<uint8_t*>(scales_v);
+  p.status = reinterpret_cast<int*>(workspace);
+  p.n = (int)n;
+  p.t = h->cfg.t;
+  p.q_per = h->q_per;
+  p.kv_per = h->kv_per;
+  return p;
+}
+}  // namespace
+
+int tp_kv_quant_write(tp_linear_t* h, int64_t T, const void* qkv, const int32_t* slot_mapping, void* codes_k,
+                      void* codes_v, void* scales_k, void* scales_v, int64_t num_blocks, int32_t block_size,
+                      void* workspace, int64_t workspace_bytes, tp_stream_t stream) {
+  int rc = check_paged_handle(h);
+  if (rc || (rc = check_T(T))) return rc;
+  if (T == 0) return ok();
+  TP_CHECK_PTR(qkv, "qkv");
+  if ((rc = check_quant(h, T, slot_mapping, codes_k, codes_v, scales_k, scales_v, num_blocks, block_size)) ||
+      (rc = check_status_ws(workspace, workspace_bytes)))
+    return rc;
+  const int64_t rows = num_blocks * block_size * h->cfg.t * h->kv_per;
+  if ((rc = check_apart({{codes_k, rows * 128, "codes_k"}, {codes_v, rows * 128, "codes_v"}, {scales_k, rows, "scales_k"},
+                         {scales_v, rows, "scales_v"}, {workspace, 4, "workspace"}},
+                        {{qkv, h->cfg.t * T * h->ws_qkv * 2, "qkv"}, {slot_mapping, 4 * T, "slot_mapping"}})))
+    return rc;
+  if ((rc = check_device(h))) return rc;
+  KvQuantParams p = quant_params(h, T, slot_mapping, codes_k, codes_v, scales_k, scales_v, num_blocks, block_size, workspace);
+  p.qkv = static_cast<const __nv_bfloat16*>(qkv);
+  p.sstride = gathered(h) ? h->ws_qkv : T * h->ws_qkv;
+  p.rstride = (int)(gathered(h) ? h->cfg.t * h->ws_qkv : h->ws_qkv);
+  const cudaError_t e = launch_kv_quant_write(p, h->nsm, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit cache write launch");
+  return ok();
+}
+
+int tp_kv_quant_read(tp_linear_t* h, int64_t n, const int32_t* slots, const void* codes_k, const void* codes_v,
+                     const void* scales_k, const void* scales_v, int64_t num_blocks, int32_t block_size, void* k_out,
+                     void* v_out, void* workspace, int64_t workspace_bytes, tp_stream_t stream) {
+  int rc = check_paged_handle(h);
+  if (rc || (rc = check_T(n))) return rc;
+  if (n == 0) return ok();
+  TP_CHECK_PTR(k_out, "k_out");
+  TP_CHECK_PTR(v_out, "v_out");
+  if ((rc = check_quant(h, n, slots, codes_k, codes_v, scales_k, scales_v, num_blocks, block_size)) ||
+      (rc = check_status_ws(workspace, workspace_bytes)))
+    return rc;
+  const int64_t rows = num_blocks * block_size * h->cfg.t * h->kv_per, out = n * h->cfg.t * h->kv_per * 256;
+  if ((rc = check_apart({{k_out, out, "k_out"}, {v_out, out, "v_out"}, {workspace, 4, "workspace"}},
+                        {{codes_k, rows * 128, "codes_k"}, {codes_v, rows * 128, "codes_v"}, {scales_k, rows, "scales_k"},
+                         {scales_v, rows, "scales_v"}, {slots, 4 * n, "slots"}})))
+    return rc;
+  if ((rc = check_device(h))) return rc;
+  KvQuantParams p = quant_params(h, n, slots, const_cast<void*>(codes_k), const_cast<void*>(codes_v),
+                                 const_cast<void*>(scales_k), const_cast<void*>(scales_v), num_blocks, block_size, workspace);
+  p.out[0] = static_cast<__nv_bfloat16*>(k_out);
+  p.out[1] = static_cast<__nv_bfloat16*>(v_out);
+  const cudaError_t e = launch_kv_quant_read(p, h->nsm, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit cache read launch");
+  return ok();
+}
+
+// Chunk attention: at most one CTA per SM, no more than there are chunks of keys. Workspace: the
+// status word, the item each CTA leaves unfinished, two partial slots per CTA.
+namespace {
+struct ChunkPlan {
+  ChunkCall call;
+  int grid, part_rows;
+  int64_t partials_off, ws_bytes;
+};
+ChunkPlan chunk_plan(const tp_linear* h, int64_t T, int n_reqs, int max_query_len, int max_seq_len) {
+  const int gq = h->q_per / h->kv_per;
+  const int64_t max_rows = (int64_t)max_query_len * gq;
+  const int rows = chunk_group_rows((int)std::min<int64_t>(max_rows, 256));
+  ChunkPlan pl{};
+  pl.call.T = (int)T;
+  pl.call.max_query_len = max_query_len;
+  pl.call.max_seq_len = max_seq_len;
+  pl.call.gq = gq;
+  pl.call.tg = chunk_group_tokens(gq, rows);
+  pl.call.full = 2 + rows / 128;
+  pl.grid = chunk_grid(h->nsm, n_reqs, h->cfg.t * h->kv_per, max_query_len, pl.call.tg, max_seq_len);
+  pl.part_rows = ((int)std::min<int64_t>(rows, max_rows) + 7) / 8 * 8;   // a slot is a multiple of 32 bytes (32-byte stores)
+  pl.partials_off = align256(256 + (int64_t)sizeof(TreeItem) * pl.grid);
+  // the workspace itself is 16-byte aligned: room to start the slots on a 32-byte boundary
+  pl.ws_bytes = align256(pl.partials_off + 32 + 2LL * pl.grid * pl.part_rows * (128 + 2) * 4);
+  return pl;
+}
+int check_chunk(const tp_linear* h, int n_reqs, int max_query_len, int max_seq_len) {
+  if (n_reqs < 1 || max_query_len < 1 || max_seq_len < max_query_len)
+    return fail(TP_ERR_SHAPE, "need n_reqs >= 1 and 1 <= max_query_len <= max_seq_len");
+  if (max_seq_len > kTreeMaxSeq) return fail(TP_ERR_UNSUPPORTED, "more than %d tokens per request", kTreeMaxSeq);
+  if (h->q_per / h->kv_per > 256) return fail(TP_ERR_UNSUPPORTED, "more than 256 q heads per kv head");
+  return TP_OK;
+}
+}  // namespace
+
+int tp_chunk_attention_workspace_size(const tp_linear_t* h, int32_t n_reqs, int32_t max_query_len,
+                                      int32_t max_seq_len, int64_t* bytes) {
+  if (bytes == nullptr) return fail(TP_ERR_ARG, "null argument");
+  int rc = check_paged_handle(h);
+  if (rc || (rc = check_chunk(h, n_reqs, max_query_len, max_seq_len))) return rc;
+  *bytes = chunk_plan(h, 0, n_reqs, max_query_len, max_seq_len).ws_bytes;
+  return ok();
+}
+
+int tp_chunk_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t* query_start_loc,
+                       const int32_t* seq_lens, int32_t n_reqs, int32_t max_query_len, int32_t max_seq_len,
+                       const int32_t* block_tables, int32_t max_blocks_per_req, int32_t window, int32_t sinks,
+                       const void* cache_k, const void* cache_v, const void* scales_k, const void* scales_v,
+                       int64_t num_blocks, int32_t block_size, void* attn_out, void* workspace,
+                       int64_t workspace_bytes, tp_stream_t stream) {
+  int rc = check_paged_handle(h);
+  if (rc || (rc = check_T(T))) return rc;
+  if (T == 0) return ok();
+  if ((rc = check_chunk(h, n_reqs, max_query_len, max_seq_len)) || (rc = check_cache_size(h, num_blocks, block_size)))
+    return rc;
+  if (window < 0 || sinks < 0) return fail(TP_ERR_ARG, "window and sinks must be >= 0 (got %d, %d)", window, sinks);
+  if (max_blocks_per_req < 1 || (int64_t)max_blocks_per_req * block_size < max_seq_len)
+    return fail(TP_ERR_SHAPE, "the block tables cannot hold max_seq_len tokens");
+  TP_CHECK_PTR(qkv, "qkv");
+  TP_CHECK_PTR(cache_k, "cache_k");
+  TP_CHECK_PTR(cache_v, "cache_v");
+  TP_CHECK_PTR(attn_out, "attn_out");
+  if ((scales_k == nullptr) != (scales_v == nullptr))
+    return fail(TP_ERR_ARG, "scales_k and scales_v: both (a cache in 8 bits) or neither (in bf16)");
+  for (const int32_t* q : {query_start_loc, seq_lens, block_tables})
+    if (!aligned4(q))
+      return fail(TP_ERR_ARG, "query_start_loc, seq_lens and block_tables must be 4-byte aligned device arrays");
+  ChunkPlan pl = chunk_plan(h, T, n_reqs, max_query_len, max_seq_len);
+  if (workspace == nullptr || !aligned16(workspace)) return fail(TP_ERR_ARG, "workspace is null or not 16-byte aligned");
+  if (workspace_bytes < pl.ws_bytes)
+    return fail(TP_ERR_ARG, "workspace too small: %lld bytes, %lld needed", (long long)workspace_bytes,
+                (long long)pl.ws_bytes);
+  const int64_t rows = num_blocks * block_size * h->cfg.t * h->kv_per, width = scales_k != nullptr ? 128 : 256;
+  const int64_t out_bytes = h->cfg.t * T * h->Ks * 2, scale_bytes = scales_k != nullptr ? rows : 0;
+  if ((rc = check_apart({{attn_out, out_bytes, "attn_out"}, {workspace, pl.ws_bytes, "workspace"}},
+                        {{qkv, h->cfg.t * T * h->ws_qkv * 2, "qkv"}, {query_start_loc, 4LL * n_reqs + 4, "query_start_loc"},
+                         {seq_lens, 4LL * n_reqs, "seq_lens"}, {block_tables, 4LL * n_reqs * max_blocks_per_req, "block_tables"},
+                         {cache_k, rows * width, "cache_k"}, {cache_v, rows * width, "cache_v"},
+                         {scales_k, scale_bytes, "scales_k"}, {scales_v, scale_bytes, "scales_v"}})))
+    return rc;
+  if ((rc = check_device(h))) return rc;
+  const bool gath = gathered(h);
+  ChunkAttnParams p{};
+  // a window as long as the longest request hides nothing; with it, positions and window keep within 2^26
+  pl.call.window = window >= max_seq_len ? 0 : window;
+  pl.call.sinks = std::min(sinks, max_seq_len);
+  p.call = pl.call;
+  p.qkv = static_cast<const __nv_bfloat16*>(qkv);
+  p.sstride_in = gath ? h->ws_qkv : T * h->ws_qkv;
+  p.rstride_in = (int)(gath ? h->cfg.t * h->ws_qkv : h->ws_qkv);
+  p.qsl = query_start_loc;
+  p.seq_lens = seq_lens;
+  p.block_tables = block_tables;
+  p.cache_k = cache_k;
+  p.cache_v = cache_v;
+  p.scales_k = static_cast<const uint8_t*>(scales_k);
+  p.scales_v = static_cast<const uint8_t*>(scales_v);
+  p.out = static_cast<__nv_bfloat16*>(attn_out);
+  p.sstride_out = gath ? h->Ks : T * h->Ks;
+  p.rstride_out = (int)(gath ? h->cfg.t * h->Ks : h->Ks);
+  p.status = reinterpret_cast<int*>(workspace);
+  p.n_reqs = n_reqs;
+  p.t = h->cfg.t;
+  p.kv_per = h->kv_per;
+  p.max_blocks = max_blocks_per_req;
+  p.num_blocks = (int)num_blocks;
+  p.block_size = block_size;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt(128.0));
+  p.items = reinterpret_cast<TreeItem*>(static_cast<char*>(workspace) + 256);
+  p.partials = reinterpret_cast<float*>(
+      (reinterpret_cast<uintptr_t>(workspace) + (uintptr_t)pl.partials_off + 31) & ~uintptr_t(31));
+  p.part_rows = pl.part_rows;
+  p.out_align32 = (reinterpret_cast<uintptr_t>(attn_out) & 31u) == 0 ? 1 : 0;
+  p.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
+  const cudaError_t e = launch_chunk_attention(p, pl.grid, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
   return ok();
 }
 

@@ -19,10 +19,12 @@
 
 #include <algorithm>
 
+#ifndef TPL_HD
 #ifdef __CUDACC__
 #define TPL_HD __host__ __device__ __forceinline__
 #else
 #define TPL_HD inline
+#endif
 #endif
 
 namespace tpl {
