@@ -294,6 +294,10 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
         const int qb = seg_no % C::kQBufs;
         if (!wait(C::Q_FULL + qb, (seg_no / C::kQBufs) & 1)) break;
         for (int j = 0; j < n && ok; ++j) {
+          // The first S of the chunk waits for its buffer before it waits for K: that P V is done, so the
+          // V that the ring's tile held before, handed on late by warp 3, has been counted, and the next
+          // phase of the tile's barrier is this K's (two phases ahead would look like the one before).
+          if (!wait(C::S_FREE + cnt[0] % C::kSBufs, ((cnt[0] / C::kSBufs) & 1) ^ 1)) break;
           if (!wait(C::FULL + ring, ring_ph)) break;
           fence_async_proxy();
 #pragma unroll
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(TreeCfg<MT>::kThreads, 1) tree_attn_kernel(con
             for (int m = 0; m < MT; ++m) {
               if (m * 128 >= rows) break;
               const int buf = m * C::kSBufs + cnt[m] % C::kSBufs;
-              if (!wait(C::S_FREE + buf, ((cnt[m] / C::kSBufs) & 1) ^ 1)) break;
+              if ((h > 0 || m > 0) && !wait(C::S_FREE + buf, ((cnt[m] / C::kSBufs) & 1) ^ 1)) break;
               ++cnt[m];
               tc_fence_after();
               if (elect_one()) {
