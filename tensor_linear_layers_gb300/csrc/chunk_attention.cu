@@ -12,7 +12,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "chunk_plan.h"
+#include "chunk_walk.cuh"
 #include "gemm_tc.cuh"
 #include "internal.h"
 #include "paged_tiles.cuh"
@@ -104,15 +104,6 @@ struct ChunkCfg {
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
-// A segment: chunks [c0, c1) of one item. b < 0: no more.
-struct __align__(16) ChunkSegment {
-  int b, r, g, tok0;                 // request, shard, kv head of the shard, first new token of the group
-  int c0, c1, q0, ctx;               // chunks; row of the request's first new token; cached tokens
-  int part, rows, bad, skip;         // partial slot or -1; query rows; V not finite; key chunks left out from sc on
-  int p0, p1, pad0, pad1;            // positions of the group's first and last token
-};
-static_assert(sizeof(ChunkSegment) == 64, "unit slots");
-
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -144,19 +135,7 @@ __device__ __forceinline__ uint32_t scale_factor(uint32_t s) {
 __device__ __forceinline__ uint32_t scale_rest(uint32_t s) {
   return (s > 134u && s < kScaleNan ? s - 7u << 7 : 0x3f80u) * 0x10001u;
 }
-// Key chunk of chunk j of an item.
-__device__ __forceinline__ int key_chunk(int j, int sc, int skip) { return j + (j >= sc ? skip : 0); }
 }  // namespace
-
-// Partial results of a slot: O as [16][rows][8] fp32 (pieces of eight dimensions, so that the
-// 32 rows of a warp write 1 KB on end), then [rows][2] (max in the exp2 domain, sum).
-// part_rows is a multiple of 8 and the first slot 32-byte aligned: every piece starts on 32 bytes.
-__device__ __forceinline__ float* chunk_part_o(const ChunkAttnParams& p, int slot, int row, int d) {
-  return p.partials + (size_t)slot * p.part_rows * (kHd + 2) + ((size_t)(d >> 3) * p.part_rows + row) * 8 + (d & 7);
-}
-__device__ __forceinline__ float2* chunk_part_ml(const ChunkAttnParams& p, int slot, int row) {
-  return reinterpret_cast<float2*>(p.partials + (size_t)slot * p.part_rows * (kHd + 2) + (size_t)p.part_rows * kHd) + row;
-}
 
 template <int MT, bool Q8>
 __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kernel(const ChunkAttnParams p) {
@@ -195,22 +174,8 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
   griddep_wait();
   const int gq = p.call.gq;                         // q heads of a kv head
   const int sc = chunk_sinks(p.call), window = p.call.window, sinks = p.call.sinks;
-  // warp 2: requests `lane`, `lane` + 32, .. of a batch of 128 (row of the first new token, new tokens, all
-  // tokens; -1: bad counts), loaded together; the first batch here, beside the set-up
-  constexpr int kStrips = 4;
-  int3 mine[kStrips];
-  auto counts = [&](int b) {
-    const ChunkReq r = chunk_request(p.call, p.qsl[b], p.qsl[b + 1], p.seq_lens[b]);
-    return make_int3(r.q0, r.ok ? r.n : -1, r.ctx + r.n);
-  };
-  auto load_batch = [&](int b0) {
-#pragma unroll
-    for (int i = 0; i < kStrips; ++i) {
-      const int b = b0 + 32 * i + lane;
-      mine[i] = b < p.n_reqs ? counts(b) : make_int3(0, 0, 0);
-    }
-  };
-  if (warp == 2) load_batch(0);
+  ChunkWalk walk;                                   // warp 2's; the first requests' counts load beside the set-up
+  if (warp == 2) walk.load(p, 0, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -245,23 +210,10 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(C::U_EMPTY + slot));
   };
-  // a key that some tokens of the item see and others do not, of those that any sees
-  auto partly_seen = [&](int key, int p0, int p1) {
-    return key > p0 || (window > 0 && key <= p1 - window && key >= sinks);
-  };
-  // whether key chunk kc has such keys
-  auto mixed_chunk = [&](int kc, int p0, int p1) {
-    const int k0 = kc * kChunkKeys, k1 = k0 + kChunkKeys - 1;
-    return p1 > p0 && (k1 > p0 || (window > 0 && k0 <= p1 - window && k1 > p0 - window && k1 >= sinks));
-  };
-  // whether any token of the item sees the key
-  auto any_sees = [&](int key, int p0, int p1) {
-    return key <= p1 && (window == 0 || key > p0 - window || key < sinks);
-  };
-  // cache row of a key of request b for shard r: a head's elements are at (row * kv_per + g) * hd; -1 on a bad block
-  auto cache_row = [&](int r, int blk, int key) {
-    return blk >= 0 && blk < p.num_blocks ? (r * p.num_blocks + blk) * p.block_size + key % p.block_size : -1;
-  };
+  auto partly_seen = [&](int key, int p0, int p1) { return chunk_partly(p.call, key, p0, p1); };
+  auto mixed_chunk = [&](int kc, int p0, int p1) { return chunk_mixed(p.call, kc, p0, p1); };
+  auto any_sees = [&](int key, int p0, int p1) { return chunk_any(p.call, key, p0, p1); };
+  auto cache_row = [&](int r, int blk, int key) { return chunk_row(p, r, blk, key); };
 
   if (warp < 4) {
     regs_dec<C::kRegs0>();
@@ -391,157 +343,11 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
       __syncwarp();
     } else if (warp == 2) {
       // ------------------------------------------------------------ segments
-      const int heads = p.t * p.kv_per;
-      auto request = [&](int3 m) {                    // the request of its counts (none where they are bad)
-        return chunk_request(p.call, m.x, m.x + max(m.y, 0), m.z);
-      };
-      auto broadcast = [&](int3 m, int from) {
-        return request(make_int3(__shfl_sync(0xffffffffu, m.x, from), __shfl_sync(0xffffffffu, m.y, from),
-                                 __shfl_sync(0xffffffffu, m.z, from)));
-      };
-      auto sum = [&](long long v) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        return v;
-      };
-      // a head's places of all requests with an item cost of 0 and its items; CTA 0 reports bad counts.
-      // A batch's places are kept: they are looked up again for the CTA's first request.
-      long long places = 0, items = 0, kept[kStrips];
-      int widest = 1;
-      for (int b0 = 0; b0 < p.n_reqs; b0 += 32 * kStrips) {
-        if (b0 > 0) load_batch(b0);
-#pragma unroll
-        for (int i = 0; i < kStrips; ++i) {
-          if (mine[i].y < 0 && blockIdx.x == 0) atomicExch(p.status, kStatusShape);
-          const ChunkReq q = request(mine[i]);
-          kept[i] = chunk_head(p.call, q, 0);
-          places += kept[i];
-          items += q.groups;
-          widest = max(widest, chunk_widest(p.call, q));
-        }
-      }
-      places = heads * sum(places);
-      const int cost = chunk_cost(places, p.call.full, gridDim.x);
-      const long long total = places + heads * cost * sum(items);
-      const long long per = chunk_per(total, gridDim.x, __reduce_max_sync(0xffffffffu, widest));
-      long long pos = per * blockIdx.x;
-      const long long end = min(total, pos + per);
-      // the request that holds the first place, and the places before it
-      ChunkReq r{};
-      int b = 0;
-      long long before = 0, head_places = 0;
-      if (pos < end) {
-        bool found = false;
-        for (int b0 = 0; b0 < p.n_reqs && !found; b0 += 32 * kStrips) {
-          const bool again = p.n_reqs > 32 * kStrips;
-          if (again) load_batch(b0);
-#pragma unroll
-          for (int i = 0; i < kStrips; ++i) {
-            if (found) break;
-            const ChunkReq q = request(mine[i]);
-            const long long one = (again ? chunk_head(p.call, q, 0) : kept[i]) + (long long)cost * q.groups, w = heads * one;
-            long long pre = w;                        // the strip's places up to and with this lane's
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const long long up = __shfl_up_sync(0xffffffffu, pre, o);
-              if (lane >= o) pre += up;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, before + pre > pos);
-            if (hit != 0u) {
-              const int f = __ffs(hit) - 1;
-              b = b0 + 32 * i + f;
-              before += __shfl_sync(0xffffffffu, pre - w, f);
-              head_places = __shfl_sync(0xffffffffu, one, f);
-              r = broadcast(mine[i], f);
-              found = true;
-            } else {
-              before += __shfl_sync(0xffffffffu, pre, 31);
-            }
-          }
-        }
-      }
-      // the item that holds the first place: head, group and its own first place on the line
-      int head = 0, group = 0;
-      long long begin = 0;
-      if (pos < end) {
-        head = (int)((pos - before) / head_places);
-        const long long at = pos - before - head * head_places;
-        // the last group whose prefix is not past `at`: 32 candidates at a time
-        int lo = 0, n = r.groups;
-        while (n > 1) {
-          const int step = (n + 31) / 32, g = lo + lane * step;
-          const bool in = g < lo + n && chunk_prefix(p.call, r, g, cost) <= at;
-          const int last = 31 - __clz(__ballot_sync(0xffffffffu, in));
-          n = min(step, lo + n - (lo + last * step));
-          lo += last * step;
-        }
-        group = lo;
-        begin = before + head * head_places + chunk_prefix(p.call, r, group, cost);
-      }
-      // no item of this CTA is continued by others, unless a segment says so below
-      if (lane == 0) p.items[blockIdx.x].rows = 0;
-      __syncwarp();
+      walk.start(p, lane);
       for (int u = 0;; ++u) {
         const int slot = u % kUnitSlots;
         if (!wait(C::U_EMPTY + slot, ((u / kUnitSlots) & 1) ^ 1)) break;
-        ChunkSegment s;
-        s.b = -1;
-        while (pos < end) {
-          const ChunkKeys keys = chunk_item_keys(p.call, r, group);
-          const int width = chunk_width(p.call, r, group);
-          const long long item = cost + (long long)keys.count * width, p1 = min(item, end - begin);
-          const ChunkPart q = chunk_part(pos - begin, p1, cost, width, keys.count, blockIdx.x);
-          const int it_head = head, it_group = group, it_b = b;
-          const ChunkReq it = r;
-          const long long it_begin = begin;
-          pos = begin + p1;
-          if (p1 == item && pos < end) {               // on to the next item
-            begin = pos;
-            if (++group == r.groups) {
-              group = 0;
-              if (++head == heads) {
-                head = 0;
-                for (;; b += 32) {                     // the next request with new tokens
-                  const int next = b + 1 + lane;
-                  const int3 m = next < p.n_reqs ? counts(next) : make_int3(0, 0, 0);
-                  const unsigned hit = __ballot_sync(0xffffffffu, m.y > 0);
-                  if (hit != 0u) {
-                    const int f = __ffs(hit) - 1;
-                    b += 1 + f;
-                    r = broadcast(m, f);
-                    break;
-                  }
-                  if (b + 32 >= p.n_reqs) {            // cannot be: a place before `end` belongs to a request
-                    pos = end;
-                    break;
-                  }
-                }
-              }
-            }
-          }
-          if (q.c0 == q.c1) continue;                  // no chunk begins in these places
-          s.b = it_b;
-          s.r = it_head / p.kv_per;
-          s.g = it_head - s.r * p.kv_per;
-          s.tok0 = it_group * p.call.tg;
-          s.c0 = q.c0;
-          s.c1 = q.c1;
-          s.q0 = it.q0;
-          s.ctx = it.ctx;
-          s.part = q.slot;
-          const int tokens = min(p.call.tg, it.n - s.tok0);
-          s.rows = tokens * gq;
-          s.bad = 0;
-          s.skip = keys.skip;
-          s.p0 = it.ctx + s.tok0;
-          s.p1 = s.p0 + tokens - 1;
-          s.pad0 = s.pad1 = 0;
-          if (q.c0 == 0 && q.slot >= 0 && lane == 0) {
-            const int last = chunk_last(it_begin, cost, width, keys.count, per);
-            p.items[blockIdx.x] = TreeItem{s.r, s.g, 0, s.rows, s.q0 + s.tok0, last, 0, 0};
-          }
-          break;
-        }
+        const ChunkSegment s = walk.next(p, lane);
         if (lane == 0) {
           s_seg[slot] = s;
           mbar_arrive(bar(C::U_FULL + slot));
@@ -1056,9 +862,9 @@ __global__ void __launch_bounds__(32 * kMergeRows) chunk_merge_kernel(const Chun
   for (int c = cta; c <= it.last; ++c) {
     const float2 x = ml(c);
     const float4 v = *reinterpret_cast<const float4*>(chunk_part_o(p, slot(c), row, 4 * lane));
-    if (x.x != -INFINITY) {                          // else the row sees no key of that part
+    if (x.y != 0.f) {                                // else the row sees no key of that part
       const float w = exp2f(x.x - m);
-      l += w * x.y;
+      l += exp2f(log2f(x.y) + (x.x - m));            // in the exponent: l is far from 1 where v's scales differ much
       o.x += w * v.x;
       o.y += w * v.y;
       o.z += w * v.z;
@@ -1074,7 +880,8 @@ __global__ void __launch_bounds__(32 * kMergeRows) chunk_merge_kernel(const Chun
                             (it.g * gq + row - tok * gq) * kHd + 4 * lane) = out;
 }
 
-int chunk_group_rows(int max_rows) { return max_rows <= 128 ? 128 : 256; }
+// Rows of an item: with up to 16 of them the warp-level kernel (chunk_decode.cu).
+int chunk_group_rows(int max_rows) { return max_rows <= 16 ? 16 : max_rows <= 128 ? 128 : 256; }
 
 template <int MT, bool Q8>
 static cudaError_t launch_chunk(const ChunkAttnParams& p, int grid, cudaStream_t st) {
@@ -1100,9 +907,11 @@ static cudaError_t launch_chunk(const ChunkAttnParams& p, int grid, cudaStream_t
 }
 
 cudaError_t launch_chunk_attention(const ChunkAttnParams& p, int grid, cudaStream_t st) {
-  const bool one = p.call.full == 3, q8 = p.scales_k != nullptr;
-  cudaError_t e = one ? (q8 ? launch_chunk<1, true>(p, grid, st) : launch_chunk<1, false>(p, grid, st))
-                      : (q8 ? launch_chunk<2, true>(p, grid, st) : launch_chunk<2, false>(p, grid, st));
+  const int rows = chunk_group_rows(std::min(p.call.max_query_len, 256) * p.call.gq);
+  const bool q8 = p.scales_k != nullptr;
+  cudaError_t e = rows == 16    ? launch_chunk_decode(p, grid, st)
+                  : rows == 128 ? (q8 ? launch_chunk<1, true>(p, grid, st) : launch_chunk<1, false>(p, grid, st))
+                                : (q8 ? launch_chunk<2, true>(p, grid, st) : launch_chunk<2, false>(p, grid, st));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = programmatic(dim3(grid, (p.part_rows + kMergeRows - 1) / kMergeRows), 32 * kMergeRows, 0, st, attr);

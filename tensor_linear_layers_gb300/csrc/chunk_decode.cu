@@ -1,0 +1,602 @@
+// Attention of few query rows over the paged KV cache: decoding requests, whose new tokens x the q
+// heads of a kv head are up to 16 rows. The mathematics, the masks and the work split are those of
+// chunk_attention.cu, whose 128-row tiles such rows leave empty: there one warp does the whole
+// softmax of a chunk while the other lanes have no row.
+//
+// Here the keys are the long side of the tiles: warp-level m16n8k16 products
+//   S^T = K Q^T   (16 keys x 8 rows),   O^T = V^T P^T   (16 head dimensions x 8 rows)
+// so that 8 rows cost 8 columns. A CTA's eight warps take 16 keys each of every chunk of 128 and
+// keep their own running max, sum and O, all in registers. Each copies its own keys through the
+// block table with 16-byte cp.async into a ring of its own, two chunks ahead across segments, so
+// that within a segment no warp waits for another; they meet at its end. Segments come in batches
+// of up to three, walked by warp 0 (chunk_walk.cuh), their queries loaded together.
+//
+// 8 bits: a warp reads the codes as they are stored, 16 bytes of a row per lane, and one
+// conversion instruction makes two f16 of two codes, exactly. Which dimensions of K a lane's codes
+// are is a permutation that Q's operand takes too; V's codes of two keys are interleaved by byte
+// before the conversion. The scales never touch the codes:
+//   x_j = s_j log2(e) + e_j (e_j: exponent of v's scale),   w_j = 2^(x_j - m),   m = max_j x_j - 7
+//   O = sum_j w_j code_j,   l = sum_j 2^(x_j - e_j - m)
+// with k's scale in the factor of the raw product. w is at most 2^15 (m moves when a row exceeds it by
+// 2^8 more than it was taken at) and rounded to f16, 2^-11 of it down to 2^-29 of the largest. q goes
+// to f16 with a power of two per row that brings its largest element to [2^8, 2^9): exact for
+// elements down to 2^-16 of that, off by 2^-33 of it below.
+// bf16: operands come through ldmatrix; m = max_j x_j + 17 as in chunk_attention.cu, w in bf16.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "chunk_walk.cuh"
+#include "gemm_tc.cuh"
+#include "internal.h"
+#include "paged_tiles.cuh"
+
+namespace tpl {
+
+namespace {
+constexpr int kHd = 128;
+constexpr int kWarps = 8;                      // consumers: 16 keys of a chunk each
+constexpr int kThreads = 32 * kWarps;
+constexpr int kBatch = 3;                      // segments of a batch
+constexpr float kRescaleLog2 = 8.0f;
+
+template <int NT, bool Q8>
+struct DecodeCfg {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kCtas = Q8 && NT == 1 ? 2 : 1;        // per SM
+  static constexpr int kRowBytes = Q8 ? kHd : 2 * kHd;
+  static constexpr int kTile = 16 * kRowBytes;               // K or V of a warp's keys
+  static constexpr int kStages = Q8 && NT == 2 ? 6 : 3;
+  static constexpr int kRing = kStages * 2 * kTile;          // of one warp
+  static constexpr int kQBytes = kRows * kHd * 2;
+  static constexpr int kQOff = kWarps * kRing;
+  static constexpr int kExOff = kQOff + kBatch * kQBytes;    // exchange: [warp][8 rows][8][4] fp32
+  static constexpr int kMlOff = kExOff + kWarps * 1024;      // [warp][row] (max, sum)
+  static constexpr int kSegOff = kMlOff + kWarps * kRows * 8;
+  static constexpr int kWalkOff = kSegOff + kBatch * 64;
+  static constexpr int kBarOff = kWalkOff + (int)((sizeof(ChunkWalk) + 15) / 16 * 16);
+  enum { READY = 0, X_FULL, X_EMPTY, NBARS };
+  static constexpr int kMiscOff = kBarOff + 8 * NBARS;       // abort flag, segments of the batch
+  static constexpr int kSmem = kMiscOff + 8 + 128;           // 128: alignment of the base
+  static_assert((kSmem + 1024) * kCtas <= 233472, "shared memory of the CTAs of one SM");
+  static constexpr float kHead = Q8 ? -7.0f : 17.0f;         // m above the largest x when it is taken
+};
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// two codes (low or high 16 bits of w) as an f16 pair
+__device__ __forceinline__ uint32_t f16x2_lo(uint32_t w) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(d) : "r"(w));
+  return d;
+}
+__device__ __forceinline__ uint32_t f16x2_hi(uint32_t w) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(d) : "r"(w));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 8 x 8 matrix of 16-bit elements in an operand's layout, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+  return d;
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+// 2^(s - 127) of a scale byte: 0 is a subnormal number, 255 NaN
+__device__ __forceinline__ float scale_value(uint32_t s) {
+  return __uint_as_float(s == 0u ? 0x00400000u : s == 255u ? 0x7fc00000u : s << 23);
+}
+__device__ __forceinline__ float scale_exponent(uint32_t s) { return s == 255u ? __int_as_float(0x7fffffff) : (float)((int)s - 127); }
+}  // namespace
+
+template <int NT, bool Q8>
+__global__ void __launch_bounds__(kThreads, DecodeCfg<NT, Q8>::kCtas) chunk_decode_kernel(const ChunkAttnParams p) {
+  using C = DecodeCfg<NT, Q8>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 127u) & ~127u;
+  uint8_t* base_ptr = smem_raw + (base - smem_u32(smem_raw));
+  auto bar = [&](int b) { return base + C::kBarOff + 8u * b; };
+  volatile int* s_abort = reinterpret_cast<volatile int*>(base_ptr + C::kMiscOff);
+  volatile int* s_count = s_abort + 1;
+  ChunkSegment* s_seg = reinterpret_cast<ChunkSegment*>(base_ptr + C::kSegOff);
+  ChunkWalk* s_walk = reinterpret_cast<ChunkWalk*>(base_ptr + C::kWalkOff);   // warp 0's between batches
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < C::NBARS; ++b) mbar_init(bar(b), kWarps);
+    *s_abort = 0;
+    fence_barrier_init();
+  }
+  griddep_wait();
+  const int gq = p.call.gq, sc = chunk_sinks(p.call), window = p.call.window, sinks = p.call.sinks;
+  const unsigned long long timeout = p.timeout_ns;
+  const unsigned gq_magic = 0xffffffffu / (unsigned)gq + 1u;
+  auto token_of = [&](int row) { return gq == 1 ? row : (int)__umulhi((unsigned)row, gq_magic); };
+  __syncthreads();
+  bool ok = true;
+  // all warps arrive and wait for all (bounded: a warp that gave up arrives nowhere)
+  auto meet = [&](int b, uint32_t ph) -> bool {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(b));
+    bool w = mbar_wait_bounded(bar(b), ph, s_abort, timeout);
+    w = __all_sync(0xffffffffu, w);
+    if (!w) {
+      if (lane == 0 && !*s_abort) {
+        atomicExch(p.status, kStatusTimeout);
+        *s_abort = 1;
+      }
+      ok = false;
+    }
+    return w;
+  };
+  const int g = lane >> 2, t = lane & 3;
+  const uint64_t pol = policy_evict_first();                 // every key is read once
+  const uint8_t* cache_k = static_cast<const uint8_t*>(p.cache_k);
+  const uint8_t* cache_v = static_cast<const uint8_t*>(p.cache_v);
+  // copies: this lane brings piece `piece` of rows kPer k + sub of the warp's 16
+  constexpr int kPieces = C::kRowBytes / 16, kPer = 32 / kPieces;
+  const int piece = lane % kPieces, sub = lane / kPieces;
+  const uint32_t ring = base + warp * C::kRing;
+  uint32_t xph = 0;
+  float o[8][NT][4];
+  for (uint32_t batch = 0;; ++batch) {
+    if (warp == 0) {
+      ChunkWalk walk;
+      if (batch == 0) {
+        walk.load(p, 0, lane);
+        walk.start(p, lane);
+      } else {
+        walk.resume(*s_walk);
+      }
+      int n = 0;
+      for (; n < kBatch; ++n) {
+        const ChunkSegment s = walk.next(p, lane);
+        if (s.b < 0) break;
+        if (lane == 0) s_seg[n] = s;
+      }
+      __syncwarp();
+      if (lane == 0) {
+        walk.keep(*s_walk);
+        *s_count = n;
+      }
+    }
+    if (!meet(C::READY, batch & 1)) break;
+    const int segs = *s_count;
+    if (segs == 0) break;
+    // ---------------------------------------------------------- the batch's queries, and the first keys
+    for (int i = threadIdx.x; i < segs * C::kRows * 16; i += kThreads) {
+      const int k = i / (C::kRows * 16), j = i / 16 % C::kRows, tok = token_of(j), x = i & 15;
+      const ChunkSegment& s = s_seg[k];
+      const bool in = j < s.rows;
+      const __nv_bfloat16* q = p.qkv + (size_t)s.r * p.sstride_in + (size_t)(s.q0 + s.tok0 + tok) * p.rstride_in +
+                               (s.g * gq + j - tok * gq) * kHd + x * 8;
+      cp_async16(base + C::kQOff + i * 16, in ? q : p.qkv, in ? 16 : 0, pol);
+    }
+    cp_async_commit();
+    // the issuing cursor: chunk a_c of segment a_s; lanes 0 - 15 have a key each, its block loaded before
+    int a_s = 0, a_c = s_seg[0].c0, blk = 0, issued = 0;
+    struct Flight { uint32_t k, v; };                        // scale bytes of the lane's key
+    auto find = [&]() {
+      blk = -1;
+      if (a_s < segs && lane < 16) {
+        const ChunkSegment& s = s_seg[a_s];
+        const int key = key_chunk(a_c, sc, s.skip) * kChunkKeys + 16 * warp + lane;
+        if (chunk_any(p.call, key, s.p0, s.p1)) {
+          blk = p.block_tables[(size_t)s.b * p.max_blocks + key / p.block_size];
+          if (blk < 0) blk = p.num_blocks;                   // (-1: not seen)
+        }
+      }
+    };
+    auto issue = [&](Flight& f) {
+      f.k = f.v = 127u;
+      if (a_s < segs) {
+        const ChunkSegment& s = s_seg[a_s];
+        int row = -1;                                        // cache row of the lane's key; -1: zeros
+        if (blk != -1) {
+          row = chunk_row(p, s.r, blk, key_chunk(a_c, sc, s.skip) * kChunkKeys + 16 * warp + lane);
+          if (row < 0) atomicExch(p.status, kChunkStatusShape);
+        }
+        const int hg = s.g;
+        if constexpr (Q8) {
+          if (row >= 0) {
+            const size_t at = (size_t)row * p.kv_per + hg;
+            f.k = p.scales_k[at];
+            f.v = p.scales_v[at];
+          }
+        }
+        if (__any_sync(0xffffffffu, lane < 16 && blk != -1)) {
+          const uint32_t kd = ring + issued % C::kStages * (2 * C::kTile) + sub * C::kRowBytes, vd = kd + C::kTile;
+          const uint8_t* ck = cache_k + (size_t)hg * C::kRowBytes + piece * 16;
+          const uint8_t* cv = cache_v + (size_t)hg * C::kRowBytes + piece * 16;
+          const unsigned stride = (unsigned)(p.kv_per * C::kRowBytes);
+#pragma unroll
+          for (int k = 0; k < 16 / kPer; ++k) {
+            const int rw = __shfl_sync(0xffffffffu, row, kPer * k + sub), x = kPer * k + sub;
+            const size_t off = (size_t)(unsigned)max(rw, 0) * stride;
+            const int bytes = rw >= 0 ? 16 : 0;
+            // pieces are permuted so that the reads below meet no bank twice
+            const int kp = Q8 ? piece ^ ((x & 1) << 2) : piece ^ (x & 7), vp = Q8 ? piece ^ (((x >> 1) & 3) << 1) : kp;
+            cp_async16(kd + kPer * k * C::kRowBytes + kp * 16, ck + off, bytes, pol);
+            cp_async16(vd + kPer * k * C::kRowBytes + vp * 16, cv + off, bytes, pol);
+          }
+        }
+        if (++a_c == s.c1) {
+          if (++a_s < segs) a_c = s_seg[a_s].c0;
+        }
+      }
+      cp_async_commit();
+      ++issued;
+      find();
+    };
+    Flight f[C::kStages];
+    find();
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) issue(f[i]);
+    cp_async_wait<C::kStages - 1>();                         // the queries
+    if (!meet(C::X_FULL, xph) || !meet(C::X_EMPTY, xph)) break;
+    xph ^= 1u;
+    int used = 0;                                            // chunks computed
+    for (int u = 0; u < segs; ++u) {
+    const int c0 = s_seg[u].c0, c1 = s_seg[u].c1, p0 = s_seg[u].p0, p1 = s_seg[u].p1, skip = s_seg[u].skip;
+    // Q as the second operand: rows g of every n-tile
+    uint32_t q[NT][8][2];
+    float factor[NT][2];                                     // log2(e) / sqrt(hd), and q's power of two: rows 2 t, 2 t + 1
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint32_t qs = base + C::kQOff + u * C::kQBytes + (8 * n + g) * 256;
+      if constexpr (Q8) {
+        // the 32 elements of dimensions 64 j + 16 t + (0 .. 15)
+        uint4 x[4];
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[j] = lds128(qs + (j >> 1) * 128 + t * 32 + (j & 1) * 16);
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[j].x & 0x7fff7fffu, x[j].y & 0x7fff7fffu),
+                                       __vmaxu2(x[j].z & 0x7fff7fffu, x[j].w & 0x7fff7fffu)));
+        }
+        uint32_t m = max(top & 0xffffu, top >> 16);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int e = max((int)(m >> 7), 10);                // biased exponent of the row's largest element
+        const float f = __uint_as_float((unsigned)(262 - e) << 23);            // 2^(8 - (e - 127))
+        const float back = p.scale_log2 * __uint_as_float((unsigned)(e - 8) << 23);
+        factor[n][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+        factor[n][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+        auto half2 = [&](uint32_t w) { return pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f); };
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          q[n][2 * j][0] = half2(x[j].x);
+          q[n][2 * j][1] = half2(x[j].y);
+          q[n][2 * j + 1][0] = half2(x[j].z);
+          q[n][2 * j + 1][1] = half2(x[j].w);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          q[n][k][0] = lds32(qs + k * 32 + t * 4);
+          q[n][k][1] = lds32(qs + k * 32 + 16 + t * 4);
+        }
+        factor[n][0] = factor[n][1] = p.scale_log2;
+      }
+    }
+    int pos[NT][2];                                          // positions of rows 2 t, 2 t + 1
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        pos[n][h] = min(p0 + token_of(8 * n + 2 * t + h), p1);
+        m[n][h] = -INFINITY;
+        l[n][h] = 0.f;
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) o[i][n][h] = 0.f;
+    bool bad = false;                                        // bf16: a V that only some rows see was not finite
+    for (int c = c0; c < c1; ++c) {
+      issue(f[C::kStages - 1]);
+      cp_async_wait<C::kStages - 1>();
+      __syncwarp();
+      const int key = key_chunk(c, sc, skip) * kChunkKeys + 16 * warp;         // the warp's first key
+      const uint32_t ks = ring + used % C::kStages * (2 * C::kTile), vs = ks + C::kTile;
+      // else nothing of the warp's keys is seen: past the last token, or in the gap before the window
+      if (key <= p1 && (window == 0 || key + 15 > p0 - window || key < sinks)) {
+        float s[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int h = 0; h < 4; ++h) s[n][h] = 0.f;
+        float k0 = 1.f, k1 = 1.f, e0 = 0.f, e1 = 0.f;        // scales of keys g, g + 8: k's value, v's exponent
+        if constexpr (Q8) {
+          k0 = scale_value(__shfl_sync(0xffffffffu, f[0].k, g));
+          k1 = scale_value(__shfl_sync(0xffffffffu, f[0].k, g + 8));
+          e0 = scale_exponent(__shfl_sync(0xffffffffu, f[0].v, g));
+          e1 = scale_exponent(__shfl_sync(0xffffffffu, f[0].v, g + 8));
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t at = ks + g * 128 + (((4 * j + t) ^ ((g & 1) << 2)) << 4);
+            const uint4 a = lds128(at), b = lds128(at + 8 * 128);
+            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t a0 = f16x2_lo(aw[w]), a1 = f16x2_lo(bw[w]), a2 = f16x2_hi(aw[w]), a3 = f16x2_hi(bw[w]);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma16816<true>(s[n], a0, a1, a2, a3, q[n][4 * j + w][0], q[n][4 * j + w][1]);
+            }
+          }
+        } else {
+          const int r = lane & 15;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint32_t a[4];
+            ldsm4(a, ks + r * 256 + (((2 * k + (lane >> 4)) ^ (r & 7)) << 4));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<false>(s[n], a[0], a[1], a[2], a[3], q[n][k][0], q[n][k][1]);
+          }
+        }
+        // x: the weights' exponents; elements 0, 1 of key g, 2, 3 of key g + 8
+        float x[NT][4];
+        bool over = false;
+        const bool partly = key + 15 > p0 || (window > 0 && key <= p1 - window && key + 15 >= sinks);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float f0 = factor[n][0], f1 = factor[n][1];
+          s[n][0] *= f0 * k0;
+          s[n][1] *= f1 * k0;
+          s[n][2] *= f0 * k1;
+          s[n][3] *= f1 * k1;
+          x[n][0] = s[n][0] + e0;
+          x[n][1] = s[n][1] + e0;
+          x[n][2] = s[n][2] + e1;
+          x[n][3] = s[n][3] + e1;
+          if (partly) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const int j = key + g + (h >> 1) * 8, at = pos[n][h & 1];
+              if (!(j <= at && (window == 0 || j > at - window || j < sinks))) s[n][h] = x[n][h] = -INFINITY;
+            }
+          }
+          over |= fmaxf(x[n][0], x[n][2]) > m[n][0] + (kRescaleLog2 - C::kHead);
+          over |= fmaxf(x[n][1], x[n][3]) > m[n][1] + (kRescaleLog2 - C::kHead);
+        }
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float top = fmaxf(x[n][h], x[n][2 + h]);
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) + C::kHead;
+              if (top > m[n][h]) {
+                const float f = fast_exp2(m[n][h] - top);    // 0 where nothing was seen before
+                m[n][h] = top;
+                l[n][h] *= f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  o[i][n][h] *= f;
+                  o[i][n][2 + h] *= f;
+                }
+              }
+            }
+        }
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float w[4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const float mu = m[n][h & 1] == -INFINITY ? 0.f : m[n][h & 1];     // nothing seen yet: x = -inf, w = 0
+            w[h] = fast_exp2(x[n][h] - mu);
+            l[n][h & 1] += Q8 ? fast_exp2(s[n][h] - mu) : w[h];
+          }
+          pb[n][0] = transpose8(Q8 ? pack_f16x2(w[0], w[1]) : pack_bf16x2(w[0], w[1]));
+          pb[n][1] = transpose8(Q8 ? pack_f16x2(w[2], w[3]) : pack_bf16x2(w[2], w[3]));
+        }
+        if constexpr (Q8) {
+          // 16 codes (dimensions 16 g ..) of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+          const uint32_t at = vs + 2 * t * 128 + ((g ^ (2 * t)) << 4);
+          const uint4 v0 = lds128(at), v1 = lds128(at + 128), v2 = lds128(at + 8 * 128), v3 = lds128(at + 9 * 128);
+          const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+          const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a = __byte_perm(w0[j], w1[j], h ? 0x7362 : 0x5140), b = __byte_perm(w2[j], w3[j], h ? 0x7362 : 0x5140);
+              const uint32_t a0 = f16x2_lo(a), a1 = f16x2_hi(a), a2 = f16x2_lo(b), a3 = f16x2_hi(b);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma16816<true>(o[2 * j + h][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+            }
+          }
+        } else {
+          if (partly && p1 > p0) {
+            // values that some rows do not see and that are not finite: zeros (added again below)
+            uint8_t* v = base_ptr + (vs - base);
+            bool found = false;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int row = 2 * k + (lane >> 4);
+              if (!chunk_partly(p.call, key + row, p0, p1)) continue;
+              uint4* at = reinterpret_cast<uint4*>(v + row * 256 + (lane & 15) * 16);
+              uint4 d = *at;
+              const bool a = drop_nonfinite(d.x), b = drop_nonfinite(d.y), e = drop_nonfinite(d.z), f = drop_nonfinite(d.w);
+              if (a || b || e || f) {
+                *at = d;
+                found = true;
+              }
+            }
+            bad |= __any_sync(0xffffffffu, found);
+            __syncwarp();
+          }
+          const int r = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t a[4];
+            ldsm4_t(a, vs + r * 256 + (((2 * i + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<false>(o[i][n], a[0], a[1], a[2], a[3], pb[n][0], pb[n][1]);
+          }
+        }
+      }
+      __syncwarp();                                          // the ring's place is free for the copies issued next
+      ++used;
+#pragma unroll
+      for (int i = 0; i + 1 < C::kStages; ++i) f[i] = f[i + 1];
+    }
+    // ------------------------------------------------------------ the warps' parts of the segment, joined in order
+    float2* s_ml = reinterpret_cast<float2*>(base_ptr + C::kMlOff);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x = l[n][h];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        if (g == 0) s_ml[warp * C::kRows + 8 * n + 2 * t + h] = make_float2(m[n][h], x);
+      }
+    if (bad && lane == 0) *reinterpret_cast<volatile int*>(&s_seg[u].bad) = 1;
+    const int r = s_seg[u].r, hg = s_seg[u].g, part = s_seg[u].part, rows = s_seg[u].rows, b = s_seg[u].b;
+    const int q0 = s_seg[u].q0 + s_seg[u].tok0;
+    float4* ex = reinterpret_cast<float4*>(base_ptr + C::kExOff);
+    const int jg = lane >> 2, jj = lane & 3;                 // joining: row `warp` of an n-tile, dimensions by lane
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = 8 * n + warp;
+      float fw[kWarps], inv = 0.f, mt = -INFINITY, lt = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {                          // 32 dimensions at a time: products 2 k, 2 k + 1
+        ex[(warp * 8 + 2 * t) * 8 + (g ^ (2 * t))] = make_float4(o[2 * k][n][0], o[2 * k][n][2], o[2 * k + 1][n][0], o[2 * k + 1][n][2]);
+        ex[(warp * 8 + 2 * t + 1) * 8 + (g ^ (2 * t + 1))] = make_float4(o[2 * k][n][1], o[2 * k][n][3], o[2 * k + 1][n][1], o[2 * k + 1][n][3]);
+        if (!meet(C::X_FULL, xph)) break;
+        if (k == 0) {
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, s_ml[w * C::kRows + row].x);
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float2 y = s_ml[w * C::kRows + row];       // sum 0: the row sees none of the warp's keys
+            fw[w] = y.y == 0.f ? 0.f : fast_exp2(y.x - mt);
+            // in the exponent: where v's scales differ much, l is far from 1
+            lt += y.y == 0.f ? 0.f : fast_exp2(__log2f(y.y) + (y.x - mt));
+          }
+          inv = lt == 0.f ? 0.f : 1.0f / lt;
+        }
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float y = reinterpret_cast<const float*>(&ex[(w * 8 + warp) * 8 + (jg ^ warp)])[jj];
+          v += fw[w] == 0.f ? 0.f : fw[w] * y;
+        }
+        const int dim = Q8 ? 16 * jg + 4 * k + jj : 32 * k + 8 * jj + jg;
+        if (row < rows) {
+          const int tok = token_of(row);
+          if constexpr (!Q8) {
+            if (*reinterpret_cast<volatile int*>(&s_seg[u].bad)) {
+              // V values that were dropped, added to the rows that see their keys
+              const int* bt = p.block_tables + (size_t)b * p.max_blocks;
+              for (int c = c0; c < c1; ++c) {
+                const int kc = key_chunk(c, sc, skip);
+                if (!chunk_mixed(p.call, kc, p0, p1)) continue;
+                for (int key = kc * kChunkKeys; key < (kc + 1) * kChunkKeys; ++key) {
+                  if (!chunk_partly(p.call, key, p0, p1) || !chunk_any(p.call, key, p0 + tok, p0 + tok)) continue;
+                  const int rw = chunk_row(p, r, bt[key / p.block_size], key);
+                  if (rw < 0) continue;
+                  const float y = __bfloat162float(static_cast<const __nv_bfloat16*>(p.cache_v)[((size_t)rw * p.kv_per + hg) * kHd + dim]);
+                  if (!(fabsf(y) < INFINITY)) v += y;
+                }
+              }
+            }
+          }
+          if (part >= 0) {
+            *chunk_part_o(p, part, row, dim) = v;
+            if (k == 0 && lane == 0) *chunk_part_ml(p, part, row) = make_float2(mt, lt);
+          } else {
+            p.out[(size_t)r * p.sstride_out + (size_t)(q0 + tok) * p.rstride_out + (hg * gq + row - tok * gq) * kHd + dim] =
+                __float2bfloat16_rn(v * inv);
+          }
+        }
+        if (!meet(C::X_EMPTY, xph)) break;
+        xph ^= 1u;
+      }
+      if (!ok) break;
+    }
+    if (!ok) break;
+    }
+    if (!ok || segs < kBatch) break;
+  }
+  cp_async_wait_all();       // no copy into this CTA's shared memory may outlive it
+}
+
+template <int NT, bool Q8>
+static cudaError_t launch_decode(const ChunkAttnParams& p, int grid, cudaStream_t st) {
+  using C = DecodeCfg<NT, Q8>;
+  static std::atomic<uint64_t> attr_done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(chunk_decode_kernel<NT, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    attr_done.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = programmatic(dim3(grid), kThreads, C::kSmem, st, attr);
+  return cudaLaunchKernelEx(&cfg, chunk_decode_kernel<NT, Q8>, p);
+}
+
+int chunk_decode_ctas(int max_rows, bool q8) { return max_rows <= 8 && q8 ? DecodeCfg<1, true>::kCtas : 1; }
+
+cudaError_t launch_chunk_decode(const ChunkAttnParams& p, int grid, cudaStream_t st) {
+  const bool one = p.call.max_query_len * p.call.gq <= 8, q8 = p.scales_k != nullptr;
+  return one ? (q8 ? launch_decode<1, true>(p, grid, st) : launch_decode<1, false>(p, grid, st))
+             : (q8 ? launch_decode<2, true>(p, grid, st) : launch_decode<2, false>(p, grid, st));
+}
+
+}  // namespace tpl

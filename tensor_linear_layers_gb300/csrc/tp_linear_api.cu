@@ -1937,7 +1937,7 @@ int tp_kv_quant_read(tp_linear_t* h, int64_t n, const int32_t* slots, const void
   return ok();
 }
 
-// Chunk attention: at most one CTA per SM, no more than there are chunks of keys. Workspace: the
+// Chunk attention: at most one CTA per SM (two for few rows on an 8-bit cache), no more than there are chunks of keys. Workspace: the
 // status word, the item each CTA leaves unfinished, two partial slots per CTA.
 namespace {
 struct ChunkPlan {
@@ -1945,7 +1945,7 @@ struct ChunkPlan {
   int grid, part_rows;
   int64_t partials_off, ws_bytes;
 };
-ChunkPlan chunk_plan(const tp_linear* h, int64_t T, int n_reqs, int max_query_len, int max_seq_len) {
+ChunkPlan chunk_plan(const tp_linear* h, int64_t T, int n_reqs, int max_query_len, int max_seq_len, bool q8) {
   const int gq = h->q_per / h->kv_per;
   const int64_t max_rows = (int64_t)max_query_len * gq;
   const int rows = chunk_group_rows((int)std::min<int64_t>(max_rows, 256));
@@ -1955,8 +1955,9 @@ ChunkPlan chunk_plan(const tp_linear* h, int64_t T, int n_reqs, int max_query_le
   pl.call.max_seq_len = max_seq_len;
   pl.call.gq = gq;
   pl.call.tg = chunk_group_tokens(gq, rows);
-  pl.call.full = 2 + rows / 128;
-  pl.grid = chunk_grid(h->nsm, n_reqs, h->cfg.t * h->kv_per, max_query_len, pl.call.tg, max_seq_len);
+  pl.call.full = 2 + (rows + 127) / 128;
+  const int ctas = rows == 16 ? chunk_decode_ctas((int)max_rows, q8) : 1;
+  pl.grid = chunk_grid(h->nsm * ctas, n_reqs, h->cfg.t * h->kv_per, max_query_len, pl.call.tg, max_seq_len);
   pl.part_rows = ((int)std::min<int64_t>(rows, max_rows) + 7) / 8 * 8;   // a slot is a multiple of 32 bytes (32-byte stores)
   pl.partials_off = align256(256 + (int64_t)sizeof(TreeItem) * pl.grid);
   // the workspace itself is 16-byte aligned: room to start the slots on a 32-byte boundary
@@ -1977,7 +1978,7 @@ int tp_chunk_attention_workspace_size(const tp_linear_t* h, int32_t n_reqs, int3
   if (bytes == nullptr) return fail(TP_ERR_ARG, "null argument");
   int rc = check_paged_handle(h);
   if (rc || (rc = check_chunk(h, n_reqs, max_query_len, max_seq_len))) return rc;
-  *bytes = chunk_plan(h, 0, n_reqs, max_query_len, max_seq_len).ws_bytes;
+  *bytes = chunk_plan(h, 0, n_reqs, max_query_len, max_seq_len, true).ws_bytes;   // of the larger grid
   return ok();
 }
 
@@ -2004,7 +2005,7 @@ int tp_chunk_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t
   for (const int32_t* q : {query_start_loc, seq_lens, block_tables})
     if (!aligned4(q))
       return fail(TP_ERR_ARG, "query_start_loc, seq_lens and block_tables must be 4-byte aligned device arrays");
-  ChunkPlan pl = chunk_plan(h, T, n_reqs, max_query_len, max_seq_len);
+  ChunkPlan pl = chunk_plan(h, T, n_reqs, max_query_len, max_seq_len, scales_k != nullptr);
   if (workspace == nullptr || !aligned16(workspace)) return fail(TP_ERR_ARG, "workspace is null or not 16-byte aligned");
   if (workspace_bytes < pl.ws_bytes)
     return fail(TP_ERR_ARG, "workspace too small: %lld bytes, %lld needed", (long long)workspace_bytes,

@@ -28,7 +28,7 @@ int item_chunks(int p0, int p1, int window, int sinks, int* out) {
 
 // Head prefixes of a request in closed form against the sum of its items; 0 where all agree.
 int prefixes(int n, int ctx, int gq, int rows, int window, int sinks, int cost) {
-  ChunkCall c{1 << 24, n, ctx + n, gq, chunk_group_tokens(gq, rows), window, sinks, 2 + rows / 128};
+  ChunkCall c{1 << 24, n, ctx + n, gq, chunk_group_tokens(gq, rows), window, sinks, 2 + (rows + 127) / 128};
   const ChunkReq r = chunk_request(c, 0, n, ctx + n);
   long long at = 0;
   for (int g = 0; g < r.groups; ++g) {
@@ -44,7 +44,7 @@ int split(int nsm, int heads, int gq, int rows, int max_q, int max_len, int wind
           const int* lens, int* out) {
   int T = 0;
   for (int b = 0; b < n_reqs; ++b) T += n[b];
-  ChunkCall c{T, max_q, max_len, gq, chunk_group_tokens(gq, rows), window, sinks, 2 + rows / 128};
+  ChunkCall c{T, max_q, max_len, gq, chunk_group_tokens(gq, rows), window, sinks, 2 + (rows + 127) / 128};
   std::vector<ChunkReq> reqs;
   int q0 = 0, widest = 1;
   long long places = 0, items = 0;
