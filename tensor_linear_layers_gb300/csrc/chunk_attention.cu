@@ -70,7 +70,8 @@ constexpr int kTmemCols = 512;
 
 template <int MT, bool Q8>
 struct ChunkCfg {
-  static constexpr int kThreads = 256 + 128 * MT;
+  static constexpr int kCopyWarps = Q8 ? 8 : 4;
+  static constexpr int kThreads = 128 + 32 * kCopyWarps + 128 * MT;
   static constexpr int kTiles = Q8 ? 3 : 5;                // K/V ring
   static constexpr int kAhead = 4;                         // tiles of codes in flight
   static constexpr int kQBufs = MT == 1 ? 2 : 1;
@@ -82,9 +83,11 @@ struct ChunkCfg {
   static constexpr int kCodeOff = kRingOff + kTiles * kTileBytes;
   static constexpr int kBarOff = kCodeOff + (Q8 ? kAhead * kCodeBytes : 0);
   // registers: issuers, copies, softmax
-  static constexpr int kRegs0 = 80, kRegs1 = MT == 1 ? 152 : 96, kRegsS = MT == 1 ? 232 : 168;
-  static constexpr int kLaunchRegs = MT == 1 ? 168 : 128;
-  static_assert(128 * (kRegs0 + kRegs1 + MT * kRegsS) <= kThreads * kLaunchRegs, "register split within the launch's");
+  static constexpr int kRegs0 = Q8 && MT == 2 ? 64 : 80, kRegs1 = Q8 ? (MT == 1 ? 88 : 64) : MT == 1 ? 152 : 96;
+  static constexpr int kRegsS = MT == 1 ? (Q8 ? 216 : 232) : Q8 ? 144 : 168;
+  static constexpr int kRegsAll = 128 * kRegs0 + 32 * kCopyWarps * kRegs1 + 128 * MT * kRegsS;
+  static constexpr int kLaunchRegs = MT == 1 ? (Q8 ? 128 : 168) : Q8 ? 96 : 128;
+  static_assert(kRegsAll <= kThreads * kLaunchRegs, "register split within the launch's");
   // tensor memory: MT = 1: S/P at 0, 128, 256, O at 384; MT = 2: tile m S/P at 256 m and 256 m + 64, O at 256 m + 128
   static __device__ __forceinline__ uint32_t s_col(int tile, int buf) { return tile * 256 + (buf - tile * kSBufs) * kSub; }
   static __device__ __forceinline__ uint32_t o_col(int tile) { return MT == 1 ? 384 : tile * 256 + 128; }
@@ -121,10 +124,12 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-// Codes 2 h and 2 h + 1 of a word as bf16, 2^-120 of their values.
+// Codes 2 h and 2 h + 1 of a word as bf16, 2^-120 of their values: each code widened with its sign to 16
+// bits (a byte permutation can repeat a byte's sign), times 16, and the sign's copies between taken out.
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int h) {
-  const uint32_t r = __byte_perm(w, 0u, h == 0 ? 0x1404 : 0x3424);
-  return (r & 0x80008000u) | ((r >> 4) & 0x07f007f0u);
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(w), "r"(h == 0 ? 0x9180 : 0xb3a2));
+  return (r * 16u) & 0x87f087f0u;
 }
 // 2^(s - 127 + 120) of a scale byte twice as bf16; past the largest power the rest is in the second
 // factor. kDropRow: 0.
@@ -154,12 +159,12 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
     for (int b = lane; b < C::NBARS; b += 32) {
       int count = 1;
       if (b < C::Q_EMPTY) count = Q8 ? 32 : 128;                                // every thread that copies queries
-      if (b >= C::FULL && b < C::EMPTY) count = 128;                            // every copying thread
+      if (b >= C::FULL && b < C::EMPTY) count = 32 * C::kCopyWarps;              // every copying thread
       if (b >= C::P_READY && b < C::S_FREE) count = 4;                          // the tile's softmax warps
       if (b >= C::S_FREE && b < C::O_FREE) count = 2;                           // the MMAs, and their issuer
       if (b >= C::O_FREE && b < C::LANDED) count = 4;
       if (b >= C::LANDED && b < C::U_FULL) count = 128;
-      if (b >= C::U_EMPTY && b < C::DONE_S) count = 3 + 4 + 4 * MT;             // issuers, warp 3, copy and softmax warps
+      if (b >= C::U_EMPTY && b < C::DONE_S) count = 3 + C::kCopyWarps + 4 * MT; // issuers, warp 3, copy and softmax warps
       mbar_init(bar(b), count);
     }
     if (lane == 0) *s_abort = 0;
@@ -175,7 +180,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
   const int gq = p.call.gq;                         // q heads of a kv head
   const int sc = chunk_sinks(p.call), window = p.call.window, sinks = p.call.sinks;
   ChunkWalk walk;                                   // warp 2's; the first requests' counts load beside the set-up
-  if (warp == 2) walk.load(p, 0, lane);
+  if (warp == 2) walk.load(p, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -392,18 +397,35 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
           if (mixed_chunk(kc, p0, p1)) {
             if (!wait(C::LANDED + ring, phases >> ring & 1u)) break;
             phases ^= 1u << ring;
-            // a row is 8 pieces of 16 bytes in each of two boxes, in any order
+            // a row is 8 pieces of 16 bytes in each of two boxes, in any order; a lane has piece `piece` of box `box`
+            // of rows lane / 16, + 2, ..: of those that are partly seen the largest size first, as whole numbers
+            // (without the sign, bf16 bits are ordered so, infinity and NaN last)
             const int k0 = kc * kChunkKeys, box = (lane >> 3) & 1, piece = lane & 7;
             uint8_t* v = base_ptr + C::kRingOff + ring * kTileBytes + box * (kTileBytes / 2) + piece * 16;
-#pragma unroll 4
-            for (int row = lane >> 4; row < kChunkKeys; row += 2) {
-              if (!partly_seen(k0 + row, p0, p1)) continue;
-              uint4* q = reinterpret_cast<uint4*>(v + row * 128);
-              uint4 d = *q;
-              const bool x = drop_nonfinite(d.x), y = drop_nonfinite(d.y), z = drop_nonfinite(d.z), w = drop_nonfinite(d.w);
-              if (x || y || z || w) {
-                *q = d;
-                bad = true;
+            // rows [a0, a1) are before the window of the item's last token, rows [b0, 128) after its first token
+            const int a1 = window > 0 ? min(max(p1 - window + 1 - k0, 0), kChunkKeys) : 0, b0 = max(p0 + 1 - k0, 0);
+            unsigned top = 0u;
+#pragma unroll 8
+            for (int row = lane >> 4; row < a1; row += 2) {
+              const uint4 d = *reinterpret_cast<const uint4*>(v + row * 128);
+              top = __vmaxu2(top, __vmaxu2(__vmaxu2(d.x & 0x7fff7fffu, d.y & 0x7fff7fffu), __vmaxu2(d.z & 0x7fff7fffu, d.w & 0x7fff7fffu)));
+            }
+            // (the rows past the last token are zeros)
+#pragma unroll 8
+            for (int row = b0 + (lane >> 4); row < min(p1 + 1 - k0, kChunkKeys); row += 2) {
+              const uint4 d = *reinterpret_cast<const uint4*>(v + row * 128);
+              top = __vmaxu2(top, __vmaxu2(__vmaxu2(d.x & 0x7fff7fffu, d.y & 0x7fff7fffu), __vmaxu2(d.z & 0x7fff7fffu, d.w & 0x7fff7fffu)));
+            }
+            if (__any_sync(0xffffffffu, (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u)) {
+              for (int row = lane >> 4; row < kChunkKeys; row += 2) {
+                if (!partly_seen(k0 + row, p0, p1)) continue;
+                uint4* q = reinterpret_cast<uint4*>(v + row * 128);
+                uint4 d = *q;
+                const bool x = drop_nonfinite(d.x), y = drop_nonfinite(d.y), z = drop_nonfinite(d.z), w = drop_nonfinite(d.w);
+                if (x || y || z || w) {
+                  *q = d;
+                  bad = true;
+                }
               }
             }
             bad = __any_sync(0xffffffffu, bad);
@@ -420,7 +442,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
         release_segment(slot);
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < 4 + C::kCopyWarps) {
     // ------------------------------------------------------------ copies
     regs_dec<C::kRegs1>();
     const int w4 = warp - 4;
@@ -468,12 +490,12 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
         const int* bt = p.block_tables + (size_t)s.b * p.max_blocks;
         auto block_of = [&](int c) -> int {            // block id of this lane's key of chunk c
           const int key = key_chunk(c, sc, s.skip) * kChunkKeys + my_row;
-          return any_sees(key, s.p0, s.p1) ? bt[key / p.block_size] : 0;
+          return any_sees(key, s.p0, s.p1) ? bt[chunk_page(p, key)] : 0;
         };
         int blk = block_of(s.c0);
         // with one Q buffer the last segment's queries may still be read: the first K tile goes before
         // (and the queries' rows, 256 bytes each, start for L2: their copy is what S waits for)
-        const bool q_first = C::kQBufs > 1 || seg_no == 0;
+        constexpr bool q_first = C::kQBufs > 1;
         if (q_first) {
           load_q(s, seg_no);
         } else {
@@ -511,12 +533,13 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
         release_segment(slot);
       }
     } else {
-      // this warp has rows 32 w4 + (0 .. 31) of a tile; the thread copies and converts 16-byte piece
-      // c8 of rows 32 w4 + 4 k + sub, and finds the cache row of row 32 w4 + lane
-      const int c8 = lane & 7, sub = lane >> 3;
+      // this warp has rows 16 w4 + (0 .. 15) of a tile; the thread copies and converts 16-byte piece
+      // c8 of rows 16 w4 + 4 k + sub, and lanes 0 - 15 find the cache row of row 16 w4 + lane. Eight lanes
+      // have four pieces of one box of two rows, which they write to eight different groups of banks.
+      const int c8 = (lane & 3) | (lane >> 3 & 1) << 2, sub = (lane >> 2 & 1) | lane >> 4 << 1;
       const uint8_t* cache_k = static_cast<const uint8_t*>(p.cache_k);
       const uint8_t* cache_v = static_cast<const uint8_t*>(p.cache_v);
-      const uint32_t raw = base + C::kCodeOff + (threadIdx.x - 128) * 16;    // + tile, + 2048 k: read by this thread alone
+      const uint32_t raw = base + C::kCodeOff + (threadIdx.x - 128) * 16;    // + tile, + 4096 k: read by this thread alone
       int issued = 0, converted = 0;                  // tiles so far: their buffers of codes
       // the two cursors: chunks are issued two ahead of those converted
       int a_slot = -1, a_c = 0, a_c1 = 0, blk = 0;
@@ -525,8 +548,8 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
       // a chunk in flight: its scale bytes for this lane's row; V of that row is only partly seen
       struct Flight { uint32_t k, v; bool part; };
       auto block_of = [&](int c) -> int {
-        const int key = key_chunk(c, sc, s.skip) * kChunkKeys + 32 * w4 + lane;
-        return any_sees(key, s.p0, s.p1) ? p.block_tables[(size_t)s.b * p.max_blocks + key / p.block_size] : 0;
+        const int key = key_chunk(c, sc, s.skip) * kChunkKeys + 16 * w4 + lane;
+        return lane < 16 && any_sees(key, s.p0, s.p1) ? p.block_tables[(size_t)s.b * p.max_blocks + chunk_page(p, key)] : 0;
       };
       int row = -1;
       // moves the issuing cursor to its next chunk: `row` and the scale bytes of that; false at the end
@@ -543,11 +566,11 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
           a_c1 = s.c1;
           blk = block_of(a_c);
         }
-        const int key = key_chunk(a_c, sc, s.skip) * kChunkKeys + 32 * w4 + lane;
+        const int key = key_chunk(a_c, sc, s.skip) * kChunkKeys + 16 * w4 + lane;
         row = -1;
         f.k = f.v = 127u;
         f.part = false;
-        if (any_sees(key, s.p0, s.p1)) {
+        if (lane < 16 && any_sees(key, s.p0, s.p1)) {
           row = cache_row(s.r, blk, key);
           if (row < 0) atomicExch(p.status, kStatusShape);
           f.part = partly_seen(key, s.p0, s.p1);
@@ -565,9 +588,9 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
         const uint8_t* src = cache + s.g * kHd + c8 * 16;
         const uint32_t dst = raw + (issued % C::kAhead) * kCodeBytes;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 4; ++k) {
           const int rw = __shfl_sync(0xffffffffu, row, 4 * k + sub);
-          cp_async16(dst + k * 2048, src + (size_t)max(rw, 0) * p.kv_per * kHd, rw >= 0 ? 16 : 0, pol);
+          cp_async16(dst + k * 4096, src + (size_t)max(rw, 0) * p.kv_per * kHd, rw >= 0 ? 16 : 0, pol);
         }
       };
       // codes of the oldest tile in flight to the next tile of the ring; scale: of this lane's row
@@ -577,16 +600,17 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
         const uint32_t src = raw + (converted % C::kAhead) * kCodeBytes;
         const uint32_t fac = scale_factor(scale), rest = scale_rest(scale);
         const bool large = __any_sync(0xffffffffu, rest != 0x3f803f80u);
-        // the piece's two 16-byte halves: chunks 2 c8 and 2 c8 + 1 of the row's sixteen; in the second
-        // box the odd one is written first, so that eight lanes write eight different banks groups
-        const int swap = c8 >> 2;
-        const uint32_t dst = base + C::kRingOff + ring * kTileBytes + (c8 >> 2) * (kTileBytes / 2) + (32 * w4 + sub) * 128;
+        // the piece's two halves: 16-byte chunks 2 c8 and 2 c8 + 1 of the row's sixteen; row & 7 is 4 (k & 1) + sub
+        const uint32_t dst = base + C::kRingOff + ring * kTileBytes + (c8 >> 2) * (kTileBytes / 2) + (16 * w4 + sub) * 128;
+        const uint32_t even = ((2 * (c8 & 3)) ^ sub) << 4, odd = ((2 * (c8 & 3) + 1) ^ sub) << 4;
+        uint4 w[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint4 w = lds128(src + k * 2048);
+        for (int k = 0; k < 4; ++k) w[k] = lds128(src + k * 4096);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
           const uint32_t f = __shfl_sync(0xffffffffu, fac, 4 * k + sub);
-          uint32_t x[8] = {code_pair(w.x, 0), code_pair(w.x, 1), code_pair(w.y, 0), code_pair(w.y, 1),
-                           code_pair(w.z, 0), code_pair(w.z, 1), code_pair(w.w, 0), code_pair(w.w, 1)};
+          uint32_t x[8] = {code_pair(w[k].x, 0), code_pair(w[k].x, 1), code_pair(w[k].y, 0), code_pair(w[k].y, 1),
+                           code_pair(w[k].z, 0), code_pair(w[k].z, 1), code_pair(w[k].w, 0), code_pair(w[k].w, 1)};
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = mul_bf16x2(x[i], f);
           if (large) {
@@ -594,16 +618,9 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = mul_bf16x2(x[i], f2);
           }
-          const int rr = (4 * k + sub) & 7;           // row & 7
-          const uint32_t even = ((2 * (c8 & 3)) ^ rr) << 4, odd = ((2 * (c8 & 3) + 1) ^ rr) << 4;
-          const uint32_t at = dst + 4 * k * 128;
-          if (swap) {
-            sts128(at + odd, x[4], x[5], x[6], x[7]);
-            sts128(at + even, x[0], x[1], x[2], x[3]);
-          } else {
-            sts128(at + even, x[0], x[1], x[2], x[3]);
-            sts128(at + odd, x[4], x[5], x[6], x[7]);
-          }
+          const uint32_t at = dst + 4 * k * 128, flip = (k & 1) << 6;
+          sts128(at + (even ^ flip), x[0], x[1], x[2], x[3]);
+          sts128(at + (odd ^ flip), x[4], x[5], x[6], x[7]);
         }
         fence_async_proxy();
         ++converted;
@@ -656,7 +673,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
   } else {
     // ------------------------------------------------------------ softmax
     regs_inc<C::kRegsS>();
-    const int tile = (warp - 8) >> 2, q4 = warp & 3;
+    const int tile = (warp - 4 - C::kCopyWarps) >> 2, q4 = warp & 3;
     const int row = tile * 128 + q4 * 32 + lane;      // row of the item; tensor-memory lane row % 128
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(q4 * 32) << 16);
     const float c = p.scale_log2;
@@ -782,7 +799,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
               if (!mixed_chunk(kc, p0, p1)) continue;
               for (int key = kc * kChunkKeys; key < (kc + 1) * kChunkKeys; ++key) {
                 if (!partly_seen(key, p0, p1) || !(chunk_sees(key & ~31, pos, window, sinks) >> (key & 31) & 1u)) continue;
-                const int rw = cache_row(r, bt[key / p.block_size], key);
+                const int rw = cache_row(r, bt[chunk_page(p, key)], key);
                 if (rw < 0) continue;
                 const size_t at = (size_t)rw * p.kv_per + g;
                 if constexpr (Q8) {
@@ -838,29 +855,95 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
 }
 
 // Joins the parts of the items that more than one CTA computed. At most one item begins in a
-// CTA and goes on in the next ones: item blockIdx.x (described by that CTA), a warp per query
-// row, four head dimensions per lane, the parts in the order of their keys (the same bits
+// CTA and goes on in the next ones: item blockIdx.x (described by that CTA), four query rows per
+// warp, four head dimensions per lane, the parts in the order of their keys (the same bits
 // every time).
 //   o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i
 // Scheduled behind the attention grid's last CTAs (programmatic launch); it reads only after
-// that grid has completed.
-constexpr int kMergeRows = 8;    // rows, and warps, of a CTA
-__global__ void __launch_bounds__(32 * kMergeRows) chunk_merge_kernel(const ChunkAttnParams p) {
+// that grid has completed. Latency bounds it, a chain of three loads: the four rows of a warp are read
+// together, and 256 rows of one item per SM are one wave (one row per warp: 4 waves, 16 us after a
+// prompt of 4096 tokens).
+constexpr int kMergeWarps = 8, kMergeRows = 4 * kMergeWarps;   // of a CTA
+__global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_kernel(const ChunkAttnParams p) {
   griddep_wait();
-  const int cta = blockIdx.x, row = blockIdx.y * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  griddep_launch_dependents();
+  const int cta = blockIdx.x, row0 = blockIdx.y * kMergeRows + (threadIdx.x >> 5) * 4, lane = threadIdx.x & 31;
+  const TreeItem it = p.items[cta];
+  if (row0 >= it.rows) return;
+  auto slot = [&](int c) { return c == cta ? 2 * c + 1 : 2 * c; };
+  // rows past the item's read its last one
+  int row[4];
+  float m[4], l[4];
+  float4 o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    row[j] = min(row0 + j, it.rows - 1);
+    m[j] = -INFINITY;
+    l[j] = 0.f;
+    o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int c = cta + lane; c <= it.last; c += 32)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = fmaxf(m[j], chunk_part_ml(p, slot(c), row[j])->x);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], x));
+#pragma unroll 2
+  for (int c = cta; c <= it.last; ++c) {
+    float2 x[4];
+    float4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[j] = *chunk_part_ml(p, slot(c), row[j]);
+      v[j] = *reinterpret_cast<const float4*>(chunk_part_o(p, slot(c), row[j], 4 * lane));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (x[j].y == 0.f) continue;                   // the row sees no key of that part
+      const float w = exp2f(x[j].x - m[j]);
+      l[j] += exp2f(log2f(x[j].y) + (x[j].x - m[j]));   // in the exponent: l is far from 1 where v's scales differ much
+      o[j].x += w * v[j].x;
+      o[j].y += w * v[j].y;
+      o[j].z += w * v[j].z;
+      o[j].w += w * v[j].w;
+    }
+  }
+  const int gq = p.call.gq;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (row0 + j >= it.rows) break;
+    const float inv = l[j] == 0.f ? 0.f : 1.0f / l[j];
+    const int tok = row[j] / gq;
+    uint2 out;
+    out.x = pack_bf16x2(o[j].x * inv, o[j].y * inv);
+    out.y = pack_bf16x2(o[j].z * inv, o[j].w * inv);
+    *reinterpret_cast<uint2*>(p.out + (size_t)it.r * p.sstride_out + (size_t)(it.q0 + tok) * p.rstride_out +
+                              (it.g * gq + row[j] - tok * gq) * kHd + 4 * lane) = out;
+  }
+}
+
+// The same for items of up to 16 rows, which many CTAs may share (one request's 4000 keys: 19 CTAs per kv
+// head): a CTA per row, each of its warps an eighth of the parts, joined in order.
+__global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_few_kernel(const ChunkAttnParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int cta = blockIdx.x, row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const TreeItem it = p.items[cta];
   if (row >= it.rows) return;
+  __shared__ float4 s_o[kMergeWarps][32];
+  __shared__ float s_l[kMergeWarps];
   auto slot = [&](int c) { return c == cta ? 2 * c + 1 : 2 * c; };
-  auto ml = [&](int c) { return *chunk_part_ml(p, slot(c), row); };
   float m = -INFINITY;
-  for (int c = cta + lane; c <= it.last; c += 32) m = fmaxf(m, ml(c).x);
+  for (int c = cta + lane; c <= it.last; c += 32) m = fmaxf(m, chunk_part_ml(p, slot(c), row)->x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int n = it.last - cta + 1, per = (n + kMergeWarps - 1) / kMergeWarps, c1 = min(cta + (warp + 1) * per, it.last + 1);
 #pragma unroll 4
-  for (int c = cta; c <= it.last; ++c) {
-    const float2 x = ml(c);
+  for (int c = cta + warp * per; c < c1; ++c) {
+    const float2 x = *chunk_part_ml(p, slot(c), row);
     const float4 v = *reinterpret_cast<const float4*>(chunk_part_o(p, slot(c), row, 4 * lane));
     if (x.y != 0.f) {                                // else the row sees no key of that part
       const float w = exp2f(x.x - m);
@@ -870,6 +953,19 @@ __global__ void __launch_bounds__(32 * kMergeRows) chunk_merge_kernel(const Chun
       o.z += w * v.z;
       o.w += w * v.w;
     }
+  }
+  s_o[warp][lane] = o;
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < kMergeWarps; ++w) {
+    const float4 v = s_o[w][lane];
+    l += s_l[w];
+    o.x += v.x;
+    o.y += v.y;
+    o.z += v.z;
+    o.w += v.w;
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   const int gq = p.call.gq, tok = row / gq;
@@ -898,7 +994,7 @@ static cudaError_t launch_chunk(const ChunkAttnParams& p, int grid, cudaStream_t
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, chunk_attn_kernel<MT, Q8>);
     if (e != cudaSuccess) return e;
-    if (fa.numRegs * C::kThreads < 128 * (C::kRegs0 + C::kRegs1 + MT * C::kRegsS)) return cudaErrorInvalidConfiguration;
+    if (fa.numRegs * C::kThreads < C::kRegsAll) return cudaErrorInvalidConfiguration;
     attr_done.fetch_or(bit, std::memory_order_acq_rel);
   }
   cudaLaunchAttribute attr[1];
@@ -914,8 +1010,10 @@ cudaError_t launch_chunk_attention(const ChunkAttnParams& p, int grid, cudaStrea
                                 : (q8 ? launch_chunk<2, true>(p, grid, st) : launch_chunk<2, false>(p, grid, st));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = programmatic(dim3(grid, (p.part_rows + kMergeRows - 1) / kMergeRows), 32 * kMergeRows, 0, st, attr);
-  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel, p);
+  const int max_rows = std::min(p.call.max_query_len, 256) * p.call.gq;
+  const cudaLaunchConfig_t cfg = programmatic(dim3(grid, rows == 16 ? max_rows : (p.part_rows + kMergeRows - 1) / kMergeRows),
+                                              32 * kMergeWarps, 0, st, attr);
+  return cudaLaunchKernelEx(&cfg, rows == 16 ? chunk_merge_few_kernel : chunk_merge_kernel, p);
 }
 
 }  // namespace tpl

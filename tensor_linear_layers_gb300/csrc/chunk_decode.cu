@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<NT, Q8>::kCtas) chunk_deco
     if (warp == 0) {
       ChunkWalk walk;
       if (batch == 0) {
-        walk.load(p, 0, lane);
+        walk.load(p, lane);
         walk.start(p, lane);
       } else {
         walk.resume(*s_walk);
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<NT, Q8>::kCtas) chunk_deco
         const ChunkSegment& s = s_seg[a_s];
         const int key = key_chunk(a_c, sc, s.skip) * kChunkKeys + 16 * warp + lane;
         if (chunk_any(p.call, key, s.p0, s.p1)) {
-          blk = p.block_tables[(size_t)s.b * p.max_blocks + key / p.block_size];
+          blk = p.block_tables[(size_t)s.b * p.max_blocks + chunk_page(p, key)];
           if (blk < 0) blk = p.num_blocks;                   // (-1: not seen)
         }
       }
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<NT, Q8>::kCtas) chunk_deco
                 if (!chunk_mixed(p.call, kc, p0, p1)) continue;
                 for (int key = kc * kChunkKeys; key < (kc + 1) * kChunkKeys; ++key) {
                   if (!chunk_partly(p.call, key, p0, p1) || !chunk_any(p.call, key, p0 + tok, p0 + tok)) continue;
-                  const int rw = chunk_row(p, r, bt[key / p.block_size], key);
+                  const int rw = chunk_row(p, r, bt[chunk_page(p, key)], key);
                   if (rw < 0) continue;
                   const float y = __bfloat162float(static_cast<const __nv_bfloat16*>(p.cache_v)[((size_t)rw * p.kv_per + hg) * kHd + dim]);
                   if (!(fabsf(y) < INFINITY)) v += y;

@@ -35,9 +35,16 @@ __device__ __forceinline__ bool chunk_mixed(const ChunkCall& c, int kc, int p0, 
 __device__ __forceinline__ bool chunk_any(const ChunkCall& c, int key, int p0, int p1) {
   return key <= p1 && (c.window == 0 || key > p0 - c.window || key < c.sinks);
 }
+// Page of a key: key / block_size as a product with 2^32 / block_size rounded up, too large by one at most
+// (key < 2^26: the product is off by less than 2^-6).
+__device__ __forceinline__ int chunk_page(const ChunkAttnParams& p, int key) {
+  if (p.block_size == 1) return key;
+  const int q = (int)__umulhi((unsigned)key, p.block_magic);
+  return q * p.block_size > key ? q - 1 : q;
+}
 // Cache row of a key for shard r: a head's elements are at (row * kv_per + g) * 128; -1 on a bad block.
 __device__ __forceinline__ int chunk_row(const ChunkAttnParams& p, int r, int blk, int key) {
-  return blk >= 0 && blk < p.num_blocks ? (r * p.num_blocks + blk) * p.block_size + key % p.block_size : -1;
+  return blk >= 0 && blk < p.num_blocks ? (r * p.num_blocks + blk) * p.block_size + key - chunk_page(p, key) * p.block_size : -1;
 }
 
 constexpr int kChunkHd = 128;
@@ -52,17 +59,17 @@ __device__ __forceinline__ float2* chunk_part_ml(const ChunkAttnParams& p, int s
 }
 
 
-// One warp walks: every lane calls, with the same result.
+// One warp walks: every lane calls, with the same result. The code is kept short, each function at one
+// place: it runs once per CTA, and what bounds it is the fetch of its instructions (with four strips of
+// requests unrolled the first segment came after 7 us of a prompt's 150).
 struct ChunkWalk {
-  // requests `lane`, `lane` + 32, .. of a batch of 128 (row of the first new token, new tokens, all tokens;
-  // -1 new tokens: bad counts), loaded together
-  static constexpr int kStrips = 4;
-  int3 mine[kStrips];
+  int3 first;                       // request `lane`: row of the first new token, new tokens (-1: bad counts), all tokens
   ChunkReq r;
   long long pos, end, begin, per;   // places: where the walk is, where it ends, the first of the item it is in
   int b, head, group, heads, cost;
 
   static __device__ __forceinline__ int3 counts(const ChunkAttnParams& p, int b) {
+    if (b >= p.n_reqs) return make_int3(0, 0, 0);
     const ChunkReq q = chunk_request(p.call, p.qsl[b], p.qsl[b + 1], p.seq_lens[b]);
     return make_int3(q.q0, q.ok ? q.n : -1, q.ctx + q.n);
   }
@@ -73,94 +80,97 @@ struct ChunkWalk {
     return request(p, make_int3(__shfl_sync(0xffffffffu, m.x, from), __shfl_sync(0xffffffffu, m.y, from),
                                 __shfl_sync(0xffffffffu, m.z, from)));
   }
-  static __device__ __forceinline__ long long sum(long long v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  // sum over the lanes up to and with this one
+  static __device__ __forceinline__ long long scan(long long v, int lane) {
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += up;
+    }
     return v;
   }
 
-  __device__ __forceinline__ void load(const ChunkAttnParams& p, int b0, int lane) {
-#pragma unroll
-    for (int i = 0; i < kStrips; ++i) {
-      const int at = b0 + 32 * i + lane;
-      mine[i] = at < p.n_reqs ? counts(p, at) : make_int3(0, 0, 0);
-    }
-  }
+  __device__ __forceinline__ void load(const ChunkAttnParams& p, int lane) { first = counts(p, lane); }
 
-  // The CTA's range and the item that holds its first place; load(0) before. CTA 0 reports bad counts.
+  // The CTA's range and the item that holds its first place; load() before. CTA 0 reports bad counts.
   __device__ __forceinline__ void start(const ChunkAttnParams& p, int lane) {
     heads = p.t * p.kv_per;
-    // a head's places of all requests with an item cost of 0, and its items. A batch's places are kept:
-    // they are looked up again for the CTA's first request.
-    long long places = 0, items = 0, kept[kStrips];
-    int widest = 1;
-    for (int b0 = 0; b0 < p.n_reqs; b0 += 32 * kStrips) {
-      if (b0 > 0) load(p, b0, lane);
-#pragma unroll
-      for (int i = 0; i < kStrips; ++i) {
-        if (mine[i].y < 0 && blockIdx.x == 0) atomicExch(p.status, kChunkStatusShape);
-        const ChunkReq q = request(p, mine[i]);
-        kept[i] = chunk_head(p.call, q, 0);
-        places += kept[i];
-        items += q.groups;
-        widest = max(widest, chunk_widest(p.call, q));
-      }
-    }
-    places = heads * sum(places);
-    cost = chunk_cost(places, p.call.full, gridDim.x);
-    const long long total = places + heads * cost * sum(items);
-    per = chunk_per(total, gridDim.x, __reduce_max_sync(0xffffffffu, widest));
-    pos = per * blockIdx.x;
-    end = min(total, pos + per);
     r = ChunkReq{};
-    b = head = group = 0;
-    begin = 0;
+    b = head = group = cost = 0;
+    begin = pos = end = 0;
     // no item of this CTA is continued by others, unless a segment says so below
     if (lane == 0) p.items[blockIdx.x].rows = 0;
     __syncwarp();
-    if (pos >= end) return;
-    // the request that holds the first place, and the places before it
-    long long before = 0, head_places = 1;
+    // Twice over the requests, 32 at a time: a head's places of all of them with an item cost of 0, and its
+    // items; then the request that holds the CTA's first place, and the places before it.
+    long long places = 0, before = 0, one = 0;
+    long long items = 0;
+    int widest = 1;
     bool found = false;
-    for (int b0 = 0; b0 < p.n_reqs && !found; b0 += 32 * kStrips) {
-      const bool again = p.n_reqs > 32 * kStrips;
-      if (again) load(p, b0, lane);
-#pragma unroll
-      for (int i = 0; i < kStrips; ++i) {
-        if (found) break;
-        const ChunkReq q = request(p, mine[i]);
-        const long long one = (again ? chunk_head(p.call, q, 0) : kept[i]) + (long long)cost * q.groups, w = heads * one;
-        long long pre = w;                            // the strip's places up to and with this lane's
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long up = __shfl_up_sync(0xffffffffu, pre, o);
-          if (lane >= o) pre += up;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, before + pre > pos);
-        if (hit != 0u) {
-          const int f = __ffs(hit) - 1;
-          b = b0 + 32 * i + f;
-          before += __shfl_sync(0xffffffffu, pre - w, f);
-          head_places = __shfl_sync(0xffffffffu, one, f);
-          r = broadcast(p, mine[i], f);
-          found = true;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      int3 m = first;
+#pragma unroll 1
+      for (int b0 = 0; b0 < p.n_reqs && !found; b0 += 32) {
+        const int3 mine = m;
+        if (b0 + 32 < p.n_reqs) m = counts(p, b0 + 32 + lane);       // (the next ones, early)
+        const ChunkReq q = request(p, mine);
+        one = chunk_head(p.call, q, cost);
+        const long long pre = scan(heads * one, lane);               // the places up to and with this lane's
+        if (pass == 0) {
+          if (mine.y < 0 && blockIdx.x == 0) atomicExch(p.status, kChunkStatusShape);
+          places += __shfl_sync(0xffffffffu, pre, 31);
+          items += q.groups;
+          widest = max(widest, chunk_widest(p.call, q));
         } else {
-          before += __shfl_sync(0xffffffffu, pre, 31);
+          const unsigned hit = __ballot_sync(0xffffffffu, before + pre > pos);
+          if (hit != 0u) {
+            const int f = __ffs(hit) - 1;
+            b = b0 + f;
+            before += __shfl_sync(0xffffffffu, pre - heads * one, f);
+            one = __shfl_sync(0xffffffffu, one, f);
+            r = broadcast(p, mine, f);
+            found = true;
+          } else {
+            before += __shfl_sync(0xffffffffu, pre, 31);
+          }
         }
       }
+      if (pass == 0) {
+        cost = chunk_cost(places, p.call.full, gridDim.x);
+        const long long total = places + heads * cost * __shfl_sync(0xffffffffu, scan(items, lane), 31);
+        per = chunk_per(total, gridDim.x, __reduce_max_sync(0xffffffffu, widest));
+        pos = per * blockIdx.x;
+        end = min(total, pos + per);
+        if (pos >= end) return;
+      }
     }
-    head = (int)((pos - before) / head_places);
-    const long long at = pos - before - head * head_places;
-    // the last group whose prefix is not past `at`: 32 candidates at a time
+    // its head and the last group whose places are not all before
+    long long at = pos - before;
+    while (at >= 32 * one) {
+      at -= 32 * one;
+      head += 32;
+    }
+    const int h = 31 - __clz(__ballot_sync(0xffffffffu, lane * one <= at));
+    head += h;
+    at -= h * one;
+    begin = pos - at;                                  // the head's first place; then its group's
     int n = r.groups;
-    while (n > 1) {
+    long long skipped = 0;
+#pragma unroll 1
+    while (n > 32) {                                   // 32 candidates at a time
       const int step = (n + 31) / 32, g = group + lane * step;
-      const bool in = g < group + n && chunk_prefix(p.call, r, g, cost) <= at;
-      const int last = 31 - __clz(__ballot_sync(0xffffffffu, in));
+      const long long prefix = chunk_prefix(p.call, r, min(g, r.groups - 1), cost);
+      const int last = 31 - __clz(__ballot_sync(0xffffffffu, g < group + n && prefix <= at));
       n = min(step, n - last * step);
       group += last * step;
+      skipped = __shfl_sync(0xffffffffu, prefix, last);
     }
-    begin = before + head * head_places + chunk_prefix(p.call, r, group, cost);
+    const long long w = lane < n ? chunk_item(p.call, r, group + lane, cost) : 0;      // then 32 items' places added up
+    const long long pre = skipped + scan(w, lane) - w;
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, lane < n && pre <= at));
+    group += last;
+    begin += __shfl_sync(0xffffffffu, pre, last);
   }
 
   // What next() needs, kept elsewhere and taken up again.
@@ -182,24 +192,45 @@ struct ChunkWalk {
   __device__ __forceinline__ ChunkSegment next(const ChunkAttnParams& p, int lane) {
     ChunkSegment s;
     s.b = -1;
+#pragma unroll 1
     while (pos < end) {
       const ChunkKeys keys = chunk_item_keys(p.call, r, group);
-      const int width = chunk_width(p.call, r, group);
-      const long long item = cost + (long long)keys.count * width, p1 = min(item, end - begin);
-      const ChunkPart q = chunk_part(pos - begin, p1, cost, width, keys.count, blockIdx.x);
-      const int it_head = head, it_group = group, it_b = b;
-      const ChunkReq it = r;
-      const long long it_begin = begin;
+      const int width = chunk_width(p.call, r, group), item = cost + keys.count * width, p0 = (int)(pos - begin);
+      const bool whole = end - begin >= item;
+      const int p1 = whole ? item : (int)(end - begin);
+      const ChunkPart q = chunk_part(p0, p1, cost, width, keys.count, blockIdx.x);
+      if (q.c0 < q.c1) {                               // else no chunk begins in these places
+        s.b = b;
+        s.r = head / p.kv_per;
+        s.g = head - s.r * p.kv_per;
+        s.tok0 = group * p.call.tg;
+        s.c0 = q.c0;
+        s.c1 = q.c1;
+        s.q0 = r.q0;
+        s.ctx = r.ctx;
+        s.part = q.slot;
+        const int tokens = min(p.call.tg, r.n - s.tok0);
+        s.rows = tokens * p.call.gq;
+        s.bad = 0;
+        s.skip = keys.skip;
+        s.p0 = r.ctx + s.tok0;
+        s.p1 = s.p0 + tokens - 1;
+        s.pad0 = s.pad1 = 0;
+        if (q.c0 == 0 && q.slot >= 0 && lane == 0) {
+          const int last = chunk_last(begin, cost, width, keys.count, per, blockIdx.x, end);
+          p.items[blockIdx.x] = TreeItem{s.r, s.g, 0, s.rows, s.q0 + s.tok0, last, 0, 0};
+        }
+      }
       pos = begin + p1;
-      if (p1 == item && pos < end) {                   // on to the next item
+      if (whole && pos < end) {                        // on to the next item
         begin = pos;
         if (++group == r.groups) {
           group = 0;
           if (++head == heads) {
             head = 0;
+#pragma unroll 1
             for (;; b += 32) {                         // the next request with new tokens
-              const int next = b + 1 + lane;
-              const int3 m = next < p.n_reqs ? counts(p, next) : make_int3(0, 0, 0);
+              const int3 m = counts(p, b + 1 + lane);
               const unsigned hit = __ballot_sync(0xffffffffu, m.y > 0);
               if (hit != 0u) {
                 const int f = __ffs(hit) - 1;
@@ -215,28 +246,7 @@ struct ChunkWalk {
           }
         }
       }
-      if (q.c0 == q.c1) continue;                      // no chunk begins in these places
-      s.b = it_b;
-      s.r = it_head / p.kv_per;
-      s.g = it_head - s.r * p.kv_per;
-      s.tok0 = it_group * p.call.tg;
-      s.c0 = q.c0;
-      s.c1 = q.c1;
-      s.q0 = it.q0;
-      s.ctx = it.ctx;
-      s.part = q.slot;
-      const int tokens = min(p.call.tg, it.n - s.tok0);
-      s.rows = tokens * p.call.gq;
-      s.bad = 0;
-      s.skip = keys.skip;
-      s.p0 = it.ctx + s.tok0;
-      s.p1 = s.p0 + tokens - 1;
-      s.pad0 = s.pad1 = 0;
-      if (q.c0 == 0 && q.slot >= 0 && lane == 0) {
-        const int last = chunk_last(it_begin, cost, width, keys.count, per);
-        p.items[blockIdx.x] = TreeItem{s.r, s.g, 0, s.rows, s.q0 + s.tok0, last, 0, 0};
-      }
-      break;
+      if (s.b >= 0) break;
     }
     return s;
   }

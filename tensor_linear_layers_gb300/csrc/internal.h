@@ -230,6 +230,7 @@ struct ChunkAttnParams {
   int rstride_out;
   int* status;
   int n_reqs, t, kv_per, max_blocks, num_blocks, block_size;
+  unsigned block_magic;              // 2^32 / block_size rounded up (not used for 1)
   float scale_log2;                  // log2(e) / sqrt(hd)
   TreeItem* items;                   // [grid] the item each CTA begins and others go on with, for the merge
   float* partials;                   // [2 * grid] slots of part_rows x (128 + 2)

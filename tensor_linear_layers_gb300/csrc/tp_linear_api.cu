@@ -2045,6 +2045,7 @@ int tp_chunk_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t
   p.max_blocks = max_blocks_per_req;
   p.num_blocks = (int)num_blocks;
   p.block_size = block_size;
+  p.block_magic = (unsigned)(((1ull << 32) + block_size - 1) / block_size);
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt(128.0));
   p.items = reinterpret_cast<TreeItem*>(static_cast<char*>(workspace) + 256);
   p.partials = reinterpret_cast<float*>(

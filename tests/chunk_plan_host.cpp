@@ -79,7 +79,7 @@ int split(int nsm, int heads, int gq, int rows, int max_q, int max_len, int wind
       int head = (int)((pos - before) / one);
       const long long at = pos - before - head * one;
       int lo = 0, m = reqs[b].groups;
-      while (m > 1) {
+      while (m > 32) {
         const int step = (m + 31) / 32;
         int last = 0;
         for (int l = 0; l < 32; ++l)
@@ -87,13 +87,15 @@ int split(int nsm, int heads, int gq, int rows, int max_q, int max_len, int wind
         m = std::min(step, m - last * step);
         lo += last * step;
       }
+      long long begin = before + head * one + chunk_prefix(c, reqs[b], lo, cost);
       int group = lo;
-      long long begin = before + head * one + chunk_prefix(c, reqs[b], group, cost);
+      for (; group < lo + m - 1 && begin + chunk_item(c, reqs[b], group, cost) <= pos; ++group)
+        begin += chunk_item(c, reqs[b], group, cost);
       while (pos < end) {
         const ChunkReq& r = reqs[b];
         const int count = chunk_item_keys(c, r, group).count, width = chunk_width(c, r, group);
         const long long item = cost + (long long)count * width, p1 = std::min(item, end - begin);
-        const ChunkPart q = chunk_part(pos - begin, p1, cost, width, count, cta);
+        const ChunkPart q = chunk_part((int)(pos - begin), (int)p1, cost, width, count, cta);
         const Item it{b, head, group};
         for (int k = q.c0; k < q.c1; ++k) {
           if (!done.insert({b, head, group, k}).second) ++wrong;
@@ -101,7 +103,7 @@ int split(int nsm, int heads, int gq, int rows, int max_q, int max_len, int wind
         }
         if (q.c0 < q.c1 && q.slot >= 0) {
           slots[q.slot] = it;
-          if (q.c0 == 0) joins.push_back({it, cta, chunk_last(begin, cost, width, count, per)});
+          if (q.c0 == 0) joins.push_back({it, cta, chunk_last(begin, cost, width, count, per, cta, end)});
         }
         pos = begin + p1;
         if (p1 == item && pos < end) {
