@@ -36,14 +36,14 @@ namespace tpl {
 // per tile.
 //
 //   warp 0      issues S;  warp 1 issues P V (an elected lane of a converged warp);
-//   warp 2      walks the CTA's range and publishes segments
+//   warp 2      walks the CTA's range and publishes segments; 8 bits: copies their queries
 //   warp 3      bf16: looks over the V rows that only some rows of the item see (below);
-//               8 bits: copies the queries
-//   warps 4-7   bf16: copies K and V rows through the block table with 16-byte cp.async into
-//               128-byte-swizzled tiles (any block size: a key's row is found on its own), and Q.
-//               8 bits: the same copies bring the codes to buffers of their own, two chunks
-//               ahead; each thread turns the codes that it copied into bf16 and stores those
-//   warps 8-    softmax, a row per thread, four warps per tile; at a segment's end O / l to
+//               8 bits: finds the cache rows and scales of every chunk, up to three chunks ahead
+//   4 warps     (bf16) copy K and V rows through the block table with 16-byte cp.async into
+//               128-byte-swizzled tiles (any block size: a key's row is found on its own), and Q;
+//   8 warps     (8 bits) copy the codes to buffers of their own, three tiles ahead; each thread
+//               turns the codes that it copied into bf16 and stores those
+//   the others  softmax, a row per thread, four warps per tile; at a segment's end O / l to
 //               global memory, or the unnormalised O with (m, l) to a partial slot
 //
 // Keys that no row of the item sees are filled with zeros, not read. In chunks with keys that
@@ -61,6 +61,9 @@ constexpr int kStatusShape = -2;               // TP_ERR_SHAPE
 constexpr int kTileBytes = 128 * 128 * 2;      // 128 rows x 128 bf16: two 64-column boxes
 constexpr int kCodeBytes = 128 * 128;          // codes of 128 keys
 constexpr int kUnitSlots = 4;
+// What is known of a chunk of codes: cache rows of its keys (-1: zeros), then four factors of each, k's two
+// and v's two (below), then the kv head (-1: no more chunks) and whether a second factor is not one.
+constexpr int kLookBytes = 128 * 5 * 4 + 16;
 constexpr float kRescaleLog2 = 8.0f;           // rescale O when the row max grows by more than this
 // m is the row max and this much more, so that weights are at most 2^(8 - 17): a sum of 512 weighted
 // bf16 numbers fits fp32 (any v < 2^137 / L does for L keys), and so do products with v of 2^-100
@@ -73,7 +76,8 @@ struct ChunkCfg {
   static constexpr int kCopyWarps = Q8 ? 8 : 4;
   static constexpr int kThreads = 128 + 32 * kCopyWarps + 128 * MT;
   static constexpr int kTiles = Q8 ? 3 : 5;                // K/V ring
-  static constexpr int kAhead = 4;                         // tiles of codes in flight
+  static constexpr int kAhead = 3;                         // tiles of codes in flight
+  static constexpr int kLooks = 4;                         // chunks that are looked up
   static constexpr int kQBufs = MT == 1 ? 2 : 1;
   static constexpr int kSub = MT == 1 ? 128 : 64;          // keys of one S, softmax and P V
   static constexpr int kSubs = kChunkKeys / kSub;
@@ -81,10 +85,11 @@ struct ChunkCfg {
   static constexpr uint32_t kIdescS = idesc_bf16_f32(128, kSub);
   static constexpr int kRingOff = MT * kQBufs * kTileBytes;   // after Q
   static constexpr int kCodeOff = kRingOff + kTiles * kTileBytes;
-  static constexpr int kBarOff = kCodeOff + (Q8 ? kAhead * kCodeBytes : 0);
+  static constexpr int kLookOff = kCodeOff + (Q8 ? kAhead * kCodeBytes : 0);
+  static constexpr int kBarOff = kLookOff + (Q8 ? kLooks * kLookBytes : 0);
   // registers: issuers, copies, softmax
-  static constexpr int kRegs0 = Q8 && MT == 2 ? 64 : 80, kRegs1 = Q8 ? (MT == 1 ? 88 : 64) : MT == 1 ? 152 : 96;
-  static constexpr int kRegsS = MT == 1 ? (Q8 ? 216 : 232) : Q8 ? 144 : 168;
+  static constexpr int kRegs0 = 80, kRegs1 = Q8 ? (MT == 1 ? 88 : 48) : MT == 1 ? 152 : 96;
+  static constexpr int kRegsS = MT == 1 ? (Q8 ? 216 : 232) : Q8 ? 152 : 168;
   static constexpr int kRegsAll = 128 * kRegs0 + 32 * kCopyWarps * kRegs1 + 128 * MT * kRegsS;
   static constexpr int kLaunchRegs = MT == 1 ? (Q8 ? 128 : 168) : Q8 ? 96 : 128;
   static_assert(kRegsAll <= kThreads * kLaunchRegs, "register split within the launch's");
@@ -99,7 +104,7 @@ struct ChunkCfg {
     O_FREE = S_FREE + MT * kSBufs,    // per tile
     LANDED = O_FREE + MT,             // bf16: a V tile to be looked over, per ring tile
     U_FULL = LANDED + kTiles, U_EMPTY = U_FULL + kUnitSlots,
-    DONE_S = U_EMPTY + kUnitSlots, DONE_PV, NBARS
+    L_FULL = U_EMPTY + kUnitSlots, L_EMPTY = L_FULL + kLooks, DONE_S = L_EMPTY + kLooks, DONE_PV, NBARS
   };
   static constexpr int kMiscOff = kBarOff + 8 * NBARS;     // tensor memory address, abort flag
   static constexpr int kUnitOff = (kMiscOff + 8 + 15) / 16 * 16;
@@ -114,6 +119,11 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_gr
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
@@ -133,7 +143,7 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, int h) {
 }
 // 2^(s - 127 + 120) of a scale byte twice as bf16; past the largest power the rest is in the second
 // factor. kDropRow: 0.
-constexpr uint32_t kScaleNan = 255u, kDropRow = 256u;
+constexpr uint32_t kScaleNan = 255u, kDropRow = 256u, kScaleOne = 134u;   // up to kScaleOne the second factor is one
 __device__ __forceinline__ uint32_t scale_factor(uint32_t s) {
   return (s == kDropRow ? 0u : s == kScaleNan ? 0x7fc0u : min(s + 120u, 254u) << 7) * 0x10001u;
 }
@@ -159,12 +169,14 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
     for (int b = lane; b < C::NBARS; b += 32) {
       int count = 1;
       if (b < C::Q_EMPTY) count = Q8 ? 32 : 128;                                // every thread that copies queries
-      if (b >= C::FULL && b < C::EMPTY) count = 32 * C::kCopyWarps;              // every copying thread
+      if (b >= C::FULL && b < C::EMPTY) count = Q8 ? C::kCopyWarps : 128;        // every copying warp or thread
       if (b >= C::P_READY && b < C::S_FREE) count = 4;                          // the tile's softmax warps
       if (b >= C::S_FREE && b < C::O_FREE) count = 2;                           // the MMAs, and their issuer
       if (b >= C::O_FREE && b < C::LANDED) count = 4;
       if (b >= C::LANDED && b < C::U_FULL) count = 128;
-      if (b >= C::U_EMPTY && b < C::DONE_S) count = 3 + C::kCopyWarps + 4 * MT; // issuers, warp 3, copy and softmax warps
+      if (b >= C::U_EMPTY && b < C::L_FULL) count = 3 + (Q8 ? 0 : 4) + 4 * MT;   // issuers, warp 3, bf16 copies, softmax warps
+      if (b >= C::L_FULL && b < C::L_EMPTY) count = 32;
+      if (b >= C::L_EMPTY && b < C::DONE_S) count = C::kCopyWarps;
       mbar_init(bar(b), count);
     }
     if (lane == 0) *s_abort = 0;
@@ -359,30 +371,124 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
         }
         __syncwarp();
         if (s.b < 0) break;
+        if constexpr (Q8) {
+          // the segment's queries, once those that the buffer held are no longer read
+          const int qb = u % C::kQBufs, c16 = lane & 15;
+          if (!wait(C::Q_EMPTY + qb, ((u / C::kQBufs) & 1) ^ 1)) break;
+          const __nv_bfloat16* q = p.qkv + (size_t)s.r * p.sstride_in + (size_t)(s.q0 + s.tok0) * p.rstride_in + s.g * gq * kHd + c16 * 8;
+          const uint32_t dst = base + qb * MT * kTileBytes + (c16 >> 3) * (kTileBytes / 2);
+          const uint64_t pol = policy_evict_normal();
+          // rows past the item's keep what the buffer held: they only reach their own rows of S and O
+#pragma unroll 4
+          for (int j = lane >> 4; j < s.rows; j += 2) {
+            const int tok = token_of(j);
+            cp_async16(dst + (j >> 7) * kTileBytes + (j & 127) * 128 + (((c16 & 7) ^ (j & 7)) << 4),
+                       q + (size_t)tok * p.rstride_in + (j - tok * gq) * kHd, 16, pol);
+          }
+          cp_async_arrive(bar(C::Q_FULL + qb));
+        }
       }
+      if constexpr (Q8) cp_async_wait_all();   // no copy into this CTA's shared memory may outlive it
     } else if (Q8) {
-      // ------------------------------------------------------------ queries
-      const uint64_t pol = policy_evict_normal();
-      const int c16 = lane & 15, half = lane >> 4;
-      for (int seg_no = 0;; ++seg_no) {
+      // ------------------------------------------------------------ rows and scales of the chunks
+      // A lane has four keys on end, of one page where pages are multiples of four. The chunk's factors follow
+      // one chunk later, when its scale bytes have come.
+      const bool quads = (p.block_size & 3) == 0;
+      int n = 0;                                      // chunks begun
+      uint32_t ks[4] = {}, vs[4] = {};                // scale bytes of the last one
+      unsigned part = 0;                              // bit i: its key 4 lane + i is only partly seen
+      int at = -1, seg = 0;                           // its place, and its segment's slot
+      auto hand_on = [&]() {
+        if (at < 0) return;
+        const uint32_t look = base + C::kLookOff + at * kLookBytes;
+        const uint32_t top = max(max(max(ks[0], ks[1]), max(ks[2], ks[3])), max(max(vs[0], vs[1]), max(vs[2], vs[3])));
+        const bool large = __any_sync(0xffffffffu, top > kScaleOne);
+        if (large) {
+          bool bad = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)                 // a V row that is not finite and only partly seen: zeros, and the mark
+            if ((part >> i & 1u) && vs[i] == kScaleNan) {
+              vs[i] = kDropRow;
+              bad = true;
+            }
+          if (bad) *reinterpret_cast<volatile int*>(&s_seg[seg].bad) = 1;
+          sts128(look + 256 * 4 + 16 * lane, scale_rest(ks[0]), scale_rest(ks[1]), scale_rest(ks[2]), scale_rest(ks[3]));
+          sts128(look + 512 * 4 + 16 * lane, scale_rest(vs[0]), scale_rest(vs[1]), scale_rest(vs[2]), scale_rest(vs[3]));
+          sts128(look + 128 * 4 + 16 * lane, scale_factor(ks[0]), scale_factor(ks[1]), scale_factor(ks[2]), scale_factor(ks[3]));
+          sts128(look + 384 * 4 + 16 * lane, scale_factor(vs[0]), scale_factor(vs[1]), scale_factor(vs[2]), scale_factor(vs[3]));
+        } else {                                      // every power of two in range: its bf16 bits twice
+          constexpr uint32_t kTwice = 0x00800080u;
+          sts128(look + 128 * 4 + 16 * lane, (ks[0] + 120u) * kTwice, (ks[1] + 120u) * kTwice, (ks[2] + 120u) * kTwice, (ks[3] + 120u) * kTwice);
+          sts128(look + 384 * 4 + 16 * lane, (vs[0] + 120u) * kTwice, (vs[1] + 120u) * kTwice, (vs[2] + 120u) * kTwice, (vs[3] + 120u) * kTwice);
+        }
+        if (lane == 0) *reinterpret_cast<uint32_t*>(base_ptr + C::kLookOff + at * kLookBytes + 641 * 4) = large ? 1u : 0u;
+        mbar_arrive(bar(C::L_FULL + at));
+      };
+      for (;;) {
         const int slot = next_segment();
         if (slot < 0) break;
-        const int rows = s_seg[slot].rows, r = s_seg[slot].r, g = s_seg[slot].g, q0 = s_seg[slot].q0 + s_seg[slot].tok0;
-        release_segment(slot);
-        const int qb = seg_no % C::kQBufs;
-        if (!wait(C::Q_EMPTY + qb, ((seg_no / C::kQBufs) & 1) ^ 1)) break;
-        const __nv_bfloat16* q = p.qkv + (size_t)r * p.sstride_in + (size_t)q0 * p.rstride_in + g * gq * kHd + c16 * 8;
-        const uint32_t dst = base + qb * MT * kTileBytes + (c16 >> 3) * (kTileBytes / 2);
-        // rows past the item's keep what the buffer held: they only reach their own rows of S and O
-#pragma unroll 4
-        for (int j = half; j < rows; j += 2) {
-          const int tok = token_of(j);
-          cp_async16(dst + (j >> 7) * kTileBytes + (j & 127) * 128 + (((c16 & 7) ^ (j & 7)) << 4),
-                     q + (size_t)tok * p.rstride_in + (j - tok * gq) * kHd, 16, pol);
+        const int r = s_seg[slot].r, g = s_seg[slot].g, c1 = s_seg[slot].c1, p0 = s_seg[slot].p0, p1 = s_seg[slot].p1, skip = s_seg[slot].skip;
+        const int* bt = p.block_tables + (size_t)s_seg[slot].b * p.max_blocks;
+        int c = s_seg[slot].c0, key = key_chunk(c, sc, skip) * kChunkKeys + 4 * lane, blk[4];
+        auto blocks = [&]() {
+          if (quads) {
+            blk[0] = key <= p1 && (window == 0 || key + 3 > p0 - window || key < sinks) ? bt[chunk_page(p, key)] : 0;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) blk[i] = any_sees(key + i, p0, p1) ? bt[chunk_page(p, key + i)] : 0;
+          }
+        };
+        blocks();
+        for (; c < c1; ++c, ++n) {
+          const int place = n % C::kLooks, kc = key_chunk(c, sc, skip), k0 = kc * kChunkKeys;
+          if (!wait(C::L_EMPTY + place, ((n / C::kLooks) & 1) ^ 1)) break;
+          int row[4];
+          if (quads && k0 + kChunkKeys - 1 <= p1 && (window == 0 || k0 > p0 - window || k0 + kChunkKeys <= sinks)) {
+            row[0] = cache_row(r, blk[0], key);       // all of the chunk's keys are seen
+            if (row[0] < 0) atomicExch(p.status, kStatusShape);
+#pragma unroll
+            for (int i = 1; i < 4; ++i) row[i] = row[0] < 0 ? -1 : row[0] + i;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              row[i] = -1;
+              if (any_sees(key + i, p0, p1)) {
+                row[i] = cache_row(r, quads ? blk[0] : blk[i], key + i);
+                if (row[i] < 0) atomicExch(p.status, kStatusShape);
+              }
+            }
+          }
+          sts128(base + C::kLookOff + place * kLookBytes + 16 * lane, row[0], row[1], row[2], row[3]);
+          if (lane == 0) *reinterpret_cast<int*>(base_ptr + C::kLookOff + place * kLookBytes + 640 * 4) = g;
+          unsigned mixed = 0;
+          if (mixed_chunk(kc, p0, p1))
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mixed |= partly_seen(key + i, p0, p1) ? 1u << i : 0u;
+          key = key_chunk(c + 1, sc, skip) * kChunkKeys + 4 * lane;
+          if (c + 1 < c1) blocks();
+          hand_on();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const size_t x = (size_t)(unsigned)max(row[i], 0) * (unsigned)p.kv_per + g;
+            ks[i] = row[i] >= 0 ? p.scales_k[x] : 127u;
+            vs[i] = row[i] >= 0 ? p.scales_v[x] : 127u;
+          }
+          part = mixed;
+          at = place;
+          seg = slot;
         }
-        cp_async_arrive(bar(C::Q_FULL + qb));
+        if (!ok) break;
+        hand_on();                                    // (the mark belongs to this segment)
+        at = -1;
+        release_segment(slot);
       }
-      cp_async_wait_all();     // no copy into this CTA's shared memory may outlive it
+      if (ok) {                                       // no more chunks
+        const int place = n % C::kLooks;
+        if (wait(C::L_EMPTY + place, ((n / C::kLooks) & 1) ^ 1)) {
+          if (lane == 0) *reinterpret_cast<int*>(base_ptr + C::kLookOff + place * kLookBytes + 640 * 4) = -1;
+          mbar_arrive(bar(C::L_FULL + place));
+        }
+      }
     } else {
       // ------------------------------------------------------------ V that only some rows see
       int ring = 1;                                   // tile of the next V
@@ -533,140 +639,81 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
         release_segment(slot);
       }
     } else {
-      // this warp has rows 16 w4 + (0 .. 15) of a tile; the thread copies and converts 16-byte piece
-      // c8 of rows 16 w4 + 4 k + sub, and lanes 0 - 15 find the cache row of row 16 w4 + lane. Eight lanes
-      // have four pieces of one box of two rows, which they write to eight different groups of banks.
+      // this warp has rows 16 w4 + (0 .. 15) of a tile; the thread copies and converts 16-byte piece c8 of
+      // rows 16 w4 + 4 k + sub. Eight lanes have four pieces of one box of two rows, which they write to
+      // eight different groups of banks.
       const int c8 = (lane & 3) | (lane >> 3 & 1) << 2, sub = (lane >> 2 & 1) | lane >> 4 << 1;
-      const uint8_t* cache_k = static_cast<const uint8_t*>(p.cache_k);
-      const uint8_t* cache_v = static_cast<const uint8_t*>(p.cache_v);
+      const uint8_t* cache_k = static_cast<const uint8_t*>(p.cache_k) + c8 * 16;
+      const uint8_t* cache_v = static_cast<const uint8_t*>(p.cache_v) + c8 * 16;
       const uint32_t raw = base + C::kCodeOff + (threadIdx.x - 128) * 16;    // + tile, + 4096 k: read by this thread alone
-      int issued = 0, converted = 0;                  // tiles so far: their buffers of codes
-      // the two cursors: chunks are issued two ahead of those converted
-      int a_slot = -1, a_c = 0, a_c1 = 0, blk = 0;
-      bool a_end = false;
-      ChunkSegment s{};                               // the issuing cursor's segment
-      // a chunk in flight: its scale bytes for this lane's row; V of that row is only partly seen
-      struct Flight { uint32_t k, v; bool part; };
-      auto block_of = [&](int c) -> int {
-        const int key = key_chunk(c, sc, s.skip) * kChunkKeys + 16 * w4 + lane;
-        return lane < 16 && any_sees(key, s.p0, s.p1) ? p.block_tables[(size_t)s.b * p.max_blocks + chunk_page(p, key)] : 0;
-      };
-      int row = -1;
-      // moves the issuing cursor to its next chunk: `row` and the scale bytes of that; false at the end
-      auto next_chunk = [&](Flight& f) -> bool {
-        if (a_end) return false;
-        if (a_c == a_c1) {
-          a_slot = next_segment();
-          if (a_slot < 0) {
-            a_end = true;
-            return false;
+      const uint32_t looks = base + C::kLookOff + (16 * w4 + sub) * 4;
+      const unsigned stride = (unsigned)(p.kv_per * kHd);
+      // tiles K0 V0 K1 V1 ..: copied, and converted kAhead later
+      int issued = 0, converted = 0, last = -1;       // last: tiles in all, once known
+      bool more = true;
+      auto issue = [&]() {
+        const int c = issued >> 1, place = c % C::kLooks;
+        if (more && (issued & 1) == 0) {
+          if (!wait(C::L_FULL + place, (c / C::kLooks) & 1)) return;
+          more = (int)lds32(base + C::kLookOff + place * kLookBytes + 640 * 4) >= 0;
+          if (!more) last = issued;
+        }
+        if (more) {
+          const uint32_t look = looks + place * kLookBytes;
+          const uint8_t* src = (issued & 1 ? cache_v : cache_k) + (size_t)lds32(base + C::kLookOff + place * kLookBytes + 640 * 4) * kHd;
+          const uint32_t dst = raw + (issued % C::kAhead) * kCodeBytes;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int rw = (int)lds32(look + 16 * k);
+            cp_async16(dst + k * 4096, src + (size_t)(unsigned)max(rw, 0) * stride, rw >= 0 ? 16 : 0, pol);
           }
-          s = s_seg[a_slot];
-          a_c = s.c0;
-          a_c1 = s.c1;
-          blk = block_of(a_c);
         }
-        const int key = key_chunk(a_c, sc, s.skip) * kChunkKeys + 16 * w4 + lane;
-        row = -1;
-        f.k = f.v = 127u;
-        f.part = false;
-        if (lane < 16 && any_sees(key, s.p0, s.p1)) {
-          row = cache_row(s.r, blk, key);
-          if (row < 0) atomicExch(p.status, kStatusShape);
-          f.part = partly_seen(key, s.p0, s.p1);
-        }
-        if (row >= 0) {
-          const size_t at = (size_t)row * p.kv_per + s.g;
-          f.k = p.scales_k[at];
-          f.v = p.scales_v[at];
-        }
-        ++a_c;
-        if (a_c < a_c1) blk = block_of(a_c);
-        return true;
+        cp_async_commit();
+        ++issued;
       };
-      auto issue = [&](const uint8_t* cache) {
-        const uint8_t* src = cache + s.g * kHd + c8 * 16;
-        const uint32_t dst = raw + (issued % C::kAhead) * kCodeBytes;
+#pragma unroll 1
+      for (int i = 0; i < C::kAhead && ok; ++i) issue();
+      while (ok && converted != last) {
+        const int c = converted >> 1, place = c % C::kLooks;
+        cp_async_wait<C::kAhead - 1>();
+        const uint32_t look = looks + place * kLookBytes + (converted & 1 ? 384 : 128) * 4;
+        const uint32_t src = raw + (converted % C::kAhead) * kCodeBytes;
+        uint4 w[4];
+        uint32_t f[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int rw = __shfl_sync(0xffffffffu, row, 4 * k + sub);
-          cp_async16(dst + k * 4096, src + (size_t)max(rw, 0) * p.kv_per * kHd, rw >= 0 ? 16 : 0, pol);
+          w[k] = lds128(src + k * 4096);
+          f[k] = lds32(look + 16 * k);
         }
-      };
-      // codes of the oldest tile in flight to the next tile of the ring; scale: of this lane's row
-      auto convert = [&](uint32_t scale) -> bool {
-        cp_async_wait<C::kAhead - 1>();
-        if (!wait(C::EMPTY + ring, ring_ph ^ 1)) return false;
-        const uint32_t src = raw + (converted % C::kAhead) * kCodeBytes;
-        const uint32_t fac = scale_factor(scale), rest = scale_rest(scale);
-        const bool large = __any_sync(0xffffffffu, rest != 0x3f803f80u);
+        const bool large = lds32(base + C::kLookOff + place * kLookBytes + 641 * 4) != 0u;
+        if (!wait(C::EMPTY + ring, ring_ph ^ 1)) break;
         // the piece's two halves: 16-byte chunks 2 c8 and 2 c8 + 1 of the row's sixteen; row & 7 is 4 (k & 1) + sub
         const uint32_t dst = base + C::kRingOff + ring * kTileBytes + (c8 >> 2) * (kTileBytes / 2) + (16 * w4 + sub) * 128;
         const uint32_t even = ((2 * (c8 & 3)) ^ sub) << 4, odd = ((2 * (c8 & 3) + 1) ^ sub) << 4;
-        uint4 w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = lds128(src + k * 4096);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t f = __shfl_sync(0xffffffffu, fac, 4 * k + sub);
           uint32_t x[8] = {code_pair(w[k].x, 0), code_pair(w[k].x, 1), code_pair(w[k].y, 0), code_pair(w[k].y, 1),
                            code_pair(w[k].z, 0), code_pair(w[k].z, 1), code_pair(w[k].w, 0), code_pair(w[k].w, 1)};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = mul_bf16x2(x[i], f);
+          for (int i = 0; i < 8; ++i) x[i] = mul_bf16x2(x[i], f[k]);
           if (large) {
-            const uint32_t f2 = __shfl_sync(0xffffffffu, rest, 4 * k + sub);
+            const uint32_t rest = lds32(look + 512 + 16 * k);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = mul_bf16x2(x[i], f2);
+            for (int i = 0; i < 8; ++i) x[i] = mul_bf16x2(x[i], rest);
           }
-          const uint32_t at = dst + 4 * k * 128, flip = (k & 1) << 6;
-          sts128(at + (even ^ flip), x[0], x[1], x[2], x[3]);
-          sts128(at + (odd ^ flip), x[4], x[5], x[6], x[7]);
+          const uint32_t to = dst + 4 * k * 128, flip = (k & 1) << 6;
+          sts128(to + (even ^ flip), x[0], x[1], x[2], x[3]);
+          sts128(to + (odd ^ flip), x[4], x[5], x[6], x[7]);
         }
         fence_async_proxy();
-        ++converted;
-        return true;
-      };
-      Flight f0{}, f1{}, f2{};
-      // one chunk for each of the two places ahead; an empty group where there is none
-      auto prime = [&](Flight& f) {
-        const bool more = next_chunk(f);
-        if (more) issue(cache_k);
-        cp_async_commit();
-        ++issued;
-        if (more) issue(cache_v);
-        cp_async_commit();
-        ++issued;
-      };
-      prime(f0);
-      prime(f1);
-      for (int b_no = 0; ok; ++b_no) {
-        // the converting cursor's segment: published, as the issuing one has read it or the end
-        const int slot = b_no % kUnitSlots;
-        if (!wait(C::U_FULL + slot, (b_no / kUnitSlots) & 1)) break;
-        if (s_seg[slot].b < 0) break;
-        const int n = s_seg[slot].c1 - s_seg[slot].c0;
-        for (int j = 0; j < n && ok; ++j) {
-          const bool more = next_chunk(f2);
-          if (!ok || !convert(f0.k)) break;
+        __syncwarp();
+        if (lane == 0) {
           mbar_arrive(bar(C::FULL + ring));
-          advance();
-          if (more) issue(cache_k);
-          cp_async_commit();
-          ++issued;
-          // a V row that is not finite and only partly seen: zeros, and the mark
-          const bool drop = f0.part && f0.v == kScaleNan;
-          if (drop) *reinterpret_cast<volatile int*>(&s_seg[slot].bad) = 1;
-          if (!convert(drop ? kDropRow : f0.v)) break;
-          mbar_arrive(bar(C::FULL + ring));
-          advance();
-          if (more) issue(cache_v);
-          cp_async_commit();
-          ++issued;
-          f0 = f1;
-          f1 = f2;
+          if (converted & 1) mbar_arrive(bar(C::L_EMPTY + place));
         }
-        if (!ok) break;
-        release_segment(slot);
+        advance();
+        ++converted;
+        issue();
       }
     }
     cp_async_wait_all();       // no copy into this CTA's shared memory may outlive it

@@ -52,8 +52,7 @@ struct DecodeCfg {
   static constexpr int kRing = kStages * 2 * kTile;          // of one warp
   static constexpr int kQBytes = kRows * kHd * 2;
   static constexpr int kQOff = kWarps * kRing;
-  static constexpr int kExOff = kQOff + kBatch * kQBytes;    // exchange: [warp][8 rows][8][4] fp32
-  static constexpr int kMlOff = kExOff + kWarps * 1024;      // [warp][row] (max, sum)
+  static constexpr int kMlOff = kQOff + kBatch * kQBytes;    // [warp][row] (max, sum)
   static constexpr int kSegOff = kMlOff + kWarps * kRows * 8;
   static constexpr int kWalkOff = kSegOff + kBatch * 64;
   static constexpr int kBarOff = kWalkOff + (int)((sizeof(ChunkWalk) + 15) / 16 * 16);
@@ -61,6 +60,7 @@ struct DecodeCfg {
   static constexpr int kMiscOff = kBarOff + 8 * NBARS;       // abort flag, segments of the batch
   static constexpr int kSmem = kMiscOff + 8 + 128;           // 128: alignment of the base
   static_assert((kSmem + 1024) * kCtas <= 233472, "shared memory of the CTAs of one SM");
+  static_assert(2 * kTile >= 8 * kHd * 4, "eight rows of O in a place of the ring");
   static constexpr float kHead = Q8 ? -7.0f : 17.0f;         // m above the largest x when it is taken
 };
 
@@ -215,18 +215,21 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<NT, Q8>::kCtas) chunk_deco
       cp_async16(base + C::kQOff + i * 16, in ? q : p.qkv, in ? 16 : 0, pol);
     }
     cp_async_commit();
-    // the issuing cursor: chunk a_c of segment a_s; lanes 0 - 15 have a key each, its block loaded before
-    int a_s = 0, a_c = s_seg[0].c0, blk = 0, issued = 0;
+    // The issuing cursor, chunk a_c of segment a_s, and the one that looks up blocks two chunks before it;
+    // lanes 0 - 15 have a key each.
+    int a_s = 0, a_c = s_seg[0].c0, f_s = 0, f_c = a_c, blk = -1, blk_next = -1, issued = 0;
     struct Flight { uint32_t k, v; };                        // scale bytes of the lane's key
     auto find = [&]() {
-      blk = -1;
-      if (a_s < segs && lane < 16) {
-        const ChunkSegment& s = s_seg[a_s];
-        const int key = key_chunk(a_c, sc, s.skip) * kChunkKeys + 16 * warp + lane;
-        if (chunk_any(p.call, key, s.p0, s.p1)) {
-          blk = p.block_tables[(size_t)s.b * p.max_blocks + chunk_page(p, key)];
-          if (blk < 0) blk = p.num_blocks;                   // (-1: not seen)
+      blk = blk_next;
+      blk_next = -1;
+      if (f_s < segs) {
+        const ChunkSegment& s = s_seg[f_s];
+        const int key = key_chunk(f_c, sc, s.skip) * kChunkKeys + 16 * warp + lane;
+        if (lane < 16 && chunk_any(p.call, key, s.p0, s.p1)) {
+          blk_next = p.block_tables[(size_t)s.b * p.max_blocks + chunk_page(p, key)];
+          if (blk_next < 0) blk_next = p.num_blocks;         // (-1: not seen)
         }
+        if (++f_c == s.c1 && ++f_s < segs) f_c = s_seg[f_s].c0;
       }
     };
     auto issue = [&](Flight& f) {
@@ -262,15 +265,14 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<NT, Q8>::kCtas) chunk_deco
             cp_async16(vd + kPer * k * C::kRowBytes + vp * 16, cv + off, bytes, pol);
           }
         }
-        if (++a_c == s.c1) {
-          if (++a_s < segs) a_c = s_seg[a_s].c0;
-        }
+        if (++a_c == s.c1 && ++a_s < segs) a_c = s_seg[a_s].c0;
       }
       cp_async_commit();
       ++issued;
       find();
     };
     Flight f[C::kStages];
+    find();
     find();
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) issue(f[i]);
@@ -504,67 +506,91 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<NT, Q8>::kCtas) chunk_deco
     if (bad && lane == 0) *reinterpret_cast<volatile int*>(&s_seg[u].bad) = 1;
     const int r = s_seg[u].r, hg = s_seg[u].g, part = s_seg[u].part, rows = s_seg[u].rows, b = s_seg[u].b;
     const int q0 = s_seg[u].q0 + s_seg[u].tok0;
-    float4* ex = reinterpret_cast<float4*>(base_ptr + C::kExOff);
-    const int jg = lane >> 2, jj = lane & 3;                 // joining: row `warp` of an n-tile, dimensions by lane
+    // O of eight rows, [row][128] fp32 in pieces of four dimensions, goes to the place of every warp's ring
+    // that its last chunk left; pieces are permuted by row so that neither side meets a bank twice. Warp w
+    // then joins row w, four dimensions per lane.
+    const uint32_t place = (used + C::kStages - 1) % C::kStages * (2 * C::kTile);
+    auto piece_of = [](int x, int row) { return x ^ (Q8 ? row >> 1 : row & 6); };
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int row = 8 * n + warp;
-      float fw[kWarps], inv = 0.f, mt = -INFINITY, lt = 0.f;
+      float* mine = reinterpret_cast<float*>(base_ptr + warp * C::kRing + place);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {                          // 32 dimensions at a time: products 2 k, 2 k + 1
-        ex[(warp * 8 + 2 * t) * 8 + (g ^ (2 * t))] = make_float4(o[2 * k][n][0], o[2 * k][n][2], o[2 * k + 1][n][0], o[2 * k + 1][n][2]);
-        ex[(warp * 8 + 2 * t + 1) * 8 + (g ^ (2 * t + 1))] = make_float4(o[2 * k][n][1], o[2 * k][n][3], o[2 * k + 1][n][1], o[2 * k + 1][n][3]);
-        if (!meet(C::X_FULL, xph)) break;
-        if (k == 0) {
+      for (int h = 0; h < 2; ++h) {
+        const int row = 2 * t + h;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, s_ml[w * C::kRows + row].x);
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (Q8) {                                // dimensions 16 g + 4 k ..
+            *reinterpret_cast<float4*>(mine + row * kHd + 4 * piece_of(4 * g + k, row)) =
+                make_float4(o[2 * k][n][h], o[2 * k][n][2 + h], o[2 * k + 1][n][h], o[2 * k + 1][n][2 + h]);
+          } else {                                           // 32 k + g, + 8, + 16, + 24
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float2 y = s_ml[w * C::kRows + row];       // sum 0: the row sees none of the warp's keys
-            fw[w] = y.y == 0.f ? 0.f : fast_exp2(y.x - mt);
-            // in the exponent: where v's scales differ much, l is far from 1
-            lt += y.y == 0.f ? 0.f : fast_exp2(__log2f(y.y) + (y.x - mt));
+            for (int e = 0; e < 4; ++e) {
+              const int dim = 32 * k + 8 * e + g;
+              mine[row * kHd + 4 * piece_of(dim >> 2, row) + (dim & 3)] = o[2 * k + (e >> 1)][n][2 * (e & 1) + h];
+            }
           }
-          inv = lt == 0.f ? 0.f : 1.0f / lt;
         }
-        float v = 0.f;
+      }
+      if (!meet(C::X_FULL, xph)) break;
+      const int row = 8 * n + warp;
+      float mt = -INFINITY, lt = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float y = reinterpret_cast<const float*>(&ex[(w * 8 + warp) * 8 + (jg ^ warp)])[jj];
-          v += fw[w] == 0.f ? 0.f : fw[w] * y;
+      for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, s_ml[w * C::kRows + row].x);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 y = s_ml[w * C::kRows + row];
+        const float4 x = *reinterpret_cast<const float4*>(base_ptr + w * C::kRing + place + 4 * (warp * kHd + 4 * piece_of(lane, warp)));
+        if (y.y != 0.f) {                                    // else the row sees none of the warp's keys
+          const float f = fast_exp2(y.x - mt);
+          // in the exponent: where v's scales differ much, l is far from 1
+          lt += fast_exp2(__log2f(y.y) + (y.x - mt));
+          v.x += f * x.x;
+          v.y += f * x.y;
+          v.z += f * x.z;
+          v.w += f * x.w;
         }
-        const int dim = Q8 ? 16 * jg + 4 * k + jj : 32 * k + 8 * jj + jg;
-        if (row < rows) {
-          const int tok = token_of(row);
-          if constexpr (!Q8) {
-            if (*reinterpret_cast<volatile int*>(&s_seg[u].bad)) {
-              // V values that were dropped, added to the rows that see their keys
-              const int* bt = p.block_tables + (size_t)b * p.max_blocks;
-              for (int c = c0; c < c1; ++c) {
-                const int kc = key_chunk(c, sc, skip);
-                if (!chunk_mixed(p.call, kc, p0, p1)) continue;
-                for (int key = kc * kChunkKeys; key < (kc + 1) * kChunkKeys; ++key) {
-                  if (!chunk_partly(p.call, key, p0, p1) || !chunk_any(p.call, key, p0 + tok, p0 + tok)) continue;
-                  const int rw = chunk_row(p, r, bt[chunk_page(p, key)], key);
-                  if (rw < 0) continue;
-                  const float y = __bfloat162float(static_cast<const __nv_bfloat16*>(p.cache_v)[((size_t)rw * p.kv_per + hg) * kHd + dim]);
-                  if (!(fabsf(y) < INFINITY)) v += y;
-                }
+      }
+      if (row < rows) {
+        const int tok = token_of(row);
+        if constexpr (!Q8) {
+          if (*reinterpret_cast<volatile int*>(&s_seg[u].bad)) {
+            // V values that were dropped, added to the rows that see their keys
+            const int* bt = p.block_tables + (size_t)b * p.max_blocks;
+            for (int c = c0; c < c1; ++c) {
+              const int kc = key_chunk(c, sc, skip);
+              if (!chunk_mixed(p.call, kc, p0, p1)) continue;
+              for (int key = kc * kChunkKeys; key < (kc + 1) * kChunkKeys; ++key) {
+                if (!chunk_partly(p.call, key, p0, p1) || !chunk_any(p.call, key, p0 + tok, p0 + tok)) continue;
+                const int rw = chunk_row(p, r, bt[chunk_page(p, key)], key);
+                if (rw < 0) continue;
+                const __nv_bfloat16* y = static_cast<const __nv_bfloat16*>(p.cache_v) + ((size_t)rw * p.kv_per + hg) * kHd + 4 * lane;
+                auto add = [](float& to, __nv_bfloat16 from) {
+                  const float z = __bfloat162float(from);
+                  if (!(fabsf(z) < INFINITY)) to += z;
+                };
+                add(v.x, y[0]);
+                add(v.y, y[1]);
+                add(v.z, y[2]);
+                add(v.w, y[3]);
               }
             }
           }
-          if (part >= 0) {
-            *chunk_part_o(p, part, row, dim) = v;
-            if (k == 0 && lane == 0) *chunk_part_ml(p, part, row) = make_float2(mt, lt);
-          } else {
-            p.out[(size_t)r * p.sstride_out + (size_t)(q0 + tok) * p.rstride_out + (hg * gq + row - tok * gq) * kHd + dim] =
-                __float2bfloat16_rn(v * inv);
-          }
         }
-        if (!meet(C::X_EMPTY, xph)) break;
-        xph ^= 1u;
+        if (part >= 0) {
+          *reinterpret_cast<float4*>(chunk_part_o(p, part, row, 4 * lane)) = v;
+          if (lane == 0) *chunk_part_ml(p, part, row) = make_float2(mt, lt);
+        } else {
+          const float inv = lt == 0.f ? 0.f : 1.0f / lt;
+          uint2 out;
+          out.x = pack_bf16x2(v.x * inv, v.y * inv);
+          out.y = pack_bf16x2(v.z * inv, v.w * inv);
+          *reinterpret_cast<uint2*>(p.out + (size_t)r * p.sstride_out + (size_t)(q0 + tok) * p.rstride_out +
+                                    (hg * gq + row - tok * gq) * kHd + 4 * lane) = out;
+        }
       }
-      if (!ok) break;
+      if (!meet(C::X_EMPTY, xph)) break;
+      xph ^= 1u;
     }
     if (!ok) break;
     }
