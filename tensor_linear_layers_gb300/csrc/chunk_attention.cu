@@ -93,6 +93,7 @@ struct ChunkCfg {
   static constexpr int kRegsAll = 128 * kRegs0 + 32 * kCopyWarps * kRegs1 + 128 * MT * kRegsS;
   static constexpr int kLaunchRegs = MT == 1 ? (Q8 ? 128 : 168) : Q8 ? 96 : 128;
   static_assert(kRegsAll <= kThreads * kLaunchRegs, "register split within the launch's");
+  static_assert(kRegs0 <= kLaunchRegs && kRegs1 <= kLaunchRegs && kRegsS >= kLaunchRegs, "who gives registers up, and who takes them");
   // tensor memory: MT = 1: S/P at 0, 128, 256, O at 384; MT = 2: tile m S/P at 256 m and 256 m + 64, O at 256 m + 128
   static __device__ __forceinline__ uint32_t s_col(int tile, int buf) { return tile * 256 + (buf - tile * kSBufs) * kSub; }
   static __device__ __forceinline__ uint32_t o_col(int tile) { return MT == 1 ? 384 : tile * 256 + 128; }

@@ -405,10 +405,10 @@ def test_two_calls_at_once_with_workspaces_of_their_own():
 
 
 def test_wait_limit_runs_out_and_context_survives():
-    # in the kernel of 128-row tiles, whose softmax, looking-over and issuing warps wait for one another at an item's
-    # ends; no wait of the kernel for up to 16 rows lasts longer than the first suspended try
+    # in the kernel of 128-row tiles, whose walking warp is four items of some 100 us ahead and waits for a place;
+    # no wait of the kernel for up to 16 rows lasts longer than the first suspended try
     for q8 in (False, True):
-        reqs, ctx, n = 24, 8192, 20
+        reqs, ctx, n = 110, 8192, 20
         c = build(8, 8, 1, [ctx], [n], 16, seed=60, q8=q8)
         h = handle(8, 8, 1)
         many = dict(c, tables=np.repeat(c["tables"], reqs, 0), lens=[ctx + n] * reqs, qsl=np.arange(reqs + 1) * n,
