@@ -971,7 +971,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_kernel(const Chu
   }
 }
 
-// The same for items of up to 16 rows, which many CTAs may share (one request's 4000 keys: 19 CTAs per kv
+// The same for items of up to eight rows, which many CTAs may share (one request's 4000 keys: 19 CTAs per kv
 // head): a CTA per row, each of its warps an eighth of the parts, joined in order.
 __global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_few_kernel(const ChunkAttnParams p) {
   griddep_wait();
@@ -1024,8 +1024,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_few_kernel(const
                             (it.g * gq + row - tok * gq) * kHd + 4 * lane) = out;
 }
 
-// Rows of an item: with up to 16 of them the warp-level kernel (chunk_decode.cu).
-int chunk_group_rows(int max_rows) { return max_rows <= 16 ? 16 : max_rows <= 128 ? 128 : 256; }
+// Rows of an item: with up to eight of them the warp-level kernel (chunk_decode.cu; one request of 4000 keys 12.7 us,
+// 15.1 here). For 16 rows it would take two products for each one: 59 us for 32 requests of 2000 keys, 53 here.
+int chunk_group_rows(int max_rows) { return max_rows <= 8 ? 8 : max_rows <= 128 ? 128 : 256; }
 
 template <int MT, bool Q8>
 static cudaError_t launch_chunk(const ChunkAttnParams& p, int grid, cudaStream_t st) {
@@ -1053,15 +1054,15 @@ static cudaError_t launch_chunk(const ChunkAttnParams& p, int grid, cudaStream_t
 cudaError_t launch_chunk_attention(const ChunkAttnParams& p, int grid, cudaStream_t st) {
   const int rows = chunk_group_rows(std::min(p.call.max_query_len, 256) * p.call.gq);
   const bool q8 = p.scales_k != nullptr;
-  cudaError_t e = rows == 16    ? launch_chunk_decode(p, grid, st)
+  cudaError_t e = rows == 8    ? launch_chunk_decode(p, grid, st)
                   : rows == 128 ? (q8 ? launch_chunk<1, true>(p, grid, st) : launch_chunk<1, false>(p, grid, st))
                                 : (q8 ? launch_chunk<2, true>(p, grid, st) : launch_chunk<2, false>(p, grid, st));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   const int max_rows = std::min(p.call.max_query_len, 256) * p.call.gq;
-  const cudaLaunchConfig_t cfg = programmatic(dim3(grid, rows == 16 ? max_rows : (p.part_rows + kMergeRows - 1) / kMergeRows),
+  const cudaLaunchConfig_t cfg = programmatic(dim3(grid, rows == 8 ? max_rows : (p.part_rows + kMergeRows - 1) / kMergeRows),
                                               32 * kMergeWarps, 0, st, attr);
-  return cudaLaunchKernelEx(&cfg, rows == 16 ? chunk_merge_few_kernel : chunk_merge_kernel, p);
+  return cudaLaunchKernelEx(&cfg, rows == 8 ? chunk_merge_few_kernel : chunk_merge_kernel, p);
 }
 
 }  // namespace tpl

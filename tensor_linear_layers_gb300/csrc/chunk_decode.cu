@@ -1,5 +1,5 @@
 // Attention of few query rows over the paged KV cache: decoding requests, whose new tokens x the q
-// heads of a kv head are up to 16 rows. The mathematics, the masks and the work split are those of
+// heads of a kv head are up to eight rows. The mathematics, the masks and the work split are those of
 // chunk_attention.cu, whose 128-row tiles such rows leave empty: there one warp does the whole
 // softmax of a chunk while the other lanes have no row.
 //
@@ -40,19 +40,20 @@ constexpr int kHd = 128;
 constexpr int kWarps = 8;                      // consumers: 16 keys of a chunk each
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBatch = 3;                      // segments of a batch
+constexpr int kRows = 8;                       // query rows of an item
 constexpr float kRescaleLog2 = 8.0f;
 
-template <int NT, bool Q8>
+template <bool Q8>
 struct DecodeCfg {
-  static constexpr int kRows = 8 * NT;
-  static constexpr int kCtas = Q8 && NT == 1 ? 2 : 1;        // per SM
+  static constexpr int kCtas = Q8 ? 2 : 1;                   // per SM
   static constexpr int kRowBytes = Q8 ? kHd : 2 * kHd;
   static constexpr int kTile = 16 * kRowBytes;               // K or V of a warp's keys
-  static constexpr int kStages = Q8 && NT == 2 ? 6 : 3;
+  static constexpr int kStages = 3;
   static constexpr int kRing = kStages * 2 * kTile;          // of one warp
   static constexpr int kQBytes = kRows * kHd * 2;
   static constexpr int kQOff = kWarps * kRing;
-  static constexpr int kMlOff = kQOff + kBatch * kQBytes;    // [warp][row] (max, sum)
+  static constexpr int kFactorOff = kQOff + kBatch * kQBytes;     // [segment][row]
+  static constexpr int kMlOff = kFactorOff + kBatch * kRows * 4;  // [warp][row] (max, sum)
   static constexpr int kSegOff = kMlOff + kWarps * kRows * 8;
   static constexpr int kWalkOff = kSegOff + kBatch * 64;
   static constexpr int kBarOff = kWalkOff + (int)((sizeof(ChunkWalk) + 15) / 16 * 16);
@@ -73,6 +74,9 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -131,9 +135,9 @@ __device__ __forceinline__ float scale_value(uint32_t s) {
 __device__ __forceinline__ float scale_exponent(uint32_t s) { return s == 255u ? __int_as_float(0x7fffffff) : (float)((int)s - 127); }
 }  // namespace
 
-template <int NT, bool Q8>
-__global__ void __launch_bounds__(kThreads, DecodeCfg<NT, Q8>::kCtas) chunk_decode_kernel(const ChunkAttnParams p) {
-  using C = DecodeCfg<NT, Q8>;
+template <bool Q8>
+__global__ void __launch_bounds__(kThreads, DecodeCfg<Q8>::kCtas) chunk_decode_kernel(const ChunkAttnParams p) {
+  using C = DecodeCfg<Q8>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 127u) & ~127u;
   uint8_t* base_ptr = smem_raw + (base - smem_u32(smem_raw));
@@ -180,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<NT, Q8>::kCtas) chunk_deco
   const int piece = lane % kPieces, sub = lane / kPieces;
   const uint32_t ring = base + warp * C::kRing;
   uint32_t xph = 0;
-  float o[8][NT][4];
+  float o[8][4];
   for (uint32_t batch = 0;; ++batch) {
     if (warp == 0) {
       ChunkWalk walk;
@@ -206,8 +210,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<NT, Q8>::kCtas) chunk_deco
     const int segs = *s_count;
     if (segs == 0) break;
     // ---------------------------------------------------------- the batch's queries, and the first keys
-    for (int i = threadIdx.x; i < segs * C::kRows * 16; i += kThreads) {
-      const int k = i / (C::kRows * 16), j = i / 16 % C::kRows, tok = token_of(j), x = i & 15;
+    for (int i = threadIdx.x; i < segs * kRows * 16; i += kThreads) {
+      const int k = i / (kRows * 16), j = i / 16 % kRows, tok = token_of(j), x = i & 15;
       const ChunkSegment& s = s_seg[k];
       const bool in = j < s.rows;
       const __nv_bfloat16* q = p.qkv + (size_t)s.r * p.sstride_in + (size_t)(s.q0 + s.tok0 + tok) * p.rstride_in +
@@ -277,17 +281,14 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<NT, Q8>::kCtas) chunk_deco
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) issue(f[i]);
     cp_async_wait<C::kStages - 1>();                         // the queries
-    if (!meet(C::X_FULL, xph) || !meet(C::X_EMPTY, xph)) break;
-    xph ^= 1u;
-    int used = 0;                                            // chunks computed
-    for (int u = 0; u < segs; ++u) {
-    const int c0 = s_seg[u].c0, c1 = s_seg[u].c1, p0 = s_seg[u].p0, p1 = s_seg[u].p1, skip = s_seg[u].skip;
-    // Q as the second operand: rows g of every n-tile
-    uint32_t q[NT][8][2];
-    float factor[NT][2];                                     // log2(e) / sqrt(hd), and q's power of two: rows 2 t, 2 t + 1
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const uint32_t qs = base + C::kQOff + u * C::kQBytes + (8 * n + g) * 256;
+    if (!meet(C::X_FULL, xph)) break;
+    // A segment's queries by one warp to the second operand's layout, in their place: for lane and k-step the
+    // two registers of row g; and the rows' factors.
+    if (warp < segs) {
+      const int i = warp;
+      const uint32_t tile = base + C::kQOff + i * (8 * kHd * 2), qs = tile + g * 256;
+      uint32_t b[8][2];
+      float factor = p.scale_log2;                           // log2(e) / sqrt(hd), and (8 bits) q's power of two
       if constexpr (Q8) {
         // the 32 elements of dimensions 64 j + 16 t + (0 .. 15)
         uint4 x[4];
@@ -303,216 +304,194 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<NT, Q8>::kCtas) chunk_deco
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const int e = max((int)(m >> 7), 10);                // biased exponent of the row's largest element
         const float f = __uint_as_float((unsigned)(262 - e) << 23);            // 2^(8 - (e - 127))
-        const float back = p.scale_log2 * __uint_as_float((unsigned)(e - 8) << 23);
-        factor[n][0] = __shfl_sync(0xffffffffu, back, 8 * t);
-        factor[n][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+        factor *= __uint_as_float((unsigned)(e - 8) << 23);
         auto half2 = [&](uint32_t w) { return pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f); };
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          q[n][2 * j][0] = half2(x[j].x);
-          q[n][2 * j][1] = half2(x[j].y);
-          q[n][2 * j + 1][0] = half2(x[j].z);
-          q[n][2 * j + 1][1] = half2(x[j].w);
+          b[2 * j][0] = half2(x[j].x);
+          b[2 * j][1] = half2(x[j].y);
+          b[2 * j + 1][0] = half2(x[j].z);
+          b[2 * j + 1][1] = half2(x[j].w);
         }
       } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          q[n][k][0] = lds32(qs + k * 32 + t * 4);
-          q[n][k][1] = lds32(qs + k * 32 + 16 + t * 4);
+          b[k][0] = lds32(qs + k * 32 + t * 4);
+          b[k][1] = lds32(qs + k * 32 + 16 + t * 4);
         }
-        factor[n][0] = factor[n][1] = p.scale_log2;
       }
-    }
-    int pos[NT][2];                                          // positions of rows 2 t, 2 t + 1
-    float m[NT][2], l[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        pos[n][h] = min(p0 + token_of(8 * n + 2 * t + h), p1);
-        m[n][h] = -INFINITY;
-        l[n][h] = 0.f;
-      }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int h = 0; h < 4; ++h) o[i][n][h] = 0.f;
-    bool bad = false;                                        // bf16: a V that only some rows see was not finite
-    for (int c = c0; c < c1; ++c) {
-      issue(f[C::kStages - 1]);
-      cp_async_wait<C::kStages - 1>();
       __syncwarp();
-      const int key = key_chunk(c, sc, skip) * kChunkKeys + 16 * warp;         // the warp's first key
-      const uint32_t ks = ring + used % C::kStages * (2 * C::kTile), vs = ks + C::kTile;
-      // else nothing of the warp's keys is seen: past the last token, or in the gap before the window
-      if (key <= p1 && (window == 0 || key + 15 > p0 - window || key < sinks)) {
-        float s[NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int k = 0; k < 4; ++k) sts128(tile + k * 512 + lane * 16, b[2 * k][0], b[2 * k][1], b[2 * k + 1][0], b[2 * k + 1][1]);
+      if (t == 0) reinterpret_cast<float*>(base_ptr + C::kFactorOff)[i * 8 + g] = factor;
+    }
+    if (!meet(C::X_EMPTY, xph)) break;
+    xph ^= 1u;
+    int used = 0;                                            // chunks computed
+    for (int u = 0; u < segs; ++u) {
+      const int c0 = s_seg[u].c0, c1 = s_seg[u].c1, p0 = s_seg[u].p0, p1 = s_seg[u].p1, skip = s_seg[u].skip;
+      const uint32_t qs = base + C::kQOff + u * C::kQBytes + lane * 16;
+      const float2 factor = reinterpret_cast<const float2*>(base_ptr + C::kFactorOff)[u * 4 + t];   // of rows 2 t, 2 t + 1
+      int pos[2];                                              // positions of rows 2 t, 2 t + 1
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-          for (int h = 0; h < 4; ++h) s[n][h] = 0.f;
-        float k0 = 1.f, k1 = 1.f, e0 = 0.f, e1 = 0.f;        // scales of keys g, g + 8: k's value, v's exponent
-        if constexpr (Q8) {
-          k0 = scale_value(__shfl_sync(0xffffffffu, f[0].k, g));
-          k1 = scale_value(__shfl_sync(0xffffffffu, f[0].k, g + 8));
-          e0 = scale_exponent(__shfl_sync(0xffffffffu, f[0].v, g));
-          e1 = scale_exponent(__shfl_sync(0xffffffffu, f[0].v, g + 8));
+      for (int h = 0; h < 2; ++h) pos[h] = min(p0 + token_of(2 * t + h), p1);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t at = ks + g * 128 + (((4 * j + t) ^ ((g & 1) << 2)) << 4);
-            const uint4 a = lds128(at), b = lds128(at + 8 * 128);
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t a0 = f16x2_lo(aw[w]), a1 = f16x2_lo(bw[w]), a2 = f16x2_hi(aw[w]), a3 = f16x2_hi(bw[w]);
+        for (int h = 0; h < 4; ++h) o[i][h] = 0.f;
+      bool bad = false;                                        // bf16: a V that only some rows see was not finite
+      for (int c = c0; c < c1; ++c) {
+        issue(f[C::kStages - 1]);
+        cp_async_wait<C::kStages - 1>();
+        __syncwarp();
+        const int key = key_chunk(c, sc, skip) * kChunkKeys + 16 * warp;         // the warp's first key
+        const uint32_t ks = ring + used % C::kStages * (2 * C::kTile), vs = ks + C::kTile;
+        // else nothing of the warp's keys is seen: past the last token, or in the gap before the window
+        if (key <= p1 && (window == 0 || key + 15 > p0 - window || key < sinks)) {
+          float s[4] = {0.f, 0.f, 0.f, 0.f};
+          float k0 = 1.f, k1 = 1.f, e0 = 0.f, e1 = 0.f;        // scales of keys g, g + 8: k's value, v's exponent
+          if constexpr (Q8) {
+            k0 = scale_value(__shfl_sync(0xffffffffu, f[0].k, g));
+            k1 = scale_value(__shfl_sync(0xffffffffu, f[0].k, g + 8));
+            e0 = scale_exponent(__shfl_sync(0xffffffffu, f[0].v, g));
+            e1 = scale_exponent(__shfl_sync(0xffffffffu, f[0].v, g + 8));
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816<true>(s[n], a0, a1, a2, a3, q[n][4 * j + w][0], q[n][4 * j + w][1]);
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t at = ks + g * 128 + (((4 * j + t) ^ ((g & 1) << 2)) << 4);
+              const uint4 a = lds128(at), b = lds128(at + 8 * 128);
+              const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+              for (int w = 0; w < 4; w += 2) {
+                const uint4 q = lds128(qs + (2 * j + w / 2) * 512);   // k-steps 4 j + w and the next
+                uint32_t a0 = f16x2_lo(aw[w]), a1 = f16x2_lo(bw[w]), a2 = f16x2_hi(aw[w]), a3 = f16x2_hi(bw[w]);
+                mma16816<true>(s, a0, a1, a2, a3, q.x, q.y);
+                a0 = f16x2_lo(aw[w + 1]), a1 = f16x2_lo(bw[w + 1]), a2 = f16x2_hi(aw[w + 1]), a3 = f16x2_hi(bw[w + 1]);
+                mma16816<true>(s, a0, a1, a2, a3, q.z, q.w);
+              }
+            }
+          } else {
+            const int r = lane & 15;
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+              uint32_t a[4], a2[4];
+              const uint4 q = lds128(qs + k * 256);
+              ldsm4(a, ks + r * 256 + (((2 * k + (lane >> 4)) ^ (r & 7)) << 4));
+              ldsm4(a2, ks + r * 256 + (((2 * k + 2 + (lane >> 4)) ^ (r & 7)) << 4));
+              mma16816<false>(s, a[0], a[1], a[2], a[3], q.x, q.y);
+              mma16816<false>(s, a2[0], a2[1], a2[2], a2[3], q.z, q.w);
             }
           }
-        } else {
-          const int r = lane & 15;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            uint32_t a[4];
-            ldsm4(a, ks + r * 256 + (((2 * k + (lane >> 4)) ^ (r & 7)) << 4));
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816<false>(s[n], a[0], a[1], a[2], a[3], q[n][k][0], q[n][k][1]);
-          }
-        }
-        // x: the weights' exponents; elements 0, 1 of key g, 2, 3 of key g + 8
-        float x[NT][4];
-        bool over = false;
-        const bool partly = key + 15 > p0 || (window > 0 && key <= p1 - window && key + 15 >= sinks);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float f0 = factor[n][0], f1 = factor[n][1];
-          s[n][0] *= f0 * k0;
-          s[n][1] *= f1 * k0;
-          s[n][2] *= f0 * k1;
-          s[n][3] *= f1 * k1;
-          x[n][0] = s[n][0] + e0;
-          x[n][1] = s[n][1] + e0;
-          x[n][2] = s[n][2] + e1;
-          x[n][3] = s[n][3] + e1;
+          // x: the weights' exponents; elements 0, 1 of key g, 2, 3 of key g + 8
+          const bool partly = key + 15 > p0 || (window > 0 && key <= p1 - window && key + 15 >= sinks);
+          s[0] *= factor.x * k0;
+          s[1] *= factor.y * k0;
+          s[2] *= factor.x * k1;
+          s[3] *= factor.y * k1;
+          float x[4] = {s[0] + e0, s[1] + e0, s[2] + e1, s[3] + e1};
           if (partly) {
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-              const int j = key + g + (h >> 1) * 8, at = pos[n][h & 1];
-              if (!(j <= at && (window == 0 || j > at - window || j < sinks))) s[n][h] = x[n][h] = -INFINITY;
+              const int j = key + g + (h >> 1) * 8, at = pos[h & 1];
+              if (!(j <= at && (window == 0 || j > at - window || j < sinks))) s[h] = x[h] = -INFINITY;
             }
           }
-          over |= fmaxf(x[n][0], x[n][2]) > m[n][0] + (kRescaleLog2 - C::kHead);
-          over |= fmaxf(x[n][1], x[n][3]) > m[n][1] + (kRescaleLog2 - C::kHead);
-        }
-        if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
+          const bool over = fmaxf(x[0], x[2]) > m[0] + (kRescaleLog2 - C::kHead) || fmaxf(x[1], x[3]) > m[1] + (kRescaleLog2 - C::kHead);
+          if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              float top = fmaxf(x[n][h], x[n][2 + h]);
+              float top = fmaxf(x[h], x[2 + h]);
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) + C::kHead;
-              if (top > m[n][h]) {
-                const float f = fast_exp2(m[n][h] - top);    // 0 where nothing was seen before
-                m[n][h] = top;
-                l[n][h] *= f;
+              if (top > m[h]) {
+                const float f = fast_exp2(m[h] - top);         // 0 where nothing was seen before
+                m[h] = top;
+                l[h] *= f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                  o[i][n][h] *= f;
-                  o[i][n][2 + h] *= f;
+                  o[i][h] *= f;
+                  o[i][2 + h] *= f;
                 }
               }
             }
-        }
-        uint32_t pb[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
+          }
           float w[4];
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            const float mu = m[n][h & 1] == -INFINITY ? 0.f : m[n][h & 1];     // nothing seen yet: x = -inf, w = 0
-            w[h] = fast_exp2(x[n][h] - mu);
-            l[n][h & 1] += Q8 ? fast_exp2(s[n][h] - mu) : w[h];
+            const float mu = m[h & 1] == -INFINITY ? 0.f : m[h & 1];             // nothing seen yet: x = -inf, w = 0
+            w[h] = fast_exp2(x[h] - mu);
+            l[h & 1] += Q8 ? fast_exp2(s[h] - mu) : w[h];
           }
-          pb[n][0] = transpose8(Q8 ? pack_f16x2(w[0], w[1]) : pack_bf16x2(w[0], w[1]));
-          pb[n][1] = transpose8(Q8 ? pack_f16x2(w[2], w[3]) : pack_bf16x2(w[2], w[3]));
-        }
-        if constexpr (Q8) {
-          // 16 codes (dimensions 16 g ..) of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-          const uint32_t at = vs + 2 * t * 128 + ((g ^ (2 * t)) << 4);
-          const uint4 v0 = lds128(at), v1 = lds128(at + 128), v2 = lds128(at + 8 * 128), v3 = lds128(at + 9 * 128);
-          const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
-          const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
+          const uint32_t pb0 = transpose8(Q8 ? pack_f16x2(w[0], w[1]) : pack_bf16x2(w[0], w[1]));
+          const uint32_t pb1 = transpose8(Q8 ? pack_f16x2(w[2], w[3]) : pack_bf16x2(w[2], w[3]));
+          if constexpr (Q8) {
+            // 16 codes (dimensions 16 g ..) of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+            const uint32_t at = vs + 2 * t * 128 + ((g ^ (2 * t)) << 4);
+            const uint4 v0 = lds128(at), v1 = lds128(at + 128), v2 = lds128(at + 8 * 128), v3 = lds128(at + 9 * 128);
+            const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+            const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 4; ++j) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t a = __byte_perm(w0[j], w1[j], h ? 0x7362 : 0x5140), b = __byte_perm(w2[j], w3[j], h ? 0x7362 : 0x5140);
-              const uint32_t a0 = f16x2_lo(a), a1 = f16x2_hi(a), a2 = f16x2_lo(b), a3 = f16x2_hi(b);
-#pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816<true>(o[2 * j + h][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
-            }
-          }
-        } else {
-          if (partly && p1 > p0) {
-            // values that some rows do not see and that are not finite: zeros (added again below)
-            uint8_t* v = base_ptr + (vs - base);
-            bool found = false;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int row = 2 * k + (lane >> 4);
-              if (!chunk_partly(p.call, key + row, p0, p1)) continue;
-              uint4* at = reinterpret_cast<uint4*>(v + row * 256 + (lane & 15) * 16);
-              uint4 d = *at;
-              const bool a = drop_nonfinite(d.x), b = drop_nonfinite(d.y), e = drop_nonfinite(d.z), f = drop_nonfinite(d.w);
-              if (a || b || e || f) {
-                *at = d;
-                found = true;
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t a = __byte_perm(w0[j], w1[j], h ? 0x7362 : 0x5140), b = __byte_perm(w2[j], w3[j], h ? 0x7362 : 0x5140);
+                const uint32_t a0 = f16x2_lo(a), a1 = f16x2_hi(a), a2 = f16x2_lo(b), a3 = f16x2_hi(b);
+                mma16816<true>(o[2 * j + h], a0, a1, a2, a3, pb0, pb1);
               }
             }
-            bad |= __any_sync(0xffffffffu, found);
-            __syncwarp();
-          }
-          const int r = (lane & 7) + ((lane >> 4) << 3);
+          } else {
+            if (partly && p1 > p0) {
+              // values that some rows do not see and that are not finite: zeros (added again below)
+              uint8_t* v = base_ptr + (vs - base);
+              bool found = false;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint32_t a[4];
-            ldsm4_t(a, vs + r * 256 + (((2 * i + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
+              for (int k = 0; k < 8; ++k) {
+                const int row = 2 * k + (lane >> 4);
+                if (!chunk_partly(p.call, key + row, p0, p1)) continue;
+                uint4* at = reinterpret_cast<uint4*>(v + row * 256 + (lane & 15) * 16);
+                uint4 d = *at;
+                const bool a = drop_nonfinite(d.x), b = drop_nonfinite(d.y), e = drop_nonfinite(d.z), f = drop_nonfinite(d.w);
+                if (a || b || e || f) {
+                  *at = d;
+                  found = true;
+                }
+              }
+              bad |= __any_sync(0xffffffffu, found);
+              __syncwarp();
+            }
+            const int r = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816<false>(o[i][n], a[0], a[1], a[2], a[3], pb[n][0], pb[n][1]);
+            for (int i = 0; i < 8; ++i) {
+              uint32_t a[4];
+              ldsm4_t(a, vs + r * 256 + (((2 * i + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
+              mma16816<false>(o[i], a[0], a[1], a[2], a[3], pb0, pb1);
+            }
           }
         }
+        __syncwarp();                                          // the ring's place is free for the copies issued next
+        ++used;
+#pragma unroll
+        for (int i = 0; i + 1 < C::kStages; ++i) f[i] = f[i + 1];
       }
-      __syncwarp();                                          // the ring's place is free for the copies issued next
-      ++used;
-#pragma unroll
-      for (int i = 0; i + 1 < C::kStages; ++i) f[i] = f[i + 1];
-    }
-    // ------------------------------------------------------------ the warps' parts of the segment, joined in order
-    float2* s_ml = reinterpret_cast<float2*>(base_ptr + C::kMlOff);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
+      // ------------------------------------------------------------ the warps' parts of the segment, joined in order
+      float2* s_ml = reinterpret_cast<float2*>(base_ptr + C::kMlOff);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float x = l[n][h];
+        float x = l[h];
         x += __shfl_xor_sync(0xffffffffu, x, 4);
         x += __shfl_xor_sync(0xffffffffu, x, 8);
         x += __shfl_xor_sync(0xffffffffu, x, 16);
-        if (g == 0) s_ml[warp * C::kRows + 8 * n + 2 * t + h] = make_float2(m[n][h], x);
+        if (g == 0) s_ml[warp * kRows + 2 * t + h] = make_float2(m[h], x);
       }
-    if (bad && lane == 0) *reinterpret_cast<volatile int*>(&s_seg[u].bad) = 1;
-    const int r = s_seg[u].r, hg = s_seg[u].g, part = s_seg[u].part, rows = s_seg[u].rows, b = s_seg[u].b;
-    const int q0 = s_seg[u].q0 + s_seg[u].tok0;
-    // O of eight rows, [row][128] fp32 in pieces of four dimensions, goes to the place of every warp's ring
-    // that its last chunk left; pieces are permuted by row so that neither side meets a bank twice. Warp w
-    // then joins row w, four dimensions per lane.
-    const uint32_t place = (used + C::kStages - 1) % C::kStages * (2 * C::kTile);
-    auto piece_of = [](int x, int row) { return x ^ (Q8 ? row >> 1 : row & 6); };
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
+      if (bad && lane == 0) *reinterpret_cast<volatile int*>(&s_seg[u].bad) = 1;
+      const int r = s_seg[u].r, hg = s_seg[u].g, part = s_seg[u].part, rows = s_seg[u].rows, b = s_seg[u].b;
+      const int q0 = s_seg[u].q0 + s_seg[u].tok0;
+      // O of eight rows, [row][128] fp32 in pieces of four dimensions, goes to the place of every warp's ring
+      // that its last chunk left; pieces are permuted by row so that neither side meets a bank twice. Warp w
+      // then joins row w, four dimensions per lane.
+      const uint32_t place = (used + C::kStages - 1) % C::kStages * (2 * C::kTile);
+      auto piece_of = [](int x, int row) { return x ^ (Q8 ? row >> 1 : row & 6); };
       float* mine = reinterpret_cast<float*>(base_ptr + warp * C::kRing + place);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -521,25 +500,25 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<NT, Q8>::kCtas) chunk_deco
         for (int k = 0; k < 4; ++k) {
           if constexpr (Q8) {                                // dimensions 16 g + 4 k ..
             *reinterpret_cast<float4*>(mine + row * kHd + 4 * piece_of(4 * g + k, row)) =
-                make_float4(o[2 * k][n][h], o[2 * k][n][2 + h], o[2 * k + 1][n][h], o[2 * k + 1][n][2 + h]);
+                make_float4(o[2 * k][h], o[2 * k][2 + h], o[2 * k + 1][h], o[2 * k + 1][2 + h]);
           } else {                                           // 32 k + g, + 8, + 16, + 24
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int dim = 32 * k + 8 * e + g;
-              mine[row * kHd + 4 * piece_of(dim >> 2, row) + (dim & 3)] = o[2 * k + (e >> 1)][n][2 * (e & 1) + h];
+              mine[row * kHd + 4 * piece_of(dim >> 2, row) + (dim & 3)] = o[2 * k + (e >> 1)][2 * (e & 1) + h];
             }
           }
         }
       }
       if (!meet(C::X_FULL, xph)) break;
-      const int row = 8 * n + warp;
+      const int row = warp;
       float mt = -INFINITY, lt = 0.f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, s_ml[w * C::kRows + row].x);
+      for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, s_ml[w * kRows + row].x);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float2 y = s_ml[w * C::kRows + row];
+        const float2 y = s_ml[w * kRows + row];
         const float4 x = *reinterpret_cast<const float4*>(base_ptr + w * C::kRing + place + 4 * (warp * kHd + 4 * piece_of(lane, warp)));
         if (y.y != 0.f) {                                    // else the row sees none of the warp's keys
           const float f = fast_exp2(y.x - mt);
@@ -591,38 +570,35 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<NT, Q8>::kCtas) chunk_deco
       }
       if (!meet(C::X_EMPTY, xph)) break;
       xph ^= 1u;
-    }
-    if (!ok) break;
+      if (!ok) break;
     }
     if (!ok || segs < kBatch) break;
   }
   cp_async_wait_all();       // no copy into this CTA's shared memory may outlive it
 }
 
-template <int NT, bool Q8>
+template <bool Q8>
 static cudaError_t launch_decode(const ChunkAttnParams& p, int grid, cudaStream_t st) {
-  using C = DecodeCfg<NT, Q8>;
+  using C = DecodeCfg<Q8>;
   static std::atomic<uint64_t> attr_done{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(attr_done.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(chunk_decode_kernel<NT, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(chunk_decode_kernel<Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit, std::memory_order_acq_rel);
   }
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = programmatic(dim3(grid), kThreads, C::kSmem, st, attr);
-  return cudaLaunchKernelEx(&cfg, chunk_decode_kernel<NT, Q8>, p);
+  return cudaLaunchKernelEx(&cfg, chunk_decode_kernel<Q8>, p);
 }
 
-int chunk_decode_ctas(int max_rows, bool q8) { return max_rows <= 8 && q8 ? DecodeCfg<1, true>::kCtas : 1; }
+int chunk_decode_ctas(bool q8) { return q8 ? DecodeCfg<true>::kCtas : DecodeCfg<false>::kCtas; }
 
 cudaError_t launch_chunk_decode(const ChunkAttnParams& p, int grid, cudaStream_t st) {
-  const bool one = p.call.max_query_len * p.call.gq <= 8, q8 = p.scales_k != nullptr;
-  return one ? (q8 ? launch_decode<1, true>(p, grid, st) : launch_decode<1, false>(p, grid, st))
-             : (q8 ? launch_decode<2, true>(p, grid, st) : launch_decode<2, false>(p, grid, st));
+  return p.scales_k != nullptr ? launch_decode<true>(p, grid, st) : launch_decode<false>(p, grid, st);
 }
 
 }  // namespace tpl

@@ -66,7 +66,7 @@ struct ChunkCall {
   int window, sinks;                // 0: none
   int full;                         // places of a chunk of a full group: 2 + its tiles
 };
-// rows_per_group: 16, 128 or 256, at least gq
+// rows_per_group: 8, 128 or 256, at least gq
 TPL_HD int chunk_group_tokens(int gq, int rows_per_group) { return rows_per_group / gq; }
 
 struct ChunkReq {

@@ -238,8 +238,8 @@ struct ChunkAttnParams {
   int out_align32;                   // out is 32-byte aligned (rows are then written with 32-byte stores)
   unsigned long long timeout_ns;
 };
-int chunk_group_rows(int max_rows);  // query rows of one item: up to 16, 128 or 256
-int chunk_decode_ctas(int max_rows, bool q8);   // CTAs per SM of the kernel for up to 16 rows (chunk_decode.cu)
+int chunk_group_rows(int max_rows);  // query rows of one item: up to 8, 128 or 256
+int chunk_decode_ctas(bool q8);      // CTAs per SM of the kernel for up to 8 rows (chunk_decode.cu)
 cudaError_t launch_chunk_decode(const ChunkAttnParams& p, int grid, cudaStream_t st);
 cudaError_t launch_chunk_attention(const ChunkAttnParams& p, int grid, cudaStream_t st);
 

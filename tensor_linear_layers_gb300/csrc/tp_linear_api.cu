@@ -1956,7 +1956,7 @@ ChunkPlan chunk_plan(const tp_linear* h, int64_t T, int n_reqs, int max_query_le
   pl.call.gq = gq;
   pl.call.tg = chunk_group_tokens(gq, rows);
   pl.call.full = 2 + (rows + 127) / 128;
-  const int ctas = rows == 16 ? chunk_decode_ctas((int)max_rows, q8) : 1;
+  const int ctas = rows == 8 ? chunk_decode_ctas(q8) : 1;
   pl.grid = chunk_grid(h->nsm * ctas, n_reqs, h->cfg.t * h->kv_per, max_query_len, pl.call.tg, max_seq_len);
   pl.part_rows = ((int)std::min<int64_t>(rows, max_rows) + 7) / 8 * 8;   // a slot is a multiple of 32 bytes (32-byte stores)
   pl.partials_off = align256(256 + (int64_t)sizeof(TreeItem) * pl.grid);

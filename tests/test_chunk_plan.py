@@ -83,7 +83,7 @@ def test_places_of_the_longest_requests(lib):
 def split(lib, heads, gq, n, lens, window=0, sinks=0, max_q=None, max_len=None, nsm=152, rows=None):
     """(grid, chunks, slots read, holes, chunks computed twice or never, CTAs with work, most chunks of a CTA)."""
     max_q, max_len = max_q or max(max(n), 1), max_len or max(max(lens), 1)
-    rows = rows or (128 if max_q * gq <= 128 else 256)
+    rows = rows or (8 if max_q * gq <= 8 else 128 if max_q * gq <= 128 else 256)
     out, ints = (ctypes.c_int * 6)(), ctypes.c_int * len(n)
     grid = lib.split(nsm, heads, gq, rows, max_q, max_len, window, sinks, len(n), ints(*n), ints(*lens), out)
     assert grid >= 1
