@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
   griddep_wait();
   const int gq = p.call.gq;                         // q heads of a kv head
   const int sc = chunk_sinks(p.call), window = p.call.window, sinks = p.call.sinks;
-  ChunkWalk walk;                                   // warp 2's; the first requests' counts load beside the set-up
+  ChunkWalk<false> walk;                                   // warp 2's; the first requests' counts load beside the set-up
   if (warp == 2) walk.load(p, lane);
   tc_fence_before();
   __syncthreads();

@@ -56,7 +56,7 @@ struct DecodeCfg {
   static constexpr int kMlOff = kFactorOff + kBatch * kRows * 4;  // [warp][row] (max, sum)
   static constexpr int kSegOff = kMlOff + kWarps * kRows * 8;
   static constexpr int kWalkOff = kSegOff + kBatch * 64;
-  static constexpr int kBarOff = kWalkOff + (int)((sizeof(ChunkWalk) + 15) / 16 * 16);
+  static constexpr int kBarOff = kWalkOff + (int)((sizeof(ChunkWalk<true>) + 15) / 16 * 16);
   enum { READY = 0, X_FULL, X_EMPTY, NBARS };
   static constexpr int kMiscOff = kBarOff + 8 * NBARS;       // abort flag, segments of the batch
   static constexpr int kSmem = kMiscOff + 8 + 128;           // 128: alignment of the base
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<Q8>::kCtas) chunk_decode_k
   volatile int* s_abort = reinterpret_cast<volatile int*>(base_ptr + C::kMiscOff);
   volatile int* s_count = s_abort + 1;
   ChunkSegment* s_seg = reinterpret_cast<ChunkSegment*>(base_ptr + C::kSegOff);
-  ChunkWalk* s_walk = reinterpret_cast<ChunkWalk*>(base_ptr + C::kWalkOff);   // warp 0's between batches
+  ChunkWalk<true>* s_walk = reinterpret_cast<ChunkWalk<true>*>(base_ptr + C::kWalkOff);   // warp 0's between batches
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<Q8>::kCtas) chunk_decode_k
   float o[8][4];
   for (uint32_t batch = 0;; ++batch) {
     if (warp == 0) {
-      ChunkWalk walk;
+      ChunkWalk<true> walk;
       if (batch == 0) {
         walk.load(p, lane);
         walk.start(p, lane);

@@ -61,7 +61,8 @@ __device__ __forceinline__ float2* chunk_part_ml(const ChunkAttnParams& p, int s
 
 // One warp walks: every lane calls, with the same result. The code is kept short, each function at one
 // place: it runs once per CTA, and what bounds it is the fetch of its instructions (with four strips of
-// requests unrolled the first segment came after 7 us of a prompt's 150).
+// requests unrolled the first segment came after 7 us of a prompt's 150). ONE: every request is one group.
+template <bool ONE>
 struct ChunkWalk {
   int3 first;                       // request `lane`: row of the first new token, new tokens (-1: bad counts), all tokens
   ChunkReq r;
@@ -115,7 +116,7 @@ struct ChunkWalk {
         const int3 mine = m;
         if (b0 + 32 < p.n_reqs) m = counts(p, b0 + 32 + lane);       // (the next ones, early)
         const ChunkReq q = request(p, mine);
-        one = chunk_head(p.call, q, cost);
+        one = ONE ? (q.groups > 0 ? chunk_item(p.call, q, 0, cost) : 0) : chunk_head(p.call, q, cost);
         const long long pre = scan(heads * one, lane);               // the places up to and with this lane's
         if (pass == 0) {
           if (mine.y < 0 && blockIdx.x == 0) atomicExch(p.status, kChunkStatusShape);
@@ -155,6 +156,7 @@ struct ChunkWalk {
     head += h;
     at -= h * one;
     begin = pos - at;                                  // the head's first place; then its group's
+    if constexpr (ONE) return;
     int n = r.groups;
     long long skipped = 0;
 #pragma unroll 1
