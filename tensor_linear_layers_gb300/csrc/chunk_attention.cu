@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
           if (!wait(C::S_FREE + cnt[0] % C::kSBufs, ((cnt[0] / C::kSBufs) & 1) ^ 1)) break;
           if (!wait(C::FULL + ring, ring_ph)) break;
           fence_async_proxy();
-#pragma unroll
+#pragma unroll(Q8 ? 1 : C::kSubs)
           for (int h = 0; h < C::kSubs; ++h) {
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
         for (int j = 0; j < n && ok; ++j) {
           if (!wait(C::FULL + ring, ring_ph)) break;
           fence_async_proxy();
-#pragma unroll
+#pragma unroll(Q8 ? 1 : C::kSubs)
           for (int h = 0; h < C::kSubs; ++h) {
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
           tc_wait_ld();
           const int key = key_chunk(j / C::kSubs, sc, skip) * kChunkKeys + (j % C::kSubs) * C::kSub;
           // keys that not all of the item's tokens see: the row's mask
-          if (key + C::kSub - 1 > p0 || (window > 0 && key <= p1 - window && key + C::kSub > sinks)) {
+          if (__builtin_expect(key + C::kSub - 1 > p0 || (window > 0 && key <= p1 - window && key + C::kSub > sinks), 0)) {
 #pragma unroll
             for (int w = 0; w < C::kSub / 32; ++w) {
               const unsigned bits = chunk_sees(key + 32 * w, pos, window, sinks);
@@ -786,7 +786,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
             if (!wait_last_pv()) break;
             tc_fence_after();
             float o[32];
-#pragma unroll
+#pragma unroll(Q8 ? 1 : 4)
             for (int k = 0; k < 128; k += 32) {
               tmem_ld32(lane_addr + C::o_col(tile) + k, o);
               tc_wait_ld();
