@@ -36,11 +36,11 @@ namespace tpl {
 // per tile.
 //
 //   warp 0      issues S;  warp 1 issues P V (an elected lane of a converged warp);
-//   warp 2      walks the CTA's range and publishes segments; 8 bits: copies their queries
+//   warp 2      walks the CTA's range, publishes segments and copies their queries (TMA)
 //   warp 3      bf16: looks over the V rows that only some rows of the item see (below);
 //               8 bits: finds the cache rows and scales of every chunk, up to three chunks ahead
 //   4 warps     (bf16) copy K and V rows through the block table with 16-byte cp.async into
-//               128-byte-swizzled tiles (any block size: a key's row is found on its own), and Q;
+//               128-byte-swizzled tiles (any block size: a key's row is found on its own);
 //   8 warps     (8 bits) copy the codes to buffers of their own, three tiles ahead; each thread
 //               turns the codes that it copied into bf16 and stores those
 //   the others  softmax, a row per thread, four warps per tile; at a segment's end O / l to
@@ -154,7 +154,8 @@ __device__ __forceinline__ uint32_t scale_rest(uint32_t s) {
 }  // namespace
 
 template <int MT, bool Q8>
-__global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kernel(const ChunkAttnParams p) {
+__global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkAttnParams p) {
   using C = ChunkCfg<MT, Q8>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -169,7 +170,6 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
   if (warp == 0) {
     for (int b = lane; b < C::NBARS; b += 32) {
       int count = 1;
-      if (b < C::Q_EMPTY) count = Q8 ? 32 : 128;                                // every thread that copies queries
       if (b >= C::FULL && b < C::EMPTY) count = Q8 ? C::kCopyWarps : 128;        // every copying warp or thread
       if (b >= C::P_READY && b < C::S_FREE) count = 4;                          // the tile's softmax warps
       if (b >= C::S_FREE && b < C::O_FREE) count = 2;                           // the MMAs, and their issuer
@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
     if (lane == 0) *s_abort = 0;
     fence_barrier_init();
   }
+  if (threadIdx.x == 64) prefetch_tensormap(&map_q);
   if (warp == 1) {
     tmem_alloc(smem_u32(const_cast<uint32_t*>(s_tmem)), kTmemCols);
     tmem_relinquish();
@@ -269,12 +270,12 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
               if (elect_one()) {
                 const uint32_t d = tmem_base + C::s_col(m, buf);
                 // half h of the chunk: 64 K rows of 128 bytes further
-                const uint64_t qd = q_desc + (qb * MT + m) * kTileDesc, kd = k_desc + ring * kTileDesc + h * ((64 * 128) >> 4);
+                const uint64_t qd = q_desc + qb * MT * kTileDesc + m * (kTileDesc / 2), kd = k_desc + ring * kTileDesc + h * ((64 * 128) >> 4);
                 tc_mma_bf16_c<false>(d, qd, kd, C::kIdescS);
 #pragma unroll
                 for (int k = 1; k < 8; ++k) {
-                  const uint64_t o = (uint64_t)(((k >> 2) * (kTileBytes / 2) + (k & 3) * 32) >> 4);
-                  tc_mma_bf16_c<true>(d, qd + o, kd + o, C::kIdescS);
+                  const int box = (k >> 2) * (kTileBytes / 2), in = (k & 3) * 32;
+                  tc_mma_bf16_c<true>(d, qd + (uint64_t)((MT * box + in) >> 4), kd + (uint64_t)((box + in) >> 4), C::kIdescS);
                 }
                 tc_commit(bar(C::S_FULL + buf));
               }
@@ -362,7 +363,9 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
     } else if (warp == 2) {
       // ------------------------------------------------------------ segments
       walk.start(p, lane);
-      for (int u = 0;; ++u) {
+      const uint64_t pol = policy_evict_normal();
+      int u = 0;
+      for (;; ++u) {
         const int slot = u % kUnitSlots;
         if (!wait(C::U_EMPTY + slot, ((u / kUnitSlots) & 1) ^ 1)) break;
         const ChunkSegment s = walk.next(p, lane);
@@ -372,24 +375,28 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
         }
         __syncwarp();
         if (s.b < 0) break;
-        if constexpr (Q8) {
-          // the segment's queries, once those that the buffer held are no longer read
-          const int qb = u % C::kQBufs, c16 = lane & 15;
-          if (!wait(C::Q_EMPTY + qb, ((u / C::kQBufs) & 1) ^ 1)) break;
-          const __nv_bfloat16* q = p.qkv + (size_t)s.r * p.sstride_in + (size_t)(s.q0 + s.tok0) * p.rstride_in + s.g * gq * kHd + c16 * 8;
-          const uint32_t dst = base + qb * MT * kTileBytes + (c16 >> 3) * (kTileBytes / 2);
-          const uint64_t pol = policy_evict_normal();
-          // rows past the item's keep what the buffer held: they only reach their own rows of S and O
-#pragma unroll 4
-          for (int j = lane >> 4; j < s.rows; j += 2) {
-            const int tok = token_of(j);
-            cp_async16(dst + (j >> 7) * kTileBytes + (j & 127) * 128 + (((c16 & 7) ^ (j & 7)) << 4),
-                       q + (size_t)tok * p.rstride_in + (j - tok * gq) * kHd, 16, pol);
-          }
-          cp_async_arrive(bar(C::Q_FULL + qb));
+        // The segment's queries, once those that the buffer held are no longer read: a box of 64 dimensions x the heads
+        // x the group's tokens is the tiles' rows in order. What it holds past the item's tokens (other tokens, or
+        // zeros past the last) only reaches rows of S and O of its own.
+        const int qb = u % C::kQBufs, head = s.g * gq, tok = s.q0 + s.tok0;
+        if (elect_one()) {
+          tma_prefetch_4d(&map_q, 0, head, tok, s.r);
+          tma_prefetch_4d(&map_q, 64, head, tok, s.r);
         }
+        __syncwarp();
+        if (!wait(C::Q_EMPTY + qb, ((u / C::kQBufs) & 1) ^ 1)) break;
+        if (elect_one()) {
+          const uint32_t dst = base + qb * MT * kTileBytes;
+          mbar_arrive_expect_tx(bar(C::Q_FULL + qb), 2 * p.q_box_rows * 128);
+          tma_load_4d(dst, &map_q, bar(C::Q_FULL + qb), 0, head, tok, s.r, pol);
+          tma_load_4d(dst + MT * (kTileBytes / 2), &map_q, bar(C::Q_FULL + qb), 64, head, tok, s.r, pol);
+        }
+        __syncwarp();
       }
-      if constexpr (Q8) cp_async_wait_all();   // no copy into this CTA's shared memory may outlive it
+      // no copy into this CTA's shared memory may outlive it
+      for (int i = max(u - C::kQBufs, 0); i < u; ++i)
+        mbar_wait_bounded(bar(C::Q_FULL + i % C::kQBufs), (i / C::kQBufs) & 1, nullptr, kTeardownNs);
+      __syncwarp();
     } else if (Q8) {
       // ------------------------------------------------------------ rows and scales of the chunks
       // A lane has four keys on end, of one page where pages are multiples of four. The chunk's factors follow
@@ -571,26 +578,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
       const uint32_t dst0 = (c16 >> 3) * (kTileBytes / 2) + row_of * 128 + (((c16 & 7) ^ (row_of & 7)) << 4);
       const __nv_bfloat16* cache_k = static_cast<const __nv_bfloat16*>(p.cache_k);
       const __nv_bfloat16* cache_v = static_cast<const __nv_bfloat16*>(p.cache_v);
-      // a segment's queries, once those that the buffer held are no longer read
-      auto load_q = [&](const ChunkSegment& s, int seg_no) {
-        const int qb = seg_no % C::kQBufs;
-        if (!wait(C::Q_EMPTY + qb, ((seg_no / C::kQBufs) & 1) ^ 1)) return;
-        const __nv_bfloat16* q = p.qkv + (size_t)s.r * p.sstride_in + (size_t)(s.q0 + s.tok0) * p.rstride_in + s.g * gq * kHd + c16 * 8;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          if (m * 128 >= s.rows) break;
-          // rows past the item's keep what the buffer held: they only reach their own rows of S and O
-#pragma unroll 4
-          for (int k = 0; k < 16; ++k) {
-            const int j = m * 128 + row_of + 8 * k, tok = token_of(j);
-            if (j < s.rows)
-              cp_async16(base + (qb * MT + m) * kTileBytes + dst0 + k * 1024,
-                         q + (size_t)tok * p.rstride_in + (j - tok * gq) * kHd, 16, pol);
-          }
-        }
-        cp_async_arrive(bar(C::Q_FULL + qb));
-      };
-      for (int seg_no = 0;; ++seg_no) {
+      for (;;) {
         const int slot = next_segment();
         if (slot < 0) break;
         const ChunkSegment s = s_seg[slot];
@@ -600,18 +588,6 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
           return any_sees(key, s.p0, s.p1) ? bt[chunk_page(p, key)] : 0;
         };
         int blk = block_of(s.c0);
-        // with one Q buffer the last segment's queries may still be read: the first K tile goes before
-        // (and the queries' rows, 256 bytes each, start for L2: their copy is what S waits for)
-        constexpr bool q_first = C::kQBufs > 1;
-        if (q_first) {
-          load_q(s, seg_no);
-        } else {
-          for (int j = threadIdx.x - 128; j < 2 * s.rows; j += 128) {
-            const int tok = token_of(j >> 1);
-            prefetch_l2(p.qkv + (size_t)s.r * p.sstride_in + (size_t)(s.q0 + s.tok0 + tok) * p.rstride_in +
-                        (s.g * gq + (j >> 1) - tok * gq) * kHd + (j & 1) * 64);
-          }
-        }
         for (int c = s.c0; c < s.c1 && ok; ++c) {
           const int kc = key_chunk(c, sc, s.skip), key = kc * kChunkKeys + my_row;
           int row = -1;                                // cache row of this lane's key (-1: zeros)
@@ -632,7 +608,6 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1) chunk_attn_kern
             }
             cp_async_arrive(bar((kv == 1 && mixed_chunk(kc, s.p0, s.p1) ? C::LANDED : C::FULL) + ring));
             advance();
-            if (kv == 0 && c == s.c0 && !q_first) load_q(s, seg_no);
             if (!ok) break;
           }
         }
@@ -1029,7 +1004,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_few_kernel(const
 int chunk_group_rows(int max_rows) { return max_rows <= 8 ? 8 : max_rows <= 128 ? 128 : 256; }
 
 template <int MT, bool Q8>
-static cudaError_t launch_chunk(const ChunkAttnParams& p, int grid, cudaStream_t st) {
+static cudaError_t launch_chunk(const CUtensorMap& map_q, const ChunkAttnParams& p, int grid, cudaStream_t st) {
   using C = ChunkCfg<MT, Q8>;
   static std::atomic<uint64_t> attr_done{0};
   int dev = 0;
@@ -1048,15 +1023,15 @@ static cudaError_t launch_chunk(const ChunkAttnParams& p, int grid, cudaStream_t
   }
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = programmatic(dim3(grid), C::kThreads, C::kSmem, st, attr);
-  return cudaLaunchKernelEx(&cfg, chunk_attn_kernel<MT, Q8>, p);
+  return cudaLaunchKernelEx(&cfg, chunk_attn_kernel<MT, Q8>, map_q, p);
 }
 
-cudaError_t launch_chunk_attention(const ChunkAttnParams& p, int grid, cudaStream_t st) {
+cudaError_t launch_chunk_attention(const CUtensorMap& map_q, const ChunkAttnParams& p, int grid, cudaStream_t st) {
   const int rows = chunk_group_rows(std::min(p.call.max_query_len, 256) * p.call.gq);
   const bool q8 = p.scales_k != nullptr;
   cudaError_t e = rows == 8    ? launch_chunk_decode(p, grid, st)
-                  : rows == 128 ? (q8 ? launch_chunk<1, true>(p, grid, st) : launch_chunk<1, false>(p, grid, st))
-                                : (q8 ? launch_chunk<2, true>(p, grid, st) : launch_chunk<2, false>(p, grid, st));
+                  : rows == 128 ? (q8 ? launch_chunk<1, true>(map_q, p, grid, st) : launch_chunk<1, false>(map_q, p, grid, st))
+                                : (q8 ? launch_chunk<2, true>(map_q, p, grid, st) : launch_chunk<2, false>(map_q, p, grid, st));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   const int max_rows = std::min(p.call.max_query_len, 256) * p.call.gq;

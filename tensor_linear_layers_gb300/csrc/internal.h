@@ -235,13 +235,14 @@ struct ChunkAttnParams {
   TreeItem* items;                   // [grid] the item each CTA begins and others go on with, for the merge
   float* partials;                   // [2 * grid] slots of part_rows x (128 + 2)
   int part_rows;
+  int q_box_rows;                    // rows of a box of the map of the queries
   int out_align32;                   // out is 32-byte aligned (rows are then written with 32-byte stores)
   unsigned long long timeout_ns;
 };
 int chunk_group_rows(int max_rows);  // query rows of one item: up to 8, 128 or 256
 int chunk_decode_ctas(bool q8);      // CTAs per SM of the kernel for up to 8 rows (chunk_decode.cu)
 cudaError_t launch_chunk_decode(const ChunkAttnParams& p, int grid, cudaStream_t st);
-cudaError_t launch_chunk_attention(const ChunkAttnParams& p, int grid, cudaStream_t st);
+cudaError_t launch_chunk_attention(const CUtensorMap& map_q, const ChunkAttnParams& p, int grid, cudaStream_t st);
 
 // A cache in 8 bits (kv_quant.cu).
 struct KvQuantParams {

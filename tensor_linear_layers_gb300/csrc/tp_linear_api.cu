@@ -165,6 +165,26 @@ int make_shard_map(CUtensorMap* m, const void* ptr, int64_t w, int64_t T, int64_
   return TP_OK;
 }
 
+// 4-D tensor map of the q, k and v heads of 128 elements: (element, head of the shard, token, shard); boxes of
+// 64 elements x heads x tokens, 128-byte swizzle.
+int make_heads_map(CUtensorMap* m, const void* ptr, int64_t heads, int64_t T, int64_t t, bool gathered, int box_heads,
+                   int box_tokens) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return fail(TP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint64_t dims[4] = {128, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)t};
+  const cuuint64_t w = (cuuint64_t)heads * 256;
+  const cuuint64_t strides[3] = {256, gathered ? w * (cuuint64_t)t : w, gathered ? w : w * (cuuint64_t)T};
+  const cuuint32_t box[4] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_tokens, 1u};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(TP_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %lld heads x %lld tokens x %lld shards", (int)r,
+                (long long)heads, (long long)T, (long long)t);
+  return TP_OK;
+}
+
 // Tensor map of packed weight blocks for the CTA-pair engine: dims (64 elements,
 // 256 rows, n_blocks), each block 32 KB, boxes of 64 x 128 rows (one half of a
 // block, 16 KB). The blocks are already in the swizzled image the MMA reads, so
@@ -1942,7 +1962,7 @@ int tp_kv_quant_read(tp_linear_t* h, int64_t n, const int32_t* slots, const void
 namespace {
 struct ChunkPlan {
   ChunkCall call;
-  int grid, part_rows;
+  int rows, grid, part_rows;         // rows of a group: 8, 128 or 256
   int64_t partials_off, ws_bytes;
 };
 ChunkPlan chunk_plan(const tp_linear* h, int64_t T, int n_reqs, int max_query_len, int max_seq_len, bool q8) {
@@ -1950,6 +1970,7 @@ ChunkPlan chunk_plan(const tp_linear* h, int64_t T, int n_reqs, int max_query_le
   const int64_t max_rows = (int64_t)max_query_len * gq;
   const int rows = chunk_group_rows((int)std::min<int64_t>(max_rows, 256));
   ChunkPlan pl{};
+  pl.rows = rows;
   pl.call.T = (int)T;
   pl.call.max_query_len = max_query_len;
   pl.call.max_seq_len = max_seq_len;
@@ -2053,7 +2074,13 @@ int tp_chunk_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t
   p.part_rows = pl.part_rows;
   p.out_align32 = (reinterpret_cast<uintptr_t>(attn_out) & 31u) == 0 ? 1 : 0;
   p.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
-  const cudaError_t e = launch_chunk_attention(p, pl.grid, static_cast<cudaStream_t>(stream));
+  CUtensorMap map_q{};
+  if (pl.rows > 8) {
+    const int tokens = std::min(pl.call.tg, max_query_len);
+    p.q_box_rows = tokens * pl.call.gq;
+    if ((rc = make_heads_map(&map_q, qkv, h->ws_qkv / 128, T, h->cfg.t, gath, pl.call.gq, tokens))) return rc;
+  }
+  const cudaError_t e = launch_chunk_attention(map_q, p, pl.grid, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
   return ok();
 }
