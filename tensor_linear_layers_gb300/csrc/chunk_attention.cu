@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
   volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(base_ptr + C::kMiscOff);
   volatile int* s_abort = reinterpret_cast<volatile int*>(base_ptr + C::kMiscOff + 4);
   ChunkSegment* s_seg = reinterpret_cast<ChunkSegment*>(base_ptr + C::kUnitOff);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;   // (known to be one for all lanes)
   griddep_launch_dependents();   // the merge grid may be scheduled; it waits for this one to complete
   if (warp == 0) {
     for (int b = lane; b < C::NBARS; b += 32) {
@@ -198,7 +198,9 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = *s_tmem;
+  // a value that is one for the whole warp, known as such to the compiler (uniform registers, no divergent branches)
+  auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+  const uint32_t tmem_base = (uint32_t)uni((int)*s_tmem);
   const unsigned long long timeout = p.timeout_ns;
   // row / gq as a product: 2^32 / gq rounded up is off by less than 1, and row * gq < 2^32
   const unsigned gq_magic = 0xffffffffu / (unsigned)gq + 1u;
@@ -223,7 +225,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
     const int slot = nu % kUnitSlots;
     if (!wait(C::U_FULL + slot, (nu / kUnitSlots) & 1)) return -1;
     ++nu;
-    return s_seg[slot].b < 0 ? -1 : slot;
+    return uni(s_seg[slot].b) < 0 ? -1 : slot;
   };
   auto release_segment = [&](int slot) {
     __syncwarp();
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
       for (int seg_no = 0;; ++seg_no) {
         const int slot = next_segment();
         if (slot < 0) break;
-        const int n = s_seg[slot].c1 - s_seg[slot].c0, rows = s_seg[slot].rows;
+        const int n = uni(s_seg[slot].c1 - s_seg[slot].c0), rows = uni(s_seg[slot].rows);
         release_segment(slot);
         const int qb = seg_no % C::kQBufs;
         if (!wait(C::Q_FULL + qb, (seg_no / C::kQBufs) & 1)) break;
@@ -311,7 +313,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
       for (;;) {
         const int slot = next_segment();
         if (slot < 0) break;
-        const int n = s_seg[slot].c1 - s_seg[slot].c0, rows = s_seg[slot].rows;
+        const int n = uni(s_seg[slot].c1 - s_seg[slot].c0), rows = uni(s_seg[slot].rows);
         release_segment(slot);
         for (int j = 0; j < n && ok; ++j) {
           if (!wait(C::FULL + ring, ring_ph)) break;
