@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<Q8>::kCtas) chunk_decode_k
   volatile int* s_count = s_abort + 1;
   ChunkSegment* s_seg = reinterpret_cast<ChunkSegment*>(base_ptr + C::kSegOff);
   ChunkWalk<true>* s_walk = reinterpret_cast<ChunkWalk<true>*>(base_ptr + C::kWalkOff);   // warp 0's between batches
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;   // (known to be one for all lanes)
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
     for (int b = 0; b < C::NBARS; ++b) mbar_init(bar(b), kWarps);
