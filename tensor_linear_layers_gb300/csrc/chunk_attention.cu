@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
     if (lane == 0) mbar_arrive(bar(C::U_EMPTY + slot));
   };
   auto partly_seen = [&](int key, int p0, int p1) { return chunk_partly(p.call, key, p0, p1); };
-  auto mixed_chunk = [&](int kc, int p0, int p1) { return chunk_mixed(p.call, kc, p0, p1); };
+  auto mixed_chunk = [&](int j, int skip, int p0, int p1) { return chunk_mixed(p.call, j, sc, skip, p0, p1); };
   auto any_sees = [&](int key, int p0, int p1) { return chunk_any(p.call, key, p0, p1); };
   auto cache_row = [&](int r, int blk, int key) { return chunk_row(p, r, blk, key); };
 
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
         if (slot < 0) break;
         const int r = s_seg[slot].r, g = s_seg[slot].g, c1 = s_seg[slot].c1, p0 = s_seg[slot].p0, p1 = s_seg[slot].p1, skip = s_seg[slot].skip;
         const int* bt = p.block_tables + (size_t)s_seg[slot].b * p.max_blocks;
-        int c = s_seg[slot].c0, key = key_chunk(c, sc, skip) * kChunkKeys + 4 * lane, blk[4];
+        int c = s_seg[slot].c0, key = chunk_key(c * kChunkKeys + 4 * lane, sc, skip), blk[4];
         auto blocks = [&]() {
           if (quads) {
             blk[0] = key <= p1 && (window == 0 || key + 3 > p0 - window || key < sinks) ? bt[chunk_page(p, key)] : 0;
@@ -450,10 +450,10 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
         };
         blocks();
         for (; c < c1; ++c, ++n) {
-          const int place = n % C::kLooks, kc = key_chunk(c, sc, skip), k0 = kc * kChunkKeys;
+          const int place = n % C::kLooks, x0 = c * kChunkKeys;
           if (!wait(C::L_EMPTY + place, ((n / C::kLooks) & 1) ^ 1)) break;
           int row[4];
-          if (quads && k0 + kChunkKeys - 1 <= p1 && (window == 0 || k0 > p0 - window || k0 + kChunkKeys <= sinks)) {
+          if (quads && x0 + kChunkKeys - 1 + skip <= p1 && (window == 0 || (x0 >= sc && x0 + skip > p0 - window) || x0 + kChunkKeys <= sinks)) {
             row[0] = cache_row(r, blk[0], key);       // all of the chunk's keys are seen
             if (row[0] < 0) atomicExch(p.status, kStatusShape);
 #pragma unroll
@@ -471,10 +471,10 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
           sts128(base + C::kLookOff + place * kLookBytes + 16 * lane, row[0], row[1], row[2], row[3]);
           if (lane == 0) *reinterpret_cast<int*>(base_ptr + C::kLookOff + place * kLookBytes + 640 * 4) = g;
           unsigned mixed = 0;
-          if (mixed_chunk(kc, p0, p1))
+          if (mixed_chunk(c, skip, p0, p1))
 #pragma unroll
             for (int i = 0; i < 4; ++i) mixed |= partly_seen(key + i, p0, p1) ? 1u << i : 0u;
-          key = key_chunk(c + 1, sc, skip) * kChunkKeys + 4 * lane;
+          key = chunk_key(x0 + kChunkKeys + 4 * lane, sc, skip);
           if (c + 1 < c1) blocks();
           hand_on();
 #pragma unroll
@@ -509,16 +509,15 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
         const int c0 = s_seg[slot].c0, c1 = s_seg[slot].c1, p0 = s_seg[slot].p0, p1 = s_seg[slot].p1, skip = s_seg[slot].skip;
         bool bad = false;
         for (int c = c0; c < c1; ++c) {
-          const int kc = key_chunk(c, sc, skip);
-          if (mixed_chunk(kc, p0, p1)) {
+          if (mixed_chunk(c, skip, p0, p1)) {
             if (!wait(C::LANDED + ring, phases >> ring & 1u)) break;
             phases ^= 1u << ring;
             // a row is 8 pieces of 16 bytes in each of two boxes, in any order; a lane has piece `piece` of box `box`
             // of rows lane / 16, + 2, ..: of those that are partly seen the largest size first, as whole numbers
             // (without the sign, bf16 bits are ordered so, infinity and NaN last)
-            const int k0 = kc * kChunkKeys, box = (lane >> 3) & 1, piece = lane & 7;
+            const int x0 = c * kChunkKeys, k0 = x0 + skip, box = (lane >> 3) & 1, piece = lane & 7;
             uint8_t* v = base_ptr + C::kRingOff + ring * kTileBytes + box * (kTileBytes / 2) + piece * 16;
-            // rows [a0, a1) are before the window of the item's last token, rows [b0, 128) after its first token
+            // rows [0, a1) are before the window of the item's last token (or sinks), rows [b0, 128) after its first token
             const int a1 = window > 0 ? min(max(p1 - window + 1 - k0, 0), kChunkKeys) : 0, b0 = max(p0 + 1 - k0, 0);
             unsigned top = 0u;
 #pragma unroll 8
@@ -534,7 +533,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
             }
             if (__any_sync(0xffffffffu, (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u)) {
               for (int row = lane >> 4; row < kChunkKeys; row += 2) {
-                if (!partly_seen(k0 + row, p0, p1)) continue;
+                if (!partly_seen(chunk_key(x0 + row, sc, skip), p0, p1)) continue;
                 uint4* q = reinterpret_cast<uint4*>(v + row * 128);
                 uint4 d = *q;
                 const bool x = drop_nonfinite(d.x), y = drop_nonfinite(d.y), z = drop_nonfinite(d.z), w = drop_nonfinite(d.w);
@@ -586,12 +585,12 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
         const ChunkSegment s = s_seg[slot];
         const int* bt = p.block_tables + (size_t)s.b * p.max_blocks;
         auto block_of = [&](int c) -> int {            // block id of this lane's key of chunk c
-          const int key = key_chunk(c, sc, s.skip) * kChunkKeys + my_row;
+          const int key = chunk_key(c * kChunkKeys + my_row, sc, s.skip);
           return any_sees(key, s.p0, s.p1) ? bt[chunk_page(p, key)] : 0;
         };
         int blk = block_of(s.c0);
         for (int c = s.c0; c < s.c1 && ok; ++c) {
-          const int kc = key_chunk(c, sc, s.skip), key = kc * kChunkKeys + my_row;
+          const int key = chunk_key(c * kChunkKeys + my_row, sc, s.skip);
           int row = -1;                                // cache row of this lane's key (-1: zeros)
           if (any_sees(key, s.p0, s.p1)) {
             row = cache_row(s.r, blk, key);
@@ -608,7 +607,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
               const int rw = __shfl_sync(0xffffffffu, row, 2 * k + half);
               cp_async16(dst + k * 1024, src + (size_t)max(rw, 0) * p.kv_per * kHd, rw >= 0 ? 16 : 0, pol);
             }
-            cp_async_arrive(bar((kv == 1 && mixed_chunk(kc, s.p0, s.p1) ? C::LANDED : C::FULL) + ring));
+            cp_async_arrive(bar((kv == 1 && mixed_chunk(c, s.skip, s.p0, s.p1) ? C::LANDED : C::FULL) + ring));
             advance();
             if (!ok) break;
           }
@@ -730,12 +729,12 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < C::kSub; k += 32) tmem_ld32(sa + k, s + k);
           tc_wait_ld();
-          const int key = key_chunk(j / C::kSubs, sc, skip) * kChunkKeys + (j % C::kSubs) * C::kSub;
-          // keys that not all of the item's tokens see: the row's mask
-          if (__builtin_expect(key + C::kSub - 1 > p0 || (window > 0 && key <= p1 - window && key + C::kSub > sinks), 0)) {
+          const int x = j * C::kSub;                  // the item's keys x, x + 1 ..
+          // those that not all of its tokens see: the row's mask
+          if (__builtin_expect(chunk_masked(p.call, x, C::kSub, sc, skip, p0, p1), 0)) {
 #pragma unroll
             for (int w = 0; w < C::kSub / 32; ++w) {
-              const unsigned bits = chunk_sees(key + 32 * w, pos, window, sinks);
+              const unsigned bits = chunk_item_sees(x + 32 * w, sc, skip, pos, window, sinks);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!(bits >> i & 1u)) s[32 * w + i] = -INFINITY;
@@ -820,10 +819,10 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
             // V values that were dropped, added to the rows that see their keys
             const int* bt = p.block_tables + (size_t)b * p.max_blocks;
             for (int j = c0; j < c1; ++j) {
-              const int kc = key_chunk(j, sc, skip);
-              if (!mixed_chunk(kc, p0, p1)) continue;
-              for (int key = kc * kChunkKeys; key < (kc + 1) * kChunkKeys; ++key) {
-                if (!partly_seen(key, p0, p1) || !(chunk_sees(key & ~31, pos, window, sinks) >> (key & 31) & 1u)) continue;
+              if (!mixed_chunk(j, skip, p0, p1)) continue;
+              for (int x = j * kChunkKeys; x < (j + 1) * kChunkKeys; ++x) {
+                const int key = chunk_key(x, sc, skip);
+                if (!partly_seen(key, p0, p1) || !any_sees(key, pos, pos)) continue;
                 const int rw = cache_row(r, bt[chunk_page(p, key)], key);
                 if (rw < 0) continue;
                 const size_t at = (size_t)rw * p.kv_per + g;

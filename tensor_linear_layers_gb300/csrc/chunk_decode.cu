@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<Q8>::kCtas) chunk_decode_k
       blk_next = -1;
       if (f_s < segs) {
         const ChunkSegment& s = s_seg[f_s];
-        const int key = key_chunk(f_c, sc, s.skip) * kChunkKeys + 16 * warp + lane;
+        const int key = chunk_key(f_c * kChunkKeys + 16 * warp, sc, s.skip) + lane;
         if (lane < 16 && chunk_any(p.call, key, s.p0, s.p1)) {
           blk_next = p.block_tables[(size_t)s.b * p.max_blocks + chunk_page(p, key)];
           if (blk_next < 0) blk_next = p.num_blocks;         // (-1: not seen)
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<Q8>::kCtas) chunk_decode_k
         const ChunkSegment& s = s_seg[a_s];
         int row = -1;                                        // cache row of the lane's key; -1: zeros
         if (blk != -1) {
-          row = chunk_row(p, s.r, blk, key_chunk(a_c, sc, s.skip) * kChunkKeys + 16 * warp + lane);
+          row = chunk_row(p, s.r, blk, chunk_key(a_c * kChunkKeys + 16 * warp, sc, s.skip) + lane);
           if (row < 0) atomicExch(p.status, kChunkStatusShape);
         }
         const int hg = s.g;
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<Q8>::kCtas) chunk_decode_k
         issue(f[C::kStages - 1]);
         cp_async_wait<C::kStages - 1>();
         __syncwarp();
-        const int key = key_chunk(c, sc, skip) * kChunkKeys + 16 * warp;         // the warp's first key
+        const int key = chunk_key(c * kChunkKeys + 16 * warp, sc, skip);         // the warp's first key
         const uint32_t ks = ring + used % C::kStages * (2 * C::kTile), vs = ks + C::kTile;
         // else nothing of the warp's keys is seen: past the last token, or in the gap before the window
         if (key <= p1 && (window == 0 || key + 15 > p0 - window || key < sinks)) {
@@ -537,9 +537,9 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<Q8>::kCtas) chunk_decode_k
             // V values that were dropped, added to the rows that see their keys
             const int* bt = p.block_tables + (size_t)b * p.max_blocks;
             for (int c = c0; c < c1; ++c) {
-              const int kc = key_chunk(c, sc, skip);
-              if (!chunk_mixed(p.call, kc, p0, p1)) continue;
-              for (int key = kc * kChunkKeys; key < (kc + 1) * kChunkKeys; ++key) {
+              if (!chunk_mixed(p.call, c, sc, skip, p0, p1)) continue;
+              for (int x = c * kChunkKeys; x < (c + 1) * kChunkKeys; ++x) {
+                const int key = chunk_key(x, sc, skip);
                 if (!chunk_partly(p.call, key, p0, p1) || !chunk_any(p.call, key, p0 + tok, p0 + tok)) continue;
                 const int rw = chunk_row(p, r, bt[chunk_page(p, key)], key);
                 if (rw < 0) continue;

@@ -2,11 +2,13 @@
 //
 // Request b has t * kv_per * groups items: a kv head of a shard and a group of up to `tg` whole
 // tokens, whose tg * gq query rows (gq: q heads of the kv head) fill one or two tiles of 128. The
-// tokens of group G are those from tg * G on, the first at position p0 and the last at p1; of the
-// keys, chunks of 128, the item takes
-//   the chunks of the first `sinks` tokens    [0, sc),  sc = ceil(sinks / 128)   (with a window)
-//   and those of its window up to its end     [lo, hi), lo = (p0 - window + 1) / 128, hi = p1 / 128 + 1
-// in order: chunk j of the item is key chunk j, or j + skip from j = sc on, skip = max(0, lo - sc).
+// tokens of group G are those from tg * G on, the first at position p0 and the last at p1. The keys that
+// the item goes through, in order, are
+//   the first `sinks` tokens                  [0, sc),   sc = sinks up to a multiple of 16   (with a window)
+//   and those of its window up to its end     [lo, p1],  lo = p0 - window + 1 down to a multiple of 16
+// (or all of [0, p1] where these meet): key x of the item is key x, or x + skip from x = sc on, skip =
+// max(0, lo - sc). They go by in chunks of 128, so that a window of 1024 and a few sinks take nine chunks,
+// not the ten or eleven that they touch; 16 keys in a row stay one after another in their pages.
 //
 // Items lie on a line, requests in order, head by head and group by group. A chunk takes
 // 2 + tiles places, an item `cost` more before its first chunk for what it costs besides them.
@@ -44,6 +46,7 @@ TPL_HD long long chunk_div(long long a, long long b) {
 // steps on (a, m), each of which exchanges the axes of the lattice points under the line
 TPL_HD long long chunk_floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
   long long s = 0;
+  if (n == 0) return 0;
   for (;;) {
     const unsigned qa = m == (unsigned)kChunkKeys ? a / kChunkKeys : a / m, qb = m == (unsigned)kChunkKeys ? b / kChunkKeys : b / m;
     s += (long long)qa * ((long long)n * (n - 1LL) / 2) + (long long)qb * n;
@@ -85,19 +88,21 @@ TPL_HD ChunkReq chunk_request(const ChunkCall& c, int q0, int q1, int len) {
   return r;
 }
 
-// The key chunks of one item.
+// The keys of one item.
+constexpr int kChunkUnit = 16;      // keys that stay together
 struct ChunkKeys {
-  int count, sc, skip;              // chunks of the item; chunk j >= sc is key chunk j + skip
+  int count, sc, skip;              // chunks of the item; its key x >= sc is key x + skip
 };
 TPL_HD int chunk_sinks(const ChunkCall& c) {
-  return c.window > 0 ? (int)(((unsigned)c.sinks + kChunkKeys - 1u) / kChunkKeys) : 0;
+  return c.window > 0 ? (c.sinks + kChunkUnit - 1) / kChunkUnit * kChunkUnit : 0;
 }
+TPL_HD int chunk_key(int x, int sc, int skip) { return x + (x >= sc ? skip : 0); }
 TPL_HD ChunkKeys chunk_keys(const ChunkCall& c, int p0, int p1) {
   ChunkKeys k;
   k.sc = chunk_sinks(c);
-  const int lo = c.window > 0 && p0 >= c.window ? (p0 - c.window + 1) / kChunkKeys : 0;
+  const int lo = c.window > 0 && p0 >= c.window ? (p0 - c.window + 1) / kChunkUnit * kChunkUnit : 0;
   k.skip = lo > k.sc ? lo - k.sc : 0;
-  k.count = p1 / kChunkKeys + 1 - k.skip;
+  k.count = (p1 - k.skip) / kChunkKeys + 1;
   return k;
 }
 TPL_HD ChunkKeys chunk_item_keys(const ChunkCall& c, const ChunkReq& r, int group) {
@@ -112,16 +117,22 @@ TPL_HD long long chunk_item(const ChunkCall& c, const ChunkReq& r, int group, in
 // Places of a head's first m items, all of them full groups (m < groups).
 TPL_HD long long chunk_prefix(const ChunkCall& c, const ChunkReq& r, int m, int cost) {
   if (m <= 0) return 0;
-  // hi - skip over the groups, in closed form: both are quotients of lines by 128
-  long long n = m + chunk_floor_sum(m, kChunkKeys, c.tg, r.ctx + c.tg - 1);
+  // the first g0 groups skip nothing: their chunks are quotients of a line by 128
+  long long g0 = m;
+  const int sc = chunk_sinks(c);
   if (c.window > 0) {
-    // skip > 0 from the first group on whose window starts at key 128 (sc + 1) or later
-    const int sc = chunk_sinks(c);
-    const long long at = (sc + 1LL) * kChunkKeys + c.window - 1 - r.ctx;
-    const long long g0 = at > 0 ? (at + c.tg - 1) / c.tg : 0;
-    if (g0 < m) {
-      const int rest = (int)(m - g0), b = (int)(r.ctx + g0 * c.tg - c.window + 1);
-      n -= chunk_floor_sum(rest, kChunkKeys, c.tg, b) - (long long)rest * sc;
+    const long long at = (long long)sc + kChunkUnit + c.window - 1 - r.ctx;   // from a = p0 - window + 1 = sc + 16 on
+    g0 = at > 0 ? (at + c.tg - 1) / c.tg : 0;
+    if (g0 > m) g0 = m;
+  }
+  long long n = m + chunk_floor_sum((unsigned)g0, kChunkKeys, c.tg, r.ctx + c.tg - 1);
+  if (g0 < m) {
+    // the others go through sc + window + tg - 1 keys and a mod 16 more
+    const int rest = (int)(m - g0), keys = c.window + c.tg - 2 + sc, edge = kChunkKeys - keys % kChunkKeys;
+    n += (long long)rest * (keys / kChunkKeys);
+    if (edge < kChunkUnit) {                         // one chunk more where a mod 16 >= edge
+      const int a = (int)(r.ctx + g0 * c.tg - c.window + 1);
+      n += chunk_floor_sum(rest, kChunkUnit, c.tg, a + kChunkUnit - edge) - chunk_floor_sum(rest, kChunkUnit, c.tg, a);
     }
   }
   return (long long)m * cost + n * c.full;
@@ -176,6 +187,20 @@ TPL_HD unsigned chunk_sees(int key, int pos, int window, int sinks) {
   unsigned bits = chunk_low(pos - key + 1);
   if (window > 0) bits &= ~chunk_low(pos - window + 1 - key) | chunk_low(sinks - key);
   return bits;
+}
+
+// The same for keys x to x + 31 of an item (x a multiple of 16).
+TPL_HD unsigned chunk_item_sees(int x, int sc, int skip, int pos, int window, int sinks) {
+  unsigned bits = chunk_sees(x + skip, pos, window, sinks);
+  if (skip > 0 && x < sc) {          // the sinks, long past, and what fills their last unit
+    const unsigned first = chunk_low(sc - x);
+    bits = (bits & ~first) | (chunk_low(sinks - x) & first);
+  }
+  return bits;
+}
+// Whether keys x to x + n - 1 of an item may be seen by some of its tokens and not by others, or by none.
+TPL_HD bool chunk_masked(const ChunkCall& c, int x, int n, int sc, int skip, int p0, int p1) {
+  return x + n - 1 + skip > p0 || (c.window > 0 && x + n > c.sinks && ((skip > 0 && x < sc) || x + skip <= p1 - c.window));
 }
 
 }  // namespace tpl

@@ -12,7 +12,7 @@ namespace tpl {
 struct __align__(16) ChunkSegment {
   int b, r, g, tok0;                 // request, shard, kv head of the shard, first new token of the group
   int c0, c1, q0, ctx;               // chunks; row of the request's first new token; cached tokens
-  int part, rows, bad, skip;         // partial slot or -1; query rows; V not finite; key chunks left out from sc on
+  int part, rows, bad, skip;         // partial slot or -1; query rows; V not finite; keys left out from key sc of the item on
   int p0, p1, pad0, pad1;            // positions of the group's first and last token
 };
 static_assert(sizeof(ChunkSegment) == 64, "unit slots");
@@ -20,16 +20,13 @@ static_assert(sizeof(ChunkSegment) == 64, "unit slots");
 
 constexpr int kChunkStatusShape = -2;   // TP_ERR_SHAPE
 
-// Key chunk of chunk j of an item.
-__device__ __forceinline__ int key_chunk(int j, int sc, int skip) { return j + (j >= sc ? skip : 0); }
 // A key that some tokens (at positions p0 to p1) see and others do not, of those that any sees.
 __device__ __forceinline__ bool chunk_partly(const ChunkCall& c, int key, int p0, int p1) {
   return key > p0 || (c.window > 0 && key <= p1 - c.window && key >= c.sinks);
 }
-// Whether key chunk kc has such keys.
-__device__ __forceinline__ bool chunk_mixed(const ChunkCall& c, int kc, int p0, int p1) {
-  const int k0 = kc * kChunkKeys, k1 = k0 + kChunkKeys - 1;
-  return p1 > p0 && (k1 > p0 || (c.window > 0 && k0 <= p1 - c.window && k1 > p0 - c.window && k1 >= c.sinks));
+// Whether chunk j of an item has such keys.
+__device__ __forceinline__ bool chunk_mixed(const ChunkCall& c, int j, int sc, int skip, int p0, int p1) {
+  return p1 > p0 && chunk_masked(c, j * kChunkKeys, kChunkKeys, sc, skip, p0, p1);
 }
 // Whether any of the tokens sees the key.
 __device__ __forceinline__ bool chunk_any(const ChunkCall& c, int key, int p0, int p1) {
@@ -116,7 +113,10 @@ struct ChunkWalk {
         const int3 mine = m;
         if (b0 + 32 < p.n_reqs) m = counts(p, b0 + 32 + lane);       // (the next ones, early)
         const ChunkReq q = request(p, mine);
-        one = ONE ? (q.groups > 0 ? chunk_item(p.call, q, 0, cost) : 0) : chunk_head(p.call, q, cost);
+        if (pass == 0 || p.n_reqs > 32)
+          one = ONE ? (q.groups > 0 ? chunk_item(p.call, q, 0, cost) : 0) : chunk_head(p.call, q, cost);
+        else
+          one += q.groups * (long long)cost;                         // (the first pass's, with a cost of 0)
         const long long pre = scan(heads * one, lane);               // the places up to and with this lane's
         if (pass == 0) {
           if (mine.y < 0 && blockIdx.x == 0) atomicExch(p.status, kChunkStatusShape);

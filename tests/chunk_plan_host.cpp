@@ -16,14 +16,30 @@ long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) { return chu
 
 unsigned sees(int key, int pos, int window, int sinks) { return chunk_sees(key, pos, window, sinks); }
 
-// Key chunks of an item in order; returns their number.
-int item_chunks(int p0, int p1, int window, int sinks, int* out) {
+// Keys that an item goes through, in order; returns their number (whole chunks).
+int item_keys(int p0, int p1, int window, int sinks, int* out) {
   ChunkCall c{};
   c.window = window;
   c.sinks = sinks;
   const ChunkKeys k = chunk_keys(c, p0, p1);
-  for (int j = 0; j < k.count; ++j) out[j] = j + (j >= k.sc ? k.skip : 0);
-  return k.count;
+  for (int x = 0; x < k.count * kChunkKeys; ++x) out[x] = chunk_key(x, k.sc, k.skip);
+  return k.count * kChunkKeys;
+}
+
+// Bits of the item's keys x to x + 31 to a token, and whether x to x + n - 1 are taken through the masks.
+unsigned item_sees(int p0, int p1, int window, int sinks, int x, int pos) {
+  ChunkCall c{};
+  c.window = window;
+  c.sinks = sinks;
+  const ChunkKeys k = chunk_keys(c, p0, p1);
+  return chunk_item_sees(x, k.sc, k.skip, pos, window, sinks);
+}
+int item_masked(int p0, int p1, int window, int sinks, int x, int n) {
+  ChunkCall c{};
+  c.window = window;
+  c.sinks = sinks;
+  const ChunkKeys k = chunk_keys(c, p0, p1);
+  return chunk_masked(c, x, n, k.sc, k.skip, p0, p1);
 }
 
 // Head prefixes of a request in closed form against the sum of its items; 0 where all agree.

@@ -18,7 +18,7 @@ def lib(tmp_path_factory):
                    check=True, capture_output=True)
     L = ctypes.CDLL(so)
     L.floor_sum.restype = ctypes.c_longlong
-    L.sees.restype = ctypes.c_uint
+    L.sees.restype = L.item_sees.restype = ctypes.c_uint
     return L
 
 
@@ -45,20 +45,29 @@ def test_visibility_bits(lib, window, sinks):
 
 @pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (1, 1), (100, 5), (128, 128), (129, 129), (300, 0), (17, 260), (1000, 1)])
 @pytest.mark.parametrize("tokens", [1, 2, 36, 64, 256])
-def test_item_takes_the_chunks_that_its_tokens_see(lib, window, sinks, tokens):
-    out = (ctypes.c_int * 64)()
+def test_item_goes_through_the_keys_that_its_tokens_see(lib, window, sinks, tokens):
+    out = (ctypes.c_int * 8192)()
     for p0 in (0, 1, 100, 127, 128, 255, 300, 511, 640, 1000):
         p1 = p0 + tokens - 1
-        n = lib.item_chunks(p0, p1, window, sinks, out)
-        got = list(out[:n])
-        need = {j // 128 for p in (p0, p1) for j in visible(p, window, sinks)}
-        for p in range(p0, p1 + 1):
-            need |= {j // 128 for j in (p, max(p - window + 1, 0) if window else 0)}
-        need |= set(range(min(-(-sinks // 128), p1 // 128 + 1))) if window else set()
-        assert got == sorted(set(got)) and need <= set(got) and max(got) == p1 // 128
-        # no chunk but those, and those between
-        lo = max(p0 - window + 1, 0) // 128 if window else 0
-        assert set(got) <= need | set(range(lo, p1 // 128 + 1))
+        got = list(out[:lib.item_keys(p0, p1, window, sinks, out)])
+        see = {p: visible(p, window, sinks) for p in {p0, (p0 + p1) // 2, p1}}
+        need = set().union(*see.values()) | set(range(p0, p1 + 1))
+        # every key once, in order, 16 on end at a time; none of a chunk without need
+        assert got == sorted(set(got)) and need <= set(got)
+        assert all(got[i + 15] == got[i] + 15 and got[i] % 16 == 0 for i in range(0, len(got), 16))
+        lo = max(p0 - window + 1, 0) if window else 0
+        listed = {j for j in range(p1 + 1) if j >= lo // 16 * 16 or j < -(-sinks // 16) * 16}
+        assert len(got) == -(-len(listed) // 128) * 128 or set(got) == set(range(len(got)))
+        for x in range(0, len(got), 16):
+            for p in see:
+                want = sum(1 << i for i in range(min(32, len(got) - x)) if got[x + i] in see[p])
+                bits = lib.item_sees(p0, p1, window, sinks, x, p) & ((1 << min(32, len(got) - x)) - 1)
+                assert bits == want, (p0, p, x)
+        # keys that are not masked are seen by all
+        for n in (64, 128):
+            for x in range(0, len(got), n):
+                if not lib.item_masked(p0, p1, window, sinks, x, n):
+                    assert all(set(got[x:x + n]) <= see[p] for p in see), (p0, x, n)
 
 
 @pytest.mark.parametrize("seed", range(60))
