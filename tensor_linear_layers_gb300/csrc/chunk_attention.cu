@@ -153,6 +153,61 @@ __device__ __forceinline__ uint32_t scale_rest(uint32_t s) {
 }
 }  // namespace
 
+// Parts of an item that several CTAs compute, joined in the order of their keys (the same bits every time):
+//   o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i
+// The CTAs' warps of the same 32 rows count their parts; the one that comes last joins them. Mostly that is
+// the CTA that began the item, at the end of its range: the others are there then, and its own part goes to the
+// sum from tensor memory. (A kernel of its own after this one took 13 us of a prompt's 135.)
+__device__ __forceinline__ int chunk_part_slot(int c, int first) { return c == first ? 2 * c + 1 : 2 * c; }
+// o += the part of CTA c, dimensions k to k + N - 1 of a row
+template <int N>
+__device__ __forceinline__ void chunk_add_part(const ChunkAttnParams& p, int slot, int row, int k, float m, float* o) {
+  const float2 x = __ldcg(chunk_part_ml(p, slot, row));
+  float v[N / 8][8];
+#pragma unroll
+  for (int i = 0; i < N / 8; ++i) ld_global_v8_cg(v[i], chunk_part_o(p, slot, row, k + 8 * i));
+  if (x.y == 0.f) return;                             // the row sees no key of that part
+  const float w = exp2f(x.x - m);
+#pragma unroll
+  for (int i = 0; i < N; ++i) o[i] += w * v[i / 8][i % 8];
+}
+// In the exponent: l is far from 1 where v's scales differ much.
+__device__ __forceinline__ float chunk_part_l(float m, float l, float mt) { return l == 0.f ? 0.f : exp2f(log2f(l) + (m - mt)); }
+// After a part of this warp's rows has been written: counted, and joined if it was the last.
+__device__ __forceinline__ void chunk_join(const ChunkAttnParams& p, int first, int last, unsigned* counter, int row, bool in, __nv_bfloat16* dst) {
+  __syncwarp();
+  unsigned before = 0;
+  if ((threadIdx.x & 31) == 0) before = atom_acq_rel_add(counter, 1);   // after every lane's part (__syncwarp)
+  before = __shfl_sync(0xffffffffu, before, 0);
+  __syncwarp();
+  if (before != (unsigned)(last - first)) return;
+  if ((threadIdx.x & 31) == 0) *counter = 0;          // as the next call needs it
+  if (!in) return;
+  float m = -INFINITY, l = 0.f;
+  for (int c = first; c <= last; ++c) m = fmaxf(m, __ldcg(chunk_part_ml(p, chunk_part_slot(c, first), row)).x);
+  for (int c = first; c <= last; ++c) {
+    const float2 x = __ldcg(chunk_part_ml(p, chunk_part_slot(c, first), row));
+    l += chunk_part_l(x.x, x.y, m);
+  }
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll 1
+  for (int k = 0; k < kHd; k += 32) {
+    float o[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = 0.f;
+#pragma unroll 2
+    for (int c = first; c <= last; ++c) chunk_add_part<32>(p, chunk_part_slot(c, first), row, k, m, o);
+#pragma unroll
+    for (int i = 0; i < 32; i += 16) {
+      uint32_t y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = pack_bf16x2(o[i + 2 * e] * inv, o[i + 2 * e + 1] * inv);
+      *reinterpret_cast<uint4*>(dst + k + i) = make_uint4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint4*>(dst + k + i + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+    }
+  }
+}
+
 template <int MT, bool Q8>
 __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkAttnParams p) {
@@ -166,7 +221,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
   volatile int* s_abort = reinterpret_cast<volatile int*>(base_ptr + C::kMiscOff + 4);
   ChunkSegment* s_seg = reinterpret_cast<ChunkSegment*>(base_ptr + C::kUnitOff);
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;   // (known to be one for all lanes)
-  griddep_launch_dependents();   // the merge grid may be scheduled; it waits for this one to complete
+  griddep_launch_dependents();   // the grid after this one may be scheduled; it waits for this one to complete
   if (warp == 0) {
     for (int b = lane; b < C::NBARS; b += 32) {
       int count = 1;
@@ -801,19 +856,40 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
         ++cnt;
       }
       if (!ok) break;
+      // a part of an item, and whether the other ones are there already
+      const int part = uni(s_seg[slot].part), first = uni(s_seg[slot].first), last = uni(s_seg[slot].last);
+      unsigned* counter = p.counters + first * 8 + tile * 4 + q4;
+      bool join = false;
+      if (part >= 0 && first == (int)blockIdx.x && !idle) {
+        unsigned n = 0;
+        if (lane == 0) n = ld_acquire(counter);
+        join = uni((int)n) == last - first;
+        __syncwarp();
+      }
+      float mt = m, lt = l;
+      if (join) {
+        if (lane == 0) *counter = 0;                  // as the next call needs it
+        const int at = min(row, rows - 1);
+        for (int c = first + 1; c <= last; ++c) mt = fmaxf(mt, __ldcg(chunk_part_ml(p, 2 * c, at)).x);
+        lt = chunk_part_l(m, l, mt);
+        for (int c = first + 1; c <= last; ++c) {
+          const float2 x = __ldcg(chunk_part_ml(p, 2 * c, at));
+          lt += chunk_part_l(x.x, x.y, mt);
+        }
+      }
       if (!wait_last_pv()) break;
       if (!idle) {
         tc_fence_after();
         const int bad = *reinterpret_cast<volatile int*>(&s_seg[slot].bad);
-        const int r = s_seg[slot].r, g = s_seg[slot].g, b = s_seg[slot].b, part = s_seg[slot].part;
-        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        const int r = s_seg[slot].r, g = s_seg[slot].g, b = s_seg[slot].b;
+        const float inv = lt == 0.f ? 0.f : 1.0f / lt;
         __nv_bfloat16* dst = p.out + (size_t)r * p.sstride_out +
                              (size_t)(s_seg[slot].q0 + s_seg[slot].tok0 + tok) * p.rstride_out + (g * gq + row - tok * gq) * kHd;
+        // (32 dimensions at a time, not unrolled: what this code costs most is the fetch of its instructions)
 #pragma unroll 1
-        for (int k = 0; k < 128; k += C::kSub) {
+        for (int k = 0; k < 128; k += 32) {
           __syncwarp();
-#pragma unroll
-          for (int i = 0; i < C::kSub; i += 32) tmem_ld32(lane_addr + C::o_col(tile) + k + i, s + i);
+          tmem_ld32(lane_addr + C::o_col(tile) + k, s);
           tc_wait_ld();
           if (bad && row < rows) {
             // V values that were dropped, added to the rows that see their keys
@@ -829,11 +905,11 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
                 if constexpr (Q8) {
                   if (p.scales_v[at] != kScaleNan) continue;
 #pragma unroll
-                  for (int i = 0; i < C::kSub; ++i) s[i] = __int_as_float(0x7fffffff);
+                  for (int i = 0; i < 32; ++i) s[i] = __int_as_float(0x7fffffff);
                 } else {
                   const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.cache_v) + at * kHd + k;
 #pragma unroll
-                  for (int i = 0; i < C::kSub; ++i) {
+                  for (int i = 0; i < 32; ++i) {
                     const float x = __bfloat162float(v[i]);
                     if (!(fabsf(x) < INFINITY)) s[i] += x;
                   }
@@ -841,14 +917,20 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
               }
             }
           }
-          if (row < rows) {
-            if (part >= 0) {
+          if (join) {
+            const float w = l == 0.f ? 0.f : exp2f(m - mt);
 #pragma unroll
-              for (int i = 0; i < C::kSub; i += 8)
+            for (int i = 0; i < 32; ++i) s[i] = l == 0.f ? 0.f : w * s[i];
+            for (int c = first + 1; c <= last; ++c) chunk_add_part<32>(p, 2 * c, min(row, rows - 1), k, mt, s);
+          }
+          if (row < rows) {
+            if (part >= 0 && !join) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8)
                 st_global_v8(chunk_part_o(p, part, row, k + i), *reinterpret_cast<const uint32_t(*)[8]>(s + i));
             } else {
 #pragma unroll
-              for (int i = 0; i < C::kSub; i += 16) {
+              for (int i = 0; i < 32; i += 16) {
                 uint32_t v[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = pack_bf16x2(s[i + 2 * e] * inv, s[i + 2 * e + 1] * inv);
@@ -862,11 +944,15 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
             }
           }
         }
-        if (row < rows && part >= 0) *chunk_part_ml(p, part, row) = make_float2(m, l);
+        if (row < rows && part >= 0 && !join) *chunk_part_ml(p, part, row) = make_float2(m, l);
         tc_fence_before();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::O_FREE + tile));
+      if (part >= 0 && !join && !idle)
+        chunk_join(p, first, last, counter, row, row < rows,
+                   p.out + (size_t)s_seg[slot].r * p.sstride_out + (size_t)(s_seg[slot].q0 + s_seg[slot].tok0 + tok) * p.rstride_out +
+                       (s_seg[slot].g * gq + row - tok * gq) * kHd);
       release_segment(slot);
     }
   }
@@ -878,78 +964,13 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
   }
 }
 
-// Joins the parts of the items that more than one CTA computed. At most one item begins in a
-// CTA and goes on in the next ones: item blockIdx.x (described by that CTA), four query rows per
-// warp, four head dimensions per lane, the parts in the order of their keys (the same bits
-// every time).
-//   o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i
-// Scheduled behind the attention grid's last CTAs (programmatic launch); it reads only after
-// that grid has completed. Latency bounds it, a chain of three loads: the four rows of a warp are read
-// together, and 256 rows of one item per SM are one wave (one row per warp: 4 waves, 16 us after a
-// prompt of 4096 tokens).
-constexpr int kMergeWarps = 8, kMergeRows = 4 * kMergeWarps;   // of a CTA
+// Joins the parts of items of up to eight rows, which many CTAs may share (one request's 4000 keys: 19 CTAs per kv
+// head), by the formula of chunk_join: a CTA per row, each of its warps an eighth of the parts, joined in order. At
+// most one item begins in a CTA and goes on in the next ones: item blockIdx.x, described by that CTA. Scheduled
+// behind the attention grid's last CTAs (programmatic launch); it reads only after that grid has completed.
+// Latency bounds it, a chain of three loads.
+constexpr int kMergeWarps = 8;
 __global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_kernel(const ChunkAttnParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int cta = blockIdx.x, row0 = blockIdx.y * kMergeRows + (threadIdx.x >> 5) * 4, lane = threadIdx.x & 31;
-  const TreeItem it = p.items[cta];
-  if (row0 >= it.rows) return;
-  auto slot = [&](int c) { return c == cta ? 2 * c + 1 : 2 * c; };
-  // rows past the item's read its last one
-  int row[4];
-  float m[4], l[4];
-  float4 o[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    row[j] = min(row0 + j, it.rows - 1);
-    m[j] = -INFINITY;
-    l[j] = 0.f;
-    o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  for (int c = cta + lane; c <= it.last; c += 32)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m[j] = fmaxf(m[j], chunk_part_ml(p, slot(c), row[j])->x);
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], x));
-#pragma unroll 2
-  for (int c = cta; c <= it.last; ++c) {
-    float2 x[4];
-    float4 v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[j] = *chunk_part_ml(p, slot(c), row[j]);
-      v[j] = *reinterpret_cast<const float4*>(chunk_part_o(p, slot(c), row[j], 4 * lane));
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (x[j].y == 0.f) continue;                   // the row sees no key of that part
-      const float w = exp2f(x[j].x - m[j]);
-      l[j] += exp2f(log2f(x[j].y) + (x[j].x - m[j]));   // in the exponent: l is far from 1 where v's scales differ much
-      o[j].x += w * v[j].x;
-      o[j].y += w * v[j].y;
-      o[j].z += w * v[j].z;
-      o[j].w += w * v[j].w;
-    }
-  }
-  const int gq = p.call.gq;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (row0 + j >= it.rows) break;
-    const float inv = l[j] == 0.f ? 0.f : 1.0f / l[j];
-    const int tok = row[j] / gq;
-    uint2 out;
-    out.x = pack_bf16x2(o[j].x * inv, o[j].y * inv);
-    out.y = pack_bf16x2(o[j].z * inv, o[j].w * inv);
-    *reinterpret_cast<uint2*>(p.out + (size_t)it.r * p.sstride_out + (size_t)(it.q0 + tok) * p.rstride_out +
-                              (it.g * gq + row[j] - tok * gq) * kHd + 4 * lane) = out;
-  }
-}
-
-// The same for items of up to eight rows, which many CTAs may share (one request's 4000 keys: 19 CTAs per kv
-// head): a CTA per row, each of its warps an eighth of the parts, joined in order.
-__global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_few_kernel(const ChunkAttnParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int cta = blockIdx.x, row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1033,12 +1054,10 @@ cudaError_t launch_chunk_attention(const CUtensorMap& map_q, const ChunkAttnPara
   cudaError_t e = rows == 8    ? launch_chunk_decode(p, grid, st)
                   : rows == 128 ? (q8 ? launch_chunk<1, true>(map_q, p, grid, st) : launch_chunk<1, false>(map_q, p, grid, st))
                                 : (q8 ? launch_chunk<2, true>(map_q, p, grid, st) : launch_chunk<2, false>(map_q, p, grid, st));
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || rows > 8) return e;
   cudaLaunchAttribute attr[1];
-  const int max_rows = std::min(p.call.max_query_len, 256) * p.call.gq;
-  const cudaLaunchConfig_t cfg = programmatic(dim3(grid, rows == 8 ? max_rows : (p.part_rows + kMergeRows - 1) / kMergeRows),
-                                              32 * kMergeWarps, 0, st, attr);
-  return cudaLaunchKernelEx(&cfg, rows == 8 ? chunk_merge_few_kernel : chunk_merge_kernel, p);
+  const cudaLaunchConfig_t cfg = programmatic(dim3(grid, p.call.max_query_len * p.call.gq), 32 * kMergeWarps, 0, st, attr);
+  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel, p);
 }
 
 }  // namespace tpl

@@ -17,7 +17,7 @@
 // call's widest chunk: inside an item every CTA then holds some chunk's first place and writes
 // its slot. An item that crosses a boundary is computed in parts: CTA c writes the part that
 // continues an item begun by an earlier CTA to slot 2 c, the part that begins one it does not
-// finish to slot 2 c + 1, and the merge kernel joins them in order.
+// finish to slot 2 c + 1; they are joined in order.
 #pragma once
 
 #include <algorithm>
@@ -167,11 +167,9 @@ TPL_HD ChunkPart chunk_part(int p0, int p1, int cost, int width, int count, int 
   s.slot = s.c0 > 0 ? 2 * cta : s.c1 < count ? 2 * cta + 1 : -1;
   return s;
 }
-// The CTA that holds the last chunk of an item that CTA cta, whose places end at `end`, does not finish;
-// begin: the item's first place.
-TPL_HD int chunk_last(long long begin, int cost, int width, int count, long long per, int cta, long long end) {
-  const unsigned at = (unsigned)(begin + cost + (long long)(count - 1) * width - end);
-  return cta + 1 + (int)(per < (1LL << 24) ? at / (unsigned)per : 0u);
+// The CTA that holds chunk j of an item whose first place is `begin`.
+TPL_HD int chunk_holder(long long begin, int cost, int width, int j, long long per) {
+  return (int)chunk_div(begin + cost + (long long)j * width, per);
 }
 
 // CTAs of the grid: one per SM, no more than a call of these bounds has chunks.

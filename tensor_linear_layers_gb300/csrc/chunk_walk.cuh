@@ -13,7 +13,7 @@ struct __align__(16) ChunkSegment {
   int b, r, g, tok0;                 // request, shard, kv head of the shard, first new token of the group
   int c0, c1, q0, ctx;               // chunks; row of the request's first new token; cached tokens
   int part, rows, bad, skip;         // partial slot or -1; query rows; V not finite; keys left out from key sc of the item on
-  int p0, p1, pad0, pad1;            // positions of the group's first and last token
+  int p0, p1, first, last;           // positions of the group's first and last token; of a part: the item's first and last CTA
 };
 static_assert(sizeof(ChunkSegment) == 64, "unit slots");
 
@@ -97,7 +97,7 @@ struct ChunkWalk {
     b = head = group = cost = 0;
     begin = pos = end = 0;
     // no item of this CTA is continued by others, unless a segment says so below
-    if (lane == 0) p.items[blockIdx.x].rows = 0;
+    if (ONE && lane == 0) p.items[blockIdx.x].rows = 0;
     __syncwarp();
     // Twice over the requests, 32 at a time: a head's places of all of them with an item cost of 0, and its
     // items; then the request that holds the CTA's first place, and the places before it.
@@ -217,10 +217,11 @@ struct ChunkWalk {
         s.skip = keys.skip;
         s.p0 = r.ctx + s.tok0;
         s.p1 = s.p0 + tokens - 1;
-        s.pad0 = s.pad1 = 0;
-        if (q.c0 == 0 && q.slot >= 0 && lane == 0) {
-          const int last = chunk_last(begin, cost, width, keys.count, per, blockIdx.x, end);
-          p.items[blockIdx.x] = TreeItem{s.r, s.g, 0, s.rows, s.q0 + s.tok0, last, 0, 0};
+        s.first = s.last = blockIdx.x;
+        if (q.slot >= 0) {
+          s.first = chunk_holder(begin, cost, width, 0, per);
+          s.last = chunk_holder(begin, cost, width, keys.count - 1, per);
+          if (ONE && q.c0 == 0 && lane == 0) p.items[blockIdx.x] = TreeItem{s.r, s.g, 0, s.rows, s.q0 + s.tok0, s.last, 0, 0};
         }
       }
       pos = begin + p1;

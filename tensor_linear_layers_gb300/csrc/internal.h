@@ -232,7 +232,8 @@ struct ChunkAttnParams {
   int n_reqs, t, kv_per, max_blocks, num_blocks, block_size;
   unsigned block_magic;              // 2^32 / block_size rounded up (not used for 1)
   float scale_log2;                  // log2(e) / sqrt(hd)
-  TreeItem* items;                   // [grid] the item each CTA begins and others go on with, for the merge
+  unsigned* counters;                // [SMs][8] parts that are there, of the item that a CTA begins; 0 between calls (more than 8 rows)
+  TreeItem* items;                   // [grid] the item each CTA begins and others go on with, for the merge (up to 8 rows)
   float* partials;                   // [2 * grid] slots of part_rows x (128 + 2)
   int part_rows;
   int q_box_rows;                    // rows of a box of the map of the queries

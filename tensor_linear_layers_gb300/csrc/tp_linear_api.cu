@@ -1958,12 +1958,12 @@ int tp_kv_quant_read(tp_linear_t* h, int64_t n, const int32_t* slots, const void
 }
 
 // Chunk attention: at most one CTA per SM (two for few rows on an 8-bit cache), no more than there are chunks of keys. Workspace: the
-// status word, the item each CTA leaves unfinished, two partial slots per CTA.
+// status word, counters of parts, the item each CTA leaves unfinished, two partial slots per CTA.
 namespace {
 struct ChunkPlan {
   ChunkCall call;
   int rows, grid, part_rows;         // rows of a group: 8, 128 or 256
-  int64_t partials_off, ws_bytes;
+  int64_t items_off, partials_off, ws_bytes;
 };
 ChunkPlan chunk_plan(const tp_linear* h, int64_t T, int n_reqs, int max_query_len, int max_seq_len, bool q8) {
   const int gq = h->q_per / h->kv_per;
@@ -1980,7 +1980,8 @@ ChunkPlan chunk_plan(const tp_linear* h, int64_t T, int n_reqs, int max_query_le
   const int ctas = rows == 8 ? chunk_decode_ctas(q8) : 1;
   pl.grid = chunk_grid(h->nsm * ctas, n_reqs, h->cfg.t * h->kv_per, max_query_len, pl.call.tg, max_seq_len);
   pl.part_rows = ((int)std::min<int64_t>(rows, max_rows) + 7) / 8 * 8;   // a slot is a multiple of 32 bytes (32-byte stores)
-  pl.partials_off = align256(256 + (int64_t)sizeof(TreeItem) * pl.grid);
+  pl.items_off = align256(256 + 4LL * 8 * h->nsm);             // after the counters, which are where they are for all bounds
+  pl.partials_off = align256(pl.items_off + (int64_t)sizeof(TreeItem) * pl.grid);
   // the workspace itself is 16-byte aligned: room to start the slots on a 32-byte boundary
   pl.ws_bytes = align256(pl.partials_off + 32 + 2LL * pl.grid * pl.part_rows * (128 + 2) * 4);
   return pl;
@@ -1999,7 +2000,14 @@ int tp_chunk_attention_workspace_size(const tp_linear_t* h, int32_t n_reqs, int3
   if (bytes == nullptr) return fail(TP_ERR_ARG, "null argument");
   int rc = check_paged_handle(h);
   if (rc || (rc = check_chunk(h, n_reqs, max_query_len, max_seq_len))) return rc;
-  *bytes = chunk_plan(h, 0, n_reqs, max_query_len, max_seq_len, true).ws_bytes;   // of the larger grid
+  // of the larger grid (8 bits); and what smaller bounds take, whose items of fewer rows can be more CTAs'
+  *bytes = 0;
+  const int gq = h->q_per / h->kv_per;
+  for (const int rows : {8, 128, 256}) {
+    const int q = std::min(max_query_len, rows / gq > 0 ? rows / gq : 1);
+    *bytes = std::max(*bytes, chunk_plan(h, 0, n_reqs, q, max_seq_len, true).ws_bytes);
+  }
+  *bytes = std::max(*bytes, chunk_plan(h, 0, n_reqs, max_query_len, max_seq_len, true).ws_bytes);
   return ok();
 }
 
@@ -2068,7 +2076,8 @@ int tp_chunk_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t
   p.block_size = block_size;
   p.block_magic = (unsigned)(((1ull << 32) + block_size - 1) / block_size);
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt(128.0));
-  p.items = reinterpret_cast<TreeItem*>(static_cast<char*>(workspace) + 256);
+  p.counters = reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + 256);
+  p.items = reinterpret_cast<TreeItem*>(static_cast<char*>(workspace) + pl.items_off);
   p.partials = reinterpret_cast<float*>(
       (reinterpret_cast<uintptr_t>(workspace) + (uintptr_t)pl.partials_off + 31) & ~uintptr_t(31));
   p.part_rows = pl.part_rows;

@@ -83,6 +83,7 @@ int split(int nsm, int heads, int gq, int rows, int max_q, int max_len, int wind
     int cta, last;
   };
   std::vector<Join> joins;
+  std::map<Item, std::pair<int, int>> named;
   for (int cta = 0; cta < grid; ++cta) {
     long long pos = per * cta;
     const long long end = std::min(total, pos + per);
@@ -119,7 +120,12 @@ int split(int nsm, int heads, int gq, int rows, int max_q, int max_len, int wind
         }
         if (q.c0 < q.c1 && q.slot >= 0) {
           slots[q.slot] = it;
-          if (q.c0 == 0) joins.push_back({it, cta, chunk_last(begin, cost, width, count, per, cta, end)});
+          // every part names the same CTAs, the first of which begins the item
+          const int first = chunk_holder(begin, cost, width, 0, per), last = chunk_holder(begin, cost, width, count - 1, per);
+          if (q.c0 == 0) joins.push_back({it, cta, last});
+          wrong += (q.c0 == 0) != (cta == first) || (q.c1 == count) != (cta == last) || first == last;
+          const auto known = named.insert({it, {first, last}});
+          wrong += known.first->second != std::make_pair(first, last);
         }
         pos = begin + p1;
         if (p1 == item && pos < end) {

@@ -282,6 +282,27 @@ def test_one_workspace_for_calls_of_other_bounds():
             check(out, c, window, sinks)
 
 
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("nq,nkv,t", [(8, 2, 2), (7, 1, 1), (64, 1, 1), (32, 8, 4)])
+def test_a_workspace_of_larger_bounds_serves_smaller_ones(nq, nkv, t, q8):
+    h = handle(nq, nkv, t)
+    bounds = [(r, q, m) for r in (1, 3, 100) for q in (1, 2, 3, 20, 40, 300) for m in (300, 5000)]
+    size = {b: h.chunk_attention_workspace_size(*b) for b in bounds}
+    for a in bounds:
+        for b in bounds:
+            if all(x <= y for x, y in zip(a, b)):
+                assert size[a] <= size[b], (a, b)
+    # and the calls of them all in one, in turn, with the results of workspaces of their own
+    ws = torch.zeros(size[(100, 300, 5000)], dtype=torch.uint8, device="cuda")
+    calls = [build(nq, nkv, t, ctx, n, 16, seed=i, q8=q8) for i, (ctx, n) in enumerate((
+        ([2000], [1]), ([2000, 70], [2, 1]), ([3000], [300]), ([40] * 100, [1] * 100), ([400] * 20, [3] * 20), ([4000], [20])))]
+    want = [run(h, c, 900, 5)[0] for c in calls]
+    for _ in range(2):
+        for c, x in zip(calls, want):
+            out, _ = run(h, c, 900, 5, ws=ws)
+            assert status(ws) == 0 and torch.equal(out, x)
+
+
 def test_workspace_and_output_on_16_byte_boundaries():
     for nq, nkv, t, n in ((8, 2, 4, 9), (4, 4, 2, 5), (9, 3, 1, 43), (9, 3, 1, 9)):
         c = build(nq, nkv, t, [700, 64], [n, 2], 16, seed=n)
