@@ -155,9 +155,10 @@ __device__ __forceinline__ uint32_t scale_rest(uint32_t s) {
 
 // Parts of an item that several CTAs compute, joined in the order of their keys (the same bits every time):
 //   o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i
-// The CTAs' warps of the same 32 rows count their parts; the one that comes last joins them. Mostly that is
-// the CTA that began the item, at the end of its range: the others are there then, and its own part goes to the
-// sum from tensor memory. (A kernel of its own after this one took 13 us of a prompt's 135.)
+// Where the call has many items the CTAs' warps of the same 32 rows count their parts, and the one that comes
+// last joins them. Mostly that is the CTA that began the item, at the end of its range: the others are there
+// then, and its own part goes into the sum from tensor memory (a kernel after this one took 13 us of a prompt's
+// 135). Where it has few, whose parts are many, a kernel does (below).
 __device__ __forceinline__ int chunk_part_slot(int c, int first) { return c == first ? 2 * c + 1 : 2 * c; }
 // o += the part of CTA c, dimensions k to k + N - 1 of a row
 template <int N>
@@ -173,8 +174,60 @@ __device__ __forceinline__ void chunk_add_part(const ChunkAttnParams& p, int slo
 }
 // In the exponent: l is far from 1 where v's scales differ much.
 __device__ __forceinline__ float chunk_part_l(float m, float l, float mt) { return l == 0.f ? 0.f : exp2f(log2f(l) + (m - mt)); }
-// After a part of this warp's rows has been written: counted, and joined if it was the last.
-__device__ __forceinline__ void chunk_join(const ChunkAttnParams& p, int first, int last, unsigned* counter, int row, bool in, __nv_bfloat16* dst) {
+// Four rows of an item from row0 on (those past its last one repeat that), by one warp, four dimensions per lane;
+// out: shard's and head's first element of the item's first token.
+__device__ __forceinline__ void chunk_join_rows(const ChunkAttnParams& p, int first, int last, int row0, int rows, __nv_bfloat16* out) {
+  const int lane = threadIdx.x & 31, gq = p.call.gq;
+  int row[4];
+  float m[4], l[4];
+  float4 o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    row[j] = min(row0 + j, rows - 1);
+    m[j] = -INFINITY;
+    l[j] = 0.f;
+    o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int c = first + lane; c <= last; c += 32)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = fmaxf(m[j], __ldcg(chunk_part_ml(p, chunk_part_slot(c, first), row[j])).x);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], x));
+#pragma unroll 2
+  for (int c = first; c <= last; ++c) {
+    float2 x[4];
+    float4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[j] = __ldcg(chunk_part_ml(p, chunk_part_slot(c, first), row[j]));
+      v[j] = __ldcg(reinterpret_cast<const float4*>(chunk_part_o(p, chunk_part_slot(c, first), row[j], 4 * lane)));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (x[j].y == 0.f) continue;                    // the row sees no key of that part
+      const float w = exp2f(x[j].x - m[j]);
+      l[j] += chunk_part_l(x[j].x, x[j].y, m[j]);
+      o[j].x += w * v[j].x;
+      o[j].y += w * v[j].y;
+      o[j].z += w * v[j].z;
+      o[j].w += w * v[j].w;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (row0 + j >= rows) break;
+    const float inv = l[j] == 0.f ? 0.f : 1.0f / l[j];
+    const int tok = row[j] / gq;
+    uint2 y;
+    y.x = pack_bf16x2(o[j].x * inv, o[j].y * inv);
+    y.y = pack_bf16x2(o[j].z * inv, o[j].w * inv);
+    *reinterpret_cast<uint2*>(out + (size_t)tok * p.rstride_out + (row[j] - tok * gq) * kHd + 4 * lane) = y;
+  }
+}
+// After a part of this warp's 32 rows has been written: counted, and joined if it was the last.
+__device__ __forceinline__ void chunk_join(const ChunkAttnParams& p, int first, int last, unsigned* counter, int row0, int rows, __nv_bfloat16* out) {
   __syncwarp();
   unsigned before = 0;
   if ((threadIdx.x & 31) == 0) before = atom_acq_rel_add(counter, 1);   // after every lane's part (__syncwarp)
@@ -182,30 +235,8 @@ __device__ __forceinline__ void chunk_join(const ChunkAttnParams& p, int first, 
   __syncwarp();
   if (before != (unsigned)(last - first)) return;
   if ((threadIdx.x & 31) == 0) *counter = 0;          // as the next call needs it
-  if (!in) return;
-  float m = -INFINITY, l = 0.f;
-  for (int c = first; c <= last; ++c) m = fmaxf(m, __ldcg(chunk_part_ml(p, chunk_part_slot(c, first), row)).x);
-  for (int c = first; c <= last; ++c) {
-    const float2 x = __ldcg(chunk_part_ml(p, chunk_part_slot(c, first), row));
-    l += chunk_part_l(x.x, x.y, m);
-  }
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
 #pragma unroll 1
-  for (int k = 0; k < kHd; k += 32) {
-    float o[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = 0.f;
-#pragma unroll 2
-    for (int c = first; c <= last; ++c) chunk_add_part<32>(p, chunk_part_slot(c, first), row, k, m, o);
-#pragma unroll
-    for (int i = 0; i < 32; i += 16) {
-      uint32_t y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = pack_bf16x2(o[i + 2 * e] * inv, o[i + 2 * e + 1] * inv);
-      *reinterpret_cast<uint4*>(dst + k + i) = make_uint4(y[0], y[1], y[2], y[3]);
-      *reinterpret_cast<uint4*>(dst + k + i + 8) = make_uint4(y[4], y[5], y[6], y[7]);
-    }
-  }
+  for (int j = 0; j < 32 && row0 + j < rows; j += 4) chunk_join_rows(p, first, last, row0 + j, rows, out);
 }
 
 template <int MT, bool Q8>
@@ -860,7 +891,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
       const int part = uni(s_seg[slot].part), first = uni(s_seg[slot].first), last = uni(s_seg[slot].last);
       unsigned* counter = p.counters + first * 8 + tile * 4 + q4;
       bool join = false;
-      if (part >= 0 && first == (int)blockIdx.x && !idle) {
+      if (part >= 0 && p.counters != nullptr && first == (int)blockIdx.x && last - first < 8 && !idle) {
         unsigned n = 0;
         if (lane == 0) n = ld_acquire(counter);
         join = uni((int)n) == last - first;
@@ -949,10 +980,10 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::O_FREE + tile));
-      if (part >= 0 && !join && !idle)
-        chunk_join(p, first, last, counter, row, row < rows,
-                   p.out + (size_t)s_seg[slot].r * p.sstride_out + (size_t)(s_seg[slot].q0 + s_seg[slot].tok0 + tok) * p.rstride_out +
-                       (s_seg[slot].g * gq + row - tok * gq) * kHd);
+      if (part >= 0 && p.counters != nullptr && !join && !idle)
+        chunk_join(p, first, last, counter, tile * 128 + q4 * 32, rows,
+                   p.out + (size_t)s_seg[slot].r * p.sstride_out + (size_t)(s_seg[slot].q0 + s_seg[slot].tok0) * p.rstride_out +
+                       s_seg[slot].g * gq * kHd);
       release_segment(slot);
     }
   }
@@ -964,16 +995,31 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
   }
 }
 
-// Joins the parts of items of up to eight rows, which many CTAs may share (one request's 4000 keys: 19 CTAs per kv
-// head), by the formula of chunk_join: a CTA per row, each of its warps an eighth of the parts, joined in order. At
-// most one item begins in a CTA and goes on in the next ones: item blockIdx.x, described by that CTA. Scheduled
-// behind the attention grid's last CTAs (programmatic launch); it reads only after that grid has completed.
-// Latency bounds it, a chain of three loads.
+// The parts of a call with few items, which many CTAs share (one request's 4000 keys: 19 CTAs per kv head): a CTA
+// per row, each of its warps an eighth of the parts, joined in order. At most one item begins in a CTA and goes
+// on in the next ones, as that CTA describes it. blockIdx.x is that CTA (up to eight rows), or counts the CTAs that
+// left one: a grid of all of them times 256 rows would be 39 000 CTAs, nearly all without work. Scheduled behind
+// the attention grid's last CTAs (programmatic launch); it reads only after that grid has completed. Latency
+// bounds it, a chain of three or four loads (four rows per warp, whole items' parts in turn: one request of 64
+// tokens over 30 000 keys 65 us, this 47).
 constexpr int kMergeWarps = 8;
-__global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_kernel(const ChunkAttnParams p) {
+__global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_kernel(const ChunkAttnParams p, int ctas) {
   griddep_wait();
   griddep_launch_dependents();
-  const int cta = blockIdx.x, row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int cta = blockIdx.x;
+  if (p.group_rows > 8) {
+    __shared__ unsigned s_left[kMergeWarps];         // one bit per CTA: at most 256
+    const unsigned left = __ballot_sync(0xffffffffu, (int)threadIdx.x < ctas && p.items[threadIdx.x].rows > 0);
+    if (lane == 0) s_left[warp] = left;
+    __syncthreads();
+    int rank = cta, w = 0;
+    for (; w < kMergeWarps && rank >= __popc(s_left[w]); ++w) rank -= __popc(s_left[w]);
+    if (w == kMergeWarps) return;
+    unsigned bits = s_left[w];
+    for (; rank > 0; --rank) bits &= bits - 1u;
+    cta = 32 * w + __ffs(bits) - 1;
+  }
   const TreeItem it = p.items[cta];
   if (row >= it.rows) return;
   __shared__ float4 s_o[kMergeWarps][32];
@@ -1021,9 +1067,15 @@ __global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_kernel(const Chu
                             (it.g * gq + row - tok * gq) * kHd + 4 * lane) = out;
 }
 
-// Rows of an item: with up to eight of them the warp-level kernel (chunk_decode.cu; one request of 4000 keys 12.7 us,
-// 15.1 here). For 16 rows it would take two products for each one: 59 us for 32 requests of 2000 keys, 53 here.
-int chunk_group_rows(int max_rows) { return max_rows <= 8 ? 8 : max_rows <= 128 ? 128 : 256; }
+// Up to eight rows go to the warp-level kernel (chunk_decode.cu): one request of 4000 keys 12 us, 15 by tiles; 32
+// requests of 2000 keys in 8 bits 39 us, 57 by tiles. Tiles where they stream faster, in bf16, once the call has
+// an item for every SM and contexts are long: 32 requests of 2000 keys 55 us by warps, 52 by tiles, 48 of 4100 keys
+// of a window 69 and 67; but 64 requests of 300 keys 30 and 34. Up to 128 rows are one tile: 8 requests of 30 tokens
+// (120 rows) over 4000 keys 38 us in bf16 and 42 in 8 bits, 40 and 47 as two tiles.
+int chunk_group_rows(int max_rows, bool q8, bool many, int max_keys) {
+  if (max_rows <= 8 && (q8 || !many || max_keys < 1024)) return 8;
+  return max_rows <= 128 ? 128 : 256;
+}
 
 template <int MT, bool Q8>
 static cudaError_t launch_chunk(const CUtensorMap& map_q, const ChunkAttnParams& p, int grid, cudaStream_t st) {
@@ -1049,15 +1101,17 @@ static cudaError_t launch_chunk(const CUtensorMap& map_q, const ChunkAttnParams&
 }
 
 cudaError_t launch_chunk_attention(const CUtensorMap& map_q, const ChunkAttnParams& p, int grid, cudaStream_t st) {
-  const int rows = chunk_group_rows(std::min(p.call.max_query_len, 256) * p.call.gq);
+  const int rows = p.group_rows;
   const bool q8 = p.scales_k != nullptr;
   cudaError_t e = rows == 8    ? launch_chunk_decode(p, grid, st)
                   : rows == 128 ? (q8 ? launch_chunk<1, true>(map_q, p, grid, st) : launch_chunk<1, false>(map_q, p, grid, st))
                                 : (q8 ? launch_chunk<2, true>(map_q, p, grid, st) : launch_chunk<2, false>(map_q, p, grid, st));
-  if (e != cudaSuccess || rows > 8) return e;
+  if (e != cudaSuccess || p.counters != nullptr) return e;
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = programmatic(dim3(grid, p.call.max_query_len * p.call.gq), 32 * kMergeWarps, 0, st, attr);
-  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel, p);
+  const int items = p.n_reqs * p.t * p.kv_per * ((p.call.max_query_len + p.call.tg - 1) / p.call.tg);   // (fewer than SMs)
+  const int rows_of = std::min(p.call.max_query_len, p.call.tg) * p.call.gq;
+  const cudaLaunchConfig_t cfg = programmatic(dim3(rows == 8 ? grid : std::min(items, grid), rows_of), 32 * kMergeWarps, 0, st, attr);
+  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel, p, grid);
 }
 
 }  // namespace tpl

@@ -97,7 +97,7 @@ struct ChunkWalk {
     b = head = group = cost = 0;
     begin = pos = end = 0;
     // no item of this CTA is continued by others, unless a segment says so below
-    if (ONE && lane == 0) p.items[blockIdx.x].rows = 0;
+    if (p.counters == nullptr && lane == 0) p.items[blockIdx.x].rows = 0;
     __syncwarp();
     // Twice over the requests, 32 at a time: a head's places of all of them with an item cost of 0, and its
     // items; then the request that holds the CTA's first place, and the places before it.
@@ -221,7 +221,7 @@ struct ChunkWalk {
         if (q.slot >= 0) {
           s.first = chunk_holder(begin, cost, width, 0, per);
           s.last = chunk_holder(begin, cost, width, keys.count - 1, per);
-          if (ONE && q.c0 == 0 && lane == 0) p.items[blockIdx.x] = TreeItem{s.r, s.g, 0, s.rows, s.q0 + s.tok0, s.last, 0, 0};
+          if (p.counters == nullptr && q.c0 == 0 && lane == 0) p.items[blockIdx.x] = TreeItem{s.r, s.g, 0, s.rows, s.q0 + s.tok0, s.last, 0, 0};
         }
       }
       pos = begin + p1;

@@ -232,15 +232,17 @@ struct ChunkAttnParams {
   int n_reqs, t, kv_per, max_blocks, num_blocks, block_size;
   unsigned block_magic;              // 2^32 / block_size rounded up (not used for 1)
   float scale_log2;                  // log2(e) / sqrt(hd)
-  unsigned* counters;                // [SMs][8] parts that are there, of the item that a CTA begins; 0 between calls (more than 8 rows)
-  TreeItem* items;                   // [grid] the item each CTA begins and others go on with, for the merge (up to 8 rows)
+  unsigned* counters;                // [SMs][8] parts that are there, of the item that a CTA begins; 0 between calls. Null: a kernel joins them
+  TreeItem* items;                   // [grid] the item each CTA begins and others go on with, for that kernel
   float* partials;                   // [2 * grid] slots of part_rows x (128 + 2)
+  int group_rows;                    // query rows of a group: up to 8, 128 or 256
   int part_rows;
   int q_box_rows;                    // rows of a box of the map of the queries
   int out_align32;                   // out is 32-byte aligned (rows are then written with 32-byte stores)
   unsigned long long timeout_ns;
 };
-int chunk_group_rows(int max_rows);  // query rows of one item: up to 8, 128 or 256
+// Query rows of a group of a call; many: it has an item for every SM; max_keys: the most that a token sees.
+int chunk_group_rows(int max_rows, bool q8, bool many, int max_keys);
 int chunk_decode_ctas(bool q8);      // CTAs per SM of the kernel for up to 8 rows (chunk_decode.cu)
 cudaError_t launch_chunk_decode(const ChunkAttnParams& p, int grid, cudaStream_t st);
 cudaError_t launch_chunk_attention(const CUtensorMap& map_q, const ChunkAttnParams& p, int grid, cudaStream_t st);
@@ -258,7 +260,7 @@ struct KvQuantParams {
   int* status;
   int n, t, q_per, kv_per;
 };
-cudaError_t launch_kv_quant_write(const KvQuantParams& p, int nsm, cudaStream_t st);
+cudaError_t launch_kv_quant_write(const KvQuantParams& p, cudaStream_t st);
 cudaError_t launch_kv_quant_read(const KvQuantParams& p, int nsm, cudaStream_t st);
 
 // Mixture of experts (moe.cu): routing sort, row gather, weighted combine.

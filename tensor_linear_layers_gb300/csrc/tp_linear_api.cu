@@ -1926,7 +1926,7 @@ int tp_kv_quant_write(tp_linear_t* h, int64_t T, const void* qkv, const int32_t*
   p.qkv = static_cast<const __nv_bfloat16*>(qkv);
   p.sstride = gathered(h) ? h->ws_qkv : T * h->ws_qkv;
   p.rstride = (int)(gathered(h) ? h->cfg.t * h->ws_qkv : h->ws_qkv);
-  const cudaError_t e = launch_kv_quant_write(p, h->nsm, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_kv_quant_write(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "8-bit cache write launch");
   return ok();
 }
@@ -1965,10 +1965,10 @@ struct ChunkPlan {
   int rows, grid, part_rows;         // rows of a group: 8, 128 or 256
   int64_t items_off, partials_off, ws_bytes;
 };
-ChunkPlan chunk_plan(const tp_linear* h, int64_t T, int n_reqs, int max_query_len, int max_seq_len, bool q8) {
+bool chunk_many(const tp_linear* h, int n_reqs, int64_t groups) { return (double)n_reqs * h->cfg.t * h->kv_per * groups >= h->nsm; }
+ChunkPlan chunk_plan(const tp_linear* h, int64_t T, int n_reqs, int max_query_len, int max_seq_len, bool q8, int rows) {
   const int gq = h->q_per / h->kv_per;
   const int64_t max_rows = (int64_t)max_query_len * gq;
-  const int rows = chunk_group_rows((int)std::min<int64_t>(max_rows, 256));
   ChunkPlan pl{};
   pl.rows = rows;
   pl.call.T = (int)T;
@@ -2004,10 +2004,10 @@ int tp_chunk_attention_workspace_size(const tp_linear_t* h, int32_t n_reqs, int3
   *bytes = 0;
   const int gq = h->q_per / h->kv_per;
   for (const int rows : {8, 128, 256}) {
-    const int q = std::min(max_query_len, rows / gq > 0 ? rows / gq : 1);
-    *bytes = std::max(*bytes, chunk_plan(h, 0, n_reqs, q, max_seq_len, true).ws_bytes);
+    if (gq > rows) continue;
+    const int q = rows == 256 ? max_query_len : std::min(max_query_len, rows / gq);
+    *bytes = std::max(*bytes, chunk_plan(h, 0, n_reqs, q, max_seq_len, true, rows).ws_bytes);
   }
-  *bytes = std::max(*bytes, chunk_plan(h, 0, n_reqs, max_query_len, max_seq_len, true).ws_bytes);
   return ok();
 }
 
@@ -2034,7 +2034,11 @@ int tp_chunk_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t
   for (const int32_t* q : {query_start_loc, seq_lens, block_tables})
     if (!aligned4(q))
       return fail(TP_ERR_ARG, "query_start_loc, seq_lens and block_tables must be 4-byte aligned device arrays");
-  ChunkPlan pl = chunk_plan(h, T, n_reqs, max_query_len, max_seq_len, scales_k != nullptr);
+  const int64_t max_rows = (int64_t)max_query_len * (h->q_per / h->kv_per);
+  const int64_t max_keys = window > 0 ? std::min<int64_t>(max_seq_len, (int64_t)window + sinks) : max_seq_len;
+  const int group_rows = chunk_group_rows((int)std::min<int64_t>(max_rows, 256), scales_k != nullptr, chunk_many(h, n_reqs, 1),
+                                          (int)max_keys);
+  ChunkPlan pl = chunk_plan(h, T, n_reqs, max_query_len, max_seq_len, scales_k != nullptr, group_rows);
   if (workspace == nullptr || !aligned16(workspace)) return fail(TP_ERR_ARG, "workspace is null or not 16-byte aligned");
   if (workspace_bytes < pl.ws_bytes)
     return fail(TP_ERR_ARG, "workspace too small: %lld bytes, %lld needed", (long long)workspace_bytes,
@@ -2076,7 +2080,11 @@ int tp_chunk_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t
   p.block_size = block_size;
   p.block_magic = (unsigned)(((1ull << 32) + block_size - 1) / block_size);
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt(128.0));
-  p.counters = reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + 256);
+  // With an item or more for every SM an item has two or three parts, which a CTA joins; fewer items have many each,
+  // joined by a kernel over all of them (one request of 4000 keys, eight rows a head: 15 us, 39 by the CTAs).
+  p.group_rows = pl.rows;
+  if (pl.rows > 8 && chunk_many(h, n_reqs, (max_query_len + pl.call.tg - 1) / pl.call.tg))
+    p.counters = reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + 256);
   p.items = reinterpret_cast<TreeItem*>(static_cast<char*>(workspace) + pl.items_off);
   p.partials = reinterpret_cast<float*>(
       (reinterpret_cast<uintptr_t>(workspace) + (uintptr_t)pl.partials_off + 31) & ~uintptr_t(31));
