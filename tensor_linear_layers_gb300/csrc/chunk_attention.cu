@@ -525,57 +525,56 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
         if (slot < 0) break;
         const int r = s_seg[slot].r, g = s_seg[slot].g, c1 = s_seg[slot].c1, p0 = s_seg[slot].p0, p1 = s_seg[slot].p1, skip = s_seg[slot].skip;
         const int* bt = p.block_tables + (size_t)s_seg[slot].b * p.max_blocks;
-        int c = s_seg[slot].c0, key = chunk_key(c * kChunkKeys + 4 * lane, sc, skip), blk[4];
-        auto blocks = [&]() {
-          if (quads) {
-            blk[0] = key <= p1 && (window == 0 || key + 3 > p0 - window || key < sinks) ? bt[chunk_page(p, key)] : 0;
-          } else {
+        // every step at one place in the code: a turn before the first chunk looks up its blocks, one after the last
+        // hands that on
+        const int c0 = s_seg[slot].c0;
+        int key = 0, blk[4] = {};
+        for (int c = c0 - 1;; ++c) {
+          const bool here = c >= c0 && c < c1;
+          const int place = n % C::kLooks;
+          int row[4] = {-1, -1, -1, -1};              // cache rows of the lane's keys (-1: zeros)
+          unsigned mixed = 0;
+          if (here) {
+            if (!wait(C::L_EMPTY + place, ((n / C::kLooks) & 1) ^ 1)) break;
+            const int first = cache_row(r, blk[0], key);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) blk[i] = any_sees(key + i, p0, p1) ? bt[chunk_page(p, key + i)] : 0;
-          }
-        };
-        blocks();
-        for (; c < c1; ++c, ++n) {
-          const int place = n % C::kLooks, x0 = c * kChunkKeys;
-          if (!wait(C::L_EMPTY + place, ((n / C::kLooks) & 1) ^ 1)) break;
-          int row[4];
-          if (quads && x0 + kChunkKeys - 1 + skip <= p1 && (window == 0 || (x0 >= sc && x0 + skip > p0 - window) || x0 + kChunkKeys <= sinks)) {
-            row[0] = cache_row(r, blk[0], key);       // all of the chunk's keys are seen
-            if (row[0] < 0) atomicExch(p.status, kStatusShape);
-#pragma unroll
-            for (int i = 1; i < 4; ++i) row[i] = row[0] < 0 ? -1 : row[0] + i;
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              row[i] = -1;
+            for (int i = 0; i < 4; ++i)
               if (any_sees(key + i, p0, p1)) {
-                row[i] = cache_row(r, quads ? blk[0] : blk[i], key + i);
+                row[i] = quads ? (first < 0 ? -1 : first + i) : cache_row(r, blk[i], key + i);
                 if (row[i] < 0) atomicExch(p.status, kStatusShape);
               }
+            sts128(base + C::kLookOff + place * kLookBytes + 16 * lane, row[0], row[1], row[2], row[3]);
+            if (lane == 0) *reinterpret_cast<int*>(base_ptr + C::kLookOff + place * kLookBytes + 640 * 4) = g;
+            if (mixed_chunk(c, skip, p0, p1))
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mixed |= partly_seen(key + i, p0, p1) ? 1u << i : 0u;
+          }
+          if (c + 1 < c1) {
+            key = chunk_key((c + 1) * kChunkKeys + 4 * lane, sc, skip);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (i > 0 && quads) break;              // one block for the four
+              const bool seen = key + i <= p1 && (window == 0 || key + (quads ? 3 : i) > p0 - window || key + i < sinks);
+              blk[i] = seen ? bt[chunk_page(p, key + i)] : 0;
             }
           }
-          sts128(base + C::kLookOff + place * kLookBytes + 16 * lane, row[0], row[1], row[2], row[3]);
-          if (lane == 0) *reinterpret_cast<int*>(base_ptr + C::kLookOff + place * kLookBytes + 640 * 4) = g;
-          unsigned mixed = 0;
-          if (mixed_chunk(c, skip, p0, p1))
+          hand_on();                                  // (the mark belongs to this segment)
+          at = -1;
+          if (c == c1) break;
+          if (here) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mixed |= partly_seen(key + i, p0, p1) ? 1u << i : 0u;
-          key = chunk_key(x0 + kChunkKeys + 4 * lane, sc, skip);
-          if (c + 1 < c1) blocks();
-          hand_on();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const size_t x = (size_t)(unsigned)max(row[i], 0) * (unsigned)p.kv_per + g;
-            ks[i] = row[i] >= 0 ? p.scales_k[x] : 127u;
-            vs[i] = row[i] >= 0 ? p.scales_v[x] : 127u;
+            for (int i = 0; i < 4; ++i) {
+              const size_t x = (size_t)(unsigned)max(row[i], 0) * (unsigned)p.kv_per + g;
+              ks[i] = row[i] >= 0 ? p.scales_k[x] : 127u;
+              vs[i] = row[i] >= 0 ? p.scales_v[x] : 127u;
+            }
+            part = mixed;
+            at = place;
+            seg = slot;
+            ++n;
           }
-          part = mixed;
-          at = place;
-          seg = slot;
         }
         if (!ok) break;
-        hand_on();                                    // (the mark belongs to this segment)
-        at = -1;
         release_segment(slot);
       }
       if (ok) {                                       // no more chunks
@@ -734,9 +733,11 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
         cp_async_commit();
         ++issued;
       };
-#pragma unroll 1
-      for (int i = 0; i < C::kAhead && ok; ++i) issue();
-      while (ok && converted != last) {
+      for (;;) {
+        issue();
+        if (!ok) break;
+        if (issued < C::kAhead) continue;
+        if (converted == last) break;
         const int c = converted >> 1, place = c % C::kLooks;
         cp_async_wait<C::kAhead - 1>();
         const uint32_t look = looks + place * kLookBytes + (converted & 1 ? 384 : 128) * 4;
@@ -776,7 +777,6 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
         }
         advance();
         ++converted;
-        issue();
       }
     }
     cp_async_wait_all();       // no copy into this CTA's shared memory may outlive it
