@@ -42,7 +42,7 @@ namespace tpl {
 //   4 warps     (bf16) copy K and V rows through the block table with 16-byte cp.async into
 //               128-byte-swizzled tiles (any block size: a key's row is found on its own);
 //   8 warps     (8 bits) copy the codes to buffers of their own, three tiles ahead; each thread
-//               turns the codes that it copied into bf16 and stores those
+//               turns the codes that it copied into bf16 and stores those (four warps: 1606 us for 1048)
 //   the others  softmax, a row per thread, four warps per tile; at a segment's end O / l to
 //               global memory, or the unnormalised O with (m, l) to a partial slot
 //
@@ -51,6 +51,17 @@ namespace tpl {
 // window between the first and the last of them), values of V that are not finite become zero in
 // shared memory, so that 0 * v stays 0 for the rows that do not see the key; the rows that see it
 // get the value added at the end.
+//
+// What bounds it, at two tiles. bf16: 1.63 us a chunk of 128 keys x 256 rows (2048 tokens over 32 049 keys 690 us,
+// 0.78 of what a large matrix product reaches): S by halves reads Q again for each, 48 cycles of shared memory an
+// MMA for 32 of products, and the softmax of 64 keys is a chain of some 1200 cycles after it, behind which two
+// buffers per tile hide most of that. (S by whole chunks, without that, takes turns with softmax and P V: 895 us.)
+// 8 bits: 1.88 us a chunk (793 us); 68 % of the issue slots go to the conversion and the softmax.
+// Code size counts here: all roles run at once, and with twenty warps' hot code beyond the SM's instruction cache
+// every chunk fetched it again from the cache that the SMs of a GPC share (8 bits: 1019 us; the SMs of the GPC that
+// has fewest ran 15 % faster). So loops that are seldom run or have time are rolled, each step of a role stands at
+// one place in the code, and the warp's index is known to be uniform.
+// An item costs some 3 us besides its chunks (chunk_item_cost): the drain of the last products, its output.
 //
 // Codes become bf16 with integer operations and one product: e4m3 is s eeee mmm with bias 7, and
 // those bits put at s 0000eeee mmm0000 of a bf16 (bias 127) are the value times 2^-120, subnormal
@@ -346,7 +357,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
           if (!wait(C::S_FREE + cnt[0] % C::kSBufs, ((cnt[0] / C::kSBufs) & 1) ^ 1)) break;
           if (!wait(C::FULL + ring, ring_ph)) break;
           fence_async_proxy();
-#pragma unroll(Q8 ? 1 : C::kSubs)
+#pragma unroll(Q8 ? 1 : C::kSubs)                       // (code size)
           for (int h = 0; h < C::kSubs; ++h) {
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
@@ -404,7 +415,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
         for (int j = 0; j < n && ok; ++j) {
           if (!wait(C::FULL + ring, ring_ph)) break;
           fence_async_proxy();
-#pragma unroll(Q8 ? 1 : C::kSubs)
+#pragma unroll(Q8 ? 1 : C::kSubs)                       // (code size)
           for (int h = 0; h < C::kSubs; ++h) {
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
@@ -646,7 +657,8 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
     // ------------------------------------------------------------ copies
     regs_dec<C::kRegs1>();
     const int w4 = warp - 4;
-    // the cache is read once a call by one item (evicted first) or by its groups of rows
+    // the cache is read once a call by one item (evicted first: 8 requests of 30 tokens over 4000 keys 38.3 us, 41.5
+    // without) or by its groups of rows
     const uint64_t pol = p.call.max_query_len > p.call.tg ? policy_evict_normal() : policy_evict_first();
     int ring = 0;
     uint32_t ring_ph = 0;
@@ -848,7 +860,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
             if (!wait_last_pv()) break;
             tc_fence_after();
             float o[32];
-#pragma unroll(Q8 ? 1 : 4)
+#pragma unroll(Q8 ? 1 : 4)                            // (see above: code size)
             for (int k = 0; k < 128; k += 32) {
               tmem_ld32(lane_addr + C::o_col(tile) + k, o);
               tc_wait_ld();
@@ -1108,9 +1120,10 @@ cudaError_t launch_chunk_attention(const CUtensorMap& map_q, const ChunkAttnPara
                                 : (q8 ? launch_chunk<2, true>(map_q, p, grid, st) : launch_chunk<2, false>(map_q, p, grid, st));
   if (e != cudaSuccess || p.counters != nullptr) return e;
   cudaLaunchAttribute attr[1];
-  const int items = p.n_reqs * p.t * p.kv_per * ((p.call.max_query_len + p.call.tg - 1) / p.call.tg);   // (fewer than SMs)
+  int items = grid;
+  if (rows > 8) items = std::min(items, p.n_reqs * p.t * p.kv_per * ((p.call.max_query_len + p.call.tg - 1) / p.call.tg));   // fewer than SMs
   const int rows_of = std::min(p.call.max_query_len, p.call.tg) * p.call.gq;
-  const cudaLaunchConfig_t cfg = programmatic(dim3(rows == 8 ? grid : std::min(items, grid), rows_of), 32 * kMergeWarps, 0, st, attr);
+  const cudaLaunchConfig_t cfg = programmatic(dim3(items, rows_of), 32 * kMergeWarps, 0, st, attr);
   return cudaLaunchKernelEx(&cfg, chunk_merge_kernel, p, grid);
 }
 

@@ -33,8 +33,9 @@
 namespace tpl {
 
 constexpr int kChunkKeys = 128;
-// Places that an item costs besides its chunks: its queries, the first products, its output. Measured at
-// two row tiles as 5 us against 1.8 us of a chunk, 4 places.
+// Places that an item costs besides its chunks: the drain of its products and its output. Measured at two row
+// tiles as some 3.5 us against 1.65 us of a chunk, 4 places (a prompt of 4096 tokens: 145 us without this cost, 126
+// with 6 to 10 places, 128 with 13 or 16).
 TPL_HD int chunk_item_cost(int full) { return full == 4 ? 10 : 4; }
 
 // a / b of places (a >= 0, b > 0): in 32 bits where they fit, a quarter of the instructions
@@ -143,7 +144,8 @@ TPL_HD long long chunk_head(const ChunkCall& c, const ChunkReq& r, int cost) {
 }
 TPL_HD int chunk_widest(const ChunkCall& c, const ChunkReq& r) { return r.groups > 1 ? c.full : r.groups > 0 ? r.last : 0; }
 
-// Few chunks per CTA: they are spread over as many CTAs as there are, so an item costs nothing besides them.
+// Few chunks per CTA: they are spread over as many CTAs as there are, so an item costs nothing besides them (one
+// request of 4000 keys 12.4 us, 12.8 with a cost).
 TPL_HD int chunk_cost(long long places, int full, int grid) { return places >= 4LL * full * grid ? chunk_item_cost(full) : 0; }
 TPL_HD long long chunk_per(long long total, int grid, int widest) {
   const long long even = chunk_div(total + grid - 1, grid);
