@@ -17,16 +17,17 @@
 // before the conversion. The scales never touch the codes:
 //   x_j = s_j log2(e) + e_j (e_j: exponent of v's scale),   w_j = 2^(x_j - m),   m = max_j x_j - 7
 //   O = sum_j w_j code_j,   l = sum_j 2^(x_j - e_j - m)
-// with k's scale in the factor of the raw product. w is at most 2^15 (m moves when a row exceeds it by
-// 2^8 more than it was taken at) and rounded to f16, 2^-11 of it down to 2^-29 of the largest. q goes
-// to f16 with a power of two per row that brings its largest element to [2^8, 2^9): exact for
-// elements down to 2^-16 of that, off by 2^-33 of it below.
-// Two CTAs of 128 registers per SM in 8 bits (one CTA: 32 requests of
-// 2000 keys 48.5 us for 39.4, 4 x 131 072 keys 287 for 187), one of 232 in bf16, whose rings fill shared memory.
-// HBM bounds it while it streams, 0.86 of a copy (4 x 131 072 keys, 64 q heads: 187 us for 160 of bytes); a batch of 32
-// requests of 255 - 4095 keys takes 39 us for 21 of bytes: 6 of launch, 3.5 until the walk's and the tables'
-// dependent loads have given the first rows, 4 of the merge behind the grid.
+// with k's scale in the factor of the raw product. w is 2^7 at the row's largest x, at most 2^15 (m moves when a
+// row exceeds it by 2^8 more than it was taken at), and rounded to f16: 2^-11 of it down to 2^-21 of the
+// largest, 2^-32 of the largest below. q goes to f16 with a power of two per row that brings its largest
+// element to [2^8, 2^9): exact for elements down to 2^-16 of that, off by 2^-33 of it below.
 // bf16: operands come through ldmatrix; m = max_j x_j + 17 as in chunk_attention.cu, w in bf16.
+//
+// Two CTAs of 128 registers per SM in 8 bits (one CTA: 32 requests of 2000 keys 48.5 us for 39.4, 4 x 131 072
+// keys 287 for 187), one of 232 in bf16, whose rings fill shared memory. HBM bounds it while it streams, 0.86 of a
+// copy (4 x 131 072 keys, 64 q heads: 187 us for 160 of bytes); a batch of 32 requests of 255 - 4095 keys takes 39 us
+// for 21 of bytes: 6 of launch, 3.5 until the walk's and the tables' dependent loads have given the first rows, 4 of
+// the merge behind the grid.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

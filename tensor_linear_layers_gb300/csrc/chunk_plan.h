@@ -174,7 +174,7 @@ TPL_HD int chunk_holder(long long begin, int cost, int width, int j, long long p
   return (int)chunk_div(begin + cost + (long long)j * width, per);
 }
 
-// CTAs of the grid: one per SM, no more than a call of these bounds has chunks.
+// CTAs of the grid: as many as run at once, no more than a call of these bounds has chunks.
 inline int chunk_grid(int nsm, int n_reqs, int heads, int max_query_len, int tg, int max_seq_len) {
   const double groups = (max_query_len + tg - 1) / tg;
   const double chunks = (double)n_reqs * heads * groups * ((max_seq_len + kChunkKeys - 1) / kChunkKeys);
