@@ -550,12 +550,17 @@ class TPLinear:
     def _quant(self, codes_k: torch.Tensor, codes_v: torch.Tensor, scales_k: torch.Tensor, scales_v: torch.Tensor):
         """(blocks, block size, the four device pointers) of a cache in 8 bits on this handle's device."""
         nb, bs, shape = self._cache_shape(codes_k)
-        dev = self._index
-        for name, x, dtype, want in (("codes_k", codes_k, _E4M3, shape), ("codes_v", codes_v, _E4M3, shape),
-                                     ("scales_k", scales_k, torch.uint8, shape[:-1]),
-                                     ("scales_v", scales_v, torch.uint8, shape[:-1])):
-            if x.dtype is not dtype or x.get_device() != dev or not x.is_contiguous() or x.shape != want:
-                raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(want)} on cuda:{dev}")
+        dev, flat = self._index, shape[:-1]
+        if not (codes_k.dtype is codes_v.dtype is _E4M3 and scales_k.dtype is scales_v.dtype is torch.uint8
+                and codes_v.shape == shape and scales_k.shape == flat and scales_v.shape == flat and codes_k.shape == shape
+                and codes_k.get_device() == codes_v.get_device() == scales_k.get_device() == scales_v.get_device() == dev
+                and codes_k.is_contiguous() and codes_v.is_contiguous() and scales_k.is_contiguous()
+                and scales_v.is_contiguous()):
+            for name, x, dtype, want in (("codes_k", codes_k, _E4M3, shape), ("codes_v", codes_v, _E4M3, shape),
+                                         ("scales_k", scales_k, torch.uint8, flat),
+                                         ("scales_v", scales_v, torch.uint8, flat)):
+                if x.dtype is not dtype or x.get_device() != dev or not x.is_contiguous() or x.shape != want:
+                    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(want)} on cuda:{dev}")
         return nb, bs, codes_k.data_ptr(), codes_v.data_ptr(), scales_k.data_ptr(), scales_v.data_ptr()
 
     def kv_quant_write(self, qkv: torch.Tensor, slot_mapping: torch.Tensor, codes_k: torch.Tensor,
