@@ -26,8 +26,8 @@
 // Two CTAs of 128 registers per SM in 8 bits (one CTA: 32 requests of 2000 keys 48.5 us for 39.4, 4 x 131 072
 // keys 287 for 187), one of 232 in bf16, whose rings fill shared memory. HBM bounds it while it streams, 0.86 of a
 // copy (4 x 131 072 keys, 64 q heads: 187 us for 160 of bytes); a batch of 32 requests of 255 - 4095 keys takes 39 us
-// for 21 of bytes: 6 of launch, 3.5 until the walk's and the tables' dependent loads have given the first rows, 4 of
-// the merge behind the grid.
+// for 21 of bytes: 3.5 until the walk is done and 2 until the tables' and scales' dependent loads have given the first
+// rows, 25 of streaming, 4 of the merge behind the grid, the rest the ends of uneven CTAs.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -13,8 +13,8 @@
 // a row, 16 elements each, so that a row's codes are one 128-byte line in 16-byte pieces and its largest
 // element takes three exchanges; 32 lanes of four elements would take five and four-byte stores.
 // Measured: 65 536 tokens of 16 heads read in 65 us, 6.2 TB/s (93 % of a plain copy); 8192 tokens of 16
-// heads written in 10.8 us, of which 7.5 are the bytes; calls of a few hundred tokens are latency, 8 us with
-// the launch.
+// heads written in 10.8 us, of which 7.5 are the bytes; calls of a few hundred tokens are 7 us of the host's
+// call and 1.6 on the device.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
