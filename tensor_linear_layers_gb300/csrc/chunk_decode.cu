@@ -409,8 +409,10 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<Q8>::kCtas) chunk_decode_k
               float top = fmaxf(x[h], x[2 + h]);
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) + C::kHead;
-              if (top > m[h]) {
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+              // each row by its own threshold, as `over`: another row's scores do not move its reference
+              if (top > m[h] + (kRescaleLog2 - C::kHead)) {
+                top += C::kHead;
                 const float f = fast_exp2(m[h] - top);         // 0 where nothing was seen before
                 m[h] = top;
                 l[h] *= f;
