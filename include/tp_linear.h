@@ -419,7 +419,8 @@ int tp_kv_quant_read(tp_linear_t* h, int64_t n, const int32_t* slots, const void
  * tp_kv_quant_write). The token at position p sees position j <= p if window = 0, j > p - window
  * (its own and the window - 1 before it) or j < sinks (first tokens that stay visible; without a
  * window they have no effect). What a token does not see has no effect on it, NaN and infinities
- * included; pages that no token sees are not read, and their block table entries not looked at.
+ * included; pages that no token sees are not read, and their block table entries not looked at. A
+ * token whose scores are all -inf gets NaN, as its softmax has no value.
  * Other arguments, layouts, bounds and errors as for tp_paged_attention; max_seq_len <= 2^26, at
  * most 256 q heads per kv head; attn_out and the workspace apart from what the call reads. Rows of
  * attn_out that belong to no request are left as they were. Scores, softmax and sums in fp32

@@ -229,7 +229,7 @@ __device__ __forceinline__ void chunk_join_rows(const ChunkAttnParams& p, int fi
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (row0 + j >= rows) break;
-    const float inv = l[j] == 0.f ? 0.f : 1.0f / l[j];
+    const float inv = 1.0f / l[j];                     // (a sum of 0: see the softmax)
     const int tok = row[j] / gq;
     uint2 y;
     y.x = pack_bf16x2(o[j].x * inv, o[j].y * inv);
@@ -925,7 +925,9 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
         tc_fence_after();
         const int bad = *reinterpret_cast<volatile int*>(&s_seg[slot].bad);
         const int r = s_seg[slot].r, g = s_seg[slot].g, b = s_seg[slot].b;
-        const float inv = lt == 0.f ? 0.f : 1.0f / lt;
+        // A token sees itself at least: a sum of 0 is a row whose scores are all -inf, and 0 * inf gives the NaN that
+        // its softmax is. (Unused for a part that another joins, whose sum may well be 0.)
+        const float inv = 1.0f / lt;
         __nv_bfloat16* dst = p.out + (size_t)r * p.sstride_out +
                              (size_t)(s_seg[slot].q0 + s_seg[slot].tok0 + tok) * p.rstride_out + (g * gq + row - tok * gq) * kHd;
         // (32 dimensions at a time, not unrolled: what this code costs most is the fetch of its instructions)
@@ -1070,7 +1072,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_kernel(const Chu
     o.z += v.z;
     o.w += v.w;
   }
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  const float inv = 1.0f / l;                         // (0: all the row's scores are -inf, and the output is NaN)
   const int gq = p.call.gq, tok = row / gq;
   uint2 out;
   out.x = pack_bf16x2(o.x * inv, o.y * inv);

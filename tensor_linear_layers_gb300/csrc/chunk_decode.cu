@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<Q8>::kCtas) chunk_decode_k
           *reinterpret_cast<float4*>(chunk_part_o(p, part, row, 4 * lane)) = v;
           if (lane == 0) *chunk_part_ml(p, part, row) = make_float2(mt, lt);
         } else {
-          const float inv = lt == 0.f ? 0.f : 1.0f / lt;
+          const float inv = 1.0f / lt;                         // (0: all the row's scores are -inf, and the output is NaN)
           uint2 out;
           out.x = pack_bf16x2(v.x * inv, v.y * inv);
           out.y = pack_bf16x2(v.z * inv, v.w * inv);
