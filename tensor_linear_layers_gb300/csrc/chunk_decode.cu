@@ -356,10 +356,11 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<Q8>::kCtas) chunk_decode_k
         // else nothing of the warp's keys is seen: past the last token, or in the gap before the window
         if (key <= p1 && (window == 0 || key + 15 > p0 - window || key < sinks)) {
           float s[4] = {0.f, 0.f, 0.f, 0.f};
-          float k0 = 1.f, k1 = 1.f, e0 = 0.f, e1 = 0.f;        // scales of keys g, g + 8: k's value, v's exponent
+          uint32_t k0 = 127u, k1 = 127u;                       // scales of keys g, g + 8: k's byte, v's exponent
+          float e0 = 0.f, e1 = 0.f;
           if constexpr (Q8) {
-            k0 = scale_value(__shfl_sync(0xffffffffu, f[0].k, g));
-            k1 = scale_value(__shfl_sync(0xffffffffu, f[0].k, g + 8));
+            k0 = __shfl_sync(0xffffffffu, f[0].k, g);
+            k1 = __shfl_sync(0xffffffffu, f[0].k, g + 8);
             e0 = scale_exponent(__shfl_sync(0xffffffffu, f[0].v, g));
             e1 = scale_exponent(__shfl_sync(0xffffffffu, f[0].v, g + 8));
 #pragma unroll
@@ -390,10 +391,19 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<Q8>::kCtas) chunk_decode_k
           }
           // x: the weights' exponents; elements 0, 1 of key g, 2, 3 of key g + 8
           const bool partly = key + 15 > p0 || (window > 0 && key <= p1 - window && key + 15 >= sinks);
-          s[0] *= factor.x * k0;
-          s[1] *= factor.y * k0;
-          s[2] *= factor.x * k1;
-          s[3] *= factor.y * k1;
+          if constexpr (Q8) {
+            // k's scale before the row's factor where it is below one, after it where it is above, so that nothing on the
+            // way is larger than the raw product and the score are (the product of both factors may well be)
+            const float low0 = scale_value(min(k0, 127u)), high0 = scale_value(max(k0, 127u));
+            const float low1 = scale_value(min(k1, 127u)), high1 = scale_value(max(k1, 127u));
+            s[0] = s[0] * low0 * factor.x * high0;
+            s[1] = s[1] * low0 * factor.y * high0;
+            s[2] = s[2] * low1 * factor.x * high1;
+            s[3] = s[3] * low1 * factor.y * high1;
+          } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) s[h] *= h & 1 ? factor.y : factor.x;
+          }
           float x[4] = {s[0] + e0, s[1] + e0, s[2] + e1, s[3] + e1};
           if (partly) {
 #pragma unroll

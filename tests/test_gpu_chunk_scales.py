@@ -1,0 +1,78 @@
+"""Attention of chunks of new tokens over an 8-bit cache where scales and queries are far from one: every kernel gives the
+oracle's result."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from test_gpu_chunk import build, caches64, run
+from test_gpu_kv_quant import built, handle, status  # noqa: F401 (built: the module's fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def check(got, c, window=0, sinks=0):
+    """Within what the roundings allow: those of test_gpu_chunk.check, and, in the kernel for up to eight rows, those of the
+    f16 weights w_j = 2^(x_j - m), x_j the score's exponent and v's scale together, the largest at 2^7 or more where
+    some v has a scale of 2^-86 or more, at 2^-7 or more where none has. Under f16's normal numbers a weight is off by
+    2^-25 at most: 2^-32 of the largest (2^-18), times 448 in O for each of the keys."""
+    nq, nkv, t = c["heads"]
+    ck, cv = caches64(c)
+    ref, size, spread, score = oracle.chunk_attention(oracle.bf16_to_f64(c["qkv"]), c["qsl"], c["lens"], c["tables"], ck, cv,
+                                                      nq, nkv, 128, t, c["bs"], window, sinks, bound=True)
+    top = int(c["sv"].max()) - 127
+    lost = max(c["lens"]) * (2.0 ** -109 * np.abs(cv).max() + 2.0 ** (-32 + max(0, -86 - top)) * 448 * 2.0 ** top)
+    off = 4 * 130 * 2.0 ** -24 * np.repeat(score, 128, -1) + 2.0 ** -20 + (max(c["lens"]) / 16 + 8) * 2.0 ** -22
+    tol = 2.0 ** -8 * (np.minimum(size, 7 * spread) * (1 + 2.0 ** -8) + np.abs(ref)) + off * size + lost
+    g = got.double().cpu().numpy()
+    assert np.isfinite(g).all()
+    err = np.abs(g - ref) - tol
+    assert err.max() <= 0, f"over by {err.max():.3e} at {np.unravel_index(err.argmax(), err.shape)}, tolerance {tol.min():.3e}"
+    return ref
+
+
+SIZES = [([200], [1]), ([200], [2]), ([5000], [2]), ([200], [20]), ([5000], [150])]    # up to eight rows, one tile, two
+
+
+@pytest.mark.parametrize("ctx,n", SIZES)
+@pytest.mark.parametrize("end,sk", [(27, 127), (245, 127), (140, 135), (127, 140), (41, 127), (0, 127)])
+def test_both_ends_of_the_scales(ctx, n, end, sk):
+    # v rows of 2^-100 and 2^118 times a code, also none but rows that were never written (byte 0, codes 0); and k rows
+    # whose second factor is not one
+    c = build(4, 2, 1, ctx, n, 16, seed=end, q8=True)
+    c["sv"] = torch.full_like(c["sv"], end)
+    if end == 0:
+        c["cv"] = torch.zeros_like(c["cv"].view(torch.uint8)).view(torch.float8_e4m3fn)
+    c["sk"] = torch.full_like(c["sk"], sk if sk > 134 else sk - 8)        # codes reach 448: keep the scores moderate
+    if sk > 134:
+        c["qkv"] = (c["qkv"].float() * 2.0 ** (119 - sk)).to(torch.bfloat16)
+    out, ws = run(handle(4, 2, 1), c)
+    assert status(ws) == 0
+    check(out, c)
+
+
+@pytest.mark.parametrize("ctx,n", SIZES)
+@pytest.mark.parametrize("power", [-100, -60, 60, 100, 114])
+def test_scales_of_k_that_a_query_makes_up_for(ctx, n, power):
+    # q of 2^-power against k of 2^power: moderate scores
+    c = build(4, 2, 1, ctx, n, 16, seed=300 + power, q8=True)
+    c["sk"] = torch.full_like(c["sk"], 119 + power)
+    c["qkv"] = (c["qkv"].float() * 2.0 ** -power).to(torch.bfloat16)
+    out, ws = run(handle(4, 2, 1), c)
+    assert status(ws) == 0
+    check(out, c)
+
+
+@pytest.mark.parametrize("ctx,n", SIZES)
+@pytest.mark.parametrize("q,k", [(60, 90), (39, 118), (118, 118)])
+def test_products_of_zero_of_large_queries_and_large_scales(ctx, n, q, k):
+    # k has codes of 0 wherever q is not 0: every score is 0, however large both factors are
+    c = build(4, 2, 1, ctx, n, 16, seed=310, q8=True)
+    c["sk"] = torch.full_like(c["sk"], 127 + k)
+    c["ck"] = c["ck"].clone()
+    c["ck"].view(torch.uint8)[..., 64:] = 0
+    c["qkv"] = (c["qkv"].float().clamp(-3, 3) * 2.0 ** q).to(torch.bfloat16)
+    c["qkv"].view(1, c["T"], -1, 128)[..., :64] = 0
+    out, ws = run(handle(4, 2, 1), c)
+    assert status(ws) == 0
+    check(out, c)
