@@ -426,8 +426,9 @@ int tp_kv_quant_read(tp_linear_t* h, int64_t n, const int32_t* slots, const void
  * attn_out that belong to no request are left as they were. Scores, softmax and sums in fp32
  * (values of v under 2^137 / L, L the tokens seen, do not overflow), P rounded to bf16 for the
  * P V product (in 8 bits, where max_query_len makes at most eight query rows of a kv head, P times
- * v's scale to f16: 2^-11 of it down to 2^-21 of the row's largest, 2^-32 of the largest below),
- * output rounded to bf16. The workspace (tp_chunk_attention_workspace_size; caller-owned,
+ * v's scale to f16: 2^-11 of it down to 2^-21 of the row's largest, 2^-32 of the largest below, v's
+ * scales under 2^-86 counted as that in the largest), output rounded to bf16. Slots of an 8-bit cache
+ * that were zero-filled and never written stand for zeros. The workspace (tp_chunk_attention_workspace_size; caller-owned,
  * ZERO-FILLED before first use) holds the status word and partial results; one of larger bounds
  * serves too, and calls of any bounds that it serves may follow one another in it.
  */

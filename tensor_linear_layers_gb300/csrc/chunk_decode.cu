@@ -15,11 +15,13 @@
 // conversion instruction makes two f16 of two codes, exactly. Which dimensions of K a lane's codes
 // are is a permutation that Q's operand takes too; V's codes of two keys are interleaved by byte
 // before the conversion. The scales never touch the codes:
-//   x_j = s_j log2(e) + e_j (e_j: exponent of v's scale),   w_j = 2^(x_j - m),   m = max_j x_j - 7
+//   x_j = s_j log2(e) + e_j (e_j: exponent of v's scale),   w_j = 2^(x_j - m)
+//   m = max_j (s_j log2(e) + max(e_j, -86)) - 7
 //   O = sum_j w_j code_j,   l = sum_j 2^(x_j - e_j - m)
 // with k's scale in the factor of the raw product. w is 2^7 at the row's largest x, at most 2^15 (m moves when a
 // row exceeds it by 2^8 more than it was taken at), and rounded to f16: 2^-11 of it down to 2^-21 of the
-// largest, 2^-32 of the largest below. q goes to f16 with a power of two per row that brings its largest
+// largest, 2^-32 of the largest below. (-86: slots that were never written have a scale of 2^-127, and keys of those
+// alone would take l to 2^134. Where all of v's scales are smaller, the largest w is smaller by as much.) q goes to f16 with a power of two per row that brings its largest
 // element to [2^8, 2^9): exact for elements down to 2^-16 of that, off by 2^-33 of it below.
 // bf16: operands come through ldmatrix; m = max_j x_j + 17 as in chunk_attention.cu, w in bf16.
 //
@@ -48,6 +50,9 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kBatch = 3;                      // segments of a batch
 constexpr int kRows = 8;                       // query rows of an item
 constexpr float kRescaleLog2 = 8.0f;
+// 8 bits: an exponent of v's scale below this counts as this where m is taken, so that l, whose weights are without
+// v's scale, is at most 2^(86 + 15) for each of 2^26 keys, and finite
+constexpr float kLeastExponent = -86.0f;
 
 template <bool Q8>
 struct DecodeCfg {
@@ -412,11 +417,14 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<Q8>::kCtas) chunk_decode_k
               if (!(j <= at && (window == 0 || j > at - window || j < sinks))) s[h] = x[h] = -INFINITY;
             }
           }
-          const bool over = fmaxf(x[0], x[2]) > m[0] + (kRescaleLog2 - C::kHead) || fmaxf(x[1], x[3]) > m[1] + (kRescaleLog2 - C::kHead);
+          float y[4];                                          // what m is taken from
+#pragma unroll
+          for (int h = 0; h < 4; ++h) y[h] = Q8 ? fmaxf(x[h], s[h] + kLeastExponent) : x[h];
+          const bool over = fmaxf(y[0], y[2]) > m[0] + (kRescaleLog2 - C::kHead) || fmaxf(y[1], y[3]) > m[1] + (kRescaleLog2 - C::kHead);
           if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              float top = fmaxf(x[h], x[2 + h]);
+              float top = fmaxf(y[h], y[2 + h]);
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));

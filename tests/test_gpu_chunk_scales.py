@@ -76,3 +76,24 @@ def test_products_of_zero_of_large_queries_and_large_scales(ctx, n, q, k):
     out, ws = run(handle(4, 2, 1), c)
     assert status(ws) == 0
     check(out, c)
+
+
+@pytest.mark.parametrize("ctx,n", SIZES + [([40, 700], [1, 2]), ([20000], [1])])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 20)])
+def test_slots_that_were_never_written_count_as_zeros(ctx, n, window, sinks):
+    # a cache as kv_quant_cache makes it, some of its pages without a write (byte 0 and codes 0): keys and values of 0,
+    # which have weight like any others, whole warps' keys and whole parts of items among them
+    bs = 16
+    c = build(4, 2, 1, ctx, n, bs, seed=330 + len(ctx), q8=True)
+    rng = np.random.default_rng(5)
+    for name in ("ck", "cv", "sk", "sv"):
+        c[name] = c[name].clone()
+    for b, x in enumerate(ctx):
+        pages = np.nonzero(rng.random(x // bs) < 0.4)[0]
+        pages = np.unique(np.concatenate([[1], pages, np.arange(x // bs // 2, x // bs // 2 + x // bs // 5)]))
+        at = torch.from_numpy(c["tables"][b, pages])
+        for name in ("ck", "cv", "sk", "sv"):
+            c[name].view(torch.uint8)[:, at] = 0
+    out, ws = run(handle(4, 2, 1), c, window, sinks)
+    assert status(ws) == 0
+    check(out, c, window, sinks)
