@@ -68,7 +68,6 @@ namespace tpl {
 // numbers too; a product with 2^120 and the head's scale, exact, gives the value.
 namespace {
 constexpr int kHd = 128;
-constexpr int kStatusShape = -2;               // TP_ERR_SHAPE
 constexpr int kTileBytes = 128 * 128 * 2;      // 128 rows x 128 bf16: two 64-column boxes
 constexpr int kCodeBytes = 128 * 128;          // codes of 128 keys
 constexpr int kUnitSlots = 4;
@@ -124,23 +123,6 @@ struct ChunkCfg {
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -552,7 +534,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
             for (int i = 0; i < 4; ++i)
               if (any_sees(key + i, p0, p1)) {
                 row[i] = quads ? (first < 0 ? -1 : first + i) : cache_row(r, blk[i], key + i);
-                if (row[i] < 0) atomicExch(p.status, kStatusShape);
+                if (row[i] < 0) atomicExch(p.status, kChunkStatusShape);
               }
             sts128(base + C::kLookOff + place * kLookBytes + 16 * lane, row[0], row[1], row[2], row[3]);
             if (lane == 0) *reinterpret_cast<int*>(base_ptr + C::kLookOff + place * kLookBytes + 640 * 4) = g;
@@ -691,7 +673,7 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
           int row = -1;                                // cache row of this lane's key (-1: zeros)
           if (any_sees(key, s.p0, s.p1)) {
             row = cache_row(s.r, blk, key);
-            if (row < 0) atomicExch(p.status, kStatusShape);
+            if (row < 0) atomicExch(p.status, kChunkStatusShape);
           }
           if (c + 1 < s.c1) blk = block_of(c + 1);
 #pragma unroll 1

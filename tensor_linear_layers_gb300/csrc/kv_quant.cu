@@ -32,7 +32,6 @@ constexpr int kThreads = 256;
 constexpr int kRowLanes = 8;
 constexpr int kScaleNan = 255;
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 // two fp32 as e4m3, lo in the low byte
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t d;
@@ -101,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) kv_quant_write_kernel(const KvQuantP
   // the largest size: without the sign, bf16 bits are ordered as whole numbers, NaN above infinity
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max_u16x2(top, w[i] & 0x7fff7fffu);
+  for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
   int m = max((int)(top & 0xffffu), (int)(top >> 16));
 #pragma unroll
   for (int o = kRowLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
