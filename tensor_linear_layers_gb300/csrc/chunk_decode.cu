@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<Q8>::kCtas) chunk_decode_k
               mma16816<false>(s, a2[0], a2[1], a2[2], a2[3], q.z, q.w);
             }
           }
-          // x: the weights' exponents; elements 0, 1 of key g, 2, 3 of key g + 8
+          // s, and v's exponent x: elements 0, 1 of key g, 2, 3 of key g + 8
           const bool partly = key + 15 > p0 || (window > 0 && key <= p1 - window && key + 15 >= sinks);
           if constexpr (Q8) {
             // k's scale before the row's factor where it is below one, after it where it is above, so that nothing on the
@@ -393,17 +393,20 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<Q8>::kCtas) chunk_decode_k
 #pragma unroll
             for (int h = 0; h < 4; ++h) s[h] *= h & 1 ? factor.y : factor.x;
           }
-          float x[4] = {s[0] + e0, s[1] + e0, s[2] + e1, s[3] + e1};
+          float x[4] = {e0, e0, e1, e1};
           if (partly) {
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
               const int j = key + g + (h >> 1) * 8, at = pos[h & 1];
-              if (!(j <= at && (window == 0 || j > at - window || j < sinks))) s[h] = x[h] = -INFINITY;
+              if (!(j <= at && (window == 0 || j > at - window || j < sinks))) {
+                s[h] = -INFINITY;
+                x[h] = 0.f;                                    // (v's scale may be NaN)
+              }
             }
           }
           float y[4];                                          // what m is taken from
 #pragma unroll
-          for (int h = 0; h < 4; ++h) y[h] = Q8 ? fmaxf(x[h], s[h] + kLeastExponent) : x[h];
+          for (int h = 0; h < 4; ++h) y[h] = Q8 ? s[h] + fmaxf(x[h], kLeastExponent) : s[h];
           const bool over = fmaxf(y[0], y[2]) > m[0] + (kRescaleLog2 - C::kHead) || fmaxf(y[1], y[3]) > m[1] + (kRescaleLog2 - C::kHead);
           if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -429,9 +432,11 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<Q8>::kCtas) chunk_decode_k
           float w[4];
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            const float mu = m[h & 1] == -INFINITY ? 0.f : m[h & 1];             // nothing seen yet: x = -inf, w = 0
-            w[h] = fast_exp2(x[h] - mu);
-            l[h & 1] += Q8 ? fast_exp2(s[h] - mu) : w[h];
+            const float mu = m[h & 1] == -INFINITY ? 0.f : m[h & 1];             // nothing seen yet: s = -inf, w = 0
+            const float p = fast_exp2(s[h] - mu);
+            // (v's exponent after the difference, which is small: beside a large score it would be rounded away)
+            w[h] = Q8 ? fast_exp2((s[h] - mu) + x[h]) : p;
+            l[h & 1] += p;
           }
           const uint32_t pb0 = transpose8(Q8 ? pack_f16x2(w[0], w[1]) : pack_bf16x2(w[0], w[1]));
           const uint32_t pb1 = transpose8(Q8 ? pack_f16x2(w[2], w[3]) : pack_bf16x2(w[2], w[3]));

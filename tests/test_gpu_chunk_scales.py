@@ -97,3 +97,54 @@ def test_slots_that_were_never_written_count_as_zeros(ctx, n, window, sinks):
     out, ws = run(handle(4, 2, 1), c, window, sinks)
     assert status(ws) == 0
     check(out, c, window, sinks)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("ctx,n", SIZES[:4] + [([900], [70])])
+def test_scores_of_millions(ctx, n, q8):
+    # scores up to 2^22, the largest that the interface names: the key with the largest takes all the weight. A score is off by
+    # 130 * 2^-24 of its products' sizes at most, far less than the two largest differ by (asserted); the weight's
+    # rounding to bf16 and the output's are 2^-8 each.
+    c = build(4, 2, 1, ctx, n, 16, seed=390 + n[0], q8=q8)
+    ck = caches64(c)[0]
+    heads = oracle.bf16_to_f64(c["qkv"]).reshape(c["T"], -1, 128)[:, :4]
+    slots = [oracle.slot_of(c["tables"], 0, j, 16) for j in range(c["lens"][0])]
+    keys = ck[0].reshape(-1, 2, 128)[slots].repeat(2, 1)
+    score = np.einsum("ihd,jhd->ihj", heads, keys) / np.sqrt(128)
+    power = int(np.floor(np.log2(2.0 ** 22 / np.abs(score).max())))
+    c["qkv"] = (c["qkv"].float() * 2.0 ** power).to(torch.bfloat16)
+    score *= 2.0 ** power
+    score[~(np.arange(c["lens"][0]) <= ctx[0] + np.arange(n[0])[:, None])[:, None].repeat(4, 1)] = -np.inf
+    best = np.sort(score, -1)[..., -2:]
+    size = np.einsum("ihd,jhd->ihj", np.abs(heads), np.abs(keys)).max() * 2.0 ** power / np.sqrt(128)
+    assert (best[..., 1] - best[..., 0]).min() > 4 * 130 * 2.0 ** -24 * size + 30
+    out, ws = run(handle(4, 2, 1), c)
+    assert status(ws) == 0
+    ref = oracle.chunk_attention(oracle.bf16_to_f64(c["qkv"]), c["qsl"], c["lens"], c["tables"], *caches64(c), 4, 2, 128, 1, 16)
+    assert (np.abs(out.double().cpu().numpy() - ref) <= (2 * 2.0 ** -8 + 2.0 ** -15) * np.abs(ref)).all()
+
+
+@pytest.mark.parametrize("exponent", [20, -20, 1])
+def test_a_scale_of_v_beside_a_large_score(exponent):
+    # requests of one token, which attends to itself: its output is its v, whatever the score is. Scores times log2(e) lie
+    # on both sides of 2^22, in steps of 1/4, where a sum with v's exponent loses a bit of them or more. The weight is
+    # rounded to f16 (2^-11 of it) and comes from an exponential that is good to 2^-20, the output is rounded to bf16.
+    reqs = 128
+    c = build(4, 2, 1, [0] * reqs, [1] * reqs, 16, seed=335, q8=True)
+    c["sv"] = torch.full_like(c["sv"], 127 + exponent)
+    c["sk"] = torch.full_like(c["sk"], 127)
+    c["ck"] = torch.full_like(c["ck"].view(torch.uint8), 0x38).view(torch.float8_e4m3fn)     # k = 1
+    q = torch.zeros(1, reqs, 4, 128)
+    for b in range(reqs):
+        rest = (2.0 ** 22 - 16 + b / 4) * np.sqrt(128) / np.log2(np.e)
+        for i in range(4):                                    # the score as a sum of four bf16 numbers
+            x = float(torch.tensor(rest).to(torch.bfloat16))
+            q[0, b, :, i] = x
+            rest -= x
+    c["qkv"].view(1, reqs, 8, 128)[:, :, :4] = q.to(torch.bfloat16)
+    out, ws = run(handle(4, 2, 1), c)
+    assert status(ws) == 0
+    v = caches64(c)[1]
+    slots = [oracle.slot_of(c["tables"], b, 0, 16) for b in range(reqs)]
+    want = v.reshape(-1, 2, 128)[slots].repeat(2, 1).reshape(1, reqs, 512)
+    assert (np.abs(out.double().cpu().numpy() - want) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(want)).all()
