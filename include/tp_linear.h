@@ -393,9 +393,11 @@ int tp_tree_attention(tp_linear_t* h, int64_t T, const void* qkv, const int32_t*
  *   code_i = e4m3(x_i * 2^-e), to nearest, ties to even, at most 448 in size
  * and stands for code_i * 2^e, exactly a bf16 number. A row with a NaN or an infinity gets scale
  * 255 and codes 0 and stands for NaN. Codes that are NaN (0x7f, 0xff), which no call here writes,
- * must not be in slots that are read. num_blocks, block_size: bounds as for tp_paged_attention;
- * codes 16-byte aligned, scales at any address. Status: workspace bytes [0, 4);
- * 16 bytes.
+ * must not be in slots that are read. Slots that were zero-filled and never written stand for
+ * zeros. num_blocks, block_size: bounds as for tp_paged_attention; codes 16-byte aligned, scales at
+ * any address. Status: workspace bytes [0, 4); 16 bytes. These two calls and tp_chunk_attention
+ * take such a cache; page copies and moves, tree and paged attention and the cache write of
+ * tp_qk_norm_rope take bf16 pages alone.
  *
  * tp_kv_quant_write: for every token i of qkv with slot_mapping[i] >= 0, the k and v heads of
  *   every shard quantised into that slot. A slot past the cache writes TP_ERR_SHAPE and is
@@ -424,13 +426,18 @@ int tp_kv_quant_read(tp_linear_t* h, int64_t n, const int32_t* slots, const void
  * Other arguments, layouts, bounds and errors as for tp_paged_attention; max_seq_len <= 2^26, at
  * most 256 q heads per kv head; attn_out and the workspace apart from what the call reads. Rows of
  * attn_out that belong to no request are left as they were. Scores, softmax and sums in fp32
- * (values of v under 2^137 / L, L the tokens seen, do not overflow), P rounded to bf16 for the
- * P V product (in 8 bits, where max_query_len makes at most eight query rows of a kv head, P times
- * v's scale to f16: 2^-11 of it down to 2^-21 of the row's largest, 2^-32 of the largest below, v's
- * scales under 2^-86 counted as that in the largest), output rounded to bf16. Slots of an 8-bit cache
- * that were zero-filled and never written stand for zeros. The workspace (tp_chunk_attention_workspace_size; caller-owned,
- * ZERO-FILLED before first use) holds the status word and partial results; one of larger bounds
- * serves too, and calls of any bounds that it serves may follow one another in it.
+ * (scores up to 2^22 in size and values of v under 2^137 / L, L the tokens seen, do not overflow), P
+ * rounded to bf16 for the P V product (in 8 bits, where max_query_len makes at most eight query rows
+ * of a kv head, P times v's scale to f16: 2^-11 of it down to 2^-21 of the row's largest, 2^-32 of
+ * the largest below, v's scales under 2^-86 counted as that in the largest; and q to f16 times a
+ * power of two per row: exact down to 2^-16 of the row's largest element, off by 2^-33 of that at
+ * most below), output rounded to bf16.
+ * The workspace (tp_chunk_attention_workspace_size; caller-owned, ZERO-FILLED before first use, and
+ * again after TP_ERR_TIMEOUT) holds the status word and partial results; one of larger bounds
+ * serves too, and calls of any bounds that it serves may follow one another in it. The kernel and
+ * the split of the work are chosen by max_query_len and max_seq_len: results are right for any
+ * bounds that hold, but bounds far above the requests cost time (one request of one token over 4000
+ * keys 12 us, 29 with max_query_len 4096; 64 requests of 300 keys 29, 34 with max_seq_len 8192).
  */
 int tp_chunk_attention_workspace_size(const tp_linear_t* h, int32_t n_reqs, int32_t max_query_len,
                                       int32_t max_seq_len, int64_t* bytes);

@@ -53,10 +53,10 @@ namespace tpl {
 // get the value added at the end.
 //
 // What bounds it, at two tiles. bf16: 1.63 us a chunk of 128 keys x 256 rows (2048 tokens over 32 049 keys 690 us,
-// 0.78 of what a large matrix product reaches): S by halves reads Q again for each, 48 cycles of shared memory an
+// 0.78 of what a large matrix product reaches; 725 to 740 where the power limit holds the clock): S by halves reads Q again for each, 48 cycles of shared memory an
 // MMA for 32 of products, and the softmax of 64 keys is a chain of some 1200 cycles after it, behind which two
 // buffers per tile hide most of that. (S by whole chunks, without that, takes turns with softmax and P V: 895 us.)
-// 8 bits: 1.88 us a chunk (793 us); 68 % of the issue slots go to the conversion and the softmax.
+// 8 bits: 1.88 to 1.96 us a chunk (793 to 828 us, by box and clock); 68 % of the issue slots go to the conversion and the softmax.
 // Code size counts here: all roles run at once, and with twenty warps' hot code beyond the SM's instruction cache
 // every chunk fetched it again from the cache that the SMs of a GPC share (8 bits: 1019 us; the SMs of the GPC that
 // has fewest ran 15 % faster). So loops that are seldom run or have time are rolled, each step of a role stands at
@@ -639,8 +639,8 @@ __global__ void __launch_bounds__(ChunkCfg<MT, Q8>::kThreads, 1)
     // ------------------------------------------------------------ copies
     regs_dec<C::kRegs1>();
     const int w4 = warp - 4;
-    // the cache is read once a call by one item (evicted first: 8 requests of 30 tokens over 4000 keys 38.3 us, 41.5
-    // without) or by its groups of rows
+    // the cache is read once a call by one item (evicted first: 8 requests of 30 new tokens each over 4000 keys 50.2 us,
+    // 52.4 without, 32 of 4 over 2000 keys 51.8 and 54.3) or by its groups of rows
     const uint64_t pol = p.call.max_query_len > p.call.tg ? policy_evict_normal() : policy_evict_first();
     int ring = 0;
     uint32_t ring_ph = 0;
@@ -1063,11 +1063,15 @@ __global__ void __launch_bounds__(32 * kMergeWarps) chunk_merge_kernel(const Chu
                             (it.g * gq + row - tok * gq) * kHd + 4 * lane) = out;
 }
 
-// Up to eight rows go to the warp-level kernel (chunk_decode.cu): one request of 4000 keys 12 us, 15 by tiles; 32
-// requests of 2000 keys in 8 bits 39 us, 57 by tiles. Tiles where they stream faster, in bf16, once the call has
-// an item for every SM and contexts are long: 32 requests of 2000 keys 55 us by warps, 52 by tiles, 48 of 4100 keys
-// of a window 69 and 67; but 64 requests of 300 keys 30 and 34. Up to 128 rows are one tile: 8 requests of 30 tokens
-// (120 rows) over 4000 keys 38 us in bf16 and 42 in 8 bits, 40 and 47 as two tiles.
+// Up to eight rows go to the warp-level kernel (chunk_decode.cu): one request of 4000 keys 12.4 us, 15.6 by tiles; 32
+// requests of 2000 keys in 8 bits 38 us, 57 by tiles. Tiles where they stream faster, in bf16, once the call has
+// an item for every SM and contexts are long: 32 requests of 2000 keys 53.9 us by warps, 50.0 by tiles, 48 of 4100 keys
+// of a window 73.4 and 71.0, 32 of 1100 keys 35.3 and 34.9; but 32 of 900 keys 31.3 and 32.5, 64 of 300 keys 29.3 and
+// 32.7. Up to 128 rows are one tile (every request with as many new tokens, 4 q heads per kv head; bf16, then 8 bits):
+//   8 requests of 30 tokens (120 rows) over 4000 keys  50.2 and 53.9 us as one tile, 51.7 and 56.9 as two
+//   8 of 16 (64 rows) over 4000                        40.7 and 44.6, 42.2 and 47.5
+//   32 of 4 (16 rows) over 2000                        51.8 and 57.5, 55.1 and 69.4
+// A call's bounds stand for its requests here: 64 requests of 300 keys in a call of up to 8192 keys take the tiles.
 int chunk_group_rows(int max_rows, bool q8, bool many, int max_keys) {
   if (max_rows <= 8 && (q8 || !many || max_keys < 1024)) return 8;
   return max_rows <= 128 ? 128 : 256;

@@ -20,9 +20,11 @@
 //   O = sum_j w_j code_j,   l = sum_j 2^(x_j - e_j - m)
 // with k's scale in the factor of the raw product. w is 2^7 at the row's largest x, at most 2^15 (m moves when a
 // row exceeds it by 2^8 more than it was taken at), and rounded to f16: 2^-11 of it down to 2^-21 of the
-// largest, 2^-32 of the largest below. (-86: slots that were never written have a scale of 2^-127, and keys of those
-// alone would take l to 2^134. Where all of v's scales are smaller, the largest w is smaller by as much.) q goes to f16 with a power of two per row that brings its largest
-// element to [2^8, 2^9): exact for elements down to 2^-16 of that, off by 2^-33 of it below.
+// largest, 2^-32 of the largest below. (-86: slots that were never written have a scale of 2^-127, and keys of
+// those alone would take l to 2^134. Where all of v's scales are smaller, the largest w is smaller by as much.)
+// q goes to f16 with a power of two per row that brings its largest element to [2^8, 2^9): exact for elements
+// down to 2^-16 of that, off by 2^-33 of it below.
+//
 // bf16: operands come through ldmatrix; m = max_j x_j + 17 as in chunk_attention.cu, w in bf16.
 //
 // Two CTAs of 128 registers per SM in 8 bits (one CTA: 32 requests of 2000 keys 48.5 us for 39.4, 4 x 131 072

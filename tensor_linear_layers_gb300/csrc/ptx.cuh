@@ -137,8 +137,8 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
-// 32-byte store to global memory (sm_100 and later); p 32-byte aligned.
-__device__ __forceinline__ void ld_global_v8_cg(float (&v)[8], const float* p) {   // 32-byte aligned, past L1
+// 32-byte accesses to global memory (sm_100 and later); p 32-byte aligned. The load goes past L1.
+__device__ __forceinline__ void ld_global_v8_cg(float (&v)[8], const float* p) {
   asm volatile("ld.global.cg.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                : "l"(p));

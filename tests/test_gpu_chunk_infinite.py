@@ -15,8 +15,8 @@ CASES = [  # nq, nkv, t, ctx, n
     (8, 2, 2, [6001], [1]), (8, 2, 2, [6001], [2]),         # their parts joined by a kernel
     (8, 2, 2, [60], [30]), (8, 2, 2, [60], [90]),           # one tile and two, whole
     (8, 2, 2, [6001], [30]), (8, 2, 2, [6001], [90]),       # their parts joined by a kernel
-    (8, 8, 1, [1500] * 24, [30] * 24), (16, 8, 1, [1500] * 24, [90] * 24),             # two or three parts of an item, joined by the CTAs
-    (32, 8, 4, [20000] + [0] * 39, [30] + [1] * 39), (32, 8, 4, [20000] + [0] * 39, [70] + [1] * 39),   # more than eight parts
+    (8, 8, 1, [700] * 20, [30] * 20), (16, 8, 1, [700] * 20, [90] * 20),             # two or three parts of an item, joined by the CTAs
+    (32, 8, 4, [9000] + [0] * 39, [30] + [1] * 39), (32, 8, 4, [9000] + [0] * 39, [70] + [1] * 39),   # more than eight parts
 ]
 
 
@@ -31,7 +31,7 @@ def below(x):
 
 
 @pytest.mark.parametrize("q8", [False, True])
-@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 3)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (500, 3)])
 @pytest.mark.parametrize("case", range(len(CASES)))
 def test_a_token_whose_scores_are_all_minus_infinity(case, window, sinks, q8):
     nq, nkv, t, ctx, n = CASES[case]
